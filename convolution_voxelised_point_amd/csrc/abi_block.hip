@@ -1,0 +1,180 @@
+// C entry points of the voxel-transformer operators: host-side validation,
+// workspace layout and the choice of how a walk is cut up.
+#include <cmath>
+
+#include "attn.h"
+
+using namespace ts;
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
+
+bool divides16(int64_t v) { return v % 8 == 0; }
+bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool at8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
+
+ts_status check_attn(const ts_attn* at) {
+  if (!at) return TS_ERR_INVALID_ARG;
+  if (at->dtype != TS_F32 && at->dtype != TS_F16 && at->dtype != TS_BF16) return TS_ERR_INVALID_ARG;
+  if (at->hq < 1 || at->hk < 1 || at->d < 1 || at->hq % at->hk != 0) return TS_ERR_INVALID_ARG;
+  if (at->nq < 0 || at->nk < 0 || at->n_sets < 0) return TS_ERR_INVALID_ARG;
+  if (!std::isfinite(at->scale) || !std::isfinite(at->cap) || at->cap < 0.f) return TS_ERR_INVALID_ARG;
+  if (at->dtype == TS_F32 || at->d > 128) return TS_ERR_UNSUPPORTED;
+  if (at->hq > (1 << 16) || at->nq > kMaxRows / at->hq || at->nk > kMaxRows / at->hk || at->n_sets > kMaxRows)
+    return TS_ERR_UNSUPPORTED;
+  const int64_t qw = static_cast<int64_t>(at->hq) * at->d, kw = static_cast<int64_t>(at->hk) * at->d;
+  if (at->q_stride < qw || at->o_stride < qw || at->k_stride < kw || at->v_stride < kw) return TS_ERR_INVALID_ARG;
+  if (!at->q_starts || (!at->k_starts && at->nk != at->nq)) return TS_ERR_INVALID_ARG;
+  if (at->slopes) {
+    if (at->ndim != 2 && at->ndim != 3) return TS_ERR_INVALID_ARG;
+    if (at->nq > 0 && !at->q_coords) return TS_ERR_INVALID_ARG;
+    if (at->nk > 0 && !at->k_coords && (!at->q_coords || at->nk != at->nq)) return TS_ERR_INVALID_ARG;
+  }
+  return TS_OK;
+}
+
+int padded_width(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
+
+// How the walk over `other` rows for `own` rows (both counted over all sets,
+// the heads that share a key head included) is cut up.
+AttnPlan plan_walk(int64_t own, int64_t other, int64_t n_sets, int hk, int dp, bool may_share, int max_nc) {
+  AttnPlan p{64, 1, 1, false};
+  const int64_t sets = n_sets > 0 ? n_sets : 1;
+  const int64_t own_per = ceil_div(own, sets), other_per = other / sets;
+  if (may_share && own_per <= 16) {
+    p.share_keys = true;
+    p.bm = 16;
+  } else if (max_nc >= 2 && own_per >= 256 && ceil_div<int64_t>(own, 128) * hk >= 512) {
+    p.nc = 2;
+    p.bm = 128;
+  }
+  const int64_t tiles = ceil_div<int64_t>(own, p.bm);
+  const int64_t blocks = (tiles > n_sets ? tiles : n_sets < own ? n_sets : own) * hk;
+  int64_t s = blocks > 0 ? 512 / blocks : 1;
+  const int64_t most = other_per / 256;
+  if (s > most) s = most;
+  if (s > kAttnMaxSplits) s = kAttnMaxSplits;
+  p.splits = s < 2 ? 1 : static_cast<int>(s);
+  return p;
+}
+
+AttnPlan plan_fwd(const ts_attn* at) {
+  const int dp = padded_width(at->d);
+  return plan_walk(at->nq * (at->hq / at->hk), at->nk, at->n_sets, at->hk, dp, true, dp <= 64 ? 2 : 1);
+}
+AttnPlan plan_dkv(const ts_attn* at) {
+  const int dp = padded_width(at->d);
+  return plan_walk(at->nk, at->nq * (at->hq / at->hk), at->n_sets, at->hk, dp, false, dp <= 32 ? 2 : 1);
+}
+
+size_t part_floats(const ts_attn* at, const AttnPlan& p, int64_t rows, int extra) {
+  return p.splits > 1 ? static_cast<size_t>(p.splits) * rows * (padded_width(at->d) + extra) : 0;
+}
+
+size_t fwd_bytes(const ts_attn* at) { return part_floats(at, plan_fwd(at), at->nq * at->hq, 2) * 4; }
+
+size_t delta_bytes(const ts_attn* at) { return align_up(static_cast<size_t>(at->nq) * at->hq * 4, 256); }
+size_t bwd_bytes(const ts_attn* at) {
+  const size_t q = part_floats(at, plan_fwd(at), at->nq * at->hq, 0);
+  const size_t k = 2 * part_floats(at, plan_dkv(at), at->nk * at->hk, 0);
+  return delta_bytes(at) + (q > k ? q : k) * 4;
+}
+
+bool grid_ok(const ts_attn* at, const AttnPlan& p, int64_t n, int64_t mul) {
+  return attn_tiles(n, mul, p.bm, at->n_sets) <= kMaxRows / (static_cast<int64_t>(at->hk) * p.splits);
+}
+
+AttnArgs attn_args(const ts_attn* at, const void* q, const void* k, const void* v, uint32_t* flags) {
+  AttnArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.qs = at->q_starts;
+  a.ks = at->k_starts ? at->k_starts : at->q_starts;
+  a.slopes = at->slopes;
+  a.qc = at->q_coords;
+  a.kc = at->k_coords ? at->k_coords : at->q_coords;
+  a.flags = flags;
+  a.nq = at->nq;
+  a.nk = at->nk;
+  a.n_sets = at->n_sets;
+  a.q_stride = at->q_stride;
+  a.k_stride = at->k_stride;
+  a.v_stride = at->v_stride;
+  a.o_stride = at->o_stride;
+  a.hq = at->hq;
+  a.hk = at->hk;
+  a.grp = at->hq / at->hk;
+  a.d = at->d;
+  a.ndim = at->ndim;
+  a.scale = at->scale;
+  if (at->cap > 0.f) {
+    a.c1 = 2.f * kLog2e * at->scale / at->cap;
+    a.c2 = at->cap * kLog2e;
+  } else {
+    a.c1 = at->scale * kLog2e;
+  }
+  const bool strides8 = divides16(at->q_stride) && divides16(at->k_stride) && divides16(at->v_stride) &&
+                        divides16(at->o_stride) && at->d % 8 == 0;
+  a.vec_in = strides8 && at16(q) && at16(k) && at16(v);
+  a.vec_out = at->d % 4 == 0 && at->q_stride % 4 == 0 && at->k_stride % 4 == 0 && at->v_stride % 4 == 0 &&
+              at->o_stride % 4 == 0;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ts_attn_workspace_bytes(const ts_attn* at, int backward) {
+  if (check_attn(at) != TS_OK) return 0;
+  return backward ? bwd_bytes(at) : fwd_bytes(at);
+}
+
+ts_status ts_attn_fwd(const ts_attn* at, const void* q, const void* k, const void* v, void* out, float* lse, void* ws,
+                      size_t ws_bytes, uint32_t* err_flags, hipStream_t stream) {
+  const ts_status st = check_attn(at);
+  if (st != TS_OK) return st;
+  if ((at->nq > 0 && (!q || !out || !lse)) || (at->nk > 0 && (!k || !v))) return TS_ERR_INVALID_ARG;
+  const size_t need = fwd_bytes(at);
+  if (need > 0 && (!ws || ws_bytes < need || !at16(ws))) return TS_ERR_INVALID_ARG;
+  const AttnPlan p = plan_fwd(at);
+  const int grp = at->hq / at->hk;
+  if (!grid_ok(at, p, at->nq, grp)) return TS_ERR_UNSUPPORTED;
+  if (at->nq == 0) return TS_OK;
+  AttnArgs a = attn_args(at, q, k, v, err_flags);
+  a.out = out;
+  a.lse = lse;
+  a.vec_out = a.vec_out && at8(out);
+  a.part = static_cast<float*>(ws);
+  a.part_ml = a.part + static_cast<size_t>(p.splits) * at->nq * at->hq * padded_width(at->d);
+  return launch_attn_fwd(a, p, at->dtype, at->cap > 0.f, stream) == hipSuccess ? TS_OK : TS_ERR_HIP;
+}
+
+ts_status ts_attn_bwd(const ts_attn* at, const void* q, const void* k, const void* v, const void* out,
+                      const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                      uint32_t* err_flags, hipStream_t stream) {
+  const ts_status st = check_attn(at);
+  if (st != TS_OK) return st;
+  if ((at->nq > 0 && (!q || !out || !lse || !dout || !dq)) || (at->nk > 0 && (!k || !v || !dk || !dv)))
+    return TS_ERR_INVALID_ARG;
+  const size_t need = bwd_bytes(at);
+  if (need > 0 && (!ws || ws_bytes < need || !at16(ws))) return TS_ERR_INVALID_ARG;
+  const AttnPlan pq = plan_fwd(at), pk = plan_dkv(at);
+  if (!grid_ok(at, pq, at->nq, at->hq / at->hk) || !grid_ok(at, pk, at->nk, 1)) return TS_ERR_UNSUPPORTED;
+  AttnArgs a = attn_args(at, q, k, v, err_flags);
+  a.o = out;
+  a.dout = dout;
+  a.lse = const_cast<float*>(lse);
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.vec_in = a.vec_in && at16(out) && at16(dout);
+  a.vec_out = a.vec_out && at8(dq) && at8(dk) && at8(dv);
+  a.delta = static_cast<float*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(at));
+  return launch_attn_bwd(a, pq, pk, at->dtype, at->cap > 0.f, stream) == hipSuccess ? TS_OK : TS_ERR_HIP;
+}
+
+}  // extern "C"

@@ -123,4 +123,16 @@ size_t wgrad_workspace_bytes(const ts_kmap* map, int cin, int cout);
 hipError_t launch_wgrad(const ts_kmap* map, const void* x, int cin, const void* dy, int cout, ts_dtype dt, float* dw,
                         void* ws, hipStream_t s);
 
+// attn_fwd.hip, attn_bwd.hip
+struct AttnArgs;
+constexpr int kAttnMaxSplits = 512;
+// How a walk is cut up: columns per block, column blocks per wave, whether the
+// waves of a block share one column block, and parts of the other side.
+struct AttnPlan {
+  int bm, nc, splits;
+  bool share_keys;
+};
+hipError_t launch_attn_fwd(AttnArgs& a, const AttnPlan& p, ts_dtype dt, bool cap, hipStream_t s);
+hipError_t launch_attn_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, ts_dtype dt, bool cap, hipStream_t s);
+
 }  // namespace ts

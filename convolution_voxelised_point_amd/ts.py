@@ -11,6 +11,7 @@ ask for and keep them alive next to the C structs that point into them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -59,6 +60,14 @@ class TsKmap(ctypes.Structure):
                 ("scratch", _vp), ("scratch_bytes", _sz)]
 
 
+class TsAttn(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("hq", ctypes.c_int32), ("hk", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("ndim", ctypes.c_int32), ("scale", ctypes.c_float), ("cap", ctypes.c_float), ("nq", _i64),
+                ("nk", _i64), ("n_sets", _i64), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64),
+                ("o_stride", _i64), ("q_starts", _vp), ("k_starts", _vp), ("slopes", _vp), ("q_coords", _vp),
+                ("k_coords", _vp)]
+
+
 def _sig(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -105,6 +114,10 @@ _lib_pool_fwd = _sig("ts_pool_fwd", _i32, [_P, _vp, _i32, _vp, _i32, _i32, _i32,
 _lib_conv_bwd_dgrad = _sig("ts_conv_bwd_dgrad", _i32, [_P, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _sz, _vp])
 _lib_conv_bwd_wgrad = _sig("ts_conv_bwd_wgrad", _i32, [_P, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _sz, _vp])
 _lib_conv_bwd_dgrad_noalloc = _sig("ts_conv_bwd_dgrad_noalloc", _i32, [_P, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _vp])
+_A = ctypes.POINTER(TsAttn)
+_lib_attn_workspace_bytes = _sig("ts_attn_workspace_bytes", _sz, [_A, _i32])
+_lib_attn_fwd = _sig("ts_attn_fwd", _i32, [_A, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp])
+_lib_attn_bwd = _sig("ts_attn_bwd", _i32, [_A, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp])
 _lib_debug_violations = _sig("ts_debug_violations", _i32, [ctypes.POINTER(_u32)])
 
 EXPORTED = ["ts_status_string", "ts_version", "ts_hash_capacity", "ts_hash_table_bytes", "ts_hash_build",
@@ -113,7 +126,8 @@ EXPORTED = ["ts_status_string", "ts_version", "ts_hash_capacity", "ts_hash_table
             "ts_devoxelize", "ts_kmap_bytes", "ts_kmap_build",
             "ts_conv_workspace_bytes", "ts_conv_pack_weights", "ts_conv_fwd", "ts_subm_conv_fwd", "ts_conv_fwd_strided",
             "ts_conv_fwd_generative", "ts_conv_transpose_fwd", "ts_pool_fwd", "ts_graph_conv_fwd", "ts_conv_bwd_dgrad",
-            "ts_conv_bwd_wgrad", "ts_conv_bwd_dgrad_noalloc", "ts_debug_violations"]
+            "ts_conv_bwd_wgrad", "ts_conv_bwd_dgrad_noalloc", "ts_attn_workspace_bytes", "ts_attn_fwd", "ts_attn_bwd",
+            "ts_debug_violations"]
 
 
 class TsError(RuntimeError):
@@ -132,6 +146,22 @@ def _p(t: Optional[torch.Tensor]):
         return None
     assert t.is_cuda and t.is_contiguous(), "device tensors must be contiguous CUDA/HIP tensors"
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t: torch.Tensor):
+    """Rows of [n][heads][d], the heads of a row adjacent."""
+    assert t.is_cuda and _row_stride(t) is not None, "device tensors [n][heads][d] with adjacent heads"
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _row_stride(t: torch.Tensor) -> Optional[int]:
+    """Elements between the rows of [n][heads][d], or None where the heads of a row are not adjacent."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        return None
+    width = t.shape[1] * t.shape[2]
+    if t.shape[0] <= 1:
+        return width
+    return t.stride(0) if t.stride(0) >= width else None
 
 
 def _stream(stream=None):
@@ -330,6 +360,22 @@ def ts_conv_bwd_dgrad_noalloc(kmap, dy, w, dx, stream=None) -> None:
 def ts_conv_bwd_wgrad(kmap, x, dy, dw, ws, stream=None) -> None:
     _check(_lib_conv_bwd_wgrad(ctypes.byref(kmap), _p(x), x.shape[1], _p(dy), dy.shape[1], _dt(x), _p(dw), _p(ws),
                                ws.numel(), _stream(stream)), "ts_conv_bwd_wgrad")
+
+
+def ts_attn_workspace_bytes(at: TsAttn, backward: bool) -> int:
+    return int(_lib_attn_workspace_bytes(ctypes.byref(at), 1 if backward else 0))
+
+
+def ts_attn_fwd(at: TsAttn, q, k, v, out, lse, ws=None, err_flags=None, stream=None) -> None:
+    """q, k, v, out: rows `at.*_stride` elements apart."""
+    _check(_lib_attn_fwd(ctypes.byref(at), _rows(q), _rows(k), _rows(v), _rows(out), _p(lse), _p(ws),
+                         0 if ws is None else ws.numel(), _p(err_flags), _stream(stream)), "ts_attn_fwd")
+
+
+def ts_attn_bwd(at: TsAttn, q, k, v, out, lse, dout, dq, dk, dv, ws, err_flags=None, stream=None) -> None:
+    _check(_lib_attn_bwd(ctypes.byref(at), _rows(q), _rows(k), _rows(v), _rows(out), _p(lse), _rows(dout), _rows(dq),
+                         _rows(dk), _rows(dv), _p(ws), 0 if ws is None else ws.numel(), _p(err_flags),
+                         _stream(stream)), "ts_attn_bwd")
 
 
 # ---------------------------------------------------------------- owners of buffers
@@ -597,3 +643,85 @@ def conv_wgrad(kmap: Kmap, x: torch.Tensor, dy: torch.Tensor, ws=None, stream=No
         ws = workspace(kmap, x.shape[1], dy.shape[1], TS_OP_WGRAD, x.dtype)
     ts_conv_bwd_wgrad(kmap.s, x, dy, dw, ws, stream)
     return dw
+
+
+# ---------------------------------------------------------------- voxel-transformer operators
+def _on(stream):
+    """Buffers of a call on another stream come from that stream's pool, so
+    that a freed workspace is not handed out while the call still runs."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise TsError(TS_ERR_INVALID_ARG, what)
+
+
+def attn_args(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch.Tensor,
+              k_starts: Optional[torch.Tensor] = None, scale: Optional[float] = None, cap: float = 0.0,
+              slopes: Optional[torch.Tensor] = None, q_coords: Optional[torch.Tensor] = None,
+              k_coords: Optional[torch.Tensor] = None, o_stride: Optional[int] = None) -> TsAttn:
+    """The C description of an attention call, its tensors checked against
+    each other.  scale defaults to 1 / sqrt(d); o_stride to dense rows."""
+    strides = [_row_stride(t) if t.dim() == 3 and t.is_cuda else None for t in (q, k, v)]
+    _need(None not in strides, "attention: q, k, v are device tensors [n][heads][d] with adjacent heads")
+    nq, hq, d = q.shape
+    nk, hk = k.shape[0], k.shape[1]
+    _need(v.shape == k.shape and k.shape[2] == d and q.dtype == k.dtype == v.dtype and q.dtype in _DT,
+          "attention: q, k, v differ in width, type or keys")
+    for s in (q_starts, k_starts):
+        _need(s is None or (s.is_cuda and s.dtype == torch.int64 and s.dim() == 1 and s.is_contiguous()
+                            and s.shape[0] == q_starts.shape[0] >= 1), "attention: starts are int64 [n_sets + 1]")
+    ndim = 3
+    if slopes is not None:
+        _need(slopes.is_cuda and slopes.dtype == torch.float32 and slopes.is_contiguous() and slopes.numel() == hq,
+              "attention: slopes are float32 [hq]")
+        _need(q_coords is not None, "attention: slopes need coordinates")
+        ndim = q_coords.shape[1] - 1
+        for c, n in ((q_coords, nq), (q_coords if k_coords is None else k_coords, nk)):
+            _need(c.is_cuda and c.dtype == torch.int32 and c.is_contiguous() and tuple(c.shape) == (n, ndim + 1),
+                  "attention: coordinates are int32 [n][ndim + 1]")
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    return TsAttn(_DT[q.dtype], hq, hk, d, ndim, 1.0 / d ** 0.5 if scale is None else scale, cap, nq, nk,
+                  q_starts.shape[0] - 1, *strides, hq * d if o_stride is None else o_stride, ptr(q_starts),
+                  ptr(k_starts), ptr(slopes), ptr(q_coords) if slopes is not None else None,
+                  ptr(k_coords) if slopes is not None else None)
+
+
+def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch.Tensor,
+             k_starts: Optional[torch.Tensor] = None, scale: Optional[float] = None, cap: float = 0.0,
+             slopes: Optional[torch.Tensor] = None, q_coords: Optional[torch.Tensor] = None,
+             k_coords: Optional[torch.Tensor] = None, err_flags: Optional[torch.Tensor] = None,
+             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(out [nq][hq][d], lse [nq][hq]): attention of each packed set's rows
+    over its own keys (see ts_attn in ts.h)."""
+    at = attn_args(q, k, v, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords)
+    with _on(stream):
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        n = ts_attn_workspace_bytes(at, False)
+        ws = _bytes(n, q.device) if n else None
+        ts_attn_fwd(at, q, k, v, out, lse, ws, err_flags, stream)
+    return out, lse
+
+
+def attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+             lse: torch.Tensor, q_starts: torch.Tensor, k_starts: Optional[torch.Tensor] = None,
+             scale: Optional[float] = None, cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+             q_coords: Optional[torch.Tensor] = None, k_coords: Optional[torch.Tensor] = None,
+             err_flags: Optional[torch.Tensor] = None,
+             stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dq, dk, dv) of attn_fwd with the same arguments, laid out like q, k, v."""
+    _need(out.shape == q.shape and dout.shape == q.shape and out.dtype == dout.dtype == q.dtype,
+          "attention: out and dout are like q")
+    _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:2],
+          "attention: lse is float32 [nq][hq]")
+    with _on(stream):
+        if _row_stride(dout) != _row_stride(out):
+            dout = dout.contiguous()
+            out = out.contiguous()
+        at = attn_args(q, k, v, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords, _row_stride(out))
+        dq, dk, dv = (torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device) for t in (q, k, v))
+        ws = _bytes(ts_attn_workspace_bytes(at, True), q.device)
+        ts_attn_bwd(at, q, k, v, out, lse, dout, dq, dk, dv, ws, err_flags, stream)
+    return dq, dk, dv

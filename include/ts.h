@@ -529,6 +529,73 @@ ts_status ts_conv_bwd_dgrad_noalloc(const ts_kmap* map, const void* dy, int cout
                                     ts_dtype in_dtype, ts_dtype out_dtype, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Voxel-transformer operators: attention within sets of voxels, the residual
+ * root-mean-square norm, and activations kept in 8 bits for the backward
+ * pass.  They stand beside the convolutions over the same row-major feature
+ * matrices; nothing in the pages prescribes them.
+ *
+ * Attention.  Rows of packed sets attend to the keys of their own set: set s
+ * owns query rows [q_starts[s], q_starts[s+1]) and key rows [k_starts[s],
+ * k_starts[s+1]).  For query row i, query head h, key head h / (hq / hk) and
+ * the keys j of i's set:
+ *   z_j = scale * q_i . k_j
+ *   z_j = cap * tanh(z_j / cap)                        (cap > 0)
+ *   z_j = z_j - slopes[h] * |c_i - c_j|                (slopes given)
+ *   out_i = sum_j softmax(z)_j v_j,    lse[i][h] = log sum_j exp(z_j)
+ * |c_i - c_j| is the Euclidean distance of the voxel coordinates (batch column
+ * left out), formed in float32.  slopes are constants of the call (no gradient);
+ * cap and slopes are optional.  A query row without keys, or whose scores are
+ * all -inf, and a query row that no set owns, get zeros, lse = -inf and zero
+ * gradients; so do keys that no query of theirs sees.
+ *
+ * Starts that decrease or leave [0, nq] / [0, nk] raise TS_FLAG_RANGE in
+ * err_flags (may be NULL): no access leaves the buffers, the results are
+ * undefined.
+ *
+ * Rows: q [nq][hq][d], k and v [nk][hk][d], out [nq][hq][d] with the heads of
+ * a row adjacent and rows `*_stride` elements apart (>= heads * d), so q, k, v
+ * may be columns of one projected matrix.  16-byte aligned operands with d and
+ * strides in multiples of 8 are read in 16-byte accesses; anything else works
+ * element by element.  fp16 or bf16 (TS_F32 is TS_ERR_UNSUPPORTED), 1 <= d <=
+ * 128, hk divides hq; products are accumulated in fp32, softmax statistics are
+ * fp32, probabilities and score gradients are rounded to the feature type for
+ * their products.  With fp16, score gradients below 2^-24 vanish and above
+ * 65504 overflow, as in any fp16 backward pass: scale the loss.
+ * ---------------------------------------------------------------------- */
+typedef struct ts_attn {
+  ts_dtype dtype;          /* of q, k, v, out and the gradients                   */
+  int32_t hq, hk, d;       /* query heads, key-value heads, head width            */
+  int32_t ndim;            /* 2 or 3; read with slopes only                       */
+  float scale, cap;        /* cap 0: scores are not capped                        */
+  int64_t nq, nk, n_sets;
+  int64_t q_stride, k_stride, v_stride, o_stride; /* elements between rows        */
+  const int64_t* q_starts; /* device [n_sets + 1]                                 */
+  const int64_t* k_starts; /* device [n_sets + 1]; NULL: q_starts (then nk == nq) */
+  const float* slopes;     /* device [hq], or NULL                                */
+  const int32_t* q_coords; /* device [nq][ndim + 1]; read with slopes only        */
+  const int32_t* k_coords; /* device [nk][ndim + 1]; NULL: q_coords (nk == nq)    */
+} ts_attn;
+
+/* Workspace bytes of ts_attn_fwd (backward 0) or ts_attn_bwd (backward 1); 0 is
+ * a valid answer.  It depends on the sizes only, not on the starts. */
+size_t ts_attn_workspace_bytes(const ts_attn* at, int backward);
+
+/* out [nq][hq][d] (o_stride) and lse (device float [nq][hq]); every row is
+ * written once.  Errors: TS_ERR_INVALID_ARG (null pointers, sizes, strides,
+ * a short workspace, scale or cap not finite, cap < 0), TS_ERR_UNSUPPORTED
+ * (fp32, d > 128, more than 2^31 - 1 rows times heads), TS_ERR_HIP. */
+ts_status ts_attn_fwd(const ts_attn* at, const void* q, const void* k, const void* v, void* out, float* lse, void* ws,
+                      size_t ws_bytes, uint32_t* err_flags, hipStream_t stream);
+
+/* Gradients of ts_attn_fwd from its out and lse and the gradient dout of out:
+ * dq, dk, dv with the rows and strides of q, k, v (dout those of out), every
+ * row written once; a shared key head gets the sum over its query heads.  No
+ * atomics: the same bits on every run.  Errors as ts_attn_fwd. */
+ts_status ts_attn_bwd(const ts_attn* at, const void* q, const void* k, const void* v, const void* out,
+                      const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                      uint32_t* err_flags, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Bounds-check build.  The library also builds as libts_debug.so, compiled
  * with TS_DEBUG_CHECKS: there the contraction, pooling and weight-gradient
  * kernels check every row index they read from a map (neighbour entries,
