@@ -2,6 +2,7 @@
 // workspace layout and the choice of how a walk is cut up.
 #include <cmath>
 
+#include "act8.h"
 #include "attn.h"
 
 using namespace ts;
@@ -82,7 +83,8 @@ size_t bwd_bytes(const ts_attn* at) {
 }
 
 bool grid_ok(const ts_attn* at, const AttnPlan& p, int64_t n, int64_t mul) {
-  return attn_tiles(n, mul, p.bm, at->n_sets) <= kMaxRows / (static_cast<int64_t>(at->hk) * p.splits);
+  // fewer than 2^24 blocks of 256 threads: a launch may have 2^32 threads
+  return attn_tiles(n, mul, p.bm, at->n_sets) < (int64_t{1} << 24) / (static_cast<int64_t>(at->hk) * p.splits);
 }
 
 AttnArgs attn_args(const ts_attn* at, const void* q, const void* k, const void* v, uint32_t* flags) {
@@ -121,6 +123,16 @@ AttnArgs attn_args(const ts_attn* at, const void* q, const void* k, const void* 
   a.vec_out = at->d % 4 == 0 && at->q_stride % 4 == 0 && at->k_stride % 4 == 0 && at->v_stride % 4 == 0 &&
               at->o_stride % 4 == 0;
   return a;
+}
+
+bool dtype_ok(int d) { return d == TS_F32 || d == TS_F16 || d == TS_BF16; }
+
+bool rows_ok(int64_t n, int c, ts_dtype dtype) {
+  return n >= 0 && n <= kMaxRows && c >= 1 && c <= (1 << 16) && dtype_ok(dtype);
+}
+bool act_ok(const ts_act8* a) { return a && a->codes && a->scales; }
+Act8 act_view(const ts_act8* a, int c) {
+  return a ? Act8{a->codes, a->scales, c % 8 == 0 && at8(a->codes)} : Act8{nullptr, nullptr, false};
 }
 
 }  // namespace
@@ -175,6 +187,65 @@ ts_status ts_attn_bwd(const ts_attn* at, const void* q, const void* k, const voi
   a.delta = static_cast<float*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(at));
   return launch_attn_bwd(a, pq, pk, at->dtype, at->cap > 0.f, stream) == hipSuccess ? TS_OK : TS_ERR_HIP;
+}
+
+ts_status ts_act_pack(const void* x, int64_t n, int c, ts_dtype dtype, const ts_act8* a, hipStream_t stream) {
+  if (!rows_ok(n, c, dtype)) return TS_ERR_INVALID_ARG;
+  if (n > 0 && (!x || !act_ok(a))) return TS_ERR_INVALID_ARG;
+  return launch_act_pack(x, n, c, dtype, act_view(a, c), stream) == hipSuccess ? TS_OK : TS_ERR_HIP;
+}
+
+ts_status ts_act_unpack(const ts_act8* a, int64_t n, int c, void* x, ts_dtype dtype, hipStream_t stream) {
+  if (!rows_ok(n, c, dtype)) return TS_ERR_INVALID_ARG;
+  if (n > 0 && (!x || !act_ok(a))) return TS_ERR_INVALID_ARG;
+  return launch_act_unpack(act_view(a, c), n, c, x, dtype, stream) == hipSuccess ? TS_OK : TS_ERR_HIP;
+}
+
+size_t ts_conv_wgrad_act8_workspace_bytes(const ts_kmap* map, int cin, int cout) {
+  if (!map || map->n_in < 0 || cin < 1 || cout < 1) return 0;
+  return align_up(static_cast<size_t>(map->n_in) * cin * 2, 256) +
+         ts_conv_workspace_bytes(map, cin, cout, TS_OP_WGRAD, TS_F16, TS_DATAFLOW_AUTO);
+}
+
+ts_status ts_conv_bwd_wgrad_act8(const ts_kmap* map, const ts_act8* x, int cin, const void* dy, int cout,
+                                 ts_dtype dtype, float* dw, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!map || !dtype_ok(dtype) || cin < 1 || cout < 1) return TS_ERR_INVALID_ARG;
+  if (dtype == TS_F32) return TS_ERR_UNSUPPORTED;
+  if ((map->n_in > 0 && !act_ok(x)) || !ws || ws_bytes < ts_conv_wgrad_act8_workspace_bytes(map, cin, cout))
+    return TS_ERR_INVALID_ARG;
+  const size_t xb = align_up(static_cast<size_t>(map->n_in) * cin * 2, 256);
+  const ts_status st = ts_act_unpack(x, map->n_in, cin, ws, dtype, stream);
+  if (st != TS_OK) return st;
+  return ts_conv_bwd_wgrad(map, ws, cin, dy, cout, dtype, dw, static_cast<char*>(ws) + xb, ws_bytes - xb, stream);
+}
+
+ts_status ts_norm_fwd(const void* x, const void* residual, const float* w, int64_t n, int c, float eps,
+                      ts_dtype dtype, void* h, void* y, float* rstd, const ts_act8* y8, const ts_act8* h8,
+                      hipStream_t stream) {
+  if (!rows_ok(n, c, dtype)) return TS_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.f || (n > 0 && (!x || !w))) return TS_ERR_INVALID_ARG;
+  if (!h && !y && !y8 && !h8) return TS_ERR_INVALID_ARG;
+  if (n > 0 && ((y8 && !act_ok(y8)) || (h8 && !act_ok(h8)))) return TS_ERR_INVALID_ARG;
+  return launch_norm_fwd(x, residual, w, n, c, eps, dtype, h, y, rstd, act_view(y8, c), act_view(h8, c), stream) ==
+                 hipSuccess
+             ? TS_OK
+             : TS_ERR_HIP;
+}
+
+size_t ts_norm_workspace_bytes(int64_t n, int c) {
+  return rows_ok(n, c, TS_F32) ? norm_workspace_bytes(n, c) : 0;
+}
+
+ts_status ts_norm_bwd(const void* dy, const void* h, const ts_act8* h8, const float* w, const float* rstd,
+                      const void* dh, int64_t n, int c, ts_dtype dtype, void* dx, float* dw, void* ws,
+                      size_t ws_bytes, hipStream_t stream) {
+  if (!rows_ok(n, c, dtype)) return TS_ERR_INVALID_ARG;
+  if (!dw || (n > 0 && (!dy || !w || !rstd || !dx || (h != nullptr) == (h8 != nullptr) || (h8 && !act_ok(h8)))))
+    return TS_ERR_INVALID_ARG;
+  if (n > 0 && (!ws || ws_bytes < norm_workspace_bytes(n, c))) return TS_ERR_INVALID_ARG;
+  return launch_norm_bwd(dy, h, act_view(h8, c), w, rstd, dh, n, c, dtype, dx, dw, ws, stream) == hipSuccess
+             ? TS_OK
+             : TS_ERR_HIP;
 }
 
 }  // extern "C"

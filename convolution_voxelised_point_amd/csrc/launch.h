@@ -135,4 +135,15 @@ struct AttnPlan {
 hipError_t launch_attn_fwd(AttnArgs& a, const AttnPlan& p, ts_dtype dt, bool cap, hipStream_t s);
 hipError_t launch_attn_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, ts_dtype dt, bool cap, hipStream_t s);
 
+// act8.hip, norm.hip
+struct Act8;
+hipError_t launch_act_pack(const void* x, int64_t n, int c, ts_dtype dt, const Act8& a, hipStream_t s);
+hipError_t launch_act_unpack(const Act8& a, int64_t n, int c, void* x, ts_dtype dt, hipStream_t s);
+size_t norm_workspace_bytes(int64_t n, int c);
+hipError_t launch_norm_fwd(const void* x, const void* res, const float* w, int64_t n, int c, float eps, ts_dtype dt,
+                           void* h, void* y, float* rstd, const Act8& y8, const Act8& h8, hipStream_t s);
+hipError_t launch_norm_bwd(const void* dy, const void* h, const Act8& h8, const float* w, const float* rstd,
+                           const void* dh, int64_t n, int c, ts_dtype dt, void* dx, float* dw, void* ws,
+                           hipStream_t s);
+
 }  // namespace ts

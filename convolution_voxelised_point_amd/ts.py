@@ -14,7 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple, Union
 
 import numpy as np
 import torch
@@ -39,6 +39,7 @@ TS_OP_FWD, TS_OP_DGRAD, TS_OP_WGRAD, TS_OP_TRANSPOSE = 0, 1, 2, 3
 TS_POOL_MAX, TS_POOL_AVG = 0, 1
 TS_TILE, TS_GTILE, TS_MAX_KVOL = 16, 128, 64
 TS_NOALLOC_SCRATCH_BYTES = 4 << 20
+TS_ACT8_BLOCK = 32
 TS_DEBUG_SRC_ROW, TS_DEBUG_DST_ROW = 1, 2
 
 _DT = {torch.float32: TS_F32, torch.float16: TS_F16, torch.bfloat16: TS_BF16}
@@ -66,6 +67,10 @@ class TsAttn(ctypes.Structure):
                 ("nk", _i64), ("n_sets", _i64), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64),
                 ("o_stride", _i64), ("q_starts", _vp), ("k_starts", _vp), ("slopes", _vp), ("q_coords", _vp),
                 ("k_coords", _vp)]
+
+
+class TsAct8(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp)]
 
 
 def _sig(name, res, args):
@@ -118,6 +123,14 @@ _A = ctypes.POINTER(TsAttn)
 _lib_attn_workspace_bytes = _sig("ts_attn_workspace_bytes", _sz, [_A, _i32])
 _lib_attn_fwd = _sig("ts_attn_fwd", _i32, [_A, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp])
 _lib_attn_bwd = _sig("ts_attn_bwd", _i32, [_A, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp])
+_C = ctypes.POINTER(TsAct8)
+_lib_act_pack = _sig("ts_act_pack", _i32, [_vp, _i64, _i32, _i32, _C, _vp])
+_lib_act_unpack = _sig("ts_act_unpack", _i32, [_C, _i64, _i32, _vp, _i32, _vp])
+_lib_conv_wgrad_act8_workspace_bytes = _sig("ts_conv_wgrad_act8_workspace_bytes", _sz, [_P, _i32, _i32])
+_lib_conv_bwd_wgrad_act8 = _sig("ts_conv_bwd_wgrad_act8", _i32, [_P, _C, _i32, _vp, _i32, _i32, _vp, _vp, _sz, _vp])
+_lib_norm_fwd = _sig("ts_norm_fwd", _i32, [_vp, _vp, _vp, _i64, _i32, ctypes.c_float, _i32, _vp, _vp, _vp, _C, _C, _vp])
+_lib_norm_workspace_bytes = _sig("ts_norm_workspace_bytes", _sz, [_i64, _i32])
+_lib_norm_bwd = _sig("ts_norm_bwd", _i32, [_vp, _vp, _C, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _sz, _vp])
 _lib_debug_violations = _sig("ts_debug_violations", _i32, [ctypes.POINTER(_u32)])
 
 EXPORTED = ["ts_status_string", "ts_version", "ts_hash_capacity", "ts_hash_table_bytes", "ts_hash_build",
@@ -127,7 +140,8 @@ EXPORTED = ["ts_status_string", "ts_version", "ts_hash_capacity", "ts_hash_table
             "ts_conv_workspace_bytes", "ts_conv_pack_weights", "ts_conv_fwd", "ts_subm_conv_fwd", "ts_conv_fwd_strided",
             "ts_conv_fwd_generative", "ts_conv_transpose_fwd", "ts_pool_fwd", "ts_graph_conv_fwd", "ts_conv_bwd_dgrad",
             "ts_conv_bwd_wgrad", "ts_conv_bwd_dgrad_noalloc", "ts_attn_workspace_bytes", "ts_attn_fwd", "ts_attn_bwd",
-            "ts_debug_violations"]
+            "ts_act_pack", "ts_act_unpack", "ts_conv_wgrad_act8_workspace_bytes", "ts_conv_bwd_wgrad_act8", "ts_norm_fwd",
+            "ts_norm_workspace_bytes", "ts_norm_bwd", "ts_debug_violations"]
 
 
 class TsError(RuntimeError):
@@ -376,6 +390,41 @@ def ts_attn_bwd(at: TsAttn, q, k, v, out, lse, dout, dq, dk, dv, ws, err_flags=N
     _check(_lib_attn_bwd(ctypes.byref(at), _rows(q), _rows(k), _rows(v), _rows(out), _p(lse), _rows(dout), _rows(dq),
                          _rows(dk), _rows(dv), _p(ws), 0 if ws is None else ws.numel(), _p(err_flags),
                          _stream(stream)), "ts_attn_bwd")
+
+
+def _act(a: "Optional[Act8]"):
+    return None if a is None else ctypes.byref(TsAct8(a.codes.data_ptr(), a.scales.data_ptr()))
+
+
+def ts_act_pack(x, a: "Act8", stream=None) -> None:
+    _check(_lib_act_pack(_p(x), x.shape[0], x.shape[1], _dt(x), _act(a), _stream(stream)), "ts_act_pack")
+
+
+def ts_act_unpack(a: "Act8", x, stream=None) -> None:
+    _check(_lib_act_unpack(_act(a), x.shape[0], x.shape[1], _p(x), _dt(x), _stream(stream)), "ts_act_unpack")
+
+
+def ts_conv_wgrad_act8_workspace_bytes(kmap: TsKmap, cin: int, cout: int) -> int:
+    return int(_lib_conv_wgrad_act8_workspace_bytes(ctypes.byref(kmap), cin, cout))
+
+
+def ts_conv_bwd_wgrad_act8(kmap, x: "Act8", dy, dw, ws, stream=None) -> None:
+    _check(_lib_conv_bwd_wgrad_act8(ctypes.byref(kmap), _act(x), x.codes.shape[1], _p(dy), dy.shape[1], _dt(dy), _p(dw),
+                                    _p(ws), ws.numel(), _stream(stream)), "ts_conv_bwd_wgrad_act8")
+
+
+def ts_norm_fwd(x, residual, w, eps, h=None, y=None, rstd=None, y8=None, h8=None, stream=None) -> None:
+    _check(_lib_norm_fwd(_p(x), _p(residual), _p(w), x.shape[0], x.shape[1], eps, _dt(x), _p(h), _p(y), _p(rstd),
+                         _act(y8), _act(h8), _stream(stream)), "ts_norm_fwd")
+
+
+def ts_norm_workspace_bytes(n: int, c: int) -> int:
+    return int(_lib_norm_workspace_bytes(n, c))
+
+
+def ts_norm_bwd(dy, h, h8, w, rstd, dh, dx, dw, ws, stream=None) -> None:
+    _check(_lib_norm_bwd(_p(dy), _p(h), _act(h8), _p(w), _p(rstd), _p(dh), dy.shape[0], dy.shape[1], _dt(dy), _p(dx),
+                         _p(dw), _p(ws), 0 if ws is None else ws.numel(), _stream(stream)), "ts_norm_bwd")
 
 
 # ---------------------------------------------------------------- owners of buffers
@@ -725,3 +774,107 @@ def attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
         ws = _bytes(ts_attn_workspace_bytes(at, True), q.device)
         ts_attn_bwd(at, q, k, v, out, lse, dout, dq, dk, dv, ws, err_flags, stream)
     return dq, dk, dv
+
+
+class Act8(NamedTuple):
+    """Activations in 8 bits: codes int8 [n][c], scales uint8 [n][ceil(c / 32)]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @classmethod
+    def empty(cls, n: int, c: int, device) -> "Act8":
+        return cls(torch.empty((n, c), dtype=torch.int8, device=device),
+                   torch.empty((n, -(-c // TS_ACT8_BLOCK)), dtype=torch.uint8, device=device))
+
+    def check(self, n: int, c: int) -> None:
+        _need(self.codes.dtype == torch.int8 and self.scales.dtype == torch.uint8 and self.codes.is_cuda
+              and self.scales.is_cuda and self.codes.is_contiguous() and self.scales.is_contiguous()
+              and tuple(self.codes.shape) == (n, c) and tuple(self.scales.shape) == (n, -(-c // TS_ACT8_BLOCK)),
+              f"8-bit activations of [{n}][{c}]: codes int8 [n][c], scales uint8 [n][ceil(c / 32)]")
+
+
+def _matrix(t: torch.Tensor, what: str, shape=None, dtype=None) -> None:
+    _need(t.is_cuda and t.dim() == 2 and t.is_contiguous() and t.dtype in _DT and (shape is None or t.shape == shape)
+          and (dtype is None or t.dtype == dtype), f"{what}: a dense device matrix [n][c] of the call's shape and type")
+
+
+def act_pack(x: torch.Tensor, stream=None) -> Act8:
+    """x [n][c] in 8 bits (see ts_act8 in ts.h)."""
+    _matrix(x, "act_pack")
+    with _on(stream):
+        a = Act8.empty(x.shape[0], x.shape[1], x.device)
+        ts_act_pack(x, a, stream)
+    return a
+
+
+def act_unpack(a: Act8, dtype: torch.dtype, stream=None) -> torch.Tensor:
+    """The values `a` stands for; exact in every feature type."""
+    a.check(*a.codes.shape)
+    _need(dtype in _DT, "act_unpack: a feature type")
+    with _on(stream):
+        x = torch.empty(a.codes.shape, dtype=dtype, device=a.codes.device)
+        ts_act_unpack(a, x, stream)
+    return x
+
+
+def conv_wgrad_act8(kmap: Kmap, x: Act8, dy: torch.Tensor, stream=None) -> torch.Tensor:
+    """conv_wgrad with the layer's input kept in 8 bits."""
+    cin = x.codes.shape[1]
+    x.check(kmap.s.n_in, cin)
+    _matrix(dy, "conv_wgrad_act8")
+    _need(dy.shape[0] >= kmap.s.n_out_cap, "conv_wgrad_act8: dy has the map's output rows")
+    with _on(stream):
+        dw = torch.empty((kmap.kvol, cin, dy.shape[1]), dtype=torch.float32, device=dy.device)
+        ws = _bytes(ts_conv_wgrad_act8_workspace_bytes(kmap.s, cin, dy.shape[1]), dy.device)
+        ts_conv_bwd_wgrad_act8(kmap.s, x, dy, dw, ws, stream)
+    return dw
+
+
+class Norm(NamedTuple):
+    """Results of norm_fwd: h (x itself without a residual), and those asked for."""
+    h: torch.Tensor
+    y: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+    y8: Optional[Act8]
+    h8: Optional[Act8]
+
+
+def norm_fwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             want_y: bool = True, want_rstd: bool = True, y8: bool = False, h8: bool = False, stream=None) -> Norm:
+    """Root-mean-square norm of x + residual (see ts_norm_fwd in ts.h)."""
+    _matrix(x, "norm_fwd")
+    n, c = x.shape
+    if residual is not None:
+        _matrix(residual, "norm_fwd residual", x.shape, x.dtype)
+    _need(w.is_cuda and w.dtype == torch.float32 and w.is_contiguous() and w.numel() == c, "norm_fwd: w is float32 [c]")
+    with _on(stream):
+        h = None if residual is None else torch.empty_like(x)
+        y = torch.empty_like(x) if want_y else None
+        rstd = torch.empty(n, dtype=torch.float32, device=x.device) if want_rstd else None
+        q = [Act8.empty(n, c, x.device) if want else None for want in (y8, h8)]
+        ts_norm_fwd(x, residual, w, eps, h, y, rstd, *q, stream)
+    return Norm(x if h is None else h, y, rstd, *q)
+
+
+def norm_bwd(dy: torch.Tensor, h: Union[torch.Tensor, Act8], w: torch.Tensor, rstd: torch.Tensor,
+             dh: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dw) of norm_fwd from h or its 8-bit form; dx is also the residual's
+    gradient, dh the gradient that reaches h past the norm."""
+    _matrix(dy, "norm_bwd")
+    n, c = dy.shape
+    if isinstance(h, Act8):
+        h.check(n, c)
+    else:
+        _matrix(h, "norm_bwd h", dy.shape, dy.dtype)
+    if dh is not None:
+        _matrix(dh, "norm_bwd dh", dy.shape, dy.dtype)
+    for t, m in ((w, c), (rstd, n)):
+        _need(t.is_cuda and t.dtype == torch.float32 and t.is_contiguous() and t.numel() == m,
+              "norm_bwd: w is float32 [c], rstd float32 [n]")
+    with _on(stream):
+        dx = torch.empty_like(dy)
+        dw = torch.empty(c, dtype=torch.float32, device=dy.device)
+        ws = _bytes(ts_norm_workspace_bytes(n, c), dy.device)
+        full, eight = (None, h) if isinstance(h, Act8) else (h, None)
+        ts_norm_bwd(dy, full, eight, w, rstd, dh, dx, dw, ws, stream)
+    return dx, dw

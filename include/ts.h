@@ -583,7 +583,8 @@ size_t ts_attn_workspace_bytes(const ts_attn* at, int backward);
 /* out [nq][hq][d] (o_stride) and lse (device float [nq][hq]); every row is
  * written once.  Errors: TS_ERR_INVALID_ARG (null pointers, sizes, strides,
  * a short workspace, scale or cap not finite, cap < 0), TS_ERR_UNSUPPORTED
- * (fp32, d > 128, more than 2^31 - 1 rows times heads), TS_ERR_HIP. */
+ * (fp32, d > 128, more than 2^31 - 1 rows times heads, more than 2^24 tiles of
+ * 64 rows, sets counted as at least one), TS_ERR_HIP. */
 ts_status ts_attn_fwd(const ts_attn* at, const void* q, const void* k, const void* v, void* out, float* lse, void* ws,
                       size_t ws_bytes, uint32_t* err_flags, hipStream_t stream);
 
@@ -594,6 +595,59 @@ ts_status ts_attn_fwd(const ts_attn* at, const void* q, const void* k, const voi
 ts_status ts_attn_bwd(const ts_attn* at, const void* q, const void* k, const void* v, const void* out,
                       const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
                       uint32_t* err_flags, hipStream_t stream);
+
+/* Activations in 8 bits, kept from the forward pass for the backward pass.
+ * Blocks of TS_ACT8_BLOCK consecutive channels of a row (the last one may be
+ * shorter) share a power-of-two quantum 2^(e - 127),
+ *   e = max(floor(log2(max |x|)) + 127 - 6, 1),
+ * kept as the byte e; a value is held as clamp(rint(x / quantum), -127, 127)
+ * (half to even), so it is off by at most quantum (max|x| / 64; half of it below
+ * 127 quanta).  A power of two costs up to one bit against max|x| / 127, and
+ * makes the held value exactly representable in every feature type: reading a
+ * checkpoint back never rounds.  A block that holds an infinity or a NaN gets
+ * byte 255 and reads back as NaN, so an overflow is not hidden. */
+#define TS_ACT8_BLOCK 32
+typedef struct ts_act8 {
+  int8_t* codes;   /* device [n][c]                        */
+  uint8_t* scales; /* device [n][ceil(c / TS_ACT8_BLOCK)]  */
+} ts_act8;
+
+/* Packs x[n][c] (device, row-major) into *a, and back.  Errors:
+ * TS_ERR_INVALID_ARG (null pointers, n < 0 or > 2^31 - 1, c outside
+ * [1, 65536], a type that is none), TS_ERR_HIP. */
+ts_status ts_act_pack(const void* x, int64_t n, int c, ts_dtype dtype, const ts_act8* a, hipStream_t stream);
+ts_status ts_act_unpack(const ts_act8* a, int64_t n, int c, void* x, ts_dtype dtype, hipStream_t stream);
+
+/* ts_conv_bwd_wgrad with x read from a checkpoint (n_in rows of cin channels):
+ * dy in dtype (fp16 or bf16; TS_F32 is TS_ERR_UNSUPPORTED), dw fp32, the same
+ * sums as over the unpacked x.  ws holds ts_conv_wgrad_act8_workspace_bytes. */
+size_t ts_conv_wgrad_act8_workspace_bytes(const ts_kmap* map, int cin, int cout);
+ts_status ts_conv_bwd_wgrad_act8(const ts_kmap* map, const ts_act8* x, int cin, const void* dy, int cout,
+                                 ts_dtype dtype, float* dw, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Root-mean-square norm of rows, with the residual's addition:
+ *   h = x + residual, rounded to dtype (h = x without residual)
+ *   rstd = 1 / sqrt(mean(h^2) + eps),   y = h * rstd * w
+ * x, residual, h, y: device [n][c] in dtype (fp32, fp16 or bf16); w: device
+ * float [c].  Outputs, each optional but at least one of y, y8, h8 and h given:
+ * h, y, rstd (device float [n]), and 8-bit forms of y and of h (y8, h8): y8
+ * for a layer that keeps its input in 8 bits, h8 for ts_norm_bwd.  y8 is of y
+ * before its rounding to dtype.  h and y may be x or residual themselves.
+ * Errors: TS_ERR_INVALID_ARG (null pointers, n < 0 or > 2^31 - 1, c outside
+ * [1, 65536], eps negative or not finite), TS_ERR_HIP. */
+ts_status ts_norm_fwd(const void* x, const void* residual, const float* w, int64_t n, int c, float eps,
+                      ts_dtype dtype, void* h, void* y, float* rstd, const ts_act8* y8, const ts_act8* h8,
+                      hipStream_t stream);
+
+/* Its backward pass from dy, and from h or its 8-bit form h8 (exactly one):
+ *   xn = h * rstd;  dx = rstd * (dy w - xn mean(dy w xn)) + dh;  dw = sum over rows of dy xn
+ * dx is the gradient of x and of the residual; dh (may be NULL) is the gradient
+ * that reaches h past the norm.  dw: device float [c], overwritten; no atomics.
+ * dx may be dy or dh itself.  ws holds ts_norm_workspace_bytes(n, c). */
+size_t ts_norm_workspace_bytes(int64_t n, int c);
+ts_status ts_norm_bwd(const void* dy, const void* h, const ts_act8* h8, const float* w, const float* rstd,
+                      const void* dh, int64_t n, int c, ts_dtype dtype, void* dx, float* dw, void* ws,
+                      size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Bounds-check build.  The library also builds as libts_debug.so, compiled
