@@ -9,9 +9,14 @@ using namespace ts;
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
+#define TS_TRY(expr)                        \
+  do {                                      \
+    if ((expr) != hipSuccess) return TS_ERR_HIP; \
+  } while (0)
 
-bool divides16(int64_t v) { return v % 8 == 0; }
+constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxStride = int64_t{1} << 23;
+
 bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool at8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
 
@@ -22,9 +27,12 @@ ts_status check_attn(const ts_attn* at) {
   if (at->nq < 0 || at->nk < 0 || at->n_sets < 0) return TS_ERR_INVALID_ARG;
   if (!std::isfinite(at->scale) || !std::isfinite(at->cap) || at->cap < 0.f) return TS_ERR_INVALID_ARG;
   if (at->dtype == TS_F32 || at->d > 128) return TS_ERR_UNSUPPORTED;
-  if (at->hq > (1 << 16) || at->nq > kMaxRows / at->hq || at->nk > kMaxRows / at->hk || at->n_sets > kMaxRows)
+  if (at->hq > 65535 || at->nq > kMaxRows / at->hq || at->nk > kMaxRows / at->hk || at->n_sets > kMaxRows)
     return TS_ERR_UNSUPPORTED;
   const int64_t qw = static_cast<int64_t>(at->hq) * at->d, kw = static_cast<int64_t>(at->hk) * at->d;
+  // a tile's row offsets are 32-bit
+  if (at->q_stride > kMaxStride || at->k_stride > kMaxStride || at->v_stride > kMaxStride || at->o_stride > kMaxStride)
+    return TS_ERR_UNSUPPORTED;
   if (at->q_stride < qw || at->o_stride < qw || at->k_stride < kw || at->v_stride < kw) return TS_ERR_INVALID_ARG;
   if (!at->q_starts || (!at->k_starts && at->nk != at->nq)) return TS_ERR_INVALID_ARG;
   if (at->slopes) {
@@ -40,18 +48,22 @@ int padded_width(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
 // How the walk over `other` rows for `own` rows (both counted over all sets,
 // the heads that share a key head included) is cut up.
 AttnPlan plan_walk(int64_t own, int64_t other, int64_t n_sets, int hk, int dp, bool may_share, int max_nc) {
-  AttnPlan p{64, 1, 1, false};
+  AttnPlan p{64, 1, 1, 1, false};
   const int64_t sets = n_sets > 0 ? n_sets : 1;
   const int64_t own_per = ceil_div(own, sets), other_per = other / sets;
   if (may_share && own_per <= 16) {
     p.share_keys = true;
     p.bm = 16;
-  } else if (max_nc >= 2 && own_per >= 256 && ceil_div<int64_t>(own, 128) * hk >= 512) {
+  } else if (max_nc >= 2 && own_per >= 512 && ceil_div<int64_t>(own, 128) * hk >= 512) {
     p.nc = 2;
     p.bm = 128;
+  } else if (dp <= 64 && other_per <= 512) {
+    // as many heads as leave 1024 blocks
+    const int64_t tiles = ceil_div(own, int64_t{64}) > n_sets ? ceil_div(own, int64_t{64}) : n_sets;
+    while (p.heads < 4 && p.heads * 2 <= hk && tiles * (hk / (p.heads * 2)) >= 1024) p.heads *= 2;
   }
   const int64_t tiles = ceil_div<int64_t>(own, p.bm);
-  const int64_t blocks = (tiles > n_sets ? tiles : n_sets < own ? n_sets : own) * hk;
+  const int64_t blocks = (tiles > n_sets ? tiles : n_sets < own ? n_sets : own) * ceil_div(hk, p.heads);
   int64_t s = blocks > 0 ? 512 / blocks : 1;
   const int64_t most = other_per / 256;
   if (s > most) s = most;
@@ -73,18 +85,61 @@ size_t part_floats(const ts_attn* at, const AttnPlan& p, int64_t rows, int extra
   return p.splits > 1 ? static_cast<size_t>(p.splits) * rows * (padded_width(at->d) + extra) : 0;
 }
 
-size_t fwd_bytes(const ts_attn* at) { return part_floats(at, plan_fwd(at), at->nq * at->hq, 2) * 4; }
+// The kernels read rows in 16-byte pieces.  Where the head width or a stride does
+// not allow that, the operands are copied to dense rows of heads of a multiple of
+// 8 elements in the workspace, and the results copied back.
+bool repacks(const ts_attn* at) {
+  return ((at->d | at->q_stride | at->k_stride | at->v_stride | at->o_stride) & 7) != 0;
+}
+int width8(const ts_attn* at) { return (at->d + 7) / 8 * 8; }
+size_t q_copy_bytes(const ts_attn* at) {
+  return align_up(static_cast<size_t>(at->nq) * at->hq * width8(at) * 2, 256);
+}
+size_t k_copy_bytes(const ts_attn* at) {
+  return align_up(static_cast<size_t>(at->nk) * at->hk * width8(at) * 2, 256);
+}
 
+// q, out; k, v
+size_t fwd_bytes(const ts_attn* at) {
+  return (repacks(at) ? 2 * q_copy_bytes(at) + 2 * k_copy_bytes(at) : 0) +
+         part_floats(at, plan_fwd(at), at->nq * at->hq, 2) * 4;
+}
+
+// q, out, dout, dq; k, v, dk, dv
 size_t delta_bytes(const ts_attn* at) { return align_up(static_cast<size_t>(at->nq) * at->hq * 4, 256); }
 size_t bwd_bytes(const ts_attn* at) {
   const size_t q = part_floats(at, plan_fwd(at), at->nq * at->hq, 0);
   const size_t k = 2 * part_floats(at, plan_dkv(at), at->nk * at->hk, 0);
-  return delta_bytes(at) + (q > k ? q : k) * 4;
+  return (repacks(at) ? 4 * q_copy_bytes(at) + 4 * k_copy_bytes(at) : 0) + delta_bytes(at) + (q > k ? q : k) * 4;
 }
 
+// fewer than 2^24 blocks of 256 threads along x: a launch dimension may have 2^32 threads
 bool grid_ok(const ts_attn* at, const AttnPlan& p, int64_t n, int64_t mul) {
-  // fewer than 2^24 blocks of 256 threads: a launch may have 2^32 threads
-  return attn_tiles(n, mul, p.bm, at->n_sets) < (int64_t{1} << 24) / (static_cast<int64_t>(at->hk) * p.splits);
+  return attn_tiles(n, mul, p.bm, at->n_sets) < (int64_t{1} << 24) - 64;
+}
+
+struct Carver {
+  char* base;
+  size_t off = 0;
+  void* take(size_t bytes) {
+    void* p = base + off;
+    off += bytes;
+    return p;
+  }
+};
+// *p (n rows of `heads` heads) copied into the workspace; *p and *new_stride then name the copy.
+hipError_t copy_in(const ts_attn* at, int heads, int64_t n, int64_t stride, const void** p, int64_t* new_stride,
+                   Carver& c, hipStream_t s) {
+  const int d8 = width8(at);
+  *new_stride = static_cast<int64_t>(heads) * d8;
+  void* dst = c.take(align_up(static_cast<size_t>(n) * *new_stride * 2, 256));
+  const void* src = *p;
+  *p = dst;
+  return launch_attn_repack(src, stride, at->d, dst, *new_stride, d8, n, heads, s);
+}
+hipError_t copy_out(const ts_attn* at, const void* src, int heads, int64_t n, void* dst, int64_t stride, hipStream_t s) {
+  const int d8 = width8(at);
+  return launch_attn_repack(src, static_cast<int64_t>(heads) * d8, d8, dst, stride, at->d, n, heads, s);
 }
 
 AttnArgs attn_args(const ts_attn* at, const void* q, const void* k, const void* v, uint32_t* flags) {
@@ -111,17 +166,13 @@ AttnArgs attn_args(const ts_attn* at, const void* q, const void* k, const void* 
   a.d = at->d;
   a.ndim = at->ndim;
   a.scale = at->scale;
+  a.negate = at->scale < 0.f;
   if (at->cap > 0.f) {
-    a.c1 = 2.f * kLog2e * at->scale / at->cap;
+    a.c1 = 2.f * kLog2e * fabsf(at->scale) / at->cap;
     a.c2 = at->cap * kLog2e;
   } else {
-    a.c1 = at->scale * kLog2e;
+    a.c1 = fabsf(at->scale) * kLog2e;
   }
-  const bool strides8 = divides16(at->q_stride) && divides16(at->k_stride) && divides16(at->v_stride) &&
-                        divides16(at->o_stride) && at->d % 8 == 0;
-  a.vec_in = strides8 && at16(q) && at16(k) && at16(v);
-  a.vec_out = at->d % 4 == 0 && at->q_stride % 4 == 0 && at->k_stride % 4 == 0 && at->v_stride % 4 == 0 &&
-              at->o_stride % 4 == 0;
   return a;
 }
 
@@ -158,10 +209,22 @@ ts_status ts_attn_fwd(const ts_attn* at, const void* q, const void* k, const voi
   AttnArgs a = attn_args(at, q, k, v, err_flags);
   a.out = out;
   a.lse = lse;
-  a.vec_out = a.vec_out && at8(out);
-  a.part = static_cast<float*>(ws);
+  Carver c{static_cast<char*>(ws)};
+  if (repacks(at)) {
+    TS_TRY(copy_in(at, at->hq, at->nq, at->q_stride, &a.q, &a.q_stride, c, stream));
+    TS_TRY(copy_in(at, at->hk, at->nk, at->k_stride, &a.k, &a.k_stride, c, stream));
+    TS_TRY(copy_in(at, at->hk, at->nk, at->v_stride, &a.v, &a.v_stride, c, stream));
+    a.out = c.take(q_copy_bytes(at));
+    a.o_stride = static_cast<int64_t>(at->hq) * width8(at);
+    a.d = width8(at);
+  } else if (!at16(q) || !at16(k) || !at16(v) || !at8(out)) {
+    return TS_ERR_INVALID_ARG;
+  }
+  a.part = static_cast<float*>(c.take(0));
   a.part_ml = a.part + static_cast<size_t>(p.splits) * at->nq * at->hq * padded_width(at->d);
-  return launch_attn_fwd(a, p, at->dtype, at->cap > 0.f, stream) == hipSuccess ? TS_OK : TS_ERR_HIP;
+  TS_TRY(launch_attn_fwd(a, p, at->dtype, at->cap > 0.f, stream));
+  if (repacks(at)) TS_TRY(copy_out(at, a.out, at->hq, at->nq, out, at->o_stride, stream));
+  return TS_OK;
 }
 
 ts_status ts_attn_bwd(const ts_attn* at, const void* q, const void* k, const void* v, const void* out,
@@ -182,11 +245,29 @@ ts_status ts_attn_bwd(const ts_attn* at, const void* q, const void* k, const voi
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  a.vec_in = a.vec_in && at16(out) && at16(dout);
-  a.vec_out = a.vec_out && at8(dq) && at8(dk) && at8(dv);
-  a.delta = static_cast<float*>(ws);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(at));
-  return launch_attn_bwd(a, pq, pk, at->dtype, at->cap > 0.f, stream) == hipSuccess ? TS_OK : TS_ERR_HIP;
+  Carver c{static_cast<char*>(ws)};
+  if (repacks(at)) {
+    TS_TRY(copy_in(at, at->hq, at->nq, at->q_stride, &a.q, &a.q_stride, c, stream));
+    TS_TRY(copy_in(at, at->hq, at->nq, at->o_stride, &a.o, &a.o_stride, c, stream));
+    TS_TRY(copy_in(at, at->hq, at->nq, at->o_stride, &a.dout, &a.o_stride, c, stream));
+    TS_TRY(copy_in(at, at->hk, at->nk, at->k_stride, &a.k, &a.k_stride, c, stream));
+    TS_TRY(copy_in(at, at->hk, at->nk, at->v_stride, &a.v, &a.v_stride, c, stream));
+    a.dq = c.take(q_copy_bytes(at));
+    a.dk = c.take(k_copy_bytes(at));
+    a.dv = c.take(k_copy_bytes(at));
+    a.d = width8(at);
+  } else if (!at16(q) || !at16(k) || !at16(v) || !at16(out) || !at16(dout) || !at8(dq) || !at8(dk) || !at8(dv)) {
+    return TS_ERR_INVALID_ARG;
+  }
+  a.delta = static_cast<float*>(c.take(delta_bytes(at)));
+  a.part = static_cast<float*>(c.take(0));
+  TS_TRY(launch_attn_bwd(a, pq, pk, at->dtype, at->cap > 0.f, stream));
+  if (repacks(at)) {
+    TS_TRY(copy_out(at, a.dq, at->hq, at->nq, dq, at->q_stride, stream));
+    TS_TRY(copy_out(at, a.dk, at->hk, at->nk, dk, at->k_stride, stream));
+    TS_TRY(copy_out(at, a.dv, at->hk, at->nk, dv, at->v_stride, stream));
+  }
+  return TS_OK;
 }
 
 ts_status ts_act_pack(const void* x, int64_t n, int c, ts_dtype dtype, const ts_act8* a, hipStream_t stream) {

@@ -93,33 +93,11 @@ __device__ __forceinline__ typename AMfma<T>::frag tile_frag_t(const char* tile,
                                                                  tile + tile_at<DP>(r + 16, ch) + half));
 }
 
-// Elements d0..d0+7 of a row of d elements (zeros past d).  vec: the row is
-// 16-byte aligned and d is a multiple of 8.
+// 4 consecutive results of a row, d0 a multiple of 4.
 template <typename T>
-__device__ __forceinline__ u32x4 load8(const T* row, int d0, int d, bool vec) {
-  u32x4 v{0u, 0u, 0u, 0u};
-  if (vec) {
-    if (d0 < d) v = *reinterpret_cast<const u32x4*>(row + d0);
-  } else {
-    typename AMfma<T>::frag f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = d0 + e < d ? row[d0 + e] : static_cast<T>(0.f);
-    v = __builtin_bit_cast(u32x4, f);
-  }
-  return v;
-}
-
-// 4 consecutive results of a row, d0 a multiple of 4.  vec: 8-byte aligned rows.
-template <typename T>
-__device__ __forceinline__ void store4(T* row, int d0, int d, bool vec, f32x4 x) {
+__device__ __forceinline__ void store4(T* row, int d0, int d, f32x4 x) {
   typedef T t4 __attribute__((ext_vector_type(4)));
-  if (vec) {
-    if (d0 < d) *reinterpret_cast<t4*>(row + d0) = __builtin_convertvector(x, t4);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (d0 + e < d) row[d0 + e] = static_cast<T>(x[e]);
-  }
+  if (d0 < d) *reinterpret_cast<t4*>(row + d0) = __builtin_convertvector(x, t4);
 }
 
 // x of the lane 32 away and 16 away combined with this lane's: the two halves
@@ -159,6 +137,7 @@ __device__ __forceinline__ float col_sum(float x) {
   return a + b;
 }
 
+// (heads: query head = kvh * grp + its place among those that share kvh)
 struct AttnArgs {
   const void *q, *k, *v, *o, *dout;
   void *out, *dq, *dk, *dv;
@@ -169,11 +148,12 @@ struct AttnArgs {
   const int32_t *qc, *kc;
   uint32_t* flags;
   int64_t nq, nk, n_sets, q_stride, k_stride, v_stride, o_stride, tiles;
-  int hq, hk, grp, d, ndim, splits;
-  // score s = scale q.k in units of log 2: without a cap z = c1 s'; with one
-  // z = c2 tanh(..) written with exp2(c1 s')
+  int hq, hk, grp, d, ndim, splits, heads;  // heads: key-value heads a block takes, one after the other
+  // scores in units of log 2 from s = q.k: c1 s, or with a cap
+  // c2 tanh(scale s / cap) = c2 - 2 c2 / (exp2(c1 s) + 1); c1 is made of |scale|,
+  // and negate says that q enters with its sign turned
   float c1, c2, scale;
-  bool vec_in, vec_out;
+  bool negate;
 };
 
 // Rows of set i, counted with an empty-keyed set before the first and after
@@ -196,30 +176,50 @@ struct SetTile {
   int64_t st0, st_len;       // the other side's rows of the set
 };
 
-// The set and tile of slot t (the same on every lane), by a search that reads
-// 64 boundaries at a time; false for a slot without rows.
+// The set and tile of slot t (the same on every lane); false for a slot without
+// rows.  Each step reads 64 boundaries at once: first the 64 about where sets of
+// equal length would put the slot, which holds it when lengths vary at random,
+// then evenly spaced ones over what is left of either side.  The ends of the set
+// are among the boundaries read last.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const int64_t* own, int64_t n_own, int mul, const int64_t* st, int64_t n_st,
-                                          int64_t n_sets, int64_t t, SetTile* r) {
-  int64_t lo = 0, hi = n_sets + 2;  // slot(lo) <= t < slot(hi)
+                                          int64_t n_sets, int64_t t, int64_t slots, SetTile* r) {
+  if (t >= slots) return false;
   const int lane = threadIdx.x & 63;
-  while (hi - lo > 1) {
-    const int64_t step = (hi - lo + 63) / 64;
-    const int64_t i = lo + lane * step;
-    const bool in = i < hi && set_bound(own, n_sets, n_own, i) * mul / BM + i <= t;
-    const int c = __popcll(__ballot(in));
-    const int64_t at = lo + (c > 0 ? c - 1 : 0) * step;
-    lo = at;
-    if (at + step < hi) hi = at + step;
+  int64_t lo = 0, hi = n_sets + 2;  // slot(lo) <= t < slot(hi)
+  int64_t at = static_cast<int64_t>(static_cast<float>(t) / static_cast<float>(slots) * static_cast<float>(hi)) - 31;
+  at = at < 0 ? 0 : at > hi - 63 ? (hi > 63 ? hi - 63 : 0) : at;
+  int64_t step = 1, b0, b1;
+  // each step leaves at most a 63rd: 7 do for any count; starts that decrease may never converge
+  for (int tries = 0;; ++tries) {
+    if (tries == 12) return false;
+    const int64_t i = at + lane * step;
+    const int64_t v = set_bound(own, n_sets, n_own, i < hi ? i : hi);
+    const int c = __popcll(__ballot(i < hi && v * mul / BM + i <= t));  // boundaries at or before the slot
+    if (c == 0) {  // before the window
+      hi = at;
+    } else if (c == 64) {  // after it, or after its last sample
+      lo = at + 63 * step;
+    } else {
+      lo = at + (c - 1) * step;
+      if (lo + step < hi) hi = lo + step;
+    }
+    if (hi - lo == 1 && step == 1 && c > 0 && c < 64) {
+      b0 = __shfl(v, c - 1);
+      b1 = __shfl(v, c);
+      break;
+    }
+    at = lo;
+    step = (hi - lo + 62) / 63;  // 63 steps reach hi
   }
-  const int64_t b0 = set_bound(own, n_sets, n_own, lo), b1 = set_bound(own, n_sets, n_own, lo + 1);
   r->own0 = b0;
   r->rows = (b1 - b0) * mul;
   r->row0 = (t - (b0 * mul / BM + lo)) * BM;
   r->st0 = 0;
   r->st_len = 0;
   if (lo >= 1 && lo <= n_sets) {
-    const int64_t s0 = set_bound(st, n_sets, n_st, lo), s1 = set_bound(st, n_sets, n_st, lo + 1);
+    const int64_t s0 = st == own && n_st == n_own ? b0 : set_bound(st, n_sets, n_st, lo);
+    const int64_t s1 = st == own && n_st == n_own ? b1 : set_bound(st, n_sets, n_st, lo + 1);
     r->st0 = s0;
     r->st_len = s1 > s0 ? s1 - s0 : 0;
   }
@@ -235,25 +235,22 @@ __device__ __forceinline__ void check_starts(const int64_t* starts, int64_t n, i
   if (v < 0 || v > n || (t < n_sets && starts[t + 1] < v)) atomicOr(flags, TS_FLAG_RANGE);
 }
 
-// Consecutive blocks go to the 8 XCDs in turn; numbering them so that each XCD
-// gets a contiguous range lets the tiles of a set share that XCD's L2.
-__device__ __forceinline__ uint32_t xcd_block() {
-  const uint32_t n = gridDim.x, b = blockIdx.x, x = b & 7, per = n >> 3, rest = n & 7;
-  return x * per + (x < rest ? x : rest) + (b >> 3);
+// Grid: x = tile slots, y = groups of `heads` key-value heads, z = splits.  Consecutive
+// blocks go to the 8 XCDs in turn.  With many slots, each XCD gets runs of four
+// consecutive tiles, so that the tiles of a set share that XCD's L2 while long and
+// short sets still spread over all of them (one contiguous range per XCD left the
+// XCD with the longest set running alone); x is then a multiple of 32.  With few
+// slots x is odd, so that the heads and splits of one tile lie on different XCDs.
+constexpr uint32_t kXcds = 8, kXcdRun = 4, kXcdMany = 256;
+inline unsigned attn_grid_x(int64_t tiles) {
+  if (tiles < kXcdMany) return static_cast<unsigned>(tiles) | 1u;
+  return static_cast<unsigned>((tiles + kXcds * kXcdRun - 1) / (kXcds * kXcdRun) * (kXcds * kXcdRun));
 }
-
-struct Where {
-  int64_t tile;
-  int split, kvh;
-};
-__device__ __forceinline__ Where where(const AttnArgs& a) {
-  const uint32_t id = xcd_block(), tiles = static_cast<uint32_t>(a.tiles);
-  const uint32_t rest = id / tiles;
-  Where w;
-  w.tile = id - rest * tiles;
-  w.split = static_cast<int>(rest % static_cast<uint32_t>(a.splits));
-  w.kvh = static_cast<int>(rest / static_cast<uint32_t>(a.splits));
-  return w;
+__device__ __forceinline__ int64_t block_tile() {
+  const uint32_t b = blockIdx.x;
+  if (gridDim.x < kXcdMany) return b;
+  const uint32_t i = b / kXcds;
+  return (i / kXcdRun * kXcds + b % kXcds) * kXcdRun + i % kXcdRun;
 }
 
 // The part of [0, len) that split s of `splits` walks, in whole tiles of bn.
@@ -264,14 +261,224 @@ __device__ __forceinline__ void split_range(int64_t len, int bn, int splits, int
   *e = hi < len ? hi : len;
 }
 
-__device__ __forceinline__ f32x4 load_coord(const int32_t* c, int64_t row, int ndim, float w) {
+// Distances.  Coordinates are taken relative to one row of the block (floats
+// hold them exactly) with the squared norm beside them: {x, y, z, x^2 + y^2 +
+// z^2}.  While every norm is at most 2048, |a - b|^2 = |a|^2 + |b|^2 - 2 a.b
+// is a sum of integers below 2^24, exact in fp32 in any order, and one
+// v_mfma_f32_16x16x4_f32 gives a 16 x 16 tile of squares: A = the tile row's four
+// values, B = (-2x, -2y, -2z, 1) of the column, C = the column's norm.  Beyond
+// that the differences are formed one by one (the walk's slow form).
+constexpr float kNearNorm = 4194304.f;  // 2048^2
+
+struct Origin {
+  float x, y, z;
+};
+__device__ __forceinline__ Origin load_origin(const int32_t* c, int64_t row, int ndim) {
   const int32_t* p = c + row * (ndim + 1) + 1;
-  return f32x4{static_cast<float>(p[0]), static_cast<float>(p[1]), ndim == 3 ? static_cast<float>(p[2]) : 0.f, w};
+  return Origin{static_cast<float>(p[0]), static_cast<float>(p[1]), ndim == 3 ? static_cast<float>(p[2]) : 0.f};
+}
+__device__ __forceinline__ f32x4 relative(const Origin& p, const Origin& o) {
+  const float x = p.x - o.x, y = p.y - o.y, z = p.z - o.z;
+  return f32x4{x, y, z, fmaf(x, x, fmaf(y, y, z * z))};
+}
+__device__ __forceinline__ f32x4 load_coord(const int32_t* c, int64_t row, int ndim, const Origin& o) {
+  return relative(load_origin(c, row, ndim), o);
+}
+__device__ __forceinline__ float square(const f32x4& a, const f32x4& b) {
+  const float x = a[0] - b[0], y = a[1] - b[1], z = a[2] - b[2];
+  return fmaf(x, x, fmaf(y, y, z * z));
+}
+// The column's B value of lane (g, c) for the product above.
+__device__ __forceinline__ float col_term(const f32x4& c, int g) {
+  return g == 0 ? -2.f * c[0] : g == 1 ? -2.f * c[1] : g == 2 ? -2.f * c[2] : 1.f;
 }
 
-__device__ __forceinline__ float distance(const f32x4& a, const f32x4& b) {
-  const float x = a[0] - b[0], y = a[1] - b[1], z = a[2] - b[2];
-  return __builtin_amdgcn_sqrtf(fmaf(x, x, fmaf(y, y, z * z)));
+template <bool V>
+struct Flag {
+  static constexpr bool v = V;
+};
+
+constexpr uint32_t kOutside = 0xc0000000u;  // an offset past every tile: buffer loads give zeros
+
+// A wave-uniform address, stated as such (a buffer descriptor is built from it).
+template <typename T>
+__device__ __forceinline__ T* uniform_ptr(T* p) {
+  const uint64_t x = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
+  return reinterpret_cast<T*>((static_cast<uint64_t>(hi) << 32) | lo);
 }
+
+// 16 bytes at `off` of the `bytes` bytes at `base`; zeros past them.
+static __device__ __forceinline__ u32x4 load16_in(const void* base, uint32_t bytes, uint32_t off) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+      uniform_ptr(const_cast<void*>(base)), 0, static_cast<int>(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000);
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), 0, 0));
+}
+
+// A tile of BN rows of two matrices on its way from memory to LDS.  A thread
+// moves one 16-byte chunk of every (256 / CH)-th row.  Rows past the end and chunks
+// past the head width come as zeros from the bounds check of the buffer loads (0 *
+// NaN of another set's row would be NaN), without a mask.
+template <typename T, int DP, int BN>
+struct TileLoad {
+  static constexpr int CH = DP / 8, CT = BN * CH / 256, STEP = 256 / CH;
+  u32x4 a[CT], b[CT];
+
+  static __device__ __forceinline__ int row(int i) { return i * STEP + threadIdx.x / CH; }
+  static __device__ __forceinline__ int chunk() { return threadIdx.x % CH; }
+  // fa, fb: byte offsets of the rows from the bases; na, nb: bytes up to the end of the last row.
+  template <typename FA, typename FB>
+  __device__ __forceinline__ void fetch(const T* pa, uint32_t na, FA&& fa, const T* pb, uint32_t nb, FB&& fb, int d) {
+    const uint32_t c0 = chunk() * 8 < d ? chunk() * 16u : kOutside;
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      a[i] = load16_in(pa, na, fa(i) + c0);
+      b[i] = load16_in(pb, nb, fb(i) + c0);
+    }
+  }
+  __device__ __forceinline__ void put(char* x, char* y) const {
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      const int at = tile_at<DP>(row(i), chunk());
+      *reinterpret_cast<u32x4*>(x + at) = a[i];
+      *reinterpret_cast<u32x4*>(y + at) = b[i];
+    }
+  }
+};
+
+// Coordinates of a tile's rows on their way: thread r < BN brings row r's.
+template <int BN>
+struct TileCoords {
+  Origin c;  // as read: the block's origin may still be on its way
+  __device__ __forceinline__ void fetch(const int32_t* coords, int64_t first, int rows, int ndim) {
+    const int r = threadIdx.x;
+    if (r < BN && r < rows) c = load_origin(coords, first + r, ndim);
+  }
+  // The flag of a wave's rows: whether one is too far out for the product form.
+  __device__ __forceinline__ void put(f32x4* tc, uint32_t* far_rows, const Origin& org) const {
+    if (threadIdx.x >= BN) return;
+    const f32x4 x = relative(c, org);
+    tc[threadIdx.x] = x;
+    const bool any = __any(x[3] > kNearNorm);
+    if (threadIdx.x % 64 == 0) far_rows[threadIdx.x / 64] = any;
+  }
+};
+template <int BN>
+__device__ __forceinline__ bool tile_far(const uint32_t* far_rows) {
+  uint32_t f = far_rows[0];
+  if constexpr (BN > 64) f |= far_rows[1];
+  return __builtin_amdgcn_readfirstlane(f) != 0;
+}
+
+// The key side of a walk over n_keys keys from row `first`: tiles of keys and values of one key-value head, and the
+// keys' coordinates.
+template <typename T, int DP, int BN, bool BIAS>
+struct KeyTiles {
+  TileLoad<T, DP, BN> ld;
+  TileCoords<BN> lc;
+  const T *kp, *vp;
+  int64_t first;
+  int n_keys;
+
+  __device__ __forceinline__ KeyTiles(const AttnArgs& a, int64_t first_key, int keys)
+      : kp(static_cast<const T*>(a.k) + first_key * a.k_stride),
+        vp(static_cast<const T*>(a.v) + first_key * a.v_stride),
+        first(first_key),
+        n_keys(keys) {
+    lc.c = Origin{0.f, 0.f, 0.f};
+  }
+  __device__ __forceinline__ void fetch(const AttnArgs& a, int h, int k0) {
+    const uint32_t ks = static_cast<uint32_t>(a.k_stride) * 2u, vs = static_cast<uint32_t>(a.v_stride) * 2u;
+    const uint32_t last = (n_keys - k0 < BN ? n_keys - k0 : BN) - 1, w = a.d * 2u;
+    ld.fetch(kp + k0 * a.k_stride + h * a.d, last * ks + w, [&](int i) { return ld.row(i) * ks; },
+             vp + k0 * a.v_stride + h * a.d, last * vs + w, [&](int i) { return ld.row(i) * vs; }, a.d);
+    if constexpr (BIAS) lc.fetch(a.kc, first + k0, n_keys - k0, a.ndim);
+  }
+  __device__ __forceinline__ void put(char* tk, char* tv, f32x4* tc, uint32_t* far_rows, const Origin& org) {
+    ld.put(tk, tv);
+    if constexpr (BIAS) lc.put(tc, far_rows, org);
+  }
+};
+
+// B operands of one head's columns: NC blocks of 16 rows whose byte offsets from a
+// uniform base are given (kOutside: none).
+template <typename T, int DP, int NC>
+struct ColLoad {
+  u32x4 x[NC][DP / 32];
+  __device__ __forceinline__ void fetch(const T* base, uint32_t bytes, const uint32_t (&off)[NC], int d) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int kb = 0; kb < DP / 32; ++kb) {
+        const int c = kb * 32 + g * 8;
+        x[j][kb] = load16_in(base, bytes, c < d ? off[j] + c * 2u : kOutside);
+      }
+  }
+  __device__ __forceinline__ typename AMfma<T>::frag frag(int j, int kb) const {
+    return __builtin_bit_cast(typename AMfma<T>::frag, x[j][kb]);
+  }
+  __device__ __forceinline__ typename AMfma<T>::frag frag_signed(int j, int kb, bool negate) const {
+    return __builtin_bit_cast(typename AMfma<T>::frag, negate ? x[j][kb] ^ 0x80008000u : x[j][kb]);
+  }
+};
+
+// Distances of the 16 tile rows from r0 to the columns, rows 4g..4g+3 in the lane's
+// four values; qb: col_term of the column, norm: its squared norm.  The far form
+// reads the column's coordinates again (row `row` of c): it is rare, and they
+// would cost registers everywhere else.
+__device__ __forceinline__ f32x4 distances(const f32x4* tc, int r0, float norm, float qb, bool far, int lane,
+                                           const int32_t* c, int64_t row, int ndim, const Origin& org) {
+  f32x4 d;
+  if (far) {
+    const f32x4 x = load_coord(c, row, ndim, org);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      d[e] = square(x, tc[r0 + 4 * (lane >> 4) + e]);
+      __builtin_amdgcn_sched_barrier(0);  // one row at a time, for the registers' sake
+    }
+  } else {
+    d = __builtin_amdgcn_mfma_f32_16x16x4f32(tc[r0 + (lane & 15)][lane >> 4], qb, f32x4{norm, norm, norm, norm}, 0, 0, 0);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d[e] = __builtin_amdgcn_sqrtf(d[e]);
+  return d;
+}
+
+// The query rows that are a wave's columns: NC blocks of 16 packed rows, BM columns
+// apart per block of waves.  Offsets are from the tile's first query.
+template <int NC, bool SHARE>
+struct QueryCols {
+  int64_t query0;                // uniform: query of the tile's first row
+  uint32_t dq[NC], place[NC];    // query from there, place among the heads that share a key head
+  bool live[NC], busy;
+  uint32_t last;                 // query of the tile's last row, from query0
+  __device__ __forceinline__ QueryCols(const AttnArgs& a, const SetTile& st, int bm) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t grp = a.grp, r0 = static_cast<uint32_t>(st.row0), rows = static_cast<uint32_t>(st.rows);
+    const uint32_t q0 = grp == 1 ? r0 : r0 / grp;
+    query0 = st.own0 + q0;
+    const uint32_t lr = (r0 + bm < rows ? r0 + bm : rows) - 1;
+    last = (grp == 1 ? lr : lr / grp) - q0;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const uint32_t r = r0 + (SHARE ? 0 : j * 4 + wave) * 16 + (lane & 15);
+      live[j] = r < rows;
+      const uint32_t x = live[j] ? r : r0, q = grp == 1 ? x : x / grp;
+      dq[j] = q - q0;
+      place[j] = x - q * grp;
+    }
+    // column blocks of a wave come 64 rows apart: it computes while its first is inside the set
+    busy = r0 + (SHARE ? 0 : wave * 16) < rows;
+  }
+  // byte offset of column j's row of a matrix with this row stride, from row query0 of key-value head h
+  __device__ __forceinline__ uint32_t offset(int j, int64_t stride, int d) const {
+    return live[j] ? (dq[j] * static_cast<uint32_t>(stride) + place[j] * d) * 2u : kOutside;
+  }
+  __device__ __forceinline__ uint32_t bytes(int64_t stride, int width) const {
+    return (last * static_cast<uint32_t>(stride) + width) * 2u;
+  }
+};
 
 }  // namespace ts

@@ -10,394 +10,530 @@
 //
 // 1 - tanh^2 = 4 r (1 - r) with r = 1 / (exp(2x) + 1); the 4 is taken into the
 // exponent of p (so dv is scaled back by 1/4 when it is written).
+//
+// As in the forward pass, a wave owns NC column blocks of 16 and a block takes
+// a.heads key-value heads one after the other; delta enters as the accumulator
+// that dp starts from.
 #include "attn.h"
 
 namespace ts {
 
 namespace {
 
-// p and ds of one score: s = q.k, the column's or row's terms as described
+// p and ds of one score.  s = q.k; dist the distance; base = -lse (plus c2
+// for a capped score) in units of log 2; dp has delta taken off already (it is
+// the accumulator that product starts from).
 template <bool CAP, bool BIAS>
-__device__ __forceinline__ void grad_score(const AttnArgs& a, float s, float dp, float lse2, float delta, float slope,
-                                           const f32x4& ca, const f32x4& cb, float* p, float* ds) {
-  float z, r = 0.f;
+__device__ __forceinline__ void grad_score(const AttnArgs& a, float s, float dp, float base, float slope, float dist,
+                                           float* p, float* ds) {
+  if constexpr (BIAS) base = fmaf(-slope, dist, base);
   if constexpr (CAP) {
-    r = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(s * a.c1) + 1.f);
-    z = fmaf(-2.f * a.c2, r, a.c2 - lse2);
+    const float r = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(s * a.c1) + 1.f);
+    *p = __builtin_amdgcn_exp2f(fmaf(-2.f * a.c2, r, base));
+    *ds = *p * dp * fmaf(-r, r, r);
   } else {
-    z = fmaf(s, a.c1, -lse2);
+    *p = __builtin_amdgcn_exp2f(fmaf(s, a.c1, base));
+    *ds = *p * dp;
   }
-  if constexpr (BIAS) z = fmaf(-slope, distance(ca, cb), z);
-  *p = __builtin_amdgcn_exp2f(z);
-  *ds = *p * (dp - delta);
-  if constexpr (CAP) *ds *= fmaf(-r, r, r);
 }
 
-// lse in units of log 2, less 2 where p is to hold the factor 4; rows without
-// a finite score get +inf, so their probabilities are 0.
+// What the exponent starts from: -lse in units of log 2, with c2 for a capped
+// score and 2 more where p is to hold the factor 4; rows without a finite score
+// get -inf, so their probabilities are 0.
 template <bool CAP>
-__device__ __forceinline__ float lse_term(float lse) {
-  return lse == -INFINITY ? INFINITY : fmaf(lse, kLog2e, CAP ? -2.f : 0.f);
+__device__ __forceinline__ float exp_base(const AttnArgs& a, float lse) {
+  return lse == -INFINITY ? -INFINITY : fmaf(-lse, kLog2e, CAP ? a.c2 + 2.f : 0.f);
 }
 
 template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS>
-__global__ __launch_bounds__(256, KS && DP == 128 ? 1 : 2) void k_attn_dq(const AttnArgs a) {
+__global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_attn_dq(const AttnArgs a) {
   typedef typename AMfma<T>::frag Frag;
-  constexpr int KB = DP / 32, DI = DP / 16, CH = DP / 8;
-  constexpr int BN = KS ? 128 : 64, NT = KS ? 2 : 4, BM = KS ? 16 * NC : 64 * NC;
-  constexpr int CT = BN * CH / 256;
+  constexpr int KB = DP / 32, DI = DP / 16;
+  constexpr int BN = KS ? 128 : 64, NT = KS ? 2 : 4, BM = KS ? 16 : 64 * NC;
+  constexpr int TB = BN * DP * 2;
+  constexpr bool MULTI = NC == 1 && !KS && DP <= 64;
   static_assert(!KS || NC == 1, "one column block when the waves share the keys");
-  __shared__ __attribute__((aligned(16))) char tk[2][BN * DP * 2], tv[2][BN * DP * 2];
+  __shared__ __attribute__((aligned(16))) char tk[2][TB], tv[2][TB];
   __shared__ f32x4 tc[2][BIAS ? BN : 1];
+  __shared__ uint32_t far_rows[2][2];
 
-  const Where w = where(a);
-  if (a.flags && w.kvh == 0 && w.split == 0 && threadIdx.x == 0) {
-    check_starts(a.qs, a.nq, a.n_sets, w.tile, a.flags);
-    if (a.ks != a.qs) check_starts(a.ks, a.nk, a.n_sets, w.tile, a.flags);
+  const int64_t slot = block_tile();
+  const int split = blockIdx.z;
+  if (a.flags && blockIdx.y == 0 && split == 0 && threadIdx.x == 0) {
+    check_starts(a.qs, a.nq, a.n_sets, slot, a.flags);
+    if (a.ks != a.qs) check_starts(a.ks, a.nk, a.n_sets, slot, a.flags);
   }
   SetTile st;
-  if (!find_tile<BM>(a.qs, a.nq, a.grp, a.ks, a.nk, a.n_sets, w.tile, &st)) return;
+  if (!find_tile<BM>(a.qs, a.nq, a.grp, a.ks, a.nk, a.n_sets, slot, a.tiles, &st)) return;
   int64_t kbeg, kend;
-  split_range(st.st_len, BN, a.splits, w.split, &kbeg, &kend);
+  split_range(st.st_len, BN, a.splits, split, &kbeg, &kend);
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
   const int kt0 = KS ? wave * 32 : 0;
-  const T* kp = static_cast<const T*>(a.k) + (st.st0 + kbeg) * a.k_stride + static_cast<int64_t>(w.kvh) * a.d;
-  const T* vp = static_cast<const T*>(a.v) + (st.st0 + kbeg) * a.v_stride + static_cast<int64_t>(w.kvh) * a.d;
   const int n_keys = static_cast<int>(kend - kbeg);
+  int h = blockIdx.y * a.heads;
+  const int h_end = !MULTI ? h + 1 : h + a.heads < a.hk ? h + a.heads : a.hk;
 
-  int64_t row[NC];
-  bool live[NC];
-  Frag qf[NC][KB], gf[NC][KB];
-  f32x4 qc[NC];
-  float lse2[NC], delta[NC];
+  const QueryCols<NC, KS> col(a, st, BM);
+  uint32_t qoff[NC], ooff[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const int64_t r = st.row0 + ((KS ? 0 : wave * NC) + j) * 16 + (lane & 15);
-    live[j] = r < st.rows;
-    const uint32_t rr = live[j] ? static_cast<uint32_t>(r) : 0;
-    const uint32_t qi = a.grp == 1 ? rr : rr / static_cast<uint32_t>(a.grp);
-    const int64_t query = st.own0 + qi;
-    const int head = w.kvh * a.grp + static_cast<int>(rr - qi * a.grp);
-    row[j] = query * a.hq + head;
-    const T* qp = static_cast<const T*>(a.q) + query * a.q_stride + static_cast<int64_t>(head) * a.d;
-    const int64_t oo = query * a.o_stride + static_cast<int64_t>(head) * a.d;
-    const T *gp = static_cast<const T*>(a.dout) + oo, *op = static_cast<const T*>(a.o) + oo;
-    float dl = 0.f;
+    qoff[j] = col.offset(j, a.q_stride, a.d);
+    ooff[j] = col.offset(j, a.o_stride, a.d);
+  }
+  const int width = a.grp * a.d;  // a key-value head's part of a query row
+  Origin org{0.f, 0.f, 0.f};
+  Origin qraw[NC];
+  if constexpr (BIAS) {
+    org = load_origin(a.qc, st.own0, a.ndim);
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      const u32x4 none{0u, 0u, 0u, 0u};
-      const int d0 = kb * 32 + g * 8;
-      qf[j][kb] = __builtin_bit_cast(Frag, live[j] ? load8(qp, d0, a.d, a.vec_in) : none);
-      gf[j][kb] = __builtin_bit_cast(Frag, live[j] ? load8(gp, d0, a.d, a.vec_in) : none);
-      const Frag of = __builtin_bit_cast(Frag, live[j] ? load8(op, d0, a.d, a.vec_in) : none);
+    for (int j = 0; j < NC; ++j) qraw[j] = load_origin(a.qc, col.query0 + col.dq[j], a.ndim);
+  }
+  ColLoad<T, DP, NC> qld, gld, old;
+  float next_slope[NC], next_lse[NC];
+  auto fetch_cols = [&](int hn) {
+    const int64_t q0 = col.query0 * a.q_stride + static_cast<int64_t>(hn) * width;
+    const int64_t o0 = col.query0 * a.o_stride + static_cast<int64_t>(hn) * width;
+    qld.fetch(static_cast<const T*>(a.q) + q0, col.bytes(a.q_stride, width), qoff, a.d);
+    gld.fetch(static_cast<const T*>(a.dout) + o0, col.bytes(a.o_stride, width), ooff, a.d);
+    old.fetch(static_cast<const T*>(a.o) + o0, col.bytes(a.o_stride, width), ooff, a.d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dl = fmaf(static_cast<float>(gf[j][kb][e]), static_cast<float>(of[e]), dl);
+    for (int j = 0; j < NC; ++j) {
+      const int head = hn * a.grp + static_cast<int>(col.place[j]);
+      next_lse[j] = col.live[j] ? a.lse[(col.query0 + col.dq[j]) * a.hq + head] : -INFINITY;
+      if constexpr (BIAS) next_slope[j] = a.slopes[head];
     }
-    delta[j] = col_sum(dl);
-    lse2[j] = lse_term<CAP>(live[j] ? a.lse[row[j]] : -INFINITY);
-    if (live[j] && g == 0 && w.split == 0 && (!KS || wave == 0)) a.delta[row[j]] = delta[j];
-    if constexpr (BIAS) qc[j] = load_coord(a.qc, query, a.ndim, a.slopes[head] * kLog2e);
+  };
+  fetch_cols(h);
+  KeyTiles<T, DP, BN, BIAS> keys(a, st.st0 + kbeg, n_keys);
+  if (n_keys > 0) keys.fetch(a, h, 0);
+
+  float slope[NC], qb[NC], qn[NC];
+  bool far_cols = false;
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const f32x4 c = relative(qraw[j], org);
+      qb[j] = col_term(c, g);
+      qn[j] = c[3];
+      far_cols |= __any(c[3] > kNearNorm) != 0;
+    }
   }
 
-  u32x4 rk[CT], rv[CT];
-  f32x4 rc{0.f, 0.f, 0.f, 0.f};
-  auto fetch = [&](int k0) {
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-      const int c = i * 256 + tid, r = k0 + c / CH, d0 = (c % CH) * 8;
-      const bool ok = r < n_keys;
-      rk[i] = ok ? load8(kp + static_cast<int64_t>(r) * a.k_stride, d0, a.d, a.vec_in) : u32x4{0u, 0u, 0u, 0u};
-      rv[i] = ok ? load8(vp + static_cast<int64_t>(r) * a.v_stride, d0, a.d, a.vec_in) : u32x4{0u, 0u, 0u, 0u};
-    }
-    if constexpr (BIAS)
-      if (tid < BN && k0 + tid < n_keys) rc = load_coord(a.kc, st.st0 + kbeg + k0 + tid, a.ndim, 0.f);
-  };
-  auto put = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-      const int c = i * 256 + tid, at = tile_at<DP>(c / CH, c % CH);
-      *reinterpret_cast<u32x4*>(tk[b] + at) = rk[i];
-      *reinterpret_cast<u32x4*>(tv[b] + at) = rv[i];
-    }
-    if constexpr (BIAS)
-      if (tid < BN) tc[b][tid] = rc;
-  };
-
+  const f32x4 zero{0.f, 0.f, 0.f, 0.f};
+  Frag qf[NC][KB], gf[NC][KB];
   f32x4 dq[NC][DI];
+  float base[NC], delta[NC];
+  auto begin = [&]() {
 #pragma unroll
-  for (int j = 0; j < NC; ++j)
+    for (int j = 0; j < NC; ++j) {
+      float dl = 0.f;
 #pragma unroll
-    for (int i = 0; i < DI; ++i) dq[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int kb = 0; kb < KB; ++kb) {
+        qf[j][kb] = qld.frag_signed(j, kb, a.negate);
+        gf[j][kb] = gld.frag(j, kb);
+        const Frag of = old.frag(j, kb);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dl = fmaf(static_cast<float>(gf[j][kb][e]), static_cast<float>(of[e]), dl);
+      }
+      delta[j] = col_sum(dl);
+      base[j] = exp_base<CAP>(a, next_lse[j]);
+      if constexpr (BIAS) slope[j] = next_slope[j] * kLog2e;
+      if (col.live[j] && g == 0 && split == 0 && (!KS || wave == 0))
+        a.delta[(col.query0 + col.dq[j]) * a.hq + h * a.grp + col.place[j]] = delta[j];
+#pragma unroll
+      for (int i = 0; i < DI; ++i) dq[j][i] = zero;
+    }
+  };
 
-  if (n_keys > 0) {
-    fetch(0);
-    put(0);
-  }
-  for (int k0 = 0, b = 0; k0 < n_keys; k0 += BN, b ^= 1) {
-    const bool more = k0 + BN < n_keys;
-    if (more) fetch(k0 + BN);
-    __syncthreads();
+  // 32 keys; part: keys may end inside them, distances may be long
+  auto step = [&](auto part, int b, int u, int left, bool far) {
+    constexpr bool PART = decltype(part)::v;
+    f32x4 s[NC][2], dp[NC][2];
 #pragma unroll
-    for (int u = 0; u < NT / 2; ++u) {
-      f32x4 s[NC][2], dp[NC][2];
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int kb = 0; kb < KB; ++kb) {
+        const Frag fk = tile_frag<T, DP>(tk[b], kt0 + u * 32 + n * 16, kb, lane);
+        const Frag fv = tile_frag<T, DP>(tv[b], kt0 + u * 32 + n * 16, kb, lane);
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const Frag fk = tile_frag<T, DP>(tk[b], kt0 + u * 32 + n * 16, kb, lane);
-          const Frag fv = tile_frag<T, DP>(tv[b], kt0 + u * 32 + n * 16, kb, lane);
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            s[j][n] = AMfma<T>::run(fk, qf[j][kb], kb == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j][n]);
-            dp[j][n] = AMfma<T>::run(fv, gf[j][kb], kb == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : dp[j][n]);
-          }
+        for (int j = 0; j < NC; ++j) {
+          s[j][n] = AMfma<T>::run(fk, qf[j][kb], kb == 0 ? zero : s[j][n]);
+          dp[j][n] = AMfma<T>::run(fv, gf[j][kb], kb == 0 ? f32x4{-delta[j], -delta[j], -delta[j], -delta[j]} : dp[j][n]);
         }
-      Frag df[NC];
+      }
+    Frag df[NC];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        f32x4 dist = zero;
+        if constexpr (BIAS)
+          dist = distances(tc[b], kt0 + u * 32 + n * 16, qn[j], qb[j], PART && far, lane, a.qc, col.query0 + col.dq[j],
+                           a.ndim, org);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int kr = kt0 + u * 32 + n * 16 + 4 * g + e;
-          f32x4 kc{0.f, 0.f, 0.f, 0.f};
-          if constexpr (BIAS) kc = tc[b][kr];
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            float p, ds;
-            grad_score<CAP, BIAS>(a, s[j][n][e], dp[j][n][e], lse2[j], delta[j], BIAS ? qc[j][3] : 0.f, qc[j], kc, &p, &ds);
-            if (!more) ds = k0 + kr < n_keys ? ds : 0.f;
-            df[j][n * 4 + e] = static_cast<T>(ds);
-          }
+          float p, ds;
+          grad_score<CAP, BIAS>(a, s[j][n][e], dp[j][n][e], base[j], BIAS ? slope[j] : 0.f, dist[e], &p, &ds);
+          if constexpr (PART) ds = u * 32 + n * 16 + 4 * g + e < left ? ds : 0.f;
+          df[j][n * 4 + e] = static_cast<T>(ds);
         }
-#pragma unroll
-      for (int i = 0; i < DI; ++i) {
-        const Frag f = tile_frag_t<T, DP>(tk[b], kt0 + u * 32, i, lane);
-#pragma unroll
-        for (int j = 0; j < NC; ++j) dq[j][i] = AMfma<T>::run(f, df[j], dq[j][i]);
       }
-    }
-    if (more) put(b ^ 1);
-  }
-
-  if constexpr (KS) {
-    float* jo = reinterpret_cast<float*>(tv);  // [4][16][DP]
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < DI; ++i)
-      *reinterpret_cast<f32x4*>(jo + (wave * 16 + (lane & 15)) * DP + i * 16 + g * 4) = dq[0][i];
-    __syncthreads();
-    if (wave != 0) return;
-#pragma unroll
-    for (int x = 1; x < 4; ++x)
-#pragma unroll
-      for (int i = 0; i < DI; ++i) {
-        const f32x4 y = *reinterpret_cast<const f32x4*>(jo + (x * 16 + (lane & 15)) * DP + i * 16 + g * 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dq[0][i][e] += y[e];
-      }
-  }
-
-#pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    if (!live[j]) continue;
-    const int64_t query = row[j] / a.hq;
-    T* dst = static_cast<T*>(a.dq) + query * a.q_stride + (row[j] - query * a.hq) * a.d;
-    float* part = a.part + (static_cast<int64_t>(w.split) * a.nq * a.hq + row[j]) * DP;
 #pragma unroll
     for (int i = 0; i < DI; ++i) {
-      f32x4 y = dq[j][i];
+      const Frag f = tile_frag_t<T, DP>(tk[b], kt0 + u * 32, i, lane);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] *= a.scale;
-      if (a.splits > 1)
-        *reinterpret_cast<f32x4*>(part + i * 16 + g * 4) = y;
-      else
-        store4(dst, i * 16 + g * 4, a.d, a.vec_out, y);
+      for (int j = 0; j < NC; ++j) dq[j][i] = AMfma<T>::run(f, df[j], dq[j][i]);
     }
+  };
+
+  auto finish = [&]() {
+    if constexpr (KS) {
+      float* jo = reinterpret_cast<float*>(tv);  // [4][16][DP]
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < DI; ++i)
+        *reinterpret_cast<f32x4*>(jo + (wave * 16 + (lane & 15)) * DP + i * 16 + g * 4) = dq[0][i];
+      __syncthreads();
+      if (wave != 0) return;
+#pragma unroll
+      for (int x = 1; x < 4; ++x)
+#pragma unroll
+        for (int i = 0; i < DI; ++i) {
+          const f32x4 y = *reinterpret_cast<const f32x4*>(jo + (x * 16 + (lane & 15)) * DP + i * 16 + g * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dq[0][i][e] += y[e];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      if (!col.live[j]) continue;
+      const int64_t query = col.query0 + col.dq[j];
+      const int head = h * a.grp + static_cast<int>(col.place[j]);
+      T* dst = static_cast<T*>(a.dq) + query * a.q_stride + static_cast<int64_t>(head) * a.d;
+      float* part = a.part + ((static_cast<int64_t>(split) * a.nq + query) * a.hq + head) * DP;
+#pragma unroll
+      for (int i = 0; i < DI; ++i) {
+        f32x4 y = dq[j][i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] *= a.scale;
+        if (a.splits > 1)
+          *reinterpret_cast<f32x4*>(part + i * 16 + g * 4) = y;
+        else
+          store4(dst, i * 16 + g * 4, a.d, y);
+      }
+    }
+  };
+
+  if (n_keys <= 0) {
+    for (;;) {
+      begin();
+      finish();
+      if (!MULTI || ++h >= h_end) return;
+      fetch_cols(h);
+    }
+  }
+  keys.put(tk[0], tv[0], tc[0], far_rows[0], org);
+  begin();
+  for (int k0 = 0, b = 0;; b ^= 1) {
+    const bool wrap = k0 + BN >= n_keys;
+    const int hn = wrap ? h + 1 : h, kn = wrap ? 0 : k0 + BN;
+    const bool more = hn < h_end;
+    if (more) {
+      if (MULTI && wrap) fetch_cols(hn);
+      keys.fetch(a, hn, kn);
+    }
+    __syncthreads();
+    if (col.busy) {
+      const int left = n_keys - k0 - kt0;
+      const bool far = BIAS && (far_cols || tile_far<BN>(far_rows[b]));
+#pragma unroll
+      for (int u = 0; u < NT / 2; ++u) {
+        if (u * 32 >= left) continue;
+        if (u * 32 + 32 <= left && !far)
+          step(Flag<false>{}, b, u, left, false);
+        else
+          step(Flag<true>{}, b, u, left, far);
+      }
+    }
+    if (wrap) finish();
+    if (!more) break;
+    h = hn;
+    k0 = kn;
+    if (MULTI && wrap) begin();
+    keys.put(tk[b ^ 1], tv[b ^ 1], tc[b ^ 1], far_rows[b ^ 1], org);
   }
 }
 
 template <typename T, int DP, int NC, bool CAP, bool BIAS>
-__global__ __launch_bounds__(256, 2) void k_attn_dkv(const AttnArgs a) {
+__global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(const AttnArgs a) {
   typedef typename AMfma<T>::frag Frag;
-  constexpr int KB = DP / 32, DI = DP / 16, CH = DP / 8;
-  constexpr int BN = 64, BM = 64 * NC;
-  constexpr int CT = BN * CH / 256;
-  __shared__ __attribute__((aligned(16))) char tq[2][BN * DP * 2], tg[2][BN * DP * 2];
-  __shared__ f32x4 tc[2][BIAS ? BN : 1];  // coordinates and slope of the row
-  __shared__ float tl[2][BN], td[2][BN];  // its lse term and delta
+  constexpr int KB = DP / 32, DI = DP / 16;
+  constexpr int BN = DP == 128 ? 32 : 64, BM = 64 * NC;  // 32 rows where the accumulators leave room for no more
+  constexpr int TB = BN * DP * 2;
+  constexpr bool MULTI = NC == 1 && DP <= 64;
+  __shared__ __attribute__((aligned(16))) char tq[2][TB], tg[2][TB];
+  __shared__ f32x4 tc[2][BIAS ? BN : 1];                                  // coordinates of the row
+  __shared__ __attribute__((aligned(16))) float tsl[2][BIAS ? BN : 4];    // its slope,
+  __shared__ __attribute__((aligned(16))) float tl[2][BN], td[2][BN];     // exponent base and -delta
+  __shared__ uint32_t far_rows[2][2];
 
-  const Where w = where(a);
+  const int64_t slot = block_tile();
+  const int split = blockIdx.z;
   SetTile st;
-  if (!find_tile<BM>(a.ks, a.nk, 1, a.qs, a.nq, a.n_sets, w.tile, &st)) return;
+  if (!find_tile<BM>(a.ks, a.nk, 1, a.qs, a.nq, a.n_sets, slot, a.tiles, &st)) return;
   int64_t rbeg, rend;
-  split_range(st.st_len * a.grp, BN, a.splits, w.split, &rbeg, &rend);
+  split_range(st.st_len * a.grp, BN, a.splits, split, &rbeg, &rend);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
-  const uint32_t n_rows = static_cast<uint32_t>(rend - rbeg);
+  const int n_rows = static_cast<int>(rend - rbeg);
+  int h = blockIdx.y * a.heads;
+  const int h_end = !MULTI ? h + 1 : h + a.heads < a.hk ? h + a.heads : a.hk;
+  const int width = a.grp * a.d;
 
-  int64_t key[NC];
+  // columns: keys
+  const int64_t key0 = st.own0 + st.row0;
+  const uint32_t cols = st.rows - st.row0 < BM ? static_cast<uint32_t>(st.rows - st.row0) : BM;
   bool live[NC];
-  Frag kf[NC][KB], vf[NC][KB];
-  f32x4 kc[NC];
+  uint32_t ck[NC], koff[NC], voff[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const int64_t r = st.row0 + (wave * NC + j) * 16 + (lane & 15);
-    live[j] = r < st.rows;
-    key[j] = st.own0 + (live[j] ? r : 0);
-    const T* kp = static_cast<const T*>(a.k) + key[j] * a.k_stride + static_cast<int64_t>(w.kvh) * a.d;
-    const T* vp = static_cast<const T*>(a.v) + key[j] * a.v_stride + static_cast<int64_t>(w.kvh) * a.d;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      kf[j][kb] = __builtin_bit_cast(Frag, live[j] ? load8(kp, kb * 32 + g * 8, a.d, a.vec_in) : u32x4{0u, 0u, 0u, 0u});
-      vf[j][kb] = __builtin_bit_cast(Frag, live[j] ? load8(vp, kb * 32 + g * 8, a.d, a.vec_in) : u32x4{0u, 0u, 0u, 0u});
-    }
-    if constexpr (BIAS) kc[j] = load_coord(a.kc, key[j], a.ndim, 0.f);
+    const uint32_t c = (j * 4 + wave) * 16 + (lane & 15);
+    live[j] = c < cols;
+    ck[j] = live[j] ? c : 0;
+    koff[j] = live[j] ? c * static_cast<uint32_t>(a.k_stride) * 2u : kOutside;
+    voff[j] = live[j] ? c * static_cast<uint32_t>(a.v_stride) * 2u : kOutside;
   }
-
-  u32x4 rq[CT], rg[CT];
-  f32x4 rc{0.f, 0.f, 0.f, 0.f};
-  float rl = 0.f, rd = 0.f;
-  // packed row r of this walk: its query and head
-  auto at_row = [&](uint32_t r, int64_t* query, int* head) {
-    const uint32_t x = static_cast<uint32_t>(rbeg) + r;
-    const uint32_t qi = a.grp == 1 ? x : x / static_cast<uint32_t>(a.grp);
-    *query = st.st0 + qi;
-    *head = w.kvh * a.grp + static_cast<int>(x - qi * a.grp);
-  };
-  auto fetch = [&](uint32_t r0) {
+  const bool busy = static_cast<uint32_t>(wave * 16) < cols;
+  Origin org{0.f, 0.f, 0.f};
+  Origin kraw[NC];
+  if constexpr (BIAS) {
+    org = load_origin(a.kc, st.own0, a.ndim);
 #pragma unroll
-    for (int i = 0; i < CT; ++i) {
-      const uint32_t c = i * 256 + tid, r = r0 + c / CH;
-      const int d0 = (c % CH) * 8;
-      rq[i] = rg[i] = u32x4{0u, 0u, 0u, 0u};
-      if (r < n_rows) {
-        int64_t query;
-        int head;
-        at_row(r, &query, &head);
-        rq[i] = load8(static_cast<const T*>(a.q) + query * a.q_stride + static_cast<int64_t>(head) * a.d, d0, a.d, a.vec_in);
-        rg[i] = load8(static_cast<const T*>(a.dout) + query * a.o_stride + static_cast<int64_t>(head) * a.d, d0, a.d,
-                      a.vec_in);
-      }
+    for (int j = 0; j < NC; ++j) kraw[j] = load_origin(a.kc, key0 + ck[j], a.ndim);
+  }
+  ColLoad<T, DP, NC> kld, vld;
+  auto fetch_cols = [&](int hn) {
+    kld.fetch(static_cast<const T*>(a.k) + key0 * a.k_stride + static_cast<int64_t>(hn) * a.d,
+              ((cols - 1) * static_cast<uint32_t>(a.k_stride) + a.d) * 2u, koff, a.d);
+    vld.fetch(static_cast<const T*>(a.v) + key0 * a.v_stride + static_cast<int64_t>(hn) * a.d,
+              ((cols - 1) * static_cast<uint32_t>(a.v_stride) + a.d) * 2u, voff, a.d);
+  };
+  fetch_cols(h);
+
+  // packed row r of this walk: its query, relative to the set, and its place among the heads that share a key head
+  auto at_row = [&](uint32_t r, uint32_t* query, uint32_t* place) {
+    const uint32_t x = static_cast<uint32_t>(rbeg) + r;
+    *query = a.grp == 1 ? x : x / static_cast<uint32_t>(a.grp);
+    *place = x - *query * a.grp;
+  };
+  TileLoad<T, DP, BN> ld;
+  TileCoords<BN> lc;
+  lc.c = Origin{0.f, 0.f, 0.f};
+  float rl = 0.f, rd = 0.f, rs = 0.f;
+  // Tile rows of this thread: query from the tile's first one, and place.  The same
+  // in every tile where the heads that share a key head divide BN, else formed anew.
+  uint32_t dqy[ld.CT], plc[ld.CT];
+  auto place_rows = [&](int r0, uint32_t q0) {
+#pragma unroll
+    for (int i = 0; i < ld.CT; ++i) {
+      at_row(r0 + ld.row(i), &dqy[i], &plc[i]);
+      dqy[i] -= q0;
     }
-    if (tid < BN) {
-      if (r0 + tid < n_rows) {
-        int64_t query;
-        int head;
-        at_row(r0 + tid, &query, &head);
-        rl = lse_term<CAP>(a.lse[query * a.hq + head]);
-        rd = a.delta[query * a.hq + head];
-        if constexpr (BIAS) rc = load_coord(a.qc, query, a.ndim, a.slopes[head] * kLog2e);
+  };
+  const bool even = BN % a.grp == 0;
+  {
+    uint32_t q0, p0;
+    at_row(0, &q0, &p0);
+    place_rows(0, q0);
+  }
+  auto off_q = [&](int i) { return (dqy[i] * static_cast<uint32_t>(a.q_stride) + plc[i] * a.d) * 2u; };
+  auto off_g = [&](int i) { return (dqy[i] * static_cast<uint32_t>(a.o_stride) + plc[i] * a.d) * 2u; };
+  auto fetch = [&](int hn, int r0) {
+    uint32_t q0, p0, q1, p1;
+    at_row(r0, &q0, &p0);
+    if (!even) place_rows(r0, q0);
+    const int64_t query0 = st.st0 + q0;
+    at_row(n_rows - r0 < BN ? n_rows - 1 : r0 + BN - 1, &q1, &p1);  // the last row: offsets rise with the row
+    const uint32_t end = (p1 + 1) * a.d;
+    ld.fetch(static_cast<const T*>(a.q) + query0 * a.q_stride + static_cast<int64_t>(hn) * width,
+             ((q1 - q0) * static_cast<uint32_t>(a.q_stride) + end) * 2u, off_q,
+             static_cast<const T*>(a.dout) + query0 * a.o_stride + static_cast<int64_t>(hn) * width,
+             ((q1 - q0) * static_cast<uint32_t>(a.o_stride) + end) * 2u, off_g, a.d);
+    if (tid < BN && r0 + tid < n_rows) {
+      uint32_t q, p;
+      at_row(r0 + tid, &q, &p);
+      const int64_t query = st.st0 + q;
+      const int head = hn * a.grp + static_cast<int>(p);
+      rl = a.lse[query * a.hq + head];
+      rd = a.delta[query * a.hq + head];
+      if constexpr (BIAS) {
+        lc.c = load_origin(a.qc, query, a.ndim);
+        rs = a.slopes[head];
       }
     }
   };
   auto put = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-      const int c = i * 256 + tid, at = tile_at<DP>(c / CH, c % CH);
-      *reinterpret_cast<u32x4*>(tq[b] + at) = rq[i];
-      *reinterpret_cast<u32x4*>(tg[b] + at) = rg[i];
-    }
+    ld.put(tq[b], tg[b]);
     if (tid < BN) {
-      tl[b][tid] = rl;
-      td[b][tid] = rd;
-      if constexpr (BIAS) tc[b][tid] = rc;
+      tl[b][tid] = exp_base<CAP>(a, rl);
+      td[b][tid] = -rd;
+      if constexpr (BIAS) tsl[b][tid] = rs * kLog2e;
+    }
+    if constexpr (BIAS) lc.put(tc[b], far_rows[b], org);
+  };
+  if (n_rows > 0) fetch(h, 0);
+
+  float kb_[NC], kn[NC];
+  bool far_cols = false;
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const f32x4 c = relative(kraw[j], org);
+      kb_[j] = col_term(c, g);
+      kn[j] = c[3];
+      far_cols |= __any(c[3] > kNearNorm) != 0;
+    }
+  }
+
+  const f32x4 zero{0.f, 0.f, 0.f, 0.f};
+  Frag kf[NC][KB], vf[NC][KB];
+  f32x4 dk[NC][DI], dv[NC][DI];
+  auto begin = [&]() {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        kf[j][kb] = kld.frag_signed(j, kb, a.negate);
+        vf[j][kb] = vld.frag(j, kb);
+      }
+#pragma unroll
+      for (int i = 0; i < DI; ++i) dk[j][i] = dv[j][i] = zero;
     }
   };
 
-  f32x4 dk[NC][DI], dv[NC][DI];
+  // 32 rows; part: rows may end inside them, distances may be long
+  auto step = [&](auto part, int b, int u, int left, bool far) {
+    constexpr bool PART = decltype(part)::v;
+    f32x4 s[NC][2], dp[NC][2];
 #pragma unroll
-  for (int j = 0; j < NC; ++j)
+    for (int n = 0; n < 2; ++n) {
+      const f32x4 nd = *reinterpret_cast<const f32x4*>(&td[b][u * 32 + n * 16 + 4 * g]);
 #pragma unroll
-    for (int i = 0; i < DI; ++i) dk[j][i] = dv[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  if (n_rows > 0) {
-    fetch(0);
-    put(0);
-  }
-  for (uint32_t r0 = 0, b = 0; r0 < n_rows; r0 += BN, b ^= 1) {
-    const bool more = r0 + BN < n_rows;
-    if (more) fetch(r0 + BN);
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      f32x4 s[NC][2], dp[NC][2];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const Frag fq = tile_frag<T, DP>(tq[b], u * 32 + n * 16, kb, lane);
-          const Frag fg = tile_frag<T, DP>(tg[b], u * 32 + n * 16, kb, lane);
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            s[j][n] = AMfma<T>::run(fq, kf[j][kb], kb == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j][n]);
-            dp[j][n] = AMfma<T>::run(fg, vf[j][kb], kb == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : dp[j][n]);
-          }
-        }
-      Frag pf[NC], df[NC];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int r = u * 32 + n * 16 + 4 * g;
-        const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&tl[b][r]);
-        const f32x4 delta = *reinterpret_cast<const f32x4*>(&td[b][r]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f32x4 qc{0.f, 0.f, 0.f, 0.f};
-          if constexpr (BIAS) qc = tc[b][r + e];
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            float p, ds;
-            grad_score<CAP, BIAS>(a, s[j][n][e], dp[j][n][e], lse2[e], delta[e], qc[3], kc[j], qc, &p, &ds);
-            if (!more && r0 + r + e >= n_rows) p = ds = 0.f;  // a zero row times an infinite key is NaN
-            pf[j][n * 4 + e] = static_cast<T>(p);
-            df[j][n * 4 + e] = static_cast<T>(ds);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < DI; ++i) {
-        const Frag fg = tile_frag_t<T, DP>(tg[b], u * 32, i, lane);
-        const Frag fq = tile_frag_t<T, DP>(tq[b], u * 32, i, lane);
+      for (int kb = 0; kb < KB; ++kb) {
+        const Frag fq = tile_frag<T, DP>(tq[b], u * 32 + n * 16, kb, lane);
+        const Frag fg = tile_frag<T, DP>(tg[b], u * 32 + n * 16, kb, lane);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-          dv[j][i] = AMfma<T>::run(fg, pf[j], dv[j][i]);
-          dk[j][i] = AMfma<T>::run(fq, df[j], dk[j][i]);
+          s[j][n] = AMfma<T>::run(fq, kf[j][kb], kb == 0 ? zero : s[j][n]);
+          dp[j][n] = AMfma<T>::run(fg, vf[j][kb], kb == 0 ? nd : dp[j][n]);
         }
       }
     }
-    if (more) put(b ^ 1);
-  }
-
-  const float vs = CAP ? 0.25f : 1.f;
+    Frag pf[NC], df[NC];
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    if (!live[j]) continue;
-    T* kd = static_cast<T*>(a.dk) + key[j] * a.k_stride + static_cast<int64_t>(w.kvh) * a.d;
-    T* vd = static_cast<T*>(a.dv) + key[j] * a.v_stride + static_cast<int64_t>(w.kvh) * a.d;
-    const int64_t rows = a.nk * a.hk;
-    float* part = a.part + (static_cast<int64_t>(w.split) * rows + key[j] * a.hk + w.kvh) * DP;
+    for (int n = 0; n < 2; ++n) {
+      const int r = u * 32 + n * 16 + 4 * g;
+      const f32x4 base = *reinterpret_cast<const f32x4*>(&tl[b][r]);
+      f32x4 slope = zero;
+      if constexpr (BIAS) slope = *reinterpret_cast<const f32x4*>(&tsl[b][r]);
 #pragma unroll
-    for (int i = 0; i < DI; ++i) {
-      f32x4 y = dk[j][i], x = dv[j][i];
+      for (int j = 0; j < NC; ++j) {
+        f32x4 dist = zero;
+        if constexpr (BIAS)
+          dist = distances(tc[b], u * 32 + n * 16, kn[j], kb_[j], PART && far, lane, a.kc, key0 + ck[j], a.ndim, org);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[e] *= a.scale;
-        x[e] *= vs;
-      }
-      if (a.splits > 1) {
-        *reinterpret_cast<f32x4*>(part + i * 16 + g * 4) = y;
-        *reinterpret_cast<f32x4*>(part + a.splits * rows * DP + i * 16 + g * 4) = x;
-      } else {
-        store4(kd, i * 16 + g * 4, a.d, a.vec_out, y);
-        store4(vd, i * 16 + g * 4, a.d, a.vec_out, x);
+        for (int e = 0; e < 4; ++e) {
+          float p, ds;
+          grad_score<CAP, BIAS>(a, s[j][n][e], dp[j][n][e], base[e], slope[e], dist[e], &p, &ds);
+          if constexpr (PART)
+            if (r + e >= left) p = ds = 0.f;  // a zero row times an infinite key is NaN
+          pf[j][n * 4 + e] = static_cast<T>(p);
+          df[j][n * 4 + e] = static_cast<T>(ds);
+        }
       }
     }
+#pragma unroll
+    for (int i = 0; i < DI; ++i) {
+      const Frag fg = tile_frag_t<T, DP>(tg[b], u * 32, i, lane);
+      const Frag fq = tile_frag_t<T, DP>(tq[b], u * 32, i, lane);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        dv[j][i] = AMfma<T>::run(fg, pf[j], dv[j][i]);
+        dk[j][i] = AMfma<T>::run(fq, df[j], dk[j][i]);
+      }
+    }
+  };
+
+  const float vs = CAP ? 0.25f : 1.f;
+  auto finish = [&]() {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      if (!live[j]) continue;
+      const int64_t key = key0 + ck[j], rows = a.nk * a.hk;
+      T* kd = static_cast<T*>(a.dk) + key * a.k_stride + static_cast<int64_t>(h) * a.d;
+      T* vd = static_cast<T*>(a.dv) + key * a.v_stride + static_cast<int64_t>(h) * a.d;
+      float* part = a.part + (static_cast<int64_t>(split) * rows + key * a.hk + h) * DP;
+#pragma unroll
+      for (int i = 0; i < DI; ++i) {
+        f32x4 y = dk[j][i], x = dv[j][i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] *= a.scale;
+          x[e] *= vs;
+        }
+        if (a.splits > 1) {
+          *reinterpret_cast<f32x4*>(part + i * 16 + g * 4) = y;
+          *reinterpret_cast<f32x4*>(part + a.splits * rows * DP + i * 16 + g * 4) = x;
+        } else {
+          store4(kd, i * 16 + g * 4, a.d, y);
+          store4(vd, i * 16 + g * 4, a.d, x);
+        }
+      }
+    }
+  };
+
+  if (n_rows <= 0) {
+    begin();
+    for (; h < h_end; ++h) finish();
+    return;
+  }
+  put(0);
+  begin();
+  for (int r0 = 0, b = 0;; b ^= 1) {
+    const bool wrap = r0 + BN >= n_rows;
+    const int hn = wrap ? h + 1 : h, rn = wrap ? 0 : r0 + BN;
+    const bool more = hn < h_end;
+    if (more) {
+      if (MULTI && wrap) fetch_cols(hn);
+      fetch(hn, rn);
+    }
+    __syncthreads();
+    if (busy) {
+      const int left = n_rows - r0;
+      const bool far = BIAS && (far_cols || tile_far<BN>(far_rows[b]));
+#pragma unroll
+      for (int u = 0; u < BN / 32; ++u) {
+        if (u * 32 >= left) continue;
+        if (u * 32 + 32 <= left && !far)
+          step(Flag<false>{}, b, u, left, false);
+        else
+          step(Flag<true>{}, b, u, left, far);
+      }
+    }
+    if (wrap) finish();
+    if (!more) break;
+    h = hn;
+    r0 = rn;
+    if (MULTI && wrap) begin();
+    put(b ^ 1);
   }
 }
 
 // out row r (row / heads, head row % heads) = sum over the splits, in order
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void k_attn_sum(const float* __restrict__ part, int64_t rows, int splits, int heads,
-                                                  int d, T* out, int64_t stride, bool vec) {
+                                                  int d, T* out, int64_t stride) {
   constexpr int Q = DP / 4;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = i / Q;
   const int d0 = static_cast<int>(i % Q) * 4;
@@ -409,53 +545,47 @@ __global__ __launch_bounds__(256) void k_attn_sum(const float* __restrict__ part
     for (int e = 0; e < 4; ++e) y[e] += v[e];
   }
   const int64_t n = row / heads;
-  store4(out + n * stride + (row - n * heads) * d, d0, d, vec, y);
+  store4(out + n * stride + (row - n * heads) * d, d0, d, y);
 }
 
 template <typename T, int DP>
 void run_sum(const float* part, int64_t rows, int splits, int heads, const AttnArgs& a, void* out, int64_t stride,
              hipStream_t s) {
   k_attn_sum<T, DP><<<static_cast<unsigned>(ceil_div<int64_t>(rows * (DP / 4), 256)), 256, 0, s>>>(
-      part, rows, splits, heads, a.d, static_cast<T*>(out), stride, a.vec_out);
+      part, rows, splits, heads, a.d, static_cast<T*>(out), stride);
 }
 
-// Two column blocks per wave only where their accumulators fit the registers.
-template <typename T, int DP, bool CAP, bool BIAS>
-void run_dq(const AttnArgs& a, const AttnPlan& p, unsigned grid, hipStream_t s) {
-  if constexpr (DP <= 64) {
-    if (p.nc == 2) {
-      k_attn_dq<T, DP, 2, CAP, BIAS, false><<<grid, 256, 0, s>>>(a);
-      return;
-    }
-  }
-  k_attn_dq<T, DP, 1, CAP, BIAS, false><<<grid, 256, 0, s>>>(a);
+template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS>
+void run_dq(const AttnArgs& a, hipStream_t s) {
+  k_attn_dq<T, DP, NC, CAP, BIAS, KS><<<dim3(attn_grid_x(a.tiles), ceil_div(a.hk, a.heads), a.splits), 256, 0, s>>>(a);
+}
+template <typename T, int DP, int NC, bool CAP, bool BIAS>
+void run_dkv(const AttnArgs& a, hipStream_t s) {
+  k_attn_dkv<T, DP, NC, CAP, BIAS><<<dim3(attn_grid_x(a.tiles), ceil_div(a.hk, a.heads), a.splits), 256, 0, s>>>(a);
 }
 
 template <typename T, int DP, bool CAP, bool BIAS>
 void run_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t s) {
-  a.tiles = attn_tiles(a.nq, a.grp, pq.bm, a.n_sets);
-  a.splits = pq.splits;
-  unsigned grid = static_cast<unsigned>(a.tiles * a.hk * a.splits);
   if (a.nq > 0) {
+    a.tiles = attn_tiles(a.nq, a.grp, pq.bm, a.n_sets);
+    a.splits = pq.splits;
+    a.heads = pq.heads;
     if (pq.share_keys)
-      k_attn_dq<T, DP, 1, CAP, BIAS, true><<<grid, 256, 0, s>>>(a);
+      run_dq<T, DP, 1, CAP, BIAS, true>(a, s);
+    else if (DP <= 64 && pq.nc == 2)
+      run_dq<T, DP, DP <= 64 ? 2 : 1, CAP, BIAS, false>(a, s);
     else
-      run_dq<T, DP, CAP, BIAS>(a, pq, grid, s);
+      run_dq<T, DP, 1, CAP, BIAS, false>(a, s);
     if (a.splits > 1) run_sum<T, DP>(a.part, a.nq * a.hq, a.splits, a.hq, a, a.dq, a.q_stride, s);
   }
   if (a.nk == 0) return;
   a.tiles = attn_tiles(a.nk, 1, pk.bm, a.n_sets);
   a.splits = pk.splits;
-  grid = static_cast<unsigned>(a.tiles * a.hk * a.splits);
-  if constexpr (DP <= 32) {
-    if (pk.nc == 2) {
-      k_attn_dkv<T, DP, 2, CAP, BIAS><<<grid, 256, 0, s>>>(a);
-    } else {
-      k_attn_dkv<T, DP, 1, CAP, BIAS><<<grid, 256, 0, s>>>(a);
-    }
-  } else {
-    k_attn_dkv<T, DP, 1, CAP, BIAS><<<grid, 256, 0, s>>>(a);
-  }
+  a.heads = pk.heads;
+  if (DP <= 32 && pk.nc == 2)
+    run_dkv<T, DP, DP <= 32 ? 2 : 1, CAP, BIAS>(a, s);
+  else
+    run_dkv<T, DP, 1, CAP, BIAS>(a, s);
   if (a.splits > 1) {
     const int64_t rows = a.nk * a.hk;
     run_sum<T, DP>(a.part, rows, a.splits, a.hk, a, a.dk, a.k_stride, s);

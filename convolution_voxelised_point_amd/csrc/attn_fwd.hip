@@ -1,254 +1,373 @@
 // Attention within packed sets, forward: one walk over the keys with a running
 // maximum and sum (see attn.h for the operand layout).
 //
-// Scores are kept in units of log 2, so probabilities are exp2(z - m).  The
-// maximum m that the accumulators refer to is raised only when a score passes
-// it by more than 8: probabilities stay below 2^8, which loses nothing in the
-// 16-bit operand (rounding is relative) nor in the fp32 sums, and most tiles
-// leave the accumulators as they are.  Rows without a finite score give zeros
-// and lse = -inf.
+// Vector instructions bound it (4 cycles each, 8 for exp2, rcp and sqrt, against
+// 6 cycles of matrix work per score at 64 channels), so each score gets as few
+// as possible:
+//   - scores are kept in units of log 2 and relative to the column's reference
+//     m, which is folded into the multiply-add that scales them;
+//   - m follows the maximum only when a score passes it by more than kSlack:
+//     larger probabilities cost nothing in the 16-bit operand (rounding is
+//     relative) nor in the fp32 sums, and most tiles need neither a maximum
+//     across lanes nor a change of the accumulators;
+//   - squared distances come from a matrix product (attn.h).
+// A tile that moves a reference, and the first and a partial one, take the slow
+// form: scores first, then their maximum, then p = exp2(z - m).  (It is also the
+// accurate form where z and m are large: folding -m in rounds to m's precision.)
+// Rows without a finite score give zeros and lse = -inf.
 #include "attn.h"
 
 namespace ts {
 
 namespace {
 
-constexpr float kSlack = 8.f;
+// How far a score may pass the reference: probabilities up to 2^kSlack, within
+// fp16's range; in bf16 and fp32 there would be room for far more.
+constexpr float kSlack = 12.f;
+// References up to this fold into the scores: that rounds them to 2^-24 of it.
+constexpr float kFold = 256.f;
 
-// KS (few query rows): all four waves of a block own the same 16 columns and
-// share out the keys of each tile, 32 rows each; their results are joined in
-// LDS.  Otherwise each wave owns NC column blocks of its own.
+// A wave owns NC column blocks of 16 query rows.  NC 2 (long sets): a key tile read
+// from LDS feeds both.  KS (few query rows): all four waves own the same 16 columns
+// and share out the keys of each tile, 32 each; their results are joined in LDS.
+//
+// A block takes a.heads key-value heads of its rows one after the other, as one walk
+// over (head, tile): for short sets, finding the set and the first reads would
+// cost more than a head's work, and the next head's rows are read while this one's
+// last tile is computed.
 template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS>
-__global__ __launch_bounds__(256, KS && DP == 128 ? 1 : 2) void k_attn_fwd(const AttnArgs a) {
+__global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_fwd(const AttnArgs a) {
   typedef typename AMfma<T>::frag Frag;
-  constexpr int KB = DP / 32, DI = DP / 16, CH = DP / 8;
+  constexpr int KB = DP / 32, DI = DP / 16;
   constexpr int BN = KS ? 128 : 64;  // keys per tile
   constexpr int NT = KS ? 2 : 4;     // 16-key steps of a wave per tile
-  constexpr int BM = KS ? 16 * NC : 64 * NC;
-  constexpr int CT = BN * CH / 256;  // chunks a thread stages per matrix
+  constexpr int BM = KS ? 16 : 64 * NC;
+  constexpr int TB = BN * DP * 2;
+  constexpr bool MULTI = NC == 1 && !KS && DP <= 64;  // a.heads may be more than 1
   static_assert(!KS || NC == 1, "one column block when the waves share the keys");
-  __shared__ __attribute__((aligned(16))) char tk[2][BN * DP * 2], tv[2][BN * DP * 2];
+  __shared__ __attribute__((aligned(16))) char tk[2][TB], tv[2][TB];
   __shared__ f32x4 tc[2][BIAS ? BN : 1];
+  __shared__ uint32_t far_rows[2][2];
 
-  const Where w = where(a);
-  if (a.flags && w.kvh == 0 && w.split == 0 && threadIdx.x == 0) {
-    check_starts(a.qs, a.nq, a.n_sets, w.tile, a.flags);
-    if (a.ks != a.qs) check_starts(a.ks, a.nk, a.n_sets, w.tile, a.flags);
+  const int64_t slot = block_tile();
+  const int split = blockIdx.z;
+  if (a.flags && blockIdx.y == 0 && split == 0 && threadIdx.x == 0) {
+    check_starts(a.qs, a.nq, a.n_sets, slot, a.flags);
+    if (a.ks != a.qs) check_starts(a.ks, a.nk, a.n_sets, slot, a.flags);
   }
   SetTile st;
-  if (!find_tile<BM>(a.qs, a.nq, a.grp, a.ks, a.nk, a.n_sets, w.tile, &st)) return;
+  if (!find_tile<BM>(a.qs, a.nq, a.grp, a.ks, a.nk, a.n_sets, slot, a.tiles, &st)) return;
   int64_t kbeg, kend;
-  split_range(st.st_len, BN, a.splits, w.split, &kbeg, &kend);
+  split_range(st.st_len, BN, a.splits, split, &kbeg, &kend);
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
   const int kt0 = KS ? wave * 32 : 0;
-  const T* kp = static_cast<const T*>(a.k) + (st.st0 + kbeg) * a.k_stride + static_cast<int64_t>(w.kvh) * a.d;
-  const T* vp = static_cast<const T*>(a.v) + (st.st0 + kbeg) * a.v_stride + static_cast<int64_t>(w.kvh) * a.d;
   const int n_keys = static_cast<int>(kend - kbeg);
+  int h = blockIdx.y * a.heads;
+  const int h_end = !MULTI ? h + 1 : h + a.heads < a.hk ? h + a.heads : a.hk;
 
-  // columns
-  int64_t row[NC];  // query * hq + head
-  bool live[NC];
+  const QueryCols<NC, KS> col(a, st, BM);
+  uint32_t qoff[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) qoff[j] = col.offset(j, a.q_stride, a.d);
+  const int width = a.grp * a.d;  // a key-value head's part of a query row
+  const T* qp = static_cast<const T*>(a.q) + col.query0 * a.q_stride;
+  const uint32_t qbytes = col.bytes(a.q_stride, width);
+  Origin org{0.f, 0.f, 0.f};
+  Origin qraw[NC];
+  if constexpr (BIAS) {
+    org = load_origin(a.qc, st.own0, a.ndim);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) qraw[j] = load_origin(a.qc, col.query0 + col.dq[j], a.ndim);
+  }
+  ColLoad<T, DP, NC> qld;
+  float next_slope[NC];
+  auto fetch_cols = [&](int hn) {
+    qld.fetch(qp + static_cast<int64_t>(hn) * width, qbytes, qoff, a.d);
+    if constexpr (BIAS)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) next_slope[j] = a.slopes[hn * a.grp + col.place[j]];
+  };
+  fetch_cols(h);
+  KeyTiles<T, DP, BN, BIAS> keys(a, st.st0 + kbeg, n_keys);
+  if (n_keys > 0) keys.fetch(a, h, 0);
+
+  float slope[NC], qb[NC], qn[NC];  // (the last two: for the distances)
+  bool far_cols = false;
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const f32x4 c = relative(qraw[j], org);
+      qb[j] = col_term(c, g);
+      qn[j] = c[3];
+      far_cols |= __any(c[3] > kNearNorm) != 0;
+    }
+  }
+
+  const f32x4 zero{0.f, 0.f, 0.f, 0.f};
   Frag qf[NC][KB];
-  f32x4 qc[NC];  // coordinates and the slope in units of log 2
-#pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int64_t r = st.row0 + ((KS ? 0 : wave * NC) + j) * 16 + (lane & 15);
-    live[j] = r < st.rows;
-    const uint32_t rr = live[j] ? static_cast<uint32_t>(r) : 0;
-    const uint32_t qi = a.grp == 1 ? rr : rr / static_cast<uint32_t>(a.grp);
-    const int64_t query = st.own0 + qi;
-    const int head = w.kvh * a.grp + static_cast<int>(rr - qi * a.grp);
-    row[j] = query * a.hq + head;
-    const T* qp = static_cast<const T*>(a.q) + query * a.q_stride + static_cast<int64_t>(head) * a.d;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-      qf[j][kb] = __builtin_bit_cast(Frag, live[j] ? load8(qp, kb * 32 + g * 8, a.d, a.vec_in) : u32x4{0u, 0u, 0u, 0u});
-    if constexpr (BIAS) qc[j] = load_coord(a.qc, query, a.ndim, a.slopes[head] * kLog2e);
-  }
-
-  u32x4 rk[CT], rv[CT];
-  f32x4 rc{0.f, 0.f, 0.f, 0.f};
-  auto fetch = [&](int k0) {
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-      const int c = i * 256 + tid, r = k0 + c / CH, d0 = (c % CH) * 8;
-      const bool ok = r < n_keys;  // rows past the end become zeros: 0 * NaN of another set's row would be NaN
-      rk[i] = ok ? load8(kp + static_cast<int64_t>(r) * a.k_stride, d0, a.d, a.vec_in) : u32x4{0u, 0u, 0u, 0u};
-      rv[i] = ok ? load8(vp + static_cast<int64_t>(r) * a.v_stride, d0, a.d, a.vec_in) : u32x4{0u, 0u, 0u, 0u};
-    }
-    if constexpr (BIAS)
-      if (tid < BN && k0 + tid < n_keys) rc = load_coord(a.kc, st.st0 + kbeg + k0 + tid, a.ndim, 0.f);
-  };
-  auto put = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-      const int c = i * 256 + tid, at = tile_at<DP>(c / CH, c % CH);
-      *reinterpret_cast<u32x4*>(tk[b] + at) = rk[i];
-      *reinterpret_cast<u32x4*>(tv[b] + at) = rv[i];
-    }
-    if constexpr (BIAS)
-      if (tid < BN) tc[b][tid] = rc;
-  };
-
   f32x4 o[NC][DI];
-  float m[NC], l[NC];
+  float l[NC], m[NC];  // m -inf: no finite score yet
+  bool fold;           // every column has a reference that folds
+  auto begin = [&]() {  // of head h, whose columns have been read
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    m[j] = -INFINITY;
-    l[j] = 0.f;
+    for (int j = 0; j < NC; ++j) {
+      m[j] = -INFINITY;
+      l[j] = 0.f;
 #pragma unroll
-    for (int i = 0; i < DI; ++i) o[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+      for (int i = 0; i < DI; ++i) o[j][i] = zero;
+      // a negative scale is moved into q, so that c1 >= 0
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) qf[j][kb] = qld.frag_signed(j, kb, a.negate);
+      if constexpr (BIAS) slope[j] = next_slope[j] * kLog2e;
+    }
+    fold = false;
+  };
 
-  if (n_keys > 0) {
-    fetch(0);
-    put(0);
-  }
-  for (int k0 = 0, b = 0; k0 < n_keys; k0 += BN, b ^= 1) {
-    const bool more = k0 + BN < n_keys;
-    if (more) fetch(k0 + BN);
-    __syncthreads();
+  // s = k . q of 16 keys
+  auto product = [&](int b, int n, f32x4(&s)[NC]) {
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const Frag f = tile_frag<T, DP>(tk[b], kt0 + n * 16, kb, lane);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) s[j] = AMfma<T>::run(f, qf[j][kb], kb == 0 ? zero : s[j]);
+    }
+  };
+  auto dist_of = [&](int b, int n, int j, bool far) {
+    return distances(tc[b], kt0 + n * 16, qn[j], qb[j], far, lane, a.qc, col.query0 + col.dq[j], a.ndim, org);
+  };
+  // the score relative to `base`
+  auto score = [&](int j, float s, float dist, float base) {
+    if constexpr (BIAS) base = fmaf(-slope[j], dist, base);
+    if constexpr (CAP)  // c2 tanh(x) = c2 - 2 c2 / (exp(2x) + 1)
+      return fmaf(-2.f * a.c2, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(s * a.c1) + 1.f), base);
+    else
+      return fmaf(s, a.c1, base);
+  };
+  // o += V^T p for 32 keys
+  auto gather = [&](int b, int u, const Frag(&p)[NC]) {
+#pragma unroll
+    for (int i = 0; i < DI; ++i) {
+      const Frag f = tile_frag_t<T, DP>(tv[b], kt0 + u * 32, i, lane);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) o[j][i] = AMfma<T>::run(f, p[j], o[j][i]);
+    }
+  };
+
+  // A whole tile against references that hold; false (and nothing changed) if one does not.
+  auto fast = [&](int b) {
     f32x4 s[NC][NT];
+    float base[NC], top[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      base[j] = CAP ? a.c2 - m[j] : -m[j];
+      top[j] = -INFINITY;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      f32x4 x[NC];
+      product(b, n, x);
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const Frag f = tile_frag<T, DP>(tk[b], kt0 + n * 16, kb, lane);
+      for (int j = 0; j < NC; ++j) {
+        f32x4 dist = zero;
+        if constexpr (BIAS) dist = dist_of(b, n, j, false);
 #pragma unroll
-        for (int j = 0; j < NC; ++j)
-          s[j][n] = AMfma<T>::run(f, qf[j][kb], kb == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j][n]);
+        for (int e = 0; e < 4; ++e) {
+          s[j][n][e] = score(j, x[j][e], dist[e], base[j]);
+          top[j] = fmaxf(top[j], s[j][n][e]);
+        }
       }
     }
+    bool up = false;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) up |= top[j] > kSlack;
+    if (__any(up)) return false;
+#pragma unroll
+    for (int u = 0; u < NT / 2; ++u) {
+      Frag p[NC];
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = __builtin_amdgcn_exp2f(s[j][2 * u + (e >> 2)][e & 3]);
+          l[j] += x;  // unrounded: the backward pass needs lse to fp32
+          p[j][e] = static_cast<T>(x);
+        }
+      gather(b, u, p);
+    }
+    return true;
+  };
+
+  auto slow = [&](int b, int left, bool far) {
+    f32x4 s[NC][NT];
     float top[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) top[j] = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      if (n * 16 >= left) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int kr = kt0 + n * 16 + 4 * g + e;
-        f32x4 kc;
-        if constexpr (BIAS) kc = tc[b][kr];
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          float z = s[j][n][e];
-          if constexpr (CAP) {
-            // c2 tanh(x) = c2 - 2 c2 / (exp(2x) + 1)
-            const float r = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(z * a.c1) + 1.f);
-            z = fmaf(-2.f * a.c2, r, a.c2);
-          } else {
-            z *= a.c1;
-          }
-          if constexpr (BIAS) z = fmaf(-qc[j][3], distance(qc[j], kc), z);
-          if (!more) z = k0 + kr < n_keys ? z : -INFINITY;
-          s[j][n][e] = z;
-          top[j] = fmaxf(top[j], z);
-        }
+        for (int j = 0; j < NC; ++j) s[j][n] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        continue;
       }
+      f32x4 x[NC];
+      product(b, n, x);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      top[j] = col_max(top[j]);
-      const bool raise = top[j] > m[j] + kSlack;
-      if (__any(raise)) {
-        const float mn = raise ? top[j] : m[j];
-        const float f = raise ? __builtin_amdgcn_exp2f(m[j] - mn) : 1.f;
-        m[j] = mn;
-        l[j] *= f;
+      for (int j = 0; j < NC; ++j) {
+        f32x4 dist = zero;
+        if constexpr (BIAS) dist = dist_of(b, n, j, far);
 #pragma unroll
-        for (int i = 0; i < DI; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[j][i][e] *= f;
+        for (int e = 0; e < 4; ++e) s[j][n][e] = score(j, x[j][e], dist[e], CAP ? a.c2 : 0.f);
       }
     }
-    Frag p[NC][NT / 2];
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const float ms = m[j] == -INFINITY ? 0.f : m[j];
+    if (left < NT * 16) {
+      const int own = left - 4 * g;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = __builtin_amdgcn_exp2f(s[j][n][e] - ms);
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int j = 0; j < NC; ++j) s[j][n][e] = n * 16 + e < own ? s[j][n][e] : -INFINITY;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[j] = fmaxf(top[j], s[j][n][e]);
+    fold = true;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const float t = col_max(top[j]);
+      const float mn = t > m[j] + kSlack ? t : m[j];  // t > -inf when there is no reference
+      const float f = m[j] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[j] - mn);
+      m[j] = mn;
+      l[j] *= f;
+#pragma unroll
+      for (int i = 0; i < DI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][i][e] *= f;
+      fold &= fabsf(mn) <= kFold;
+    }
+    fold = __all(fold);
+#pragma unroll
+    for (int u = 0; u < NT / 2; ++u) {
+      if (u * 32 >= left) continue;
+      Frag p[NC];
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const float ms = m[j] == -INFINITY ? 0.f : m[j];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = __builtin_amdgcn_exp2f(s[j][2 * u + (e >> 2)][e & 3] - ms);
           l[j] += x;
-          p[j][n / 2][(n & 1) * 4 + e] = static_cast<T>(x);
+          p[j][e] = static_cast<T>(x);
         }
-    }
-#pragma unroll
-    for (int u = 0; u < NT / 2; ++u)
-#pragma unroll
-      for (int i = 0; i < DI; ++i) {
-        const Frag f = tile_frag_t<T, DP>(tv[b], kt0 + u * 32, i, lane);
-#pragma unroll
-        for (int j = 0; j < NC; ++j) o[j][i] = AMfma<T>::run(f, p[j][u], o[j][i]);
       }
-    if (more) put(b ^ 1);
-  }
-
-#pragma unroll
-  for (int j = 0; j < NC; ++j) l[j] = col_sum(l[j]);
-
-  if constexpr (KS) {  // join the four waves: their shares of the sum relative to the largest maximum
-    float* jm = reinterpret_cast<float*>(tk);          // [4][16] maxima, then sums
-    float* jo = reinterpret_cast<float*>(tv);          // [4][16][DP]
-    __syncthreads();
-    if (g == 0) {
-      jm[wave * 16 + lane] = m[0];
-      jm[64 + wave * 16 + lane] = l[0];
+      gather(b, u, p);
     }
-#pragma unroll
-    for (int i = 0; i < DI; ++i)
-      *reinterpret_cast<f32x4*>(jo + (wave * 16 + (lane & 15)) * DP + i * 16 + g * 4) = o[0][i];
-    __syncthreads();
-    if (wave != 0) return;
-    float mw[4], mt = -INFINITY, lt = 0.f;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      mw[x] = jm[x * 16 + (lane & 15)];
-      mt = fmaxf(mt, mw[x]);
-    }
-#pragma unroll
-    for (int i = 0; i < DI; ++i) o[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const float f = mw[x] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mw[x] - mt);
-      lt = fmaf(f, jm[64 + x * 16 + (lane & 15)], lt);
-#pragma unroll
-      for (int i = 0; i < DI; ++i) {
-        const f32x4 y = *reinterpret_cast<const f32x4*>(jo + (x * 16 + (lane & 15)) * DP + i * 16 + g * 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[0][i][e] = fmaf(f, y[e], o[0][i][e]);
-      }
-    }
-    m[0] = mt;
-    l[0] = lt;
-  }
+  };
 
+  // Results of head h.
+  auto finish = [&]() {
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    if (!live[j]) continue;
-    if (a.splits > 1) {
-      const int64_t at = static_cast<int64_t>(w.split) * a.nq * a.hq + row[j];
+    for (int j = 0; j < NC; ++j) l[j] = col_sum(l[j]);
+    if constexpr (KS) {  // join the four waves: their shares of the sum relative to the largest maximum
+      float* jm = reinterpret_cast<float*>(tk);  // [4][16] maxima, then sums
+      float* jo = reinterpret_cast<float*>(tv);  // [4][16][DP]
+      __syncthreads();
       if (g == 0) {
-        a.part_ml[at * 2] = m[j];
-        a.part_ml[at * 2 + 1] = l[j];
+        jm[wave * 16 + lane] = m[0];
+        jm[64 + wave * 16 + lane] = l[0];
       }
-      if (n_keys > 0)
 #pragma unroll
-        for (int i = 0; i < DI; ++i) *reinterpret_cast<f32x4*>(a.part + at * DP + i * 16 + g * 4) = o[j][i];
-      continue;
+      for (int i = 0; i < DI; ++i)
+        *reinterpret_cast<f32x4*>(jo + (wave * 16 + (lane & 15)) * DP + i * 16 + g * 4) = o[0][i];
+      __syncthreads();
+      float mw[4], mt = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        mw[x] = jm[x * 16 + (lane & 15)];
+        mt = fmaxf(mt, mw[x]);
+      }
+#pragma unroll
+      for (int i = 0; i < DI; ++i) o[0][i] = zero;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float f = mw[x] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mw[x] - mt);
+        lt = fmaf(f, jm[64 + x * 16 + (lane & 15)], lt);
+#pragma unroll
+        for (int i = 0; i < DI; ++i) {
+          const f32x4 y = *reinterpret_cast<const f32x4*>(jo + (x * 16 + (lane & 15)) * DP + i * 16 + g * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[0][i][e] = fmaf(f, y[e], o[0][i][e]);
+        }
+      }
+      m[0] = mt;
+      l[0] = lt;
+      __syncthreads();  // the next head's tiles go where the shares were
+      if (wave != 0) return;
     }
-    const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
-    const int64_t query = row[j] / a.hq;
-    T* op = static_cast<T*>(a.out) + query * a.o_stride + (row[j] - query * a.hq) * a.d;
 #pragma unroll
-    for (int i = 0; i < DI; ++i) {
-      f32x4 y = o[j][i];
+    for (int j = 0; j < NC; ++j) {
+      if (!col.live[j]) continue;
+      const int64_t query = col.query0 + col.dq[j];
+      const int head = h * a.grp + static_cast<int>(col.place[j]);
+      const int64_t at = (static_cast<int64_t>(split) * a.nq + query) * a.hq + head;
+      if (a.splits > 1) {
+        if (g == 0) {
+          a.part_ml[at * 2] = m[j];
+          a.part_ml[at * 2 + 1] = l[j];
+        }
+        if (n_keys > 0)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] *= inv;
-      store4(op, i * 16 + g * 4, a.d, a.vec_out, y);
+          for (int i = 0; i < DI; ++i) *reinterpret_cast<f32x4*>(a.part + at * DP + i * 16 + g * 4) = o[j][i];
+        continue;
+      }
+      const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
+      T* op = static_cast<T*>(a.out) + query * a.o_stride + static_cast<int64_t>(head) * a.d;
+#pragma unroll
+      for (int i = 0; i < DI; ++i) {
+        f32x4 y = o[j][i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] *= inv;
+        store4(op, i * 16 + g * 4, a.d, y);
+      }
+      if (g == 0) a.lse[at] = l[j] == 0.f ? -INFINITY : (m[j] + __builtin_amdgcn_logf(l[j])) * kLn2;
     }
-    if (g == 0) a.lse[row[j]] = l[j] == 0.f ? -INFINITY : (m[j] + __builtin_amdgcn_logf(l[j])) * kLn2;
+  };
+
+  if (n_keys <= 0) {
+    for (; h < h_end; ++h) {
+      begin();
+      finish();
+    }
+    return;
+  }
+  keys.put(tk[0], tv[0], tc[0], far_rows[0], org);
+  begin();
+  for (int k0 = 0, b = 0;; b ^= 1) {
+    const bool wrap = k0 + BN >= n_keys;
+    const int hn = wrap ? h + 1 : h, kn = wrap ? 0 : k0 + BN;  // the next tile
+    const bool more = hn < h_end;
+    if (more) {
+      if (MULTI && wrap) fetch_cols(hn);
+      keys.fetch(a, hn, kn);
+    }
+    __syncthreads();
+    if (col.busy) {
+      const int left = n_keys - k0 - kt0;  // keys of this wave's part
+      const bool far = BIAS && (far_cols || tile_far<BN>(far_rows[b]));
+      bool done = false;
+      if (fold && !far && k0 + BN <= n_keys) done = fast(b);
+      if (!done) slow(b, left, far);
+    }
+    if (wrap) finish();
+    if (!more) break;
+    h = hn;
+    k0 = kn;
+    if (MULTI && wrap) begin();
+    keys.put(tk[b ^ 1], tv[b ^ 1], tc[b ^ 1], far_rows[b ^ 1], org);
   }
 }
 
@@ -306,12 +425,13 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] *= inv;
   const int64_t query = row / a.hq;
-  store4(static_cast<T*>(a.out) + query * a.o_stride + (row - query * a.hq) * a.d, d4 * 4, a.d, a.vec_out, y);
+  store4(static_cast<T*>(a.out) + query * a.o_stride + (row - query * a.hq) * a.d, d4 * 4, a.d, y);
   if (tid == 0) a.lse[row] = l == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <typename T, int DP, int NC, bool KS>
-void run_fwd(const AttnArgs& a, bool cap, unsigned grid, hipStream_t s) {
+void run_fwd(const AttnArgs& a, bool cap, hipStream_t s) {
+  const dim3 grid(attn_grid_x(a.tiles), ceil_div(a.hk, a.heads), a.splits);
   const bool bias = a.slopes != nullptr;
   if (cap && bias)
     k_attn_fwd<T, DP, NC, true, true, KS><<<grid, 256, 0, s>>>(a);
@@ -327,18 +447,13 @@ template <typename T, int DP>
 void run_fwd(AttnArgs& a, const AttnPlan& p, bool cap, hipStream_t s) {
   a.tiles = attn_tiles(a.nq, a.grp, p.bm, a.n_sets);
   a.splits = p.splits;
-  const unsigned grid = static_cast<unsigned>(a.tiles * a.hk * a.splits);
-  bool done = false;
-  if constexpr (DP <= 64) {  // two column blocks per wave only where their accumulators fit the registers
-    if (p.nc == 2) {
-      run_fwd<T, DP, 2, false>(a, cap, grid, s);
-      done = true;
-    }
-  }
-  if (!done && p.share_keys)
-    run_fwd<T, DP, 1, true>(a, cap, grid, s);
-  else if (!done)
-    run_fwd<T, DP, 1, false>(a, cap, grid, s);
+  a.heads = p.heads;
+  if (p.share_keys)
+    run_fwd<T, DP, 1, true>(a, cap, s);
+  else if (DP <= 64 && p.nc == 2)
+    run_fwd<T, DP, DP <= 64 ? 2 : 1, false>(a, cap, s);
+  else
+    run_fwd<T, DP, 1, false>(a, cap, s);
   if (a.splits > 1) k_attn_join<T, DP><<<static_cast<unsigned>(a.nq * a.hq), 256, 0, s>>>(a);
 }
 
@@ -353,6 +468,28 @@ void run_fwd(AttnArgs& a, const AttnPlan& p, bool cap, hipStream_t s) {
 }
 
 }  // namespace
+
+// Rows of `heads` heads of d elements, `stride` apart, to or from rows of heads of d8
+// elements, dense; the elements between d and d8 become zeros.
+__global__ __launch_bounds__(256) void k_attn_repack(const uint16_t* __restrict__ src, int64_t src_stride, int src_d,
+                                                     uint16_t* __restrict__ dst, int64_t dst_stride, int dst_d,
+                                                     int64_t n, int heads) {
+  const int64_t per = static_cast<int64_t>(heads) * dst_d, total = n * per;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t{256} * gridDim.x) {
+    const int64_t r = i / per;
+    const int c = static_cast<int>(i - r * per), h = c / dst_d, e = c - h * dst_d;
+    dst[r * dst_stride + c] = e < src_d ? src[r * src_stride + h * src_d + e] : uint16_t{0};
+  }
+}
+
+hipError_t launch_attn_repack(const void* src, int64_t src_stride, int src_d, void* dst, int64_t dst_stride, int dst_d,
+                              int64_t n, int heads, hipStream_t s) {
+  const int64_t total = n * heads * dst_d, blocks = ceil_div<int64_t>(total, 256), most = 1 << 16;
+  if (total == 0) return hipSuccess;
+  k_attn_repack<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, s>>>(
+      static_cast<const uint16_t*>(src), src_stride, src_d, static_cast<uint16_t*>(dst), dst_stride, dst_d, n, heads);
+  return hipGetLastError();
+}
 
 hipError_t launch_attn_fwd(AttnArgs& a, const AttnPlan& p, ts_dtype dt, bool cap, hipStream_t s) {
   if (dt == TS_F16)

@@ -126,12 +126,26 @@ hipError_t launch_wgrad(const ts_kmap* map, const void* x, int cin, const void* 
 // attn_fwd.hip, attn_bwd.hip
 struct AttnArgs;
 constexpr int kAttnMaxSplits = 512;
-// How a walk is cut up: columns per block, column blocks per wave, whether the
-// waves of a block share one column block, and parts of the other side.
+// Waves per SIMD that the registers of a kernel of this shape allow without spilling.
+constexpr int attn_waves_fwd(int dp, int nc, bool bias, bool share_keys) {
+  return share_keys ? (dp == 128 ? 1 : 2) : nc == 2 || dp == 128 ? 2 : dp == 64 ? (bias ? 2 : 3) : 4;
+}
+constexpr int attn_waves_dq(int dp, int nc, bool cap, bool bias, bool share_keys) {
+  return share_keys ? (dp == 128 ? 1 : 2) : nc == 2 || dp >= 64 || (cap && bias) ? 2 : bias ? 3 : 4;
+}
+constexpr int attn_waves_dkv(int dp, int nc, bool bias) {
+  return dp == 128 ? 1 : dp == 32 && nc == 1 ? 3 : 2;
+}
+// How a walk is cut up: columns per block, column blocks per wave, key-value heads
+// per block, parts of the other side, and whether the waves of a block share one
+// column block.
 struct AttnPlan {
-  int bm, nc, splits;
+  int bm, nc, heads, splits;
   bool share_keys;
 };
+// Rows of 16-bit heads copied to another stride and head width (zeros beyond the source's).
+hipError_t launch_attn_repack(const void* src, int64_t src_stride, int src_d, void* dst, int64_t dst_stride, int dst_d,
+                              int64_t n, int heads, hipStream_t s);
 hipError_t launch_attn_fwd(AttnArgs& a, const AttnPlan& p, ts_dtype dt, bool cap, hipStream_t s);
 hipError_t launch_attn_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, ts_dtype dt, bool cap, hipStream_t s);
 

@@ -706,6 +706,11 @@ def _need(ok: bool, what: str) -> None:
         raise TsError(TS_ERR_INVALID_ARG, what)
 
 
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """t, or a dense copy of it where the kernels could not read it in 16-byte pieces."""
+    return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
 def attn_args(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch.Tensor,
               k_starts: Optional[torch.Tensor] = None, scale: Optional[float] = None, cap: float = 0.0,
               slopes: Optional[torch.Tensor] = None, q_coords: Optional[torch.Tensor] = None,
@@ -744,8 +749,9 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch.
              stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(out [nq][hq][d], lse [nq][hq]): attention of each packed set's rows
     over its own keys (see ts_attn in ts.h)."""
-    at = attn_args(q, k, v, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords)
     with _on(stream):
+        q, k, v = _aligned(q), _aligned(k), _aligned(v)
+        at = attn_args(q, k, v, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords)
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         n = ts_attn_workspace_bytes(at, False)
@@ -766,6 +772,7 @@ def attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:2],
           "attention: lse is float32 [nq][hq]")
     with _on(stream):
+        q, k, v, out, dout = (_aligned(t) for t in (q, k, v, out, dout))
         if _row_stride(dout) != _row_stride(out):
             dout = dout.contiguous()
             out = out.contiguous()

@@ -554,9 +554,10 @@ ts_status ts_conv_bwd_dgrad_noalloc(const ts_kmap* map, const void* dy, int cout
  *
  * Rows: q [nq][hq][d], k and v [nk][hk][d], out [nq][hq][d] with the heads of
  * a row adjacent and rows `*_stride` elements apart (>= heads * d), so q, k, v
- * may be columns of one projected matrix.  16-byte aligned operands with d and
- * strides in multiples of 8 are read in 16-byte accesses; anything else works
- * element by element.  fp16 or bf16 (TS_F32 is TS_ERR_UNSUPPORTED), 1 <= d <=
+ * may be columns of one projected matrix.  Where d and the strides are multiples
+ * of 8 the operands are read as they lie and must be 16-byte aligned (results
+ * 8-byte aligned); otherwise they may lie anywhere and are copied to padded rows
+ * in the workspace first.  fp16 or bf16 (TS_F32 is TS_ERR_UNSUPPORTED), 1 <= d <=
  * 128, hk divides hq; products are accumulated in fp32, softmax statistics are
  * fp32, probabilities and score gradients are rounded to the feature type for
  * their products.  With fp16, score gradients below 2^-24 vanish and above
@@ -584,7 +585,7 @@ size_t ts_attn_workspace_bytes(const ts_attn* at, int backward);
  * written once.  Errors: TS_ERR_INVALID_ARG (null pointers, sizes, strides,
  * a short workspace, scale or cap not finite, cap < 0), TS_ERR_UNSUPPORTED
  * (fp32, d > 128, more than 2^31 - 1 rows times heads, more than 2^24 tiles of
- * 64 rows, sets counted as at least one), TS_ERR_HIP. */
+ * 64 rows, sets counted as at least one, strides above 2^23), TS_ERR_HIP. */
 ts_status ts_attn_fwd(const ts_attn* at, const void* q, const void* k, const void* v, void* out, float* lse, void* ws,
                       size_t ws_bytes, uint32_t* err_flags, hipStream_t stream);
 
