@@ -11,7 +11,6 @@ ask for and keep them alive next to the C structs that point into them.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional, Tuple, Union
@@ -170,12 +169,15 @@ def _rows(t: torch.Tensor):
 
 def _row_stride(t: torch.Tensor) -> Optional[int]:
     """Elements between the rows of [n][heads][d], or None where the heads of a row are not adjacent."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    if t.dim() != 3:
         return None
-    width = t.shape[1] * t.shape[2]
-    if t.shape[0] <= 1:
-        return width
-    return t.stride(0) if t.stride(0) >= width else None
+    n, h, d = t.shape
+    row, head, one = t.stride()
+    if (one != 1 and d > 1) or (head != d and h > 1):
+        return None
+    if n <= 1:
+        return h * d
+    return row if row >= h * d else None
 
 
 def _stream(stream=None):
@@ -695,20 +697,33 @@ def conv_wgrad(kmap: Kmap, x: torch.Tensor, dy: torch.Tensor, ws=None, stream=No
 
 
 # ---------------------------------------------------------------- voxel-transformer operators
-def _on(stream):
-    """Buffers of a call on another stream come from that stream's pool, so
-    that a freed workspace is not handed out while the call still runs."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
+# These calls are short, so they check their tensors in one pass and hand plain
+# addresses to the library.  A call on another stream runs with that stream as
+# the current one, so that its buffers come from that stream's pool (a freed
+# workspace is not handed out while the call still runs).
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise TsError(TS_ERR_INVALID_ARG, what)
 
 
+def _raw_stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _aligned(t: torch.Tensor) -> torch.Tensor:
     """t, or a dense copy of it where the kernels could not read it in 16-byte pieces."""
     return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _flag_ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    if t is None:
+        return None
+    _need(t.is_cuda and t.element_size() == 4 and t.numel() >= 1, "err_flags is a 32-bit device word")
+    return t.data_ptr()
 
 
 def attn_args(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch.Tensor,
@@ -717,29 +732,34 @@ def attn_args(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch
               k_coords: Optional[torch.Tensor] = None, o_stride: Optional[int] = None) -> TsAttn:
     """The C description of an attention call, its tensors checked against
     each other.  scale defaults to 1 / sqrt(d); o_stride to dense rows."""
-    strides = [_row_stride(t) if t.dim() == 3 and t.is_cuda else None for t in (q, k, v)]
-    _need(None not in strides, "attention: q, k, v are device tensors [n][heads][d] with adjacent heads")
+    qst, kst, vst = _row_stride(q), _row_stride(k), _row_stride(v)
+    _need(qst is not None and kst is not None and vst is not None and q.is_cuda and k.is_cuda and v.is_cuda,
+          "attention: q, k, v are device tensors [n][heads][d] with adjacent heads")
     nq, hq, d = q.shape
-    nk, hk = k.shape[0], k.shape[1]
-    _need(v.shape == k.shape and k.shape[2] == d and q.dtype == k.dtype == v.dtype and q.dtype in _DT,
+    nk, hk, dk = k.shape
+    dtype = q.dtype
+    _need(dk == d and v.shape == k.shape and k.dtype is dtype and v.dtype is dtype and dtype in _DT,
           "attention: q, k, v differ in width, type or keys")
-    for s in (q_starts, k_starts):
-        _need(s is None or (s.is_cuda and s.dtype == torch.int64 and s.dim() == 1 and s.is_contiguous()
-                            and s.shape[0] == q_starts.shape[0] >= 1), "attention: starts are int64 [n_sets + 1]")
+    n_sets = q_starts.numel() - 1
+    _need(n_sets >= 0 and q_starts.dtype is torch.int64 and q_starts.is_cuda and q_starts.is_contiguous(),
+          "attention: starts are int64 [n_sets + 1]")
+    if k_starts is not None:
+        _need(k_starts.numel() - 1 == n_sets and k_starts.dtype is torch.int64 and k_starts.is_cuda
+              and k_starts.is_contiguous(), "attention: starts are int64 [n_sets + 1]")
     ndim = 3
     if slopes is not None:
-        _need(slopes.is_cuda and slopes.dtype == torch.float32 and slopes.is_contiguous() and slopes.numel() == hq,
+        _need(slopes.is_cuda and slopes.dtype is torch.float32 and slopes.is_contiguous() and slopes.numel() == hq,
               "attention: slopes are float32 [hq]")
-        _need(q_coords is not None, "attention: slopes need coordinates")
+        _need(q_coords is not None and q_coords.dim() == 2, "attention: slopes need coordinates")
         ndim = q_coords.shape[1] - 1
         for c, n in ((q_coords, nq), (q_coords if k_coords is None else k_coords, nk)):
-            _need(c.is_cuda and c.dtype == torch.int32 and c.is_contiguous() and tuple(c.shape) == (n, ndim + 1),
+            _need(c.is_cuda and c.dtype is torch.int32 and c.is_contiguous() and c.shape == (n, ndim + 1),
                   "attention: coordinates are int32 [n][ndim + 1]")
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    return TsAttn(_DT[q.dtype], hq, hk, d, ndim, 1.0 / d ** 0.5 if scale is None else scale, cap, nq, nk,
-                  q_starts.shape[0] - 1, *strides, hq * d if o_stride is None else o_stride, ptr(q_starts),
-                  ptr(k_starts), ptr(slopes), ptr(q_coords) if slopes is not None else None,
-                  ptr(k_coords) if slopes is not None else None)
+    else:
+        q_coords = k_coords = None
+    return TsAttn(_DT[dtype], hq, hk, d, ndim, 1.0 / d ** 0.5 if scale is None else scale, cap, nq, nk, n_sets, qst, kst,
+                  vst, hq * d if o_stride is None else o_stride, q_starts.data_ptr(), _ptr(k_starts), _ptr(slopes),
+                  _ptr(q_coords), _ptr(k_coords))
 
 
 def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch.Tensor,
@@ -749,14 +769,18 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch.
              stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(out [nq][hq][d], lse [nq][hq]): attention of each packed set's rows
     over its own keys (see ts_attn in ts.h)."""
-    with _on(stream):
-        q, k, v = _aligned(q), _aligned(k), _aligned(v)
-        at = attn_args(q, k, v, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords)
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        n = ts_attn_workspace_bytes(at, False)
-        ws = _bytes(n, q.device) if n else None
-        ts_attn_fwd(at, q, k, v, out, lse, ws, err_flags, stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return attn_fwd(q, k, v, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords, err_flags)
+    q, k, v = _aligned(q), _aligned(k), _aligned(v)
+    at = attn_args(q, k, v, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords)
+    ref, dev = ctypes.byref(at), q.device
+    out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    lse = torch.empty((at.nq, at.hq), dtype=torch.float32, device=dev)
+    n = _lib_attn_workspace_bytes(ref, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    _check(_lib_attn_fwd(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), _ptr(ws), n,
+                         _flag_ptr(err_flags), _raw_stream(q)), "ts_attn_fwd")
     return out, lse
 
 
@@ -767,19 +791,26 @@ def attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
              err_flags: Optional[torch.Tensor] = None,
              stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dq, dk, dv) of attn_fwd with the same arguments, laid out like q, k, v."""
-    _need(out.shape == q.shape and dout.shape == q.shape and out.dtype == dout.dtype == q.dtype,
-          "attention: out and dout are like q")
-    _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:2],
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return attn_bwd(dout, q, k, v, out, lse, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords, err_flags)
+    _need(out.shape == q.shape and dout.shape == q.shape and out.dtype is q.dtype and dout.dtype is q.dtype
+          and out.is_cuda and dout.is_cuda, "attention: out and dout are like q")
+    _need(lse.dtype is torch.float32 and lse.is_cuda and lse.is_contiguous() and lse.shape == q.shape[:2],
           "attention: lse is float32 [nq][hq]")
-    with _on(stream):
-        q, k, v, out, dout = (_aligned(t) for t in (q, k, v, out, dout))
-        if _row_stride(dout) != _row_stride(out):
-            dout = dout.contiguous()
-            out = out.contiguous()
-        at = attn_args(q, k, v, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords, _row_stride(out))
-        dq, dk, dv = (torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device) for t in (q, k, v))
-        ws = _bytes(ts_attn_workspace_bytes(at, True), q.device)
-        ts_attn_bwd(at, q, k, v, out, lse, dout, dq, dk, dv, ws, err_flags, stream)
+    q, k, v, out, dout = (_aligned(t) for t in (q, k, v, out, dout))
+    st = _row_stride(out)
+    if st is None or _row_stride(dout) != st:
+        dout, out = dout.contiguous(), out.contiguous()
+        st = _row_stride(out)
+    at = attn_args(q, k, v, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords, st)
+    ref = ctypes.byref(at)
+    dq, dk, dv = (torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device) for t in (q, k, v))
+    n = _lib_attn_workspace_bytes(ref, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    _check(_lib_attn_bwd(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+                         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws), n, _flag_ptr(err_flags),
+                         _raw_stream(q)), "ts_attn_bwd")
     return dq, dk, dv
 
 
@@ -794,46 +825,57 @@ class Act8(NamedTuple):
                    torch.empty((n, -(-c // TS_ACT8_BLOCK)), dtype=torch.uint8, device=device))
 
     def check(self, n: int, c: int) -> None:
-        _need(self.codes.dtype == torch.int8 and self.scales.dtype == torch.uint8 and self.codes.is_cuda
-              and self.scales.is_cuda and self.codes.is_contiguous() and self.scales.is_contiguous()
-              and tuple(self.codes.shape) == (n, c) and tuple(self.scales.shape) == (n, -(-c // TS_ACT8_BLOCK)),
-              f"8-bit activations of [{n}][{c}]: codes int8 [n][c], scales uint8 [n][ceil(c / 32)]")
+        a, s = self.codes, self.scales
+        _need(a.dtype is torch.int8 and s.dtype is torch.uint8 and a.is_cuda and s.is_cuda and a.is_contiguous()
+              and s.is_contiguous() and a.shape == (n, c) and s.shape == (n, -(-c // TS_ACT8_BLOCK)),
+              "8-bit activations of [n][c]: codes int8 [n][c], scales uint8 [n][ceil(c / 32)]")
 
 
 def _matrix(t: torch.Tensor, what: str, shape=None, dtype=None) -> None:
     _need(t.is_cuda and t.dim() == 2 and t.is_contiguous() and t.dtype in _DT and (shape is None or t.shape == shape)
-          and (dtype is None or t.dtype == dtype), f"{what}: a dense device matrix [n][c] of the call's shape and type")
+          and (dtype is None or t.dtype is dtype), what)
 
 
 def act_pack(x: torch.Tensor, stream=None) -> Act8:
     """x [n][c] in 8 bits (see ts_act8 in ts.h)."""
-    _matrix(x, "act_pack")
-    with _on(stream):
-        a = Act8.empty(x.shape[0], x.shape[1], x.device)
-        ts_act_pack(x, a, stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return act_pack(x)
+    _matrix(x, "act_pack: a dense device matrix [n][c]")
+    n, c = x.shape
+    a = Act8.empty(n, c, x.device)
+    _check(_lib_act_pack(x.data_ptr(), n, c, _DT[x.dtype], _act(a), _raw_stream(x)), "ts_act_pack")
     return a
 
 
 def act_unpack(a: Act8, dtype: torch.dtype, stream=None) -> torch.Tensor:
     """The values `a` stands for; exact in every feature type."""
-    a.check(*a.codes.shape)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return act_unpack(a, dtype)
+    n, c = a.codes.shape
+    a.check(n, c)
     _need(dtype in _DT, "act_unpack: a feature type")
-    with _on(stream):
-        x = torch.empty(a.codes.shape, dtype=dtype, device=a.codes.device)
-        ts_act_unpack(a, x, stream)
+    x = torch.empty((n, c), dtype=dtype, device=a.codes.device)
+    _check(_lib_act_unpack(_act(a), n, c, x.data_ptr(), _DT[dtype], _raw_stream(x)), "ts_act_unpack")
     return x
 
 
 def conv_wgrad_act8(kmap: Kmap, x: Act8, dy: torch.Tensor, stream=None) -> torch.Tensor:
     """conv_wgrad with the layer's input kept in 8 bits."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return conv_wgrad_act8(kmap, x, dy)
     cin = x.codes.shape[1]
     x.check(kmap.s.n_in, cin)
-    _matrix(dy, "conv_wgrad_act8")
+    _matrix(dy, "conv_wgrad_act8: dy is a dense device matrix [n_out][cout]")
     _need(dy.shape[0] >= kmap.s.n_out_cap, "conv_wgrad_act8: dy has the map's output rows")
-    with _on(stream):
-        dw = torch.empty((kmap.kvol, cin, dy.shape[1]), dtype=torch.float32, device=dy.device)
-        ws = _bytes(ts_conv_wgrad_act8_workspace_bytes(kmap.s, cin, dy.shape[1]), dy.device)
-        ts_conv_bwd_wgrad_act8(kmap.s, x, dy, dw, ws, stream)
+    cout, ref = dy.shape[1], ctypes.byref(kmap.s)
+    dw = torch.empty((kmap.kvol, cin, cout), dtype=torch.float32, device=dy.device)
+    n = _lib_conv_wgrad_act8_workspace_bytes(ref, cin, cout)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dy.device)
+    _check(_lib_conv_bwd_wgrad_act8(ref, _act(x), cin, dy.data_ptr(), cout, _DT[dy.dtype], dw.data_ptr(), ws.data_ptr(), n,
+                                    _raw_stream(dy)), "ts_conv_bwd_wgrad_act8")
     return dw
 
 
@@ -849,39 +891,48 @@ class Norm(NamedTuple):
 def norm_fwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
              want_y: bool = True, want_rstd: bool = True, y8: bool = False, h8: bool = False, stream=None) -> Norm:
     """Root-mean-square norm of x + residual (see ts_norm_fwd in ts.h)."""
-    _matrix(x, "norm_fwd")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_fwd(x, w, residual, eps, want_y, want_rstd, y8, h8)
+    _matrix(x, "norm_fwd: x is a dense device matrix [n][c]")
     n, c = x.shape
     if residual is not None:
-        _matrix(residual, "norm_fwd residual", x.shape, x.dtype)
-    _need(w.is_cuda and w.dtype == torch.float32 and w.is_contiguous() and w.numel() == c, "norm_fwd: w is float32 [c]")
-    with _on(stream):
-        h = None if residual is None else torch.empty_like(x)
-        y = torch.empty_like(x) if want_y else None
-        rstd = torch.empty(n, dtype=torch.float32, device=x.device) if want_rstd else None
-        q = [Act8.empty(n, c, x.device) if want else None for want in (y8, h8)]
-        ts_norm_fwd(x, residual, w, eps, h, y, rstd, *q, stream)
-    return Norm(x if h is None else h, y, rstd, *q)
+        _matrix(residual, "norm_fwd: the residual is like x", x.shape, x.dtype)
+    _need(w.is_cuda and w.dtype is torch.float32 and w.is_contiguous() and w.numel() == c, "norm_fwd: w is float32 [c]")
+    h = None if residual is None else torch.empty_like(x)
+    y = torch.empty_like(x) if want_y else None
+    rstd = torch.empty(n, dtype=torch.float32, device=x.device) if want_rstd else None
+    qy = Act8.empty(n, c, x.device) if y8 else None
+    qh = Act8.empty(n, c, x.device) if h8 else None
+    _check(_lib_norm_fwd(x.data_ptr(), _ptr(residual), w.data_ptr(), n, c, eps, _DT[x.dtype], _ptr(h), _ptr(y), _ptr(rstd),
+                         _act(qy), _act(qh), _raw_stream(x)), "ts_norm_fwd")
+    return Norm(x if h is None else h, y, rstd, qy, qh)
 
 
 def norm_bwd(dy: torch.Tensor, h: Union[torch.Tensor, Act8], w: torch.Tensor, rstd: torch.Tensor,
              dh: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(dx, dw) of norm_fwd from h or its 8-bit form; dx is also the residual's
     gradient, dh the gradient that reaches h past the norm."""
-    _matrix(dy, "norm_bwd")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_bwd(dy, h, w, rstd, dh)
+    _matrix(dy, "norm_bwd: dy is a dense device matrix [n][c]")
     n, c = dy.shape
-    if isinstance(h, Act8):
+    eight = isinstance(h, Act8)
+    if eight:
         h.check(n, c)
     else:
-        _matrix(h, "norm_bwd h", dy.shape, dy.dtype)
+        _matrix(h, "norm_bwd: h is like dy", dy.shape, dy.dtype)
     if dh is not None:
-        _matrix(dh, "norm_bwd dh", dy.shape, dy.dtype)
+        _matrix(dh, "norm_bwd: dh is like dy", dy.shape, dy.dtype)
     for t, m in ((w, c), (rstd, n)):
-        _need(t.is_cuda and t.dtype == torch.float32 and t.is_contiguous() and t.numel() == m,
+        _need(t.is_cuda and t.dtype is torch.float32 and t.is_contiguous() and t.numel() == m,
               "norm_bwd: w is float32 [c], rstd float32 [n]")
-    with _on(stream):
-        dx = torch.empty_like(dy)
-        dw = torch.empty(c, dtype=torch.float32, device=dy.device)
-        ws = _bytes(ts_norm_workspace_bytes(n, c), dy.device)
-        full, eight = (None, h) if isinstance(h, Act8) else (h, None)
-        ts_norm_bwd(dy, full, eight, w, rstd, dh, dx, dw, ws, stream)
+    dx = torch.empty_like(dy)
+    dw = torch.empty(c, dtype=torch.float32, device=dy.device)
+    size = _lib_norm_workspace_bytes(n, c)
+    ws = torch.empty(max(size, 1), dtype=torch.uint8, device=dy.device)
+    _check(_lib_norm_bwd(dy.data_ptr(), None if eight else h.data_ptr(), _act(h) if eight else None, w.data_ptr(),
+                         rstd.data_ptr(), _ptr(dh), n, c, _DT[dy.dtype], dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), size,
+                         _raw_stream(dy)), "ts_norm_bwd")
     return dx, dw
