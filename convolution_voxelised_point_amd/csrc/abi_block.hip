@@ -283,21 +283,20 @@ ts_status ts_act_unpack(const ts_act8* a, int64_t n, int c, void* x, ts_dtype dt
 }
 
 size_t ts_conv_wgrad_act8_workspace_bytes(const ts_kmap* map, int cin, int cout) {
-  if (!map || map->n_in < 0 || cin < 1 || cout < 1) return 0;
-  return align_up(static_cast<size_t>(map->n_in) * cin * 2, 256) +
-         ts_conv_workspace_bytes(map, cin, cout, TS_OP_WGRAD, TS_F16, TS_DATAFLOW_AUTO);
+  if (!map || cin < 1 || cout < 1) return 0;
+  return wgrad_act8_workspace_bytes(map, cin, cout);
 }
 
 ts_status ts_conv_bwd_wgrad_act8(const ts_kmap* map, const ts_act8* x, int cin, const void* dy, int cout,
                                  ts_dtype dtype, float* dw, void* ws, size_t ws_bytes, hipStream_t stream) {
-  if (!map || !dtype_ok(dtype) || cin < 1 || cout < 1) return TS_ERR_INVALID_ARG;
+  if (!map || map->kvol < 1 || map->kvol > TS_MAX_KVOL || !map->fwd.row_mask) return TS_ERR_INVALID_ARG;
+  if (cin < 1 || cout < 1 || cin > (1 << 16) || cout > (1 << 16) || !dtype_ok(dtype)) return TS_ERR_INVALID_ARG;
   if (dtype == TS_F32) return TS_ERR_UNSUPPORTED;
-  if ((map->n_in > 0 && !act_ok(x)) || !ws || ws_bytes < ts_conv_wgrad_act8_workspace_bytes(map, cin, cout))
+  if (!(map->flags & TS_KMAP_PAIRS) || !dw || (map->n_in > 0 && !act_ok(x)) || (map->n_out_cap > 0 && !dy))
     return TS_ERR_INVALID_ARG;
-  const size_t xb = align_up(static_cast<size_t>(map->n_in) * cin * 2, 256);
-  const ts_status st = ts_act_unpack(x, map->n_in, cin, ws, dtype, stream);
-  if (st != TS_OK) return st;
-  return ts_conv_bwd_wgrad(map, ws, cin, dy, cout, dtype, dw, static_cast<char*>(ws) + xb, ws_bytes - xb, stream);
+  if (!ws || ws_bytes < wgrad_act8_workspace_bytes(map, cin, cout)) return TS_ERR_INVALID_ARG;
+  TS_TRY(launch_wgrad_act8(map, act_view(x, cin), cin, dy, cout, dtype, dw, ws, stream));
+  return TS_OK;
 }
 
 ts_status ts_norm_fwd(const void* x, const void* residual, const float* w, int64_t n, int c, float eps,

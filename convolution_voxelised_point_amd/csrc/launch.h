@@ -153,6 +153,9 @@ hipError_t launch_attn_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, 
 struct Act8;
 hipError_t launch_act_pack(const void* x, int64_t n, int c, ts_dtype dt, const Act8& a, hipStream_t s);
 hipError_t launch_act_unpack(const Act8& a, int64_t n, int c, void* x, ts_dtype dt, hipStream_t s);
+size_t wgrad_act8_workspace_bytes(const ts_kmap* map, int cin, int cout);  // wgrad.hip
+hipError_t launch_wgrad_act8(const ts_kmap* map, const Act8& x, int cin, const void* dy, int cout, ts_dtype dt, float* dw,
+                             void* ws, hipStream_t s);
 size_t norm_workspace_bytes(int64_t n, int c);
 hipError_t launch_norm_fwd(const void* x, const void* res, const float* w, int64_t n, int c, float eps, ts_dtype dt,
                            void* h, void* y, float* rstd, const Act8& y8, const Act8& h8, hipStream_t s);
