@@ -22,25 +22,31 @@ typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
 typedef float fx4 __attribute__((ext_vector_type(4)));
 typedef unsigned ux2 __attribute__((ext_vector_type(2)));
 
+// Channels c0..c0+7 of a row of c channels as floats, zeros past c.  vec: rows
+// and base allow 16-byte accesses (c a multiple of 8).  Otherwise a whole unit is
+// still one access, of the alignment of an element (the hardware takes it), and
+// only a row's last, partial unit goes element by element.
 template <typename T>
-struct Vec8 {
+struct __attribute__((aligned(16))) Unit {
   T e[8];
 };
-
-// Channels c0..c0+7 of a row of c channels as floats, zeros past c.  vec: rows
-// and base allow 16-byte accesses (c a multiple of 8).
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) LooseUnit {
+  T e[8];
+};
 template <typename T>
 __device__ __forceinline__ void load_unit(const T* row, int c0, int c, bool vec, float (&f)[8]) {
-  if (vec) {
-    if (c0 < c) {
-      struct __attribute__((aligned(16))) V { T e[8]; };
-      const V v = *reinterpret_cast<const V*>(row + c0);
+  if (c0 + 8 <= c) {
+    Unit<T> v;
+    if (vec) {
+      v = *reinterpret_cast<const Unit<T>*>(row + c0);
+    } else {
+      const LooseUnit<T> w = *reinterpret_cast<const LooseUnit<T>*>(row + c0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = static_cast<float>(v.e[e]);
-      return;
+      for (int e = 0; e < 8; ++e) v.e[e] = w.e[e];
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    for (int e = 0; e < 8; ++e) f[e] = static_cast<float>(v.e[e]);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = c0 + e < c ? static_cast<float>(row[c0 + e]) : 0.f;
@@ -49,13 +55,17 @@ __device__ __forceinline__ void load_unit(const T* row, int c0, int c, bool vec,
 
 template <typename T>
 __device__ __forceinline__ void store_unit(T* row, int c0, int c, bool vec, const float (&f)[8]) {
-  if (vec) {
-    if (c0 < c) {
-      struct __attribute__((aligned(16))) V { T e[8]; };
-      V v;
+  if (c0 + 8 <= c) {
+    if (vec) {
+      Unit<T> v;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v.e[e] = static_cast<T>(f[e]);
-      *reinterpret_cast<V*>(row + c0) = v;
+      *reinterpret_cast<Unit<T>*>(row + c0) = v;
+    } else {
+      LooseUnit<T> v;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v.e[e] = static_cast<T>(f[e]);
+      *reinterpret_cast<LooseUnit<T>*>(row + c0) = v;
     }
   } else {
 #pragma unroll
@@ -121,6 +131,8 @@ __device__ __forceinline__ void act8_store(const Act8& a, int64_t row, int c0, i
   int8_t* p = a.codes + row * c + c0;
   if (a.vec) {
     *reinterpret_cast<ux2*>(p) = codes;
+  } else if (c0 + 8 <= c) {
+    *reinterpret_cast<LooseUnit<int8_t>*>(p) = __builtin_bit_cast(LooseUnit<int8_t>, codes);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -139,6 +151,8 @@ __device__ __forceinline__ void act8_load(const Act8& a, int64_t row, int c0, in
   ux2 codes{0u, 0u};
   if (a.vec) {
     codes = *reinterpret_cast<const ux2*>(p);
+  } else if (c0 + 8 <= c) {
+    codes = __builtin_bit_cast(ux2, *reinterpret_cast<const LooseUnit<int8_t>*>(p));
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
