@@ -54,7 +54,7 @@ AttnPlan plan_walk(int64_t own, int64_t other, int64_t n_sets, int hk, int dp, b
   if (may_share && own_per <= 16) {
     p.share_keys = true;
     p.bm = 16;
-  } else if (max_nc >= 2 && own_per >= 512 && ceil_div<int64_t>(own, 128) * hk >= 512) {
+  } else if (max_nc >= 2 && own_per >= 512 && ceil_div<int64_t>(own, 128) * hk >= 256) {
     p.nc = 2;
     p.bm = 128;
   } else if (dp <= 64 && other_per <= 512) {
@@ -64,9 +64,15 @@ AttnPlan plan_walk(int64_t own, int64_t other, int64_t n_sets, int hk, int dp, b
   }
   const int64_t tiles = ceil_div<int64_t>(own, p.bm);
   const int64_t blocks = (tiles > n_sets ? tiles : n_sets < own ? n_sets : own) * ceil_div(hk, p.heads);
+  // Walks are split until 512 blocks run (at least 256 rows each: a short walk is
+  // mostly its beginning).  Where that leaves fewer than two rounds of blocks, long
+  // ones are split further (at least 1024 rows each), so that the last round is a
+  // small part of the whole (2 x 8192 rows, dk and dv: 1255 -> 1100 us).
   int64_t s = blocks > 0 ? 512 / blocks : 1;
-  const int64_t most = other_per / 256;
-  if (s > most) s = most;
+  if (s > other_per / 256) s = other_per / 256;
+  int64_t fine = blocks > 0 && blocks < 1024 ? 2048 / blocks : 1;
+  if (fine > other_per / 1024) fine = other_per / 1024;
+  if (s < fine) s = fine;
   if (s > kAttnMaxSplits) s = kAttnMaxSplits;
   p.splits = s < 2 ? 1 : static_cast<int>(s);
   return p;
@@ -78,7 +84,7 @@ AttnPlan plan_fwd(const ts_attn* at) {
 }
 AttnPlan plan_dkv(const ts_attn* at) {
   const int dp = padded_width(at->d);
-  return plan_walk(at->nk, at->nq * (at->hq / at->hk), at->n_sets, at->hk, dp, false, dp <= 32 ? 2 : 1);
+  return plan_walk(at->nk, at->nq * (at->hq / at->hk), at->n_sets, at->hk, dp, false, dp <= 64 ? 2 : 1);
 }
 
 size_t part_floats(const ts_attn* at, const AttnPlan& p, int64_t rows, int extra) {

@@ -261,6 +261,13 @@ __device__ __forceinline__ void split_range(int64_t len, int bn, int splits, int
   *e = hi < len ? hi : len;
 }
 
+// The value, unknown to the compiler as equal to x: what is computed from it here is
+// not computed before the walk and kept in registers through it.
+__device__ __forceinline__ uint32_t late(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Distances.  Coordinates are taken relative to one row of the block (floats
 // hold them exactly) with the squared norm beside them: {x, y, z, x^2 + y^2 +
 // z^2}.  While every norm is at most 2048, |a - b|^2 = |a|^2 + |b|^2 - 2 a.b
@@ -277,16 +284,17 @@ __device__ __forceinline__ Origin load_origin(const int32_t* c, int64_t row, int
   const int32_t* p = c + row * (ndim + 1) + 1;
   return Origin{static_cast<float>(p[0]), static_cast<float>(p[1]), ndim == 3 ? static_cast<float>(p[2]) : 0.f};
 }
+// The same of a row that is the same on every lane, in scalar registers.
+__device__ __forceinline__ Origin uniform_origin(const int32_t* c, int64_t row, int ndim) {
+  const auto u = [](float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+  };
+  const Origin o = load_origin(c, row, ndim);
+  return Origin{u(o.x), u(o.y), u(o.z)};
+}
 __device__ __forceinline__ f32x4 relative(const Origin& p, const Origin& o) {
   const float x = p.x - o.x, y = p.y - o.y, z = p.z - o.z;
   return f32x4{x, y, z, fmaf(x, x, fmaf(y, y, z * z))};
-}
-__device__ __forceinline__ f32x4 load_coord(const int32_t* c, int64_t row, int ndim, const Origin& o) {
-  return relative(load_origin(c, row, ndim), o);
-}
-__device__ __forceinline__ float square(const f32x4& a, const f32x4& b) {
-  const float x = a[0] - b[0], y = a[1] - b[1], z = a[2] - b[2];
-  return fmaf(x, x, fmaf(y, y, z * z));
 }
 // The column's B value of lane (g, c) for the product above.
 __device__ __forceinline__ float col_term(const f32x4& c, int g) {
@@ -426,16 +434,19 @@ struct ColLoad {
 
 // Distances of the 16 tile rows from r0 to the columns, rows 4g..4g+3 in the lane's
 // four values; qb: col_term of the column, norm: its squared norm.  The far form
-// reads the column's coordinates again (row `row` of c): it is rare, and they
+// reads the column's coordinates again (row first + row of c): it is rare, and they
 // would cost registers everywhere else.
 __device__ __forceinline__ f32x4 distances(const f32x4* tc, int r0, float norm, float qb, bool far, int lane,
-                                           const int32_t* c, int64_t row, int ndim, const Origin& org) {
+                                           const int32_t* c, int64_t first, uint32_t row, int ndim, const Origin& org) {
   f32x4 d;
   if (far) {
-    const f32x4 x = load_coord(c, row, ndim, org);
+    const Origin p = load_origin(c, first + late(row), ndim);
+    const float x = p.x - org.x, y = p.y - org.y, z = p.z - org.z;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      d[e] = square(x, tc[r0 + 4 * (lane >> 4) + e]);
+      const float* t = reinterpret_cast<const float*>(tc + r0 + 4 * (lane >> 4) + e);
+      const float u = x - t[0], v = y - t[1], w = z - t[2];
+      d[e] = fmaf(u, u, fmaf(v, v, w * w));
       __builtin_amdgcn_sched_barrier(0);  // one row at a time, for the registers' sake
     }
   } else {

@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   Origin org{0.f, 0.f, 0.f};
   Origin qraw[NC];
   if constexpr (BIAS) {
-    org = load_origin(a.qc, st.own0, a.ndim);
+    org = uniform_origin(a.qc, st.own0, a.ndim);
 #pragma unroll
     for (int j = 0; j < NC; ++j) qraw[j] = load_origin(a.qc, col.query0 + col.dq[j], a.ndim);
   }
@@ -169,8 +169,8 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
       for (int j = 0; j < NC; ++j) {
         f32x4 dist = zero;
         if constexpr (BIAS)
-          dist = distances(tc[b], kt0 + u * 32 + n * 16, qn[j], qb[j], PART && far, lane, a.qc, col.query0 + col.dq[j],
-                           a.ndim, org);
+          dist = distances(tc[b], kt0 + u * 32 + n * 16, qn[j], qb[j], PART && far, lane, a.qc, col.query0,
+                           col.dq[j], a.ndim, org);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float p, ds;
@@ -208,8 +208,8 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       if (!col.live[j]) continue;
-      const int64_t query = col.query0 + col.dq[j];
-      const int head = h * a.grp + static_cast<int>(col.place[j]);
+      const int64_t query = col.query0 + late(col.dq[j]);
+      const int head = h * a.grp + static_cast<int>(late(col.place[j]));
       T* dst = static_cast<T*>(a.dq) + query * a.q_stride + static_cast<int64_t>(head) * a.d;
       float* part = a.part + ((static_cast<int64_t>(split) * a.nq + query) * a.hq + head) * DP;
 #pragma unroll
@@ -269,7 +269,8 @@ template <typename T, int DP, int NC, bool CAP, bool BIAS>
 __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(const AttnArgs a) {
   typedef typename AMfma<T>::frag Frag;
   constexpr int KB = DP / 32, DI = DP / 16;
-  constexpr int BN = DP == 128 ? 32 : 64, BM = 64 * NC;  // 32 rows where the accumulators leave room for no more
+  constexpr int BN = DP == 128 ? 32 : 64;  // 32 rows where the accumulators leave room for no more
+  constexpr int BM = 64 * NC;
   constexpr int TB = BN * DP * 2;
   constexpr bool MULTI = NC == 1 && DP <= 64;
   __shared__ __attribute__((aligned(16))) char tq[2][TB], tg[2][TB];
@@ -308,7 +309,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
   Origin org{0.f, 0.f, 0.f};
   Origin kraw[NC];
   if constexpr (BIAS) {
-    org = load_origin(a.kc, st.own0, a.ndim);
+    org = uniform_origin(a.kc, st.own0, a.ndim);
 #pragma unroll
     for (int j = 0; j < NC; ++j) kraw[j] = load_origin(a.kc, key0 + ck[j], a.ndim);
   }
@@ -441,7 +442,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
       for (int j = 0; j < NC; ++j) {
         f32x4 dist = zero;
         if constexpr (BIAS)
-          dist = distances(tc[b], u * 32 + n * 16, kn[j], kb_[j], PART && far, lane, a.kc, key0 + ck[j], a.ndim, org);
+          dist = distances(tc[b], u * 32 + n * 16, kn[j], kb_[j], PART && far, lane, a.kc, key0, ck[j], a.ndim, org);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float p, ds;
@@ -470,7 +471,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       if (!live[j]) continue;
-      const int64_t key = key0 + ck[j], rows = a.nk * a.hk;
+      const int64_t key = key0 + late(ck[j]), rows = a.nk * a.hk;
       T* kd = static_cast<T*>(a.dk) + key * a.k_stride + static_cast<int64_t>(h) * a.d;
       T* vd = static_cast<T*>(a.dv) + key * a.v_stride + static_cast<int64_t>(h) * a.d;
       float* part = a.part + (static_cast<int64_t>(split) * rows + key * a.hk + h) * DP;
@@ -582,8 +583,8 @@ void run_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t s)
   a.tiles = attn_tiles(a.nk, 1, pk.bm, a.n_sets);
   a.splits = pk.splits;
   a.heads = pk.heads;
-  if (DP <= 32 && pk.nc == 2)
-    run_dkv<T, DP, DP <= 32 ? 2 : 1, CAP, BIAS>(a, s);
+  if (DP <= 64 && pk.nc == 2)
+    run_dkv<T, DP, DP <= 64 ? 2 : 1, CAP, BIAS>(a, s);
   else
     run_dkv<T, DP, 1, CAP, BIAS>(a, s);
   if (a.splits > 1) {

@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
   Origin org{0.f, 0.f, 0.f};
   Origin qraw[NC];
   if constexpr (BIAS) {
-    org = load_origin(a.qc, st.own0, a.ndim);
+    org = uniform_origin(a.qc, st.own0, a.ndim);
 #pragma unroll
     for (int j = 0; j < NC; ++j) qraw[j] = load_origin(a.qc, col.query0 + col.dq[j], a.ndim);
   }
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
     }
   };
   auto dist_of = [&](int b, int n, int j, bool far) {
-    return distances(tc[b], kt0 + n * 16, qn[j], qb[j], far, lane, a.qc, col.query0 + col.dq[j], a.ndim, org);
+    return distances(tc[b], kt0 + n * 16, qn[j], qb[j], far, lane, a.qc, col.query0, col.dq[j], a.ndim, org);
   };
   // the score relative to `base`
   auto score = [&](int j, float s, float dist, float base) {
@@ -311,17 +311,16 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       if (!col.live[j]) continue;
-      const int64_t query = col.query0 + col.dq[j];
-      const int head = h * a.grp + static_cast<int>(col.place[j]);
+      const int64_t query = col.query0 + late(col.dq[j]);
+      const int head = h * a.grp + static_cast<int>(late(col.place[j]));
       const int64_t at = (static_cast<int64_t>(split) * a.nq + query) * a.hq + head;
       if (a.splits > 1) {
         if (g == 0) {
           a.part_ml[at * 2] = m[j];
           a.part_ml[at * 2 + 1] = l[j];
         }
-        if (n_keys > 0)
 #pragma unroll
-          for (int i = 0; i < DI; ++i) *reinterpret_cast<f32x4*>(a.part + at * DP + i * 16 + g * 4) = o[j][i];
+        for (int i = 0; i < DI; ++i) *reinterpret_cast<f32x4*>(a.part + at * DP + i * 16 + g * 4) = o[j][i];
         continue;
       }
       const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
@@ -407,9 +406,9 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a) {
   const int d4 = tid % Q, sh = tid / Q;
   f32x4 y{0.f, 0.f, 0.f, 0.f};
   if (sh < SH) {
+#pragma unroll 4
     for (int s = sh; s < a.splits; s += SH) {
       const float f = wt[s];
-      if (f == 0.f) continue;  // a split without keys wrote no sums
       const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + (s * rows + row) * DP + d4 * 4);
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = fmaf(f, v[e], y[e]);
@@ -427,6 +426,39 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a) {
   const int64_t query = row / a.hq;
   store4(static_cast<T*>(a.out) + query * a.o_stride + (row - query * a.hq) * a.d, d4 * 4, a.d, y);
   if (tid == 0) a.lse[row] = l == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// The same for few splits of many rows: a thread per row and 4 elements.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void k_attn_join_few(const AttnArgs a) {
+  constexpr int Q = DP / 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = i / Q, rows = a.nq * a.hq;
+  const int d0 = static_cast<int>(i % Q) * 4;
+  if (row >= rows) return;
+  float m[kAttnFewSplits], l[kAttnFewSplits], mx = -INFINITY;
+#pragma unroll
+  for (int s = 0; s < kAttnFewSplits; ++s) {
+    m[s] = s < a.splits ? a.part_ml[(s * rows + row) * 2] : -INFINITY;
+    l[s] = s < a.splits ? a.part_ml[(s * rows + row) * 2 + 1] : 0.f;
+    mx = fmaxf(mx, m[s]);
+  }
+  f32x4 y{0.f, 0.f, 0.f, 0.f};
+  float lt = 0.f;
+#pragma unroll
+  for (int s = 0; s < kAttnFewSplits; ++s) {
+    if (s >= a.splits) continue;
+    const float f = m[s] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[s] - mx);
+    lt = fmaf(f, l[s], lt);
+    const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + (s * rows + row) * DP + d0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = fmaf(f, v[e], y[e]);
+  }
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] *= inv;
+  const int64_t query = row / a.hq;
+  store4(static_cast<T*>(a.out) + query * a.o_stride + (row - query * a.hq) * a.d, d0, a.d, y);
+  if (d0 == 0) a.lse[row] = lt == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(lt)) * kLn2;
 }
 
 template <typename T, int DP, int NC, bool KS>
@@ -454,7 +486,11 @@ void run_fwd(AttnArgs& a, const AttnPlan& p, bool cap, hipStream_t s) {
     run_fwd<T, DP, DP <= 64 ? 2 : 1, false>(a, cap, s);
   else
     run_fwd<T, DP, 1, false>(a, cap, s);
-  if (a.splits > 1) k_attn_join<T, DP><<<static_cast<unsigned>(a.nq * a.hq), 256, 0, s>>>(a);
+  const int64_t rows = a.nq * a.hq;
+  if (a.splits > kAttnFewSplits)
+    k_attn_join<T, DP><<<static_cast<unsigned>(rows), 256, 0, s>>>(a);
+  else if (a.splits > 1)
+    k_attn_join_few<T, DP><<<static_cast<unsigned>(ceil_div<int64_t>(rows * (DP / 4), 256)), 256, 0, s>>>(a);
 }
 
 template <typename T>

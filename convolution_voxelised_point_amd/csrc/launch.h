@@ -126,6 +126,7 @@ hipError_t launch_wgrad(const ts_kmap* map, const void* x, int cin, const void* 
 // attn_fwd.hip, attn_bwd.hip
 struct AttnArgs;
 constexpr int kAttnMaxSplits = 512;
+constexpr int kAttnFewSplits = 8;  // joined by a thread per 4 elements instead of a block per row
 // Waves per SIMD that the registers of a kernel of this shape allow without spilling.
 constexpr int attn_waves_fwd(int dp, int nc, bool bias, bool share_keys) {
   return share_keys ? (dp == 128 ? 1 : 2) : nc == 2 || dp == 128 ? 2 : dp == 64 ? (bias ? 2 : 3) : 4;
