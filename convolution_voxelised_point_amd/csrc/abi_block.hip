@@ -20,12 +20,15 @@ constexpr int64_t kMaxStride = int64_t{1} << 23;
 bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool at8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
 
+float cap_factor(const ts_attn* at) { return 2.f * kLog2e * fabsf(at->scale) / at->cap; }
+
 ts_status check_attn(const ts_attn* at) {
   if (!at) return TS_ERR_INVALID_ARG;
   if (at->dtype != TS_F32 && at->dtype != TS_F16 && at->dtype != TS_BF16) return TS_ERR_INVALID_ARG;
   if (at->hq < 1 || at->hk < 1 || at->d < 1 || at->hq % at->hk != 0) return TS_ERR_INVALID_ARG;
   if (at->nq < 0 || at->nk < 0 || at->n_sets < 0) return TS_ERR_INVALID_ARG;
   if (!std::isfinite(at->scale) || !std::isfinite(at->cap) || at->cap < 0.f) return TS_ERR_INVALID_ARG;
+  if (at->cap > 0.f && !std::isfinite(cap_factor(at))) return TS_ERR_INVALID_ARG;
   if (at->dtype == TS_F32 || at->d > 128) return TS_ERR_UNSUPPORTED;
   if (at->hq > 65535 || at->nq > kMaxRows / at->hq || at->nk > kMaxRows / at->hk || at->n_sets > kMaxRows)
     return TS_ERR_UNSUPPORTED;
@@ -174,7 +177,7 @@ AttnArgs attn_args(const ts_attn* at, const void* q, const void* k, const void* 
   a.scale = at->scale;
   a.negate = at->scale < 0.f;
   if (at->cap > 0.f) {
-    a.c1 = 2.f * kLog2e * fabsf(at->scale) / at->cap;
+    a.c1 = cap_factor(at);
     a.c2 = at->cap * kLog2e;
   } else {
     a.c1 = fabsf(at->scale) * kLog2e;
