@@ -15,6 +15,7 @@ namespace {
   } while (0)
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
+constexpr float kMaxCap = 1024.f;
 constexpr int64_t kMaxStride = int64_t{1} << 23;
 
 bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -29,7 +30,8 @@ ts_status check_attn(const ts_attn* at) {
   if (at->nq < 0 || at->nk < 0 || at->n_sets < 0) return TS_ERR_INVALID_ARG;
   if (!std::isfinite(at->scale) || !std::isfinite(at->cap) || at->cap < 0.f) return TS_ERR_INVALID_ARG;
   if (at->cap > 0.f && !std::isfinite(cap_factor(at))) return TS_ERR_INVALID_ARG;
-  if (at->dtype == TS_F32 || at->d > 128) return TS_ERR_UNSUPPORTED;
+  // c2 - 2 c2 / (exp + 1) keeps a score to about 2 c2 / 2^24: 2e-4 at the largest cap
+  if (at->dtype == TS_F32 || at->d > 128 || at->cap > kMaxCap) return TS_ERR_UNSUPPORTED;
   if (at->hq > 65535 || at->nq > kMaxRows / at->hq || at->nk > kMaxRows / at->hk || at->n_sets > kMaxRows)
     return TS_ERR_UNSUPPORTED;
   const int64_t qw = static_cast<int64_t>(at->hq) * at->d, kw = static_cast<int64_t>(at->hk) * at->d;

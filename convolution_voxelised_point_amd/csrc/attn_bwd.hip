@@ -11,6 +11,14 @@
 // 1 - tanh^2 = 4 r (1 - r) with r = 1 / (exp(2x) + 1); the 4 is taken into the
 // exponent of p (so dv is scaled back by 1/4 when it is written).
 //
+// Roundings to 16 bits: p for dv and ds for dk once per term.  For dq, ds goes in as
+// two parts, ds and what its rounding left, because delta is formed from an out that
+// is rounded already: that error and one rounding of ds together made dq 1.6 to 1.8
+// times as far from the exact one as its own last rounding does (now 1.2 to 1.45; the
+// second product costs 12 % of this kernel).  The sum of p (dp - delta) over a row is
+// 0 in exact arithmetic; where a block sees the whole row it adds what it finds
+// to the delta that dk uses.
+//
 // As in the forward pass, a wave owns NC column blocks of 16 and a block takes
 // a.heads key-value heads one after the other; delta enters as the accumulator
 // that dp starts from.
@@ -123,7 +131,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   const f32x4 zero{0.f, 0.f, 0.f, 0.f};
   Frag qf[NC][KB], gf[NC][KB];
   f32x4 dq[NC][DI];
-  float base[NC], delta[NC];
+  float base[NC], delta[NC], rho[NC];
   auto begin = [&]() {
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
@@ -139,8 +147,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
       delta[j] = col_sum(dl);
       base[j] = exp_base<CAP>(a, next_lse[j]);
       if constexpr (BIAS) slope[j] = next_slope[j] * kLog2e;
-      if (col.live[j] && g == 0 && split == 0 && (!KS || wave == 0))
-        a.delta[(col.query0 + col.dq[j]) * a.hq + h * a.grp + col.place[j]] = delta[j];
+      rho[j] = 0.f;
 #pragma unroll
       for (int i = 0; i < DI; ++i) dq[j][i] = zero;
     }
@@ -162,7 +169,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
           dp[j][n] = AMfma<T>::run(fv, gf[j][kb], kb == 0 ? f32x4{-delta[j], -delta[j], -delta[j], -delta[j]} : dp[j][n]);
         }
       }
-    Frag df[NC];
+    Frag df[NC], dr[NC];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -175,15 +182,18 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
         for (int e = 0; e < 4; ++e) {
           float p, ds;
           grad_score<CAP, BIAS>(a, s[j][n][e], dp[j][n][e], base[j], BIAS ? slope[j] : 0.f, dist[e], &p, &ds);
-          if constexpr (PART) ds = u * 32 + n * 16 + 4 * g + e < left ? ds : 0.f;
+          if constexpr (PART)
+            if (u * 32 + n * 16 + 4 * g + e >= left) p = ds = 0.f;
+          if constexpr (!KS) rho[j] = fmaf(p, dp[j][n][e], rho[j]);
           df[j][n * 4 + e] = static_cast<T>(ds);
+          dr[j][n * 4 + e] = static_cast<T>(ds - static_cast<float>(df[j][n * 4 + e]));
         }
       }
 #pragma unroll
     for (int i = 0; i < DI; ++i) {
       const Frag f = tile_frag_t<T, DP>(tk[b], kt0 + u * 32, i, lane);
 #pragma unroll
-      for (int j = 0; j < NC; ++j) dq[j][i] = AMfma<T>::run(f, df[j], dq[j][i]);
+      for (int j = 0; j < NC; ++j) dq[j][i] = AMfma<T>::run(f, dr[j], AMfma<T>::run(f, df[j], dq[j][i]));
     }
   };
 
@@ -207,9 +217,12 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
     }
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
+      const float over = col_sum(rho[j]);  // what delta was short of
       if (!col.live[j]) continue;
       const int64_t query = col.query0 + late(col.dq[j]);
       const int head = h * a.grp + static_cast<int>(late(col.place[j]));
+      if (g == 0 && split == 0)
+        a.delta[query * a.hq + head] = !KS && a.splits == 1 ? fmaf(over, CAP ? 0.25f : 1.f, delta[j]) : delta[j];
       T* dst = static_cast<T*>(a.dq) + query * a.q_stride + static_cast<int64_t>(head) * a.d;
       float* part = a.part + ((static_cast<int64_t>(split) * a.nq + query) * a.hq + head) * DP;
 #pragma unroll

@@ -560,7 +560,7 @@ ts_status ts_conv_bwd_dgrad_noalloc(const ts_kmap* map, const void* dy, int cout
  * in the workspace first.  fp16 or bf16 (TS_F32 is TS_ERR_UNSUPPORTED), 1 <= d <=
  * 128, hk divides hq; products are accumulated in fp32, softmax statistics are
  * fp32, probabilities and score gradients are rounded to the feature type for
- * their products.  With fp16, score gradients below 2^-24 vanish and above
+ * their products (score gradients as two parts for dq).  With fp16, score gradients below 2^-24 vanish and above
  * 65504 overflow, as in any fp16 backward pass: scale the loss.
  * ---------------------------------------------------------------------- */
 typedef struct ts_attn {
@@ -583,8 +583,8 @@ size_t ts_attn_workspace_bytes(const ts_attn* at, int backward);
 
 /* out [nq][hq][d] (o_stride) and lse (device float [nq][hq]); every row is
  * written once.  Errors: TS_ERR_INVALID_ARG (null pointers, sizes, strides,
- * a short workspace, scale or cap not finite, cap < 0), TS_ERR_UNSUPPORTED
- * (fp32, d > 128, more than 2^31 - 1 rows times heads, more than 2^24 tiles of
+ * a short workspace, scale, cap or scale / cap not finite, cap < 0),
+ * TS_ERR_UNSUPPORTED (fp32, d > 128, cap > 1024, more than 2^31 - 1 rows times heads, more than 2^24 tiles of
  * 64 rows, sets counted as at least one, strides above 2^23), TS_ERR_HIP. */
 ts_status ts_attn_fwd(const ts_attn* at, const void* q, const void* k, const void* v, void* out, float* lse, void* ws,
                       size_t ws_bytes, uint32_t* err_flags, hipStream_t stream);

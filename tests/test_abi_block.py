@@ -54,6 +54,7 @@ BAD_ATTN = [
     (dict(cap=-1.0), "INVALID_ARG"),
     (dict(cap=float("nan")), "INVALID_ARG"),
     (dict(scale=1e30, cap=1e-30), "INVALID_ARG"),         # scale / cap past the largest float
+    (dict(cap=1025.0), "UNSUPPORTED"),
     (dict(q_starts=None), "INVALID_ARG"),
     (dict(k_starts=None, nk=99), "INVALID_ARG"),          # one list of starts: one number of rows
     (dict(slopes=0x1000), "INVALID_ARG"),                 # a slope without coordinates
