@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import NamedTuple, Optional, Tuple, Union
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import numpy as np
 import torch
@@ -711,8 +711,11 @@ def _raw_stream(t: torch.Tensor) -> int:
 
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
-    """t, or a dense copy of it where the kernels could not read it in 16-byte pieces."""
-    return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+    """Rows of heads the library can take: dense copies of misaligned ones,
+    unless their width or stride makes the library copy them itself."""
+    if t.data_ptr() % 16 == 0 or t.shape[-1] % 8 or t.stride(0) % 8:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -788,16 +791,20 @@ def attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
              lse: torch.Tensor, q_starts: torch.Tensor, k_starts: Optional[torch.Tensor] = None,
              scale: Optional[float] = None, cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
              q_coords: Optional[torch.Tensor] = None, k_coords: Optional[torch.Tensor] = None,
-             err_flags: Optional[torch.Tensor] = None,
-             stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    """(dq, dk, dv) of attn_fwd with the same arguments, laid out like q, k, v."""
+             err_flags: Optional[torch.Tensor] = None, stream=None,
+             into: Optional[Sequence[torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dq, dk, dv) of attn_fwd with the same arguments, laid out like q, k, v.
+    They are written to the three tensors of `into`, say the columns of one
+    matrix, or to new ones."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return attn_bwd(dout, q, k, v, out, lse, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords, err_flags)
+            return attn_bwd(dout, q, k, v, out, lse, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords, err_flags,
+                            into=into)
     _need(out.shape == q.shape and dout.shape == q.shape and out.dtype is q.dtype and dout.dtype is q.dtype
           and out.is_cuda and dout.is_cuda, "attention: out and dout are like q")
     _need(lse.dtype is torch.float32 and lse.is_cuda and lse.is_contiguous() and lse.shape == q.shape[:2],
           "attention: lse is float32 [nq][hq]")
+    like = (q, k, v)
     q, k, v, out, dout = (_aligned(t) for t in (q, k, v, out, dout))
     st = _row_stride(out)
     if st is None or _row_stride(dout) != st:
@@ -805,12 +812,22 @@ def attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
         st = _row_stride(out)
     at = attn_args(q, k, v, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords, st)
     ref = ctypes.byref(at)
-    dq, dk, dv = (torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device) for t in (q, k, v))
+    _need(into is None or (len(into) == 3 and all(
+        g.is_cuda and g.dtype is t.dtype and g.shape == t.shape and g.stride() == t.stride()
+        for g, t in zip(into, like))), "attention: dq, dk, dv are laid out like q, k, v")
+    # their own buffers where q, k or v was copied or the library could not write there
+    direct = into is not None and all(_aligned(g) is g and t is l for g, t, l in zip(into, (q, k, v), like))
+    dq, dk, dv = into if direct else [torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
+                                      for t in (q, k, v)]
     n = _lib_attn_workspace_bytes(ref, 1)
     ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
     _check(_lib_attn_bwd(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws), n, _flag_ptr(err_flags),
                          _raw_stream(q)), "ts_attn_bwd")
+    if into is not None and not direct:
+        for g, t in zip(into, (dq, dk, dv)):
+            g.copy_(t)
+        return tuple(into)
     return dq, dk, dv
 
 
