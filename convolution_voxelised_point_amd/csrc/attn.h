@@ -171,6 +171,13 @@ __device__ __forceinline__ int64_t set_bound(const int64_t* starts, int64_t n_se
 // no table of tiles has to be built.  Number of slots for n rows:
 inline int64_t attn_tiles(int64_t n, int64_t mul, int64_t bm, int64_t n_sets) { return n * mul / bm + n_sets + 2; }
 
+// A value that is the same on every lane, in scalar registers.
+__device__ __forceinline__ int64_t lane_value(int64_t x, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(x), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(static_cast<uint64_t>(x) >> 32), lane);
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 struct SetTile {
   int64_t own0, row0, rows;  // first row of the set; first packed row of the tile; packed rows of the set
   int64_t st0, st_len;       // the other side's rows of the set
@@ -205,8 +212,8 @@ __device__ __forceinline__ bool find_tile(const int64_t* own, int64_t n_own, int
       if (lo + step < hi) hi = lo + step;
     }
     if (hi - lo == 1 && step == 1 && c > 0 && c < 64) {
-      b0 = __shfl(v, c - 1);
-      b1 = __shfl(v, c);
+      b0 = lane_value(v, c - 1);
+      b1 = lane_value(v, c);
       break;
     }
     at = lo;
@@ -220,8 +227,8 @@ __device__ __forceinline__ bool find_tile(const int64_t* own, int64_t n_own, int
   if (lo >= 1 && lo <= n_sets) {
     const int64_t s0 = st == own && n_st == n_own ? b0 : set_bound(st, n_sets, n_st, lo);
     const int64_t s1 = st == own && n_st == n_own ? b1 : set_bound(st, n_sets, n_st, lo + 1);
-    r->st0 = s0;
-    r->st_len = s1 > s0 ? s1 - s0 : 0;
+    r->st0 = lane_value(s0, 0);
+    r->st_len = s1 > s0 ? lane_value(s1 - s0, 0) : 0;
   }
   return r->row0 >= 0 && r->row0 < r->rows;
 }
@@ -280,20 +287,23 @@ constexpr float kNearNorm = 4194304.f;  // 2048^2
 struct Origin {
   float x, y, z;
 };
-__device__ __forceinline__ Origin load_origin(const int32_t* c, int64_t row, int ndim) {
+// Coordinates as read (with ndim 2, z is y): turned into floats where they are used,
+// so that the read is not waited for where it is issued.
+struct Place {
+  int32_t x, y, z;
+};
+__device__ __forceinline__ Place load_place(const int32_t* c, int64_t row, int ndim) {
   const int32_t* p = c + row * (ndim + 1) + 1;
-  return Origin{static_cast<float>(p[0]), static_cast<float>(p[1]), ndim == 3 ? static_cast<float>(p[2]) : 0.f};
+  return Place{p[0], p[1], p[ndim - 1]};
 }
-// The same of a row that is the same on every lane, in scalar registers.
-__device__ __forceinline__ Origin uniform_origin(const int32_t* c, int64_t row, int ndim) {
-  const auto u = [](float x) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
-  };
-  const Origin o = load_origin(c, row, ndim);
-  return Origin{u(o.x), u(o.y), u(o.z)};
+// Of a row that is the same on every lane, in scalar registers.
+__device__ __forceinline__ Origin uniform_origin(const Place& p, int ndim) {
+  const auto u = [](int x) { return static_cast<float>(__builtin_amdgcn_readfirstlane(x)); };
+  return Origin{u(p.x), u(p.y), ndim == 3 ? u(p.z) : 0.f};
 }
-__device__ __forceinline__ f32x4 relative(const Origin& p, const Origin& o) {
-  const float x = p.x - o.x, y = p.y - o.y, z = p.z - o.z;
+__device__ __forceinline__ f32x4 relative(const Place& p, const Origin& o, int ndim) {
+  const float x = static_cast<float>(p.x) - o.x, y = static_cast<float>(p.y) - o.y;
+  const float z = ndim == 3 ? static_cast<float>(p.z) - o.z : 0.f;
   return f32x4{x, y, z, fmaf(x, x, fmaf(y, y, z * z))};
 }
 // The column's B value of lane (g, c) for the product above.
@@ -358,15 +368,15 @@ struct TileLoad {
 // Coordinates of a tile's rows on their way: thread r < BN brings row r's.
 template <int BN>
 struct TileCoords {
-  Origin c;  // as read: the block's origin may still be on its way
+  Place c;
   __device__ __forceinline__ void fetch(const int32_t* coords, int64_t first, int rows, int ndim) {
     const int r = threadIdx.x;
-    if (r < BN && r < rows) c = load_origin(coords, first + r, ndim);
+    if (r < BN && r < rows) c = load_place(coords, first + r, ndim);
   }
   // The flag of a wave's rows: whether one is too far out for the product form.
-  __device__ __forceinline__ void put(f32x4* tc, uint32_t* far_rows, const Origin& org) const {
+  __device__ __forceinline__ void put(f32x4* tc, uint32_t* far_rows, const Origin& org, int ndim) const {
     if (threadIdx.x >= BN) return;
-    const f32x4 x = relative(c, org);
+    const f32x4 x = relative(c, org, ndim);
     tc[threadIdx.x] = x;
     const bool any = __any(x[3] > kNearNorm);
     if (threadIdx.x % 64 == 0) far_rows[threadIdx.x / 64] = any;
@@ -394,7 +404,7 @@ struct KeyTiles {
         vp(static_cast<const T*>(a.v) + first_key * a.v_stride),
         first(first_key),
         n_keys(keys) {
-    lc.c = Origin{0.f, 0.f, 0.f};
+    lc.c = Place{0, 0, 0};
   }
   __device__ __forceinline__ void fetch(const AttnArgs& a, int h, int k0) {
     const uint32_t ks = static_cast<uint32_t>(a.k_stride) * 2u, vs = static_cast<uint32_t>(a.v_stride) * 2u;
@@ -403,9 +413,9 @@ struct KeyTiles {
              vp + k0 * a.v_stride + h * a.d, last * vs + w, [&](int i) { return ld.row(i) * vs; }, a.d);
     if constexpr (BIAS) lc.fetch(a.kc, first + k0, n_keys - k0, a.ndim);
   }
-  __device__ __forceinline__ void put(char* tk, char* tv, f32x4* tc, uint32_t* far_rows, const Origin& org) {
+  __device__ __forceinline__ void put(char* tk, char* tv, f32x4* tc, uint32_t* far_rows, const Origin& org, int ndim) {
     ld.put(tk, tv);
-    if constexpr (BIAS) lc.put(tc, far_rows, org);
+    if constexpr (BIAS) lc.put(tc, far_rows, org, ndim);
   }
 };
 
@@ -440,8 +450,8 @@ __device__ __forceinline__ f32x4 distances(const f32x4* tc, int r0, float norm, 
                                            const int32_t* c, int64_t first, uint32_t row, int ndim, const Origin& org) {
   f32x4 d;
   if (far) {
-    const Origin p = load_origin(c, first + late(row), ndim);
-    const float x = p.x - org.x, y = p.y - org.y, z = p.z - org.z;
+    const f32x4 p = relative(load_place(c, first + late(row), ndim), org, ndim);
+    const float x = p[0], y = p[1], z = p[2];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float* t = reinterpret_cast<const float*>(tc + r0 + 4 * (lane >> 4) + e);
@@ -466,7 +476,7 @@ struct QueryCols {
   bool live[NC], busy;
   uint32_t last;                 // query of the tile's last row, from query0
   __device__ __forceinline__ QueryCols(const AttnArgs& a, const SetTile& st, int bm) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t grp = a.grp, r0 = static_cast<uint32_t>(st.row0), rows = static_cast<uint32_t>(st.rows);
     const uint32_t q0 = grp == 1 ? r0 : r0 / grp;
     query0 = st.own0 + q0;

@@ -76,9 +76,11 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   int64_t kbeg, kend;
   split_range(st.st_len, BN, a.splits, split, &kbeg, &kend);
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
   const int kt0 = KS ? wave * 32 : 0;
-  const int n_keys = static_cast<int>(kend - kbeg);
+  // NC 2: not held as uniform, or both forms of a step are scheduled as one and their
+  // registers do not fit (2 x 8192 rows, dk and dv: 1225 against 1020 us, dq 1010 / 945)
+  const int n_keys = static_cast<int>(NC == 2 ? late(kend - kbeg) : kend - kbeg);
   int h = blockIdx.y * a.heads;
   const int h_end = !MULTI ? h + 1 : h + a.heads < a.hk ? h + a.heads : a.hk;
 
@@ -91,11 +93,11 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   }
   const int width = a.grp * a.d;  // a key-value head's part of a query row
   Origin org{0.f, 0.f, 0.f};
-  Origin qraw[NC];
+  Place oraw, qraw[NC];
   if constexpr (BIAS) {
-    org = uniform_origin(a.qc, st.own0, a.ndim);
+    oraw = load_place(a.qc, st.own0, a.ndim);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) qraw[j] = load_origin(a.qc, col.query0 + col.dq[j], a.ndim);
+    for (int j = 0; j < NC; ++j) qraw[j] = load_place(a.qc, col.query0 + col.dq[j], a.ndim);
   }
   ColLoad<T, DP, NC> qld, gld, old;
   float next_slope[NC], next_lse[NC];
@@ -119,9 +121,10 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   float slope[NC], qb[NC], qn[NC];
   bool far_cols = false;
   if constexpr (BIAS) {
+    org = uniform_origin(oraw, a.ndim);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const f32x4 c = relative(qraw[j], org);
+      const f32x4 c = relative(qraw[j], org, a.ndim);
       qb[j] = col_term(c, g);
       qn[j] = c[3];
       far_cols |= __any(c[3] > kNearNorm) != 0;
@@ -246,7 +249,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
       fetch_cols(h);
     }
   }
-  keys.put(tk[0], tv[0], tc[0], far_rows[0], org);
+  keys.put(tk[0], tv[0], tc[0], far_rows[0], org, a.ndim);
   begin();
   for (int k0 = 0, b = 0;; b ^= 1) {
     const bool wrap = k0 + BN >= n_keys;
@@ -274,7 +277,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
     h = hn;
     k0 = kn;
     if (MULTI && wrap) begin();
-    keys.put(tk[b ^ 1], tv[b ^ 1], tc[b ^ 1], far_rows[b ^ 1], org);
+    keys.put(tk[b ^ 1], tv[b ^ 1], tc[b ^ 1], far_rows[b ^ 1], org, a.ndim);
   }
 }
 
@@ -299,8 +302,8 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
   int64_t rbeg, rend;
   split_range(st.st_len * a.grp, BN, a.splits, split, &rbeg, &rend);
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
-  const int n_rows = static_cast<int>(rend - rbeg);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4;
+  const int n_rows = static_cast<int>(NC == 2 ? late(rend - rbeg) : rend - rbeg);  // see k_attn_dq
   int h = blockIdx.y * a.heads;
   const int h_end = !MULTI ? h + 1 : h + a.heads < a.hk ? h + a.heads : a.hk;
   const int width = a.grp * a.d;
@@ -320,11 +323,11 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
   }
   const bool busy = static_cast<uint32_t>(wave * 16) < cols;
   Origin org{0.f, 0.f, 0.f};
-  Origin kraw[NC];
+  Place oraw, kraw[NC];
   if constexpr (BIAS) {
-    org = uniform_origin(a.kc, st.own0, a.ndim);
+    oraw = load_place(a.kc, st.own0, a.ndim);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) kraw[j] = load_origin(a.kc, key0 + ck[j], a.ndim);
+    for (int j = 0; j < NC; ++j) kraw[j] = load_place(a.kc, key0 + ck[j], a.ndim);
   }
   ColLoad<T, DP, NC> kld, vld;
   auto fetch_cols = [&](int hn) {
@@ -343,16 +346,18 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
   };
   TileLoad<T, DP, BN> ld;
   TileCoords<BN> lc;
-  lc.c = Origin{0.f, 0.f, 0.f};
+  lc.c = Place{0, 0, 0};
   float rl = 0.f, rd = 0.f, rs = 0.f;
-  // Tile rows of this thread: query from the tile's first one, and place.  The same
-  // in every tile where the heads that share a key head divide BN, else formed anew.
-  uint32_t dqy[ld.CT], plc[ld.CT];
+  // Tile rows of this thread: 2^16 times the query from the tile's first one, and
+  // place.  The same in every tile where the heads that share a key head divide BN,
+  // else formed anew.
+  uint32_t trow[ld.CT];
   auto place_rows = [&](int r0, uint32_t q0) {
 #pragma unroll
     for (int i = 0; i < ld.CT; ++i) {
-      at_row(r0 + ld.row(i), &dqy[i], &plc[i]);
-      dqy[i] -= q0;
+      uint32_t q, p;
+      at_row(r0 + ld.row(i), &q, &p);
+      trow[i] = (q - q0) << 16 | p;
     }
   };
   const bool even = BN % a.grp == 0;
@@ -361,8 +366,12 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
     at_row(0, &q0, &p0);
     place_rows(0, q0);
   }
-  auto off_q = [&](int i) { return (dqy[i] * static_cast<uint32_t>(a.q_stride) + plc[i] * a.d) * 2u; };
-  auto off_g = [&](int i) { return (dqy[i] * static_cast<uint32_t>(a.o_stride) + plc[i] * a.d) * 2u; };
+  auto off = [&](int i, int64_t stride) {
+    const uint32_t r = late(trow[i]);  // taken apart where it is used: two registers fewer through the walk
+    return ((r >> 16) * static_cast<uint32_t>(stride) + (r & 0xffffu) * a.d) * 2u;
+  };
+  auto off_q = [&](int i) { return off(i, a.q_stride); };
+  auto off_g = [&](int i) { return off(i, a.o_stride); };
   auto fetch = [&](int hn, int r0) {
     uint32_t q0, p0, q1, p1;
     at_row(r0, &q0, &p0);
@@ -382,7 +391,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
       rl = a.lse[query * a.hq + head];
       rd = a.delta[query * a.hq + head];
       if constexpr (BIAS) {
-        lc.c = load_origin(a.qc, query, a.ndim);
+        lc.c = load_place(a.qc, query, a.ndim);
         rs = a.slopes[head];
       }
     }
@@ -394,16 +403,17 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
       td[b][tid] = -rd;
       if constexpr (BIAS) tsl[b][tid] = rs * kLog2e;
     }
-    if constexpr (BIAS) lc.put(tc[b], far_rows[b], org);
+    if constexpr (BIAS) lc.put(tc[b], far_rows[b], org, a.ndim);
   };
   if (n_rows > 0) fetch(h, 0);
 
   float kb_[NC], kn[NC];
   bool far_cols = false;
   if constexpr (BIAS) {
+    org = uniform_origin(oraw, a.ndim);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const f32x4 c = relative(kraw[j], org);
+      const f32x4 c = relative(kraw[j], org, a.ndim);
       kb_[j] = col_term(c, g);
       kn[j] = c[3];
       far_cols |= __any(c[3] > kNearNorm) != 0;

@@ -60,7 +60,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
   int64_t kbeg, kend;
   split_range(st.st_len, BN, a.splits, split, &kbeg, &kend);
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
   const int kt0 = KS ? wave * 32 : 0;
   const int n_keys = static_cast<int>(kend - kbeg);
   int h = blockIdx.y * a.heads;
@@ -74,11 +74,11 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
   const T* qp = static_cast<const T*>(a.q) + col.query0 * a.q_stride;
   const uint32_t qbytes = col.bytes(a.q_stride, width);
   Origin org{0.f, 0.f, 0.f};
-  Origin qraw[NC];
+  Place oraw, qraw[NC];
   if constexpr (BIAS) {
-    org = uniform_origin(a.qc, st.own0, a.ndim);
+    oraw = load_place(a.qc, st.own0, a.ndim);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) qraw[j] = load_origin(a.qc, col.query0 + col.dq[j], a.ndim);
+    for (int j = 0; j < NC; ++j) qraw[j] = load_place(a.qc, col.query0 + col.dq[j], a.ndim);
   }
   ColLoad<T, DP, NC> qld;
   float next_slope[NC];
@@ -95,9 +95,10 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
   float slope[NC], qb[NC], qn[NC];  // (the last two: for the distances)
   bool far_cols = false;
   if constexpr (BIAS) {
+    org = uniform_origin(oraw, a.ndim);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const f32x4 c = relative(qraw[j], org);
+      const f32x4 c = relative(qraw[j], org, a.ndim);
       qb[j] = col_term(c, g);
       qn[j] = c[3];
       far_cols |= __any(c[3] > kNearNorm) != 0;
@@ -343,7 +344,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
     }
     return;
   }
-  keys.put(tk[0], tv[0], tc[0], far_rows[0], org);
+  keys.put(tk[0], tv[0], tc[0], far_rows[0], org, a.ndim);
   begin();
   for (int k0 = 0, b = 0;; b ^= 1) {
     const bool wrap = k0 + BN >= n_keys;
@@ -366,7 +367,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
     h = hn;
     k0 = kn;
     if (MULTI && wrap) begin();
-    keys.put(tk[b ^ 1], tv[b ^ 1], tc[b ^ 1], far_rows[b ^ 1], org);
+    keys.put(tk[b ^ 1], tv[b ^ 1], tc[b ^ 1], far_rows[b ^ 1], org, a.ndim);
   }
 }
 
