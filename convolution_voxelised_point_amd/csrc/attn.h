@@ -389,6 +389,10 @@ __device__ __forceinline__ bool tile_far(const uint32_t* far_rows) {
   return __builtin_amdgcn_readfirstlane(f) != 0;
 }
 
+// Where a block takes several heads one after the other over at most this many
+// tiles, the tiles' coordinates stay in LDS for all of them.
+constexpr int kCoordTiles = 4;
+
 // The key side of a walk over n_keys keys from row `first`: tiles of keys and values of one key-value head, and the
 // keys' coordinates.
 template <typename T, int DP, int BN, bool BIAS>
@@ -406,16 +410,17 @@ struct KeyTiles {
         n_keys(keys) {
     lc.c = Place{0, 0, 0};
   }
-  __device__ __forceinline__ void fetch(const AttnArgs& a, int h, int k0) {
+  __device__ __forceinline__ void fetch(const AttnArgs& a, int h, int k0, bool coords) {
     const uint32_t ks = static_cast<uint32_t>(a.k_stride) * 2u, vs = static_cast<uint32_t>(a.v_stride) * 2u;
     const uint32_t last = (n_keys - k0 < BN ? n_keys - k0 : BN) - 1, w = a.d * 2u;
     ld.fetch(kp + k0 * a.k_stride + h * a.d, last * ks + w, [&](int i) { return ld.row(i) * ks; },
              vp + k0 * a.v_stride + h * a.d, last * vs + w, [&](int i) { return ld.row(i) * vs; }, a.d);
-    if constexpr (BIAS) lc.fetch(a.kc, first + k0, n_keys - k0, a.ndim);
+    if (BIAS && coords) lc.fetch(a.kc, first + k0, n_keys - k0, a.ndim);
   }
-  __device__ __forceinline__ void put(char* tk, char* tv, f32x4* tc, uint32_t* far_rows, const Origin& org, int ndim) {
+  __device__ __forceinline__ void put(char* tk, char* tv, bool coords, f32x4* tc, uint32_t* far_rows, const Origin& org,
+                                      int ndim) {
     ld.put(tk, tv);
-    if constexpr (BIAS) lc.put(tc, far_rows, org, ndim);
+    if (BIAS && coords) lc.put(tc, far_rows, org, ndim);
   }
 };
 
@@ -495,7 +500,7 @@ struct QueryCols {
   }
   // byte offset of column j's row of a matrix with this row stride, from row query0 of key-value head h
   __device__ __forceinline__ uint32_t offset(int j, int64_t stride, int d) const {
-    return live[j] ? (dq[j] * static_cast<uint32_t>(stride) + place[j] * d) * 2u : kOutside;
+    return live[j] ? (late(dq[j]) * static_cast<uint32_t>(stride) + late(place[j]) * d) * 2u : kOutside;
   }
   __device__ __forceinline__ uint32_t bytes(int64_t stride, int width) const {
     return (last * static_cast<uint32_t>(stride) + width) * 2u;

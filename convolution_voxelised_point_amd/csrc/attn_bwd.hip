@@ -116,7 +116,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   };
   fetch_cols(h);
   KeyTiles<T, DP, BN, BIAS> keys(a, st.st0 + kbeg, n_keys);
-  if (n_keys > 0) keys.fetch(a, h, 0);
+  if (n_keys > 0) keys.fetch(a, h, 0, true);
 
   float slope[NC], qb[NC], qn[NC];
   bool far_cols = false;
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
       fetch_cols(h);
     }
   }
-  keys.put(tk[0], tv[0], tc[0], far_rows[0], org, a.ndim);
+  keys.put(tk[0], tv[0], true, tc[0], far_rows[0], org, a.ndim);
   begin();
   for (int k0 = 0, b = 0;; b ^= 1) {
     const bool wrap = k0 + BN >= n_keys;
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
     const bool more = hn < h_end;
     if (more) {
       if (MULTI && wrap) fetch_cols(hn);
-      keys.fetch(a, hn, kn);
+      keys.fetch(a, hn, kn, true);
     }
     __syncthreads();
     if (col.busy) {
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
     h = hn;
     k0 = kn;
     if (MULTI && wrap) begin();
-    keys.put(tk[b ^ 1], tv[b ^ 1], tc[b ^ 1], far_rows[b ^ 1], org, a.ndim);
+    keys.put(tk[b ^ 1], tv[b ^ 1], true, tc[b ^ 1], far_rows[b ^ 1], org, a.ndim);
   }
 }
 
@@ -367,7 +367,8 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
     place_rows(0, q0);
   }
   auto off = [&](int i, int64_t stride) {
-    const uint32_t r = late(trow[i]);  // taken apart where it is used: two registers fewer through the walk
+    // NC 2: taken apart where it is used, two registers fewer through the walk
+    const uint32_t r = NC == 2 ? late(trow[i]) : trow[i];
     return ((r >> 16) * static_cast<uint32_t>(stride) + (r & 0xffffu) * a.d) * 2u;
   };
   auto off_q = [&](int i) { return off(i, a.q_stride); };

@@ -36,7 +36,7 @@ constexpr float kFold = 256.f;
 // cost more than a head's work, and the next head's rows are read while this one's
 // last tile is computed.
 template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS>
-__global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_fwd(const AttnArgs a) {
+__global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_attn_fwd(const AttnArgs a) {
   typedef typename AMfma<T>::frag Frag;
   constexpr int KB = DP / 32, DI = DP / 16;
   constexpr int BN = KS ? 128 : 64;  // keys per tile
@@ -46,8 +46,9 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
   constexpr bool MULTI = NC == 1 && !KS && DP <= 64;  // a.heads may be more than 1
   static_assert(!KS || NC == 1, "one column block when the waves share the keys");
   __shared__ __attribute__((aligned(16))) char tk[2][TB], tv[2][TB];
-  __shared__ f32x4 tc[2][BIAS ? BN : 1];
-  __shared__ uint32_t far_rows[2][2];
+  constexpr int TCS = MULTI ? kCoordTiles : 2;
+  __shared__ f32x4 tc[TCS][BIAS ? BN : 1];
+  __shared__ uint32_t far_rows[TCS][2];
 
   const int64_t slot = block_tile();
   const int split = blockIdx.z;
@@ -63,13 +64,12 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
   const int kt0 = KS ? wave * 32 : 0;
   const int n_keys = static_cast<int>(kend - kbeg);
-  int h = blockIdx.y * a.heads;
+  const int h0 = blockIdx.y * a.heads;
+  int h = h0;
+  int cb = 0;  // where the tile's coordinates are
   const int h_end = !MULTI ? h + 1 : h + a.heads < a.hk ? h + a.heads : a.hk;
 
   const QueryCols<NC, KS> col(a, st, BM);
-  uint32_t qoff[NC];
-#pragma unroll
-  for (int j = 0; j < NC; ++j) qoff[j] = col.offset(j, a.q_stride, a.d);
   const int width = a.grp * a.d;  // a key-value head's part of a query row
   const T* qp = static_cast<const T*>(a.q) + col.query0 * a.q_stride;
   const uint32_t qbytes = col.bytes(a.q_stride, width);
@@ -83,6 +83,9 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
   ColLoad<T, DP, NC> qld;
   float next_slope[NC];
   auto fetch_cols = [&](int hn) {
+    uint32_t qoff[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) qoff[j] = col.offset(j, a.q_stride, a.d);
     qld.fetch(qp + static_cast<int64_t>(hn) * width, qbytes, qoff, a.d);
     if constexpr (BIAS)
 #pragma unroll
@@ -90,7 +93,8 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
   };
   fetch_cols(h);
   KeyTiles<T, DP, BN, BIAS> keys(a, st.st0 + kbeg, n_keys);
-  if (n_keys > 0) keys.fetch(a, h, 0);
+  const bool stay = MULTI && n_keys <= TCS * BN;  // tile i's coordinates are in tc[i] from the first head on
+  if (n_keys > 0) keys.fetch(a, h, 0, true);
 
   float slope[NC], qb[NC], qn[NC];  // (the last two: for the distances)
   bool far_cols = false;
@@ -135,7 +139,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
     }
   };
   auto dist_of = [&](int b, int n, int j, bool far) {
-    return distances(tc[b], kt0 + n * 16, qn[j], qb[j], far, lane, a.qc, col.query0, col.dq[j], a.ndim, org);
+    return distances(tc[cb], kt0 + n * 16, qn[j], qb[j], far, lane, a.qc, col.query0, col.dq[j], a.ndim, org);
   };
   // the score relative to `base`
   auto score = [&](int j, float s, float dist, float base) {
@@ -312,6 +316,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       if (!col.live[j]) continue;
+      const int d4 = static_cast<int>(late(g)) * 4;
       const int64_t query = col.query0 + late(col.dq[j]);
       const int head = h * a.grp + static_cast<int>(late(col.place[j]));
       const int64_t at = (static_cast<int64_t>(split) * a.nq + query) * a.hq + head;
@@ -321,7 +326,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
           a.part_ml[at * 2 + 1] = l[j];
         }
 #pragma unroll
-        for (int i = 0; i < DI; ++i) *reinterpret_cast<f32x4*>(a.part + at * DP + i * 16 + g * 4) = o[j][i];
+        for (int i = 0; i < DI; ++i) *reinterpret_cast<f32x4*>(a.part + at * DP + i * 16 + d4) = o[j][i];
         continue;
       }
       const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
@@ -331,7 +336,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
         f32x4 y = o[j][i];
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] *= inv;
-        store4(op, i * 16 + g * 4, a.d, y);
+        store4(op, i * 16 + d4, a.d, y);
       }
       if (g == 0) a.lse[at] = l[j] == 0.f ? -INFINITY : (m[j] + __builtin_amdgcn_logf(l[j])) * kLn2;
     }
@@ -344,7 +349,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
     }
     return;
   }
-  keys.put(tk[0], tv[0], tc[0], far_rows[0], org, a.ndim);
+  keys.put(tk[0], tv[0], true, tc[0], far_rows[0], org, a.ndim);
   begin();
   for (int k0 = 0, b = 0;; b ^= 1) {
     const bool wrap = k0 + BN >= n_keys;
@@ -352,12 +357,12 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
     const bool more = hn < h_end;
     if (more) {
       if (MULTI && wrap) fetch_cols(hn);
-      keys.fetch(a, hn, kn);
+      keys.fetch(a, hn, kn, !stay || hn == h0);
     }
     __syncthreads();
     if (col.busy) {
       const int left = n_keys - k0 - kt0;  // keys of this wave's part
-      const bool far = BIAS && (far_cols || tile_far<BN>(far_rows[b]));
+      const bool far = BIAS && (far_cols || tile_far<BN>(far_rows[cb]));
       bool done = false;
       if (fold && !far && k0 + BN <= n_keys) done = fast(b);
       if (!done) slow(b, left, far);
@@ -367,7 +372,8 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, BIAS, KS)) void k_attn_
     h = hn;
     k0 = kn;
     if (MULTI && wrap) begin();
-    keys.put(tk[b ^ 1], tv[b ^ 1], tc[b ^ 1], far_rows[b ^ 1], org, a.ndim);
+    cb = stay ? k0 / BN : b ^ 1;
+    keys.put(tk[b ^ 1], tv[b ^ 1], !stay || h == h0, tc[cb], far_rows[cb], org, a.ndim);
   }
 }
 

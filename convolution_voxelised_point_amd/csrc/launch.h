@@ -128,11 +128,11 @@ struct AttnArgs;
 constexpr int kAttnMaxSplits = 512;
 constexpr int kAttnFewSplits = 8;  // joined by a thread per 4 elements instead of a block per row
 // Waves per SIMD that the registers of a kernel of this shape allow without spilling.
-constexpr int attn_waves_fwd(int dp, int nc, bool bias, bool share_keys) {
-  return share_keys ? (dp == 128 ? 1 : 2) : nc == 2 || dp == 128 ? 2 : dp == 64 ? (bias ? 2 : 3) : 4;
+constexpr int attn_waves_fwd(int dp, int nc, bool cap, bool bias, bool share_keys) {
+  return share_keys ? (dp == 128 ? 1 : 2) : nc == 2 || dp == 128 ? 2 : dp == 64 ? (bias ? 2 : 3) : cap && bias ? 4 : 5;
 }
 constexpr int attn_waves_dq(int dp, int nc, bool cap, bool bias, bool share_keys) {
-  return share_keys ? (dp == 128 ? 1 : 2) : nc == 2 || dp >= 64 || (cap && bias) ? 2 : bias ? 3 : 4;
+  return share_keys ? (dp == 128 ? 1 : 2) : nc == 2 || dp >= 64 || (cap && bias) ? 2 : 4;
 }
 constexpr int attn_waves_dkv(int dp, int nc, bool bias) {
   return dp == 128 ? 1 : dp == 32 && nc == 1 ? 3 : 2;
