@@ -119,7 +119,7 @@ size_t fwd_bytes(const ts_attn* at) {
 // q, out, dout, dq; k, v, dk, dv
 size_t delta_bytes(const ts_attn* at) { return align_up(static_cast<size_t>(at->nq) * at->hq * 4, 256); }
 size_t bwd_bytes(const ts_attn* at) {
-  const size_t q = part_floats(at, plan_fwd(at), at->nq * at->hq, 0);
+  const size_t q = part_floats(at, plan_fwd(at), at->nq * at->hq, 1);
   const size_t k = 2 * part_floats(at, plan_dkv(at), at->nk * at->hk, 0);
   return (repacks(at) ? 4 * q_copy_bytes(at) + 4 * k_copy_bytes(at) : 0) + delta_bytes(at) + (q > k ? q : k) * 4;
 }
@@ -272,6 +272,7 @@ ts_status ts_attn_bwd(const ts_attn* at, const void* q, const void* k, const voi
   }
   a.delta = static_cast<float*>(c.take(delta_bytes(at)));
   a.part = static_cast<float*>(c.take(0));
+  a.part_ml = a.part + static_cast<size_t>(pq.splits) * at->nq * at->hq * padded_width(at->d);
   TS_TRY(launch_attn_bwd(a, pq, pk, at->dtype, at->cap > 0.f, stream));
   if (repacks(at)) {
     TS_TRY(copy_out(at, a.dq, at->hq, at->nq, dq, at->q_stride, stream));

@@ -16,8 +16,8 @@
 // is rounded already: that error and one rounding of ds together made dq 1.6 to 1.8
 // times as far from the exact one as its own last rounding does (now 1.2 to 1.45; the
 // second product costs 12 % of this kernel).  The sum of p (dp - delta) over a row is
-// 0 in exact arithmetic; where a block sees the whole row it adds what it finds
-// to the delta that dk uses.
+// 0 in exact arithmetic: what it comes to is added to the delta that dk uses (not
+// where the waves share a few rows' keys).
 //
 // As in the forward pass, a wave owns NC column blocks of 16 and a block takes
 // a.heads key-value heads one after the other; delta enters as the accumulator
@@ -224,8 +224,11 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
       if (!col.live[j]) continue;
       const int64_t query = col.query0 + late(col.dq[j]);
       const int head = h * a.grp + static_cast<int>(late(col.place[j]));
-      if (g == 0 && split == 0)
-        a.delta[query * a.hq + head] = !KS && a.splits == 1 ? fmaf(over, CAP ? 0.25f : 1.f, delta[j]) : delta[j];
+      if (g == 0) {
+        const float short_of = KS ? 0.f : CAP ? 0.25f * over : over;
+        if (split == 0) a.delta[query * a.hq + head] = a.splits == 1 ? delta[j] + short_of : delta[j];
+        if (a.splits > 1) a.part_ml[(static_cast<int64_t>(split) * a.nq + query) * a.hq + head] = short_of;
+      }
       T* dst = static_cast<T*>(a.dq) + query * a.q_stride + static_cast<int64_t>(head) * a.d;
       float* part = a.part + ((static_cast<int64_t>(split) * a.nq + query) * a.hq + head) * DP;
 #pragma unroll
@@ -555,10 +558,12 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
   }
 }
 
-// out row r (row / heads, head row % heads) = sum over the splits, in order
+// out row r (row / heads, head row % heads) = sum over the splits, in order; the same
+// of what the splits found delta short of
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void k_attn_sum(const float* __restrict__ part, int64_t rows, int splits, int heads,
-                                                  int d, T* out, int64_t stride) {
+                                                  int d, T* out, int64_t stride, const float* __restrict__ short_of,
+                                                  float* delta) {
   constexpr int Q = DP / 4;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = i / Q;
   const int d0 = static_cast<int>(i % Q) * 4;
@@ -571,13 +576,18 @@ __global__ __launch_bounds__(256) void k_attn_sum(const float* __restrict__ part
   }
   const int64_t n = row / heads;
   store4(out + n * stride + (row - n * heads) * d, d0, d, y);
+  if (delta && d0 == 0) {
+    float x = delta[row];
+    for (int s = 0; s < splits; ++s) x += short_of[s * rows + row];
+    delta[row] = x;
+  }
 }
 
 template <typename T, int DP>
 void run_sum(const float* part, int64_t rows, int splits, int heads, const AttnArgs& a, void* out, int64_t stride,
-             hipStream_t s) {
+             float* delta, hipStream_t s) {
   k_attn_sum<T, DP><<<static_cast<unsigned>(ceil_div<int64_t>(rows * (DP / 4), 256)), 256, 0, s>>>(
-      part, rows, splits, heads, a.d, static_cast<T*>(out), stride);
+      part, rows, splits, heads, a.d, static_cast<T*>(out), stride, a.part_ml, delta);
 }
 
 template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS>
@@ -601,7 +611,7 @@ void run_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t s)
       run_dq<T, DP, DP <= 64 ? 2 : 1, CAP, BIAS, false>(a, s);
     else
       run_dq<T, DP, 1, CAP, BIAS, false>(a, s);
-    if (a.splits > 1) run_sum<T, DP>(a.part, a.nq * a.hq, a.splits, a.hq, a, a.dq, a.q_stride, s);
+    if (a.splits > 1) run_sum<T, DP>(a.part, a.nq * a.hq, a.splits, a.hq, a, a.dq, a.q_stride, a.delta, s);
   }
   if (a.nk == 0) return;
   a.tiles = attn_tiles(a.nk, 1, pk.bm, a.n_sets);
@@ -613,8 +623,8 @@ void run_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t s)
     run_dkv<T, DP, 1, CAP, BIAS>(a, s);
   if (a.splits > 1) {
     const int64_t rows = a.nk * a.hk;
-    run_sum<T, DP>(a.part, rows, a.splits, a.hk, a, a.dk, a.k_stride, s);
-    run_sum<T, DP>(a.part + a.splits * rows * DP, rows, a.splits, a.hk, a, a.dv, a.v_stride, s);
+    run_sum<T, DP>(a.part, rows, a.splits, a.hk, a, a.dk, a.k_stride, nullptr, s);
+    run_sum<T, DP>(a.part + a.splits * rows * DP, rows, a.splits, a.hk, a, a.dv, a.v_stride, nullptr, s);
   }
 }
 
