@@ -16,8 +16,9 @@
 // is rounded already: that error and one rounding of ds together made dq 1.6 to 1.8
 // times as far from the exact one as its own last rounding does (now 1.2 to 1.45; the
 // second product costs 12 % of this kernel).  The sum of p (dp - delta) over a row is
-// 0 in exact arithmetic: what it comes to is added to the delta that dk uses (not
-// where the waves share a few rows' keys).
+// 0 in exact arithmetic: what it comes to is added to the delta that dk uses, and
+// where a row has at most 32 keys (there it matters most: with one key, dq is 0) it
+// is known before ds is needed and taken off for dq as well.
 //
 // As in the forward pass, a wave owns NC column blocks of 16 and a block takes
 // a.heads key-value heads one after the other; delta enters as the accumulator
@@ -28,20 +29,18 @@ namespace ts {
 
 namespace {
 
-// p and ds of one score.  s = q.k; dist the distance; base = -lse (plus c2
-// for a capped score) in units of log 2; dp has delta taken off already (it is
-// the accumulator that product starts from).
+// p of one score and w, with ds = w dp.  s = q.k; dist the distance; base = -lse
+// (plus c2 for a capped score) in units of log 2.
 template <bool CAP, bool BIAS>
-__device__ __forceinline__ void grad_score(const AttnArgs& a, float s, float dp, float base, float slope, float dist,
-                                           float* p, float* ds) {
+__device__ __forceinline__ void grad_score(const AttnArgs& a, float s, float base, float slope, float dist, float* p,
+                                           float* w) {
   if constexpr (BIAS) base = fmaf(-slope, dist, base);
   if constexpr (CAP) {
     const float r = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(s * a.c1) + 1.f);
     *p = __builtin_amdgcn_exp2f(fmaf(-2.f * a.c2, r, base));
-    *ds = *p * dp * fmaf(-r, r, r);
+    *w = *p * fmaf(-r, r, r);
   } else {
-    *p = __builtin_amdgcn_exp2f(fmaf(s, a.c1, base));
-    *ds = *p * dp;
+    *p = *w = __builtin_amdgcn_exp2f(fmaf(s, a.c1, base));
   }
 }
 
@@ -135,6 +134,8 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   Frag qf[NC][KB], gf[NC][KB];
   f32x4 dq[NC][DI];
   float base[NC], delta[NC], rho[NC];
+  const float rho_scale = CAP ? 0.25f : 1.f;
+  const bool whole = a.splits == 1 && n_keys <= 32;  // one step sees the whole row
   auto begin = [&]() {
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
@@ -183,15 +184,31 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
                            col.dq[j], a.ndim, org);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float p, ds;
-          grad_score<CAP, BIAS>(a, s[j][n][e], dp[j][n][e], base[j], BIAS ? slope[j] : 0.f, dist[e], &p, &ds);
+          float p, w;
+          grad_score<CAP, BIAS>(a, s[j][n][e], base[j], BIAS ? slope[j] : 0.f, dist[e], &p, &w);
           if constexpr (PART)
-            if (u * 32 + n * 16 + 4 * g + e >= left) p = ds = 0.f;
-          if constexpr (!KS) rho[j] = fmaf(p, dp[j][n][e], rho[j]);
+            if (u * 32 + n * 16 + 4 * g + e >= left) p = w = 0.f;
+          rho[j] = fmaf(p, dp[j][n][e], rho[j]);
+          s[j][n][e] = w;
+        }
+      }
+    float more[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) more[j] = 0.f;
+    if (PART && whole) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) more[j] = col_sum(rho[j]) * rho_scale;
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float ds = s[j][n][e] * (PART ? dp[j][n][e] - more[j] : dp[j][n][e]);
           df[j][n * 4 + e] = static_cast<T>(ds);
           dr[j][n * 4 + e] = static_cast<T>(ds - static_cast<float>(df[j][n * 4 + e]));
         }
-      }
 #pragma unroll
     for (int i = 0; i < DI; ++i) {
       const Frag f = tile_frag_t<T, DP>(tk[b], kt0 + u * 32, i, lane);
@@ -201,14 +218,20 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   };
 
   auto finish = [&]() {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) rho[j] = col_sum(rho[j]) * rho_scale;
     if constexpr (KS) {
       float* jo = reinterpret_cast<float*>(tv);  // [4][16][DP]
+      float* jr = reinterpret_cast<float*>(tk);  // [4][16]
       __syncthreads();
+      if (g == 0) jr[wave * 16 + lane] = rho[0];
 #pragma unroll
       for (int i = 0; i < DI; ++i)
         *reinterpret_cast<f32x4*>(jo + (wave * 16 + (lane & 15)) * DP + i * 16 + g * 4) = dq[0][i];
       __syncthreads();
       if (wave != 0) return;
+#pragma unroll
+      for (int x = 1; x < 4; ++x) rho[0] += jr[x * 16 + (lane & 15)];
 #pragma unroll
       for (int x = 1; x < 4; ++x)
 #pragma unroll
@@ -220,14 +243,13 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
     }
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const float over = col_sum(rho[j]);  // what delta was short of
       if (!col.live[j]) continue;
       const int64_t query = col.query0 + late(col.dq[j]);
       const int head = h * a.grp + static_cast<int>(late(col.place[j]));
       if (g == 0) {
-        const float short_of = KS ? 0.f : CAP ? 0.25f * over : over;
-        if (split == 0) a.delta[query * a.hq + head] = a.splits == 1 ? delta[j] + short_of : delta[j];
-        if (a.splits > 1) a.part_ml[(static_cast<int64_t>(split) * a.nq + query) * a.hq + head] = short_of;
+        // rho: what delta was short of
+        if (split == 0) a.delta[query * a.hq + head] = a.splits == 1 ? delta[j] + rho[j] : delta[j];
+        if (a.splits > 1) a.part_ml[(static_cast<int64_t>(split) * a.nq + query) * a.hq + head] = rho[j];
       }
       T* dst = static_cast<T*>(a.dq) + query * a.q_stride + static_cast<int64_t>(head) * a.d;
       float* part = a.part + ((static_cast<int64_t>(split) * a.nq + query) * a.hq + head) * DP;
@@ -269,7 +291,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
 #pragma unroll
       for (int u = 0; u < NT / 2; ++u) {
         if (u * 32 >= left) continue;
-        if (u * 32 + 32 <= left && !far)
+        if (u * 32 + 32 <= left && !far && !whole)
           step(Flag<false>{}, b, u, left, false);
         else
           step(Flag<true>{}, b, u, left, far);
@@ -472,8 +494,9 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
           dist = distances(tc[b], u * 32 + n * 16, kn[j], kb_[j], PART && far, lane, a.kc, key0, ck[j], a.ndim, org);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float p, ds;
-          grad_score<CAP, BIAS>(a, s[j][n][e], dp[j][n][e], base[e], slope[e], dist[e], &p, &ds);
+          float p, w;
+          grad_score<CAP, BIAS>(a, s[j][n][e], base[e], slope[e], dist[e], &p, &w);
+          float ds = w * dp[j][n][e];
           if constexpr (PART)
             if (r + e >= left) p = ds = 0.f;  // a zero row times an infinite key is NaN
           pf[j][n * 4 + e] = static_cast<T>(p);

@@ -378,3 +378,22 @@ def test_refusals(ts):
     assert ts.ts_attn_workspace_bytes(at, False) > 0
     with pytest.raises(ts.TsError):  # no workspace
         ts.ts_attn_fwd(at, q, h(9000, 4, 16), h(9000, 4, 16), torch.empty_like(q), torch.empty(8, 4, device="cuda"))
+
+
+@pytest.mark.parametrize("nq,cap", [(1, 0.0), (1, 6.0), (40, 0.0)])
+def test_one_key_has_no_score_gradient(ts, nq, cap):
+    """With one key a softmax is constant: dq and dk are 0.  The sum of p (dp - delta) that a row's delta is
+    corrected by is formed in fp32, p = exp(z - lse) is 1 to 2^-19 (z, lse below 32) and dp below |dout| |v|, so what
+    is left of ds is below 2^-18 |dout| |v|; from the rounded out alone it would be 2^-12 of it."""
+    d, n = 32, 50
+    g = torch.Generator("cuda").manual_seed(77)
+    q, dout = (torch.randn(n * nq, 1, d, generator=g, device="cuda").half() for _ in range(2))
+    k, v = (torch.randn(n, 1, d, generator=g, device="cuda").half() for _ in range(2))
+    qs = torch.arange(0, n * nq + 1, nq, device="cuda")
+    ks = torch.arange(0, n + 1, device="cuda")
+    out, lse = ts.attn_fwd(q, k, v, qs, ks, cap=cap)
+    dq, dk, _ = ts.attn_bwd(dout, q, k, v, out, lse, qs, ks, cap=cap)
+    largest = float(dout.float().norm(dim=2).max() * v.float().norm(dim=2).max())
+    bar = 2.0 ** -18 * largest * d ** -0.5
+    assert float(dq.float().abs().max()) <= bar * float(k.float().abs().max()) + 2.0 ** -25
+    assert float(dk.float().abs().max()) <= nq * bar * float(q.float().abs().max()) + 2.0 ** -25
