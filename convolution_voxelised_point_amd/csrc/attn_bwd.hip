@@ -174,6 +174,10 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
         }
       }
     Frag df[NC], dr[NC];
+    auto split = [&](int j, int e, float ds) {
+      df[j][e] = static_cast<T>(ds);
+      dr[j][e] = static_cast<T>(ds - static_cast<float>(df[j][e]));
+    };
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -189,26 +193,22 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
           if constexpr (PART)
             if (u * 32 + n * 16 + 4 * g + e >= left) p = w = 0.f;
           rho[j] = fmaf(p, dp[j][n][e], rho[j]);
-          s[j][n][e] = w;
+          if constexpr (PART)
+            s[j][n][e] = w;
+          else
+            split(j, n * 4 + e, w * dp[j][n][e]);
         }
       }
-    float more[NC];
+    if constexpr (PART) {
 #pragma unroll
-    for (int j = 0; j < NC; ++j) more[j] = 0.f;
-    if (PART && whole) {
+      for (int j = 0; j < NC; ++j) {
+        const float more = whole ? col_sum(rho[j]) * rho_scale : 0.f;
 #pragma unroll
-      for (int j = 0; j < NC; ++j) more[j] = col_sum(rho[j]) * rho_scale;
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split(j, n * 4 + e, s[j][n][e] * (dp[j][n][e] - more));
+      }
     }
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int j = 0; j < NC; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ds = s[j][n][e] * (PART ? dp[j][n][e] - more[j] : dp[j][n][e]);
-          df[j][n * 4 + e] = static_cast<T>(ds);
-          dr[j][n * 4 + e] = static_cast<T>(ds - static_cast<float>(df[j][n * 4 + e]));
-        }
 #pragma unroll
     for (int i = 0; i < DI; ++i) {
       const Frag f = tile_frag_t<T, DP>(tk[b], kt0 + u * 32, i, lane);
