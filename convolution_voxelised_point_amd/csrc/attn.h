@@ -390,7 +390,8 @@ __device__ __forceinline__ bool tile_far(const uint32_t* far_rows) {
 }
 
 // Where a block takes several heads one after the other over at most this many
-// tiles, the tiles' coordinates stay in LDS for all of them.
+// tiles, the tiles' coordinates stay in LDS for all of them (2400 windows forward: 183 ->
+// 174 us; in the backward kernels it gained nothing).
 constexpr int kCoordTiles = 4;
 
 // The key side of a walk over n_keys keys from row `first`: tiles of keys and values of one key-value head, and the

@@ -126,8 +126,11 @@ hipError_t launch_wgrad(const ts_kmap* map, const void* x, int cin, const void* 
 // attn_fwd.hip, attn_bwd.hip
 struct AttnArgs;
 constexpr int kAttnMaxSplits = 512;
-constexpr int kAttnFewSplits = 8;  // joined by a thread per 4 elements instead of a block per row
-// Waves per SIMD that the registers of a kernel of this shape allow without spilling.
+// Up to this many splits are joined by a thread per 4 elements instead of a block per
+// row: 131k rows of 4 splits 14 us instead of 134, 2.6k rows of 3 splits 4.1 instead of 5.3.
+constexpr int kAttnFewSplits = 8;
+// Waves per SIMD that the registers of a kernel of this shape allow without spilling
+// (windows of 32 channels: forward 5 against 4 waves 164 / 174 us, dq 4 against 3 230 / 252).
 constexpr int attn_waves_fwd(int dp, int nc, bool cap, bool bias, bool share_keys) {
   return share_keys ? (dp == 128 ? 1 : 2) : nc == 2 || dp == 128 ? 2 : dp == 64 ? (bias ? 2 : 3) : cap && bias ? 4 : 5;
 }
