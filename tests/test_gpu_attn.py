@@ -397,3 +397,20 @@ def test_one_key_has_no_score_gradient(ts, nq, cap):
     bar = 2.0 ** -18 * largest * d ** -0.5
     assert float(dq.float().abs().max()) <= bar * float(k.float().abs().max()) + 2.0 ** -25
     assert float(dk.float().abs().max()) <= nq * bar * float(q.float().abs().max()) + 2.0 ** -25
+
+
+def test_offsets_past_32_bits(ts):
+    """Rows 2^20 elements apart, 3000 of them (6 GiB a tensor): the bits of the same rows side by side."""
+    n, hq, hk, d, stride = 3000, 4, 2, 32, 1 << 20
+    g = torch.Generator("cuda").manual_seed(55)
+    dense = [torch.randn(n, h, d, generator=g, device="cuda").bfloat16() for h in (hq, hk, hk, hq)]
+    far = [torch.empty(n * stride, dtype=torch.bfloat16, device="cuda").as_strided(t.shape, (stride, d, 1)) for t in dense]
+    for t, s in zip(far, dense):
+        t.copy_(s)
+    starts = torch.tensor([0, 40, 2900, n], device="cuda")
+    results = []
+    for q, k, v, dout in (dense, far):
+        out, lse = ts.attn_fwd(q, k, v, starts)
+        results.append((out, lse, *ts.attn_bwd(dout, q, k, v, out, lse, starts)))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)

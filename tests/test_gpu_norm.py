@@ -253,3 +253,22 @@ def test_empty(ts):
     dx, dw = ts.norm_bwd(x, r.h8, w, r.rstd)
     assert dx.shape == (0, 16) and (dw == 0).all()
     assert ts.act_unpack(ts.act_pack(x), torch.float16).shape == (0, 16)
+
+
+def test_more_than_2_31_elements(ts):
+    """The last rows of a matrix of 2^31 elements and more are those of the same rows by themselves."""
+    n, c, last = (1 << 24) + 1000, 128, 1500
+    x = torch.zeros((n, c), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator("cuda").manual_seed(56)
+    x[-last:] = torch.randn(last, c, generator=g, device="cuda").bfloat16()
+    w = torch.rand(c, generator=g, device="cuda") + 0.5
+    whole, part = (ts.norm_fwd(t, w, y8=True) for t in (x, x[-last:]))
+    assert torch.equal(whole.y[-last:], part.y) and torch.equal(whole.rstd[-last:], part.rstd)
+    assert torch.equal(whole.y8.codes[-last:], part.y8.codes) and torch.equal(whole.y8.scales[-last:], part.y8.scales)
+    dx, dw = ts.norm_bwd(whole.y, x, w, whole.rstd)
+    dx_part, _ = ts.norm_bwd(part.y, x[-last:], w, part.rstd)
+    assert torch.equal(dx[-last:], dx_part)
+    packed = ts.act_pack(x)
+    values = ts.act_unpack(packed, torch.bfloat16)
+    assert torch.equal(values[-last:], ts.act_unpack(ts.act_pack(x[-last:]), torch.bfloat16))
+    assert not values[:-last].any()
