@@ -140,7 +140,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   f32x4 dq[NC][DI];
   float base[NC], delta[NC], rho[NC];
   const float rho_scale = CAP ? 0.25f : 1.f;
-  const bool whole = a.splits == 1 && n_keys <= 32;  // one step sees the whole row
+  const bool whole = a.splits == 1 && kend - kbeg <= 32;  // one step sees the whole row
   auto begin = [&]() {
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
