@@ -79,7 +79,7 @@ AttnPlan plan_walk(int64_t own, int64_t other, int64_t n_sets, int hk, int dp, b
   // 741; 13 sets of 37 queries over 1000 keys: 16 and 4, unsplit 35.  Where that leaves
   // fewer than two rounds of blocks, long ones are split further (at least 1024 rows
   // each), so that the last round is a small part of the whole (2 x 8192 rows: forward
-  // 705 -> 662 us, dq 1091 -> 1040, dk and dv 1218 -> 1030).
+  // 705 -> 662 us, dq 1091 -> 1013, dk and dv 1218 -> 1030).
   int64_t s = blocks > 0 ? 512 / blocks : 1;
   if (s > other_per / 256) s = other_per / 256;
   int64_t fine = blocks > 0 && blocks < 1024 ? 2048 / blocks : 1;

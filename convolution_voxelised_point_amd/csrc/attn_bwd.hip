@@ -24,10 +24,10 @@
 // a.heads key-value heads one after the other; delta enters as the accumulator
 // that dp starts from.
 //
-// Bound by vector instructions, as the forward pass, with one wave in two to four per
-// SIMD waiting for LDS or the matrix cores.  Measured: 2 x 8192 rows, 8 query and 4 key heads
-// of 64, cap and bias: dq 1020 us, dk and dv 1030 (NC 1: 1274 and 1325); 2400
-// windows of about 127 rows, 4 heads of 32, biased: dq 230, dk and dv 270.
+// Bound by vector instructions, as the forward pass, and with two to four waves per
+// SIMD by the latency of LDS reads and matrix results.  Measured: 2 x 8192 rows, 8
+// query and 4 key heads of 64, cap and bias: dq 1013 us, dk and dv 1030 (NC 1: 1274 and
+// 1325); 2400 windows of about 127 rows, 4 heads of 32, biased: dq 230, dk and dv 270.
 #include "attn.h"
 
 namespace ts {
