@@ -712,8 +712,9 @@ def _raw_stream(t: torch.Tensor) -> int:
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
     """Rows of heads the library can take: dense copies of misaligned ones,
-    unless their width or stride makes the library copy them itself."""
-    if t.data_ptr() % 16 == 0 or t.shape[-1] % 8 or t.stride(0) % 8:
+    unless their width or stride (the one it is told: that of a single row is
+    its width) makes the library copy them itself."""
+    if t.data_ptr() % 16 == 0 or t.shape[-1] % 8 or (_row_stride(t) or 0) % 8:
         return t
     return t.clone(memory_format=torch.contiguous_format)
 

@@ -1,0 +1,42 @@
+"""Attention within packed sets where it can go wrong at its edges: views the
+library has to be given copies of, starts without rows, rows far apart,
+coordinates far from the origin, the range of fp16, and rows that nothing is
+left of.  The reference and its bounds are those of test_gpu_attn.py."""
+import pytest
+import torch
+
+from test_gpu_attn import starts
+
+pytestmark = pytest.mark.gpu
+
+
+def half(*shape, seed, dtype=torch.float16):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+def test_one_row_at_any_address(ts):
+    """One row of a matrix of odd width is a row like any other, wherever it begins."""
+    hq, hk, d, n = 4, 2, 16, 300
+    m = half(9, 97, seed=1)
+    k, v = half(n, hk, d, seed=2), half(n, hk, d, seed=3)
+    qs, ks = starts([1]), starts([n])
+    row = lambda t, i: t[:, :hq * d].unflatten(1, (hq, d))[i:i + 1]  # noqa: E731
+    for i in range(9):
+        q, dout = row(m, i), row(m, 8 - i)
+        out, lse = ts.attn_fwd(q, k, v, qs, ks)
+        want = ts.attn_fwd(q.clone(), k, v, qs, ks)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        wide = torch.empty_like(m)
+        mine = row(wide, i)
+        mine.copy_(out)
+        back = ts.attn_bwd(dout, q, k, v, mine, lse, qs, ks)
+        for a, b in zip(back, ts.attn_bwd(dout.clone(), q.clone(), k, v, out, lse, qs, ks)):
+            assert torch.equal(a, b)
+        into = (row(torch.zeros_like(m), i), torch.zeros_like(k), torch.zeros_like(v))
+        got = ts.attn_bwd(dout, q, k, v, mine, lse, qs, ks, into=into)
+        assert all(a is b and torch.equal(a, c) for a, b, c in zip(got, into, back))
+    # one key
+    q = half(5, hq, d, seed=4)
+    k1, v1 = (m[:, o:o + hk * d].unflatten(1, (hk, d))[3:4] for o in (0, 33))
+    out, lse = ts.attn_fwd(q, k1, v1, starts([5]), starts([1]))
+    assert torch.equal(out, v1.repeat_interleave(hq // hk, 1).expand(5, hq, d))
