@@ -223,7 +223,7 @@ ts_status ts_attn_fwd(const ts_attn* at, const void* q, const void* k, const voi
   const AttnPlan p = plan_fwd(at);
   const int grp = at->hq / at->hk;
   if (!grid_ok(at, p, at->nq, grp)) return TS_ERR_UNSUPPORTED;
-  if (at->nq == 0) return TS_OK;
+  if (at->nq == 0 && !err_flags) return TS_OK;  // (without rows the blocks look at the starts and end)
   AttnArgs a = attn_args(at, q, k, v, err_flags);
   a.out = out;
   a.lse = lse;

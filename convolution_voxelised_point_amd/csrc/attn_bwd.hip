@@ -629,7 +629,7 @@ void run_dkv(const AttnArgs& a, hipStream_t s) {
 
 template <typename T, int DP, bool CAP, bool BIAS>
 void run_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t s) {
-  if (a.nq > 0) {
+  if (a.nq > 0 || a.flags) {  // k_attn_dq checks the starts
     a.tiles = attn_tiles(a.nq, a.grp, pq.bm, a.n_sets);
     a.splits = pq.splits;
     a.heads = pq.heads;

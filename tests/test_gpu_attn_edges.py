@@ -40,3 +40,20 @@ def test_one_row_at_any_address(ts):
     k1, v1 = (m[:, o:o + hk * d].unflatten(1, (hk, d))[3:4] for o in (0, 33))
     out, lse = ts.attn_fwd(q, k1, v1, starts([5]), starts([1]))
     assert torch.equal(out, v1.repeat_interleave(hq // hk, 1).expand(5, hq, d))
+
+
+def test_bad_starts_without_query_rows(ts):
+    """The flag does not need a query row to be raised."""
+    q, k = half(0, 1, 16, seed=1), half(64, 1, 16, seed=2)
+    lse = torch.zeros(0, 1, device="cuda")
+    for qs, ks, bad in (([0, 0], [0, 65], True), ([0, 0, 0], [0, 40, 30], True), ([0, 1], [0, 64], True), ([-1, 0], [0, 64], True),
+                        ([0, 0], [0, 64], False), ([0, 0, 0], [3, 3, 60], False), ([0], [64], False), ([0], [65], True)):
+        args = torch.tensor(qs, device="cuda"), torch.tensor(ks, device="cuda")
+        want = ts.TS_FLAG_RANGE if bad else 0
+        flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, _ = ts.attn_fwd(q, k, k, *args, err_flags=flags)
+        assert int(flags) == want and out.shape == (0, 1, 16), (qs, ks)
+        flags.zero_()
+        _, dk, dv = ts.attn_bwd(q, q, k, k, q, lse, *args, err_flags=flags)
+        assert int(flags) == want and not dk.any() and not dv.any(), (qs, ks)
+    ts.attn_fwd(q, k, k, torch.tensor([0, 0], device="cuda"), torch.tensor([0, 65], device="cuda"))  # nobody asks
