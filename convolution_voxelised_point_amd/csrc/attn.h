@@ -316,7 +316,10 @@ struct Flag {
   static constexpr bool v = V;
 };
 
-constexpr uint32_t kOutside = 0xc0000000u;  // an offset past every tile: buffer loads give zeros
+// An offset past every tile, for which buffer loads give zeros.  A tile has at most 128
+// rows of at most 2^23 elements (2^24 bytes) between them, so it ends at or before this,
+// and a row's offset (below 127 2^24 + 2^24) added to it stays within 32 bits.
+constexpr uint32_t kOutside = 0x80000000u;
 
 // A wave-uniform address, stated as such (a buffer descriptor is built from it).
 template <typename T>

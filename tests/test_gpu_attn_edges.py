@@ -2,10 +2,12 @@
 library has to be given copies of, starts without rows, rows far apart,
 coordinates far from the origin, the range of fp16, and rows that nothing is
 left of.  The reference and its bounds are those of test_gpu_attn.py."""
+import math
+
 import pytest
 import torch
 
-from test_gpu_attn import starts
+from test_gpu_attn import check, reference, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +59,23 @@ def test_bad_starts_without_query_rows(ts):
         _, dk, dv = ts.attn_bwd(q, q, k, k, q, lse, *args, err_flags=flags)
         assert int(flags) == want and not dk.any() and not dv.any(), (qs, ks)
     ts.attn_fwd(q, k, k, torch.tensor([0, 0], device="cuda"), torch.tensor([0, 65], device="cuda"))  # nobody asks
+
+
+@pytest.mark.parametrize("stride", [(1 << 22) + 8, 1 << 23])
+def test_padded_channels_of_rows_far_apart(ts, stride):
+    """Head widths between 32 and 64 are computed as 64 with zeros beside them, however far apart the rows of a tile are:
+    an infinite key drops itself and no other."""
+    n, d = 120, 40
+    wide = torch.empty((n - 1) * stride + 2 * d, dtype=torch.float16, device="cuda")
+    k, v = (wide[o:].as_strided((n, 1, d), (stride, d, 1)) for o in (0, d))
+    g = torch.Generator("cuda").manual_seed(7)
+    k.copy_(torch.randn(n, 1, d, generator=g, device="cuda"))
+    v.copy_(torch.randn(n, 1, d, generator=g, device="cuda"))
+    q = torch.randn(3, 1, d, generator=g, device="cuda").half().abs() + 0.1
+    k[:20, 0, 1] = -math.inf
+    qs, ks = starts([3]), starts([n])
+    out, lse = ts.attn_fwd(q, k, v, qs, ks)
+    rest, _ = ts.attn_fwd(q, k.clone(), v.clone(), qs, ks)
+    assert torch.isfinite(out).all() and torch.equal(out, rest)
+    ref, tol = reference(q, k[20:], v[20:], [0, 3], [0, n - 20], d ** -0.5)
+    check({"out": out, "lse": lse}, ref, tol, "rows far apart")
