@@ -275,18 +275,15 @@ __device__ __forceinline__ uint32_t late(uint32_t x) {
   return x;
 }
 
-// Distances.  Coordinates are taken relative to one row of the block (floats
-// hold them exactly) with the squared norm beside them: {x, y, z, x^2 + y^2 +
-// z^2}.  While every norm is at most 2048, |a - b|^2 = |a|^2 + |b|^2 - 2 a.b
+// Distances.  Coordinates are taken relative to one row of the block, in integers
+// (so they are exact wherever the set lies, and as floats too while they are below
+// 2^24), with the squared norm beside them: {x, y, z, x^2 + y^2 + z^2}.  While every norm is at most 2048, |a - b|^2 = |a|^2 + |b|^2 - 2 a.b
 // is a sum of integers below 2^24, exact in fp32 in any order, and one
 // v_mfma_f32_16x16x4_f32 gives a 16 x 16 tile of squares: A = the tile row's four
 // values, B = (-2x, -2y, -2z, 1) of the column, C = the column's norm.  Beyond
 // that the differences are formed one by one (the walk's slow form).
 constexpr float kNearNorm = 4194304.f;  // 2048^2
 
-struct Origin {
-  float x, y, z;
-};
 // Coordinates as read (with ndim 2, z is y): turned into floats where they are used,
 // so that the read is not waited for where it is issued.
 struct Place {
@@ -297,13 +294,15 @@ __device__ __forceinline__ Place load_place(const int32_t* c, int64_t row, int n
   return Place{p[0], p[1], p[ndim - 1]};
 }
 // Of a row that is the same on every lane, in scalar registers.
-__device__ __forceinline__ Origin uniform_origin(const Place& p, int ndim) {
-  const auto u = [](int x) { return static_cast<float>(__builtin_amdgcn_readfirstlane(x)); };
-  return Origin{u(p.x), u(p.y), ndim == 3 ? u(p.z) : 0.f};
+__device__ __forceinline__ Place uniform_origin(const Place& p) {
+  const auto u = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  return Place{u(p.x), u(p.y), u(p.z)};
 }
-__device__ __forceinline__ f32x4 relative(const Place& p, const Origin& o, int ndim) {
-  const float x = static_cast<float>(p.x) - o.x, y = static_cast<float>(p.y) - o.y;
-  const float z = ndim == 3 ? static_cast<float>(p.z) - o.z : 0.f;
+__device__ __forceinline__ f32x4 relative(const Place& p, const Place& o, int ndim) {
+  const auto sub = [](int32_t a, int32_t b) {
+    return static_cast<float>(static_cast<int32_t>(static_cast<uint32_t>(a) - static_cast<uint32_t>(b)));
+  };
+  const float x = sub(p.x, o.x), y = sub(p.y, o.y), z = ndim == 3 ? sub(p.z, o.z) : 0.f;
   return f32x4{x, y, z, fmaf(x, x, fmaf(y, y, z * z))};
 }
 // The column's B value of lane (g, c) for the product above.
@@ -377,7 +376,7 @@ struct TileCoords {
     if (r < BN && r < rows) c = load_place(coords, first + r, ndim);
   }
   // The flag of a wave's rows: whether one is too far out for the product form.
-  __device__ __forceinline__ void put(f32x4* tc, uint32_t* far_rows, const Origin& org, int ndim) const {
+  __device__ __forceinline__ void put(f32x4* tc, uint32_t* far_rows, const Place& org, int ndim) const {
     if (threadIdx.x >= BN) return;
     const f32x4 x = relative(c, org, ndim);
     tc[threadIdx.x] = x;
@@ -421,7 +420,7 @@ struct KeyTiles {
              vp + k0 * a.v_stride + h * a.d, last * vs + w, [&](int i) { return ld.row(i) * vs; }, a.d);
     if (BIAS && coords) lc.fetch(a.kc, first + k0, n_keys - k0, a.ndim);
   }
-  __device__ __forceinline__ void put(char* tk, char* tv, bool coords, f32x4* tc, uint32_t* far_rows, const Origin& org,
+  __device__ __forceinline__ void put(char* tk, char* tv, bool coords, f32x4* tc, uint32_t* far_rows, const Place& org,
                                       int ndim) {
     ld.put(tk, tv);
     if (BIAS && coords) lc.put(tc, far_rows, org, ndim);
@@ -456,7 +455,7 @@ struct ColLoad {
 // reads the column's coordinates again (row first + row of c): it is rare, and they
 // would cost registers everywhere else.
 __device__ __forceinline__ f32x4 distances(const f32x4* tc, int r0, float norm, float qb, bool far, int lane,
-                                           const int32_t* c, int64_t first, uint32_t row, int ndim, const Origin& org) {
+                                           const int32_t* c, int64_t first, uint32_t row, int ndim, const Place& org) {
   f32x4 d;
   if (far) {
     const f32x4 p = relative(load_place(c, first + late(row), ndim), org, ndim);

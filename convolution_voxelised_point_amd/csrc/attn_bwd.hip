@@ -96,7 +96,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
     ooff[j] = col.offset(j, a.o_stride, a.d);
   }
   const int width = a.grp * a.d;  // a key-value head's part of a query row
-  Origin org{0.f, 0.f, 0.f};
+  Place org{0, 0, 0};
   Place oraw, qraw[NC];
   if constexpr (BIAS) {
     oraw = load_place(a.qc, st.own0, a.ndim);
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   float slope[NC], qb[NC], qn[NC];
   bool far_cols = false;
   if constexpr (BIAS) {
-    org = uniform_origin(oraw, a.ndim);
+    org = uniform_origin(oraw);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const f32x4 c = relative(qraw[j], org, a.ndim);
@@ -352,7 +352,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
     voff[j] = live[j] ? c * static_cast<uint32_t>(a.v_stride) * 2u : kOutside;
   }
   const bool busy = static_cast<uint32_t>(wave * 16) < cols;
-  Origin org{0.f, 0.f, 0.f};
+  Place org{0, 0, 0};
   Place oraw, kraw[NC];
   if constexpr (BIAS) {
     oraw = load_place(a.kc, st.own0, a.ndim);
@@ -441,7 +441,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
   float kb_[NC], kn[NC];
   bool far_cols = false;
   if constexpr (BIAS) {
-    org = uniform_origin(oraw, a.ndim);
+    org = uniform_origin(oraw);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const f32x4 c = relative(kraw[j], org, a.ndim);

@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_
   const int width = a.grp * a.d;  // a key-value head's part of a query row
   const T* qp = static_cast<const T*>(a.q) + col.query0 * a.q_stride;
   const uint32_t qbytes = col.bytes(a.q_stride, width);
-  Origin org{0.f, 0.f, 0.f};
+  Place org{0, 0, 0};
   Place oraw, qraw[NC];
   if constexpr (BIAS) {
     oraw = load_place(a.qc, st.own0, a.ndim);
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_
   float slope[NC], qb[NC], qn[NC];  // (the last two: for the distances)
   bool far_cols = false;
   if constexpr (BIAS) {
-    org = uniform_origin(oraw, a.ndim);
+    org = uniform_origin(oraw);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const f32x4 c = relative(qraw[j], org, a.ndim);

@@ -543,7 +543,8 @@ ts_status ts_conv_bwd_dgrad_noalloc(const ts_kmap* map, const void* dy, int cout
  *   z_j = z_j - slopes[h] * |c_i - c_j|                (slopes given)
  *   out_i = sum_j softmax(z)_j v_j,    lse[i][h] = log sum_j exp(z_j)
  * |c_i - c_j| is the Euclidean distance of the voxel coordinates (batch column
- * left out), formed in float32.  slopes are constants of the call (no gradient);
+ * left out), formed in float32 from their differences to one row of the set: those
+ * are exact up to 2^24, and have to lie below 2^31.  slopes are constants of the call (no gradient);
  * cap and slopes are optional.  A query row without keys, or whose scores are
  * all -inf, and a query row that no set owns, get zeros, lse = -inf and zero
  * gradients; so do keys that no query of theirs sees.

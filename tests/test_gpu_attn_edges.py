@@ -79,3 +79,23 @@ def test_padded_channels_of_rows_far_apart(ts, stride):
     assert torch.isfinite(out).all() and torch.equal(out, rest)
     ref, tol = reference(q, k[20:], v[20:], [0, 3], [0, n - 20], d ** -0.5)
     check({"out": out, "lse": lse}, ref, tol, "rows far apart")
+
+
+@pytest.mark.parametrize("origin", [1 << 25, -(1 << 30), (1 << 30) - 100])
+def test_coordinates_far_from_the_origin(ts, origin):
+    """A distance depends on the coordinates' differences alone, which are exact."""
+    n, h, d = 150, 2, 32
+    q, k, v, dout = (half(n, h, d, seed=s) for s in range(4))
+    gen = torch.Generator().manual_seed(5)
+    opt = dict(slopes=torch.tensor([0.5, 1.0], device="cuda"))
+    qs = starts([90, 60])
+    for ndim in (2, 3):
+        near = torch.randint(-40, 40, (n, ndim + 1), generator=gen, dtype=torch.int32).cuda()
+        at = near + torch.tensor([0] + [origin] * ndim, dtype=torch.int32, device="cuda")
+        a, b = [], []
+        for c, res in ((near, a), (at, b)):
+            out, lse = ts.attn_fwd(q, k, v, qs, q_coords=c, **opt)
+            res += [out, lse, *ts.attn_bwd(dout, q, k, v, out, lse, qs, q_coords=c, **opt)]
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        ref, tol = reference(q, k, v, [0, 90, 150], [0, 90, 150], d ** -0.5, slopes=opt["slopes"], qc=at, kc=at, dout=dout)
+        check(dict(zip(("out", "lse", "dq", "dk", "dv"), b)), ref, tol, f"origin {origin}")
