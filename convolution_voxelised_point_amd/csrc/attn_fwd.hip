@@ -6,7 +6,7 @@
 // as possible:
 //   - scores are kept in units of log 2 and relative to the column's reference
 //     m, which is folded into the multiply-add that scales them;
-//   - m follows the maximum only when a score passes it by more than kSlack:
+//   - m follows the maximum only when a score passes it by more than a slack:
 //     larger probabilities cost nothing in the 16-bit operand (rounding is
 //     relative) nor in the fp32 sums, and most tiles need neither a maximum
 //     across lanes nor a change of the accumulators;
@@ -27,9 +27,20 @@ namespace ts {
 
 namespace {
 
-// How far a score may pass the reference: probabilities up to 2^kSlack, within
-// fp16's range; in bf16 and fp32 there would be room for far more.
-constexpr float kSlack = 12.f;
+// Where a reference is put, `lift` below the maximum that moves it, and how far a score
+// may pass it, `top`: probabilities up to 2^top.  In fp16 the whole range is used, since
+// what is 2^-24 or less is lost from the product while the sum counts it: a row's largest
+// probability lies between 2^7 and 2^15, so one has to be 2^32 times smaller to be lost,
+// and the maximum may still rise by 2^8 before the reference moves.  (From 1 to 2^12,
+// 500 keys 2^-26 below the largest were a row's error.)  bf16 has fp32's range.
+template <typename T>
+struct Reach {
+  static constexpr float lift = 0.f, top = 12.f;
+};
+template <>
+struct Reach<_Float16> {
+  static constexpr float lift = 7.f, top = 15.f;
+};
 // References up to this fold into the scores: that rounds them to 2^-24 of it.
 constexpr float kFold = 256.f;
 
@@ -193,7 +204,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_
     }
     bool up = false;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) up |= top[j] > kSlack;
+    for (int j = 0; j < NC; ++j) up |= top[j] > Reach<T>::top;
     if (__any(up)) return false;
 #pragma unroll
     for (int u = 0; u < NT / 2; ++u) {
@@ -252,7 +263,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const float t = col_max(top[j]);
-      const float mn = t > m[j] + kSlack ? t : m[j];  // t > -inf when there is no reference
+      const float mn = t > m[j] + Reach<T>::top ? t - Reach<T>::lift : m[j];  // t > -inf when there is no reference
       const float f = m[j] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[j] - mn);
       m[j] = mn;
       l[j] *= f;

@@ -99,3 +99,27 @@ def test_coordinates_far_from_the_origin(ts, origin):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
         ref, tol = reference(q, k, v, [0, 90, 150], [0, 90, 150], d ** -0.5, slopes=opt["slopes"], qc=at, kc=at, dout=dout)
         check(dict(zip(("out", "lse", "dq", "dk", "dv"), b)), ref, tol, f"origin {origin}")
+
+
+@pytest.mark.parametrize("cap", [0.0, 40.0])
+@pytest.mark.parametrize("nq,hk,n", [(1, 1, 500), (100, 2, 400), (1100, 64, 500)])
+def test_small_probabilities_in_fp16(ts, nq, hk, n, cap):
+    """Many keys 2^-26 below a row's largest are a part of its result.  A probability is rounded as an fp16 number once
+    the row's largest is at least 2^7: to 2^-11 of itself, and never by more than 2^-32 of the largest.  (A capped score
+    is good to cap 2^-21.)"""
+    d = 16
+    q = torch.zeros(nq, hk, d, dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 1.0
+    k, v = (torch.zeros(n, hk, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    v[:, :, 1] = 30000.0
+    for at in (0, n // 2, n - 1):
+        k[:, :, 0] = 0.0
+        k[at, :, 0] = 18.09375
+        v[:, :, 1] = 30000.0
+        v[at] = 0.0
+        out, _ = ts.attn_fwd(q, k, v, starts([nq]), starts([n]), scale=1.0, cap=cap)
+        top = cap * math.tanh(18.09375 / cap) if cap else 18.09375
+        small = 30000.0 / (n - 1 + math.exp(top))
+        want = (n - 1) * small
+        bar = want * (2.0 ** -10 + 2.0 ** -18 + cap * 2.0 ** -20) + (n - 1) * 30000.0 * 2.0 ** -32
+        assert float((out[:, :, 1].double() - want).abs().max()) <= bar, (at, float(out[0, 0, 1]), want)
