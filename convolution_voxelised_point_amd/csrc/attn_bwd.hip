@@ -9,7 +9,7 @@
 // are no atomics and the gradients are the same bits on every run.
 //
 // 1 - tanh^2 = 4 r (1 - r) with r = 1 / (exp(2x) + 1); the 4 is taken into the
-// exponent of p (so dv is scaled back by 1/4 when it is written).
+// exponent of p (so dv is scaled back by 1/4 when it is written; in fp16, see kValueScale).
 //
 // Roundings to 16 bits: p for dv and ds for dk once per term.  For dq, ds goes in as
 // two parts, ds and what its rounding left, because delta is formed from an out that
@@ -48,6 +48,17 @@ __device__ __forceinline__ void grad_score(const AttnArgs& a, float s, float bas
     *p = *w = __builtin_amdgcn_exp2f(fmaf(s, a.c1, base));
   }
 }
+
+// What p is multiplied by on its way into dv's product (and dv divided by): fp16 has
+// nothing below 2^-24, and over 100,000 keys p is about 2^-17, so it goes in times 2^15,
+// the most that p = 1 leaves room for; no scale of dout could do that.  bf16 has fp32's
+// range.  (A multiplication per score: 2 x 8192 fp16 rows, 8 / 4 heads of 64, dk and dv
+// 1042 -> 1080 us, windows nothing; scaled and rounded by one mixed-precision
+// instruction each 1085 to 1110.)
+template <typename T>
+constexpr float kValueScale = 1.f;
+template <>
+constexpr float kValueScale<_Float16> = 32768.f;
 
 // What the exponent starts from: -lse in units of log 2, with c2 for a capped
 // score and 2 more where p is to hold the factor 4; rows without a finite score
@@ -485,6 +496,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
         }
       }
     }
+    constexpr float PS = kValueScale<T> == 1.f ? 1.f : kValueScale<T> * (CAP ? 0.25f : 1.f);
     Frag pf[NC], df[NC];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -504,7 +516,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
           float ds = w * dp[j][n][e];
           if constexpr (PART)
             if (r + e >= left) p = ds = 0.f;  // a zero row times an infinite key is NaN
-          pf[j][n * 4 + e] = static_cast<T>(p);
+          pf[j][n * 4 + e] = static_cast<T>(PS == 1.f ? p : p * PS);
           df[j][n * 4 + e] = static_cast<T>(ds);
         }
       }
@@ -521,7 +533,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
     }
   };
 
-  const float vs = CAP ? 0.25f : 1.f;
+  const float vs = kValueScale<T> == 1.f ? (CAP ? 0.25f : 1.f) : 1.f / kValueScale<T>;
   auto finish = [&]() {
 #pragma unroll
     for (int j = 0; j < NC; ++j) {

@@ -123,3 +123,22 @@ def test_small_probabilities_in_fp16(ts, nq, hk, n, cap):
         want = (n - 1) * small
         bar = want * (2.0 ** -10 + 2.0 ** -18 + cap * 2.0 ** -20) + (n - 1) * 30000.0 * 2.0 ** -32
         assert float((out[:, :, 1].double() - want).abs().max()) <= bar, (at, float(out[0, 0, 1]), want)
+
+
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+def test_value_gradients_over_many_keys_in_fp16(ts, cap):
+    """dv = p dout where p lies far below fp16's smallest number (equal scores over 3,000,000 keys): to the result's own
+    rounding and that of p, 2^-11 each; exp2 and lse add less than 2^-18, a capped score cap 2^-21 (and its lse)."""
+    n, d = 3_000_000, 8
+    q, dout = torch.ones(1, 1, d, dtype=torch.float16, device="cuda"), torch.full((1, 1, d), 20000.0, dtype=torch.float16, device="cuda")
+    k = torch.zeros(n, 1, d, dtype=torch.float16, device="cuda")
+    v = torch.ones_like(k)
+    qs, ks = starts([1]), starts([n])
+    out, lse = ts.attn_fwd(q, k, v, qs, ks, cap=cap)
+    _, _, dv = ts.attn_bwd(dout, q, k, v, out, lse, qs, ks, cap=cap)
+    want = 20000.0 / n
+    assert float((dv.double() - want).abs().max()) <= want * (2.0 ** -10 + 2.0 ** -18 + cap * 2.0 ** -20)
+    # one key that takes everything: the largest p there is
+    out, lse = ts.attn_fwd(q, k[:1], v[:1], qs, starts([1]), cap=cap)
+    _, _, dv = ts.attn_bwd(dout, q, k[:1], v[:1], out, lse, qs, starts([1]), cap=cap)
+    assert (dv == 20000.0).all()
