@@ -20,6 +20,15 @@
 // where a row has at most 32 keys (there it matters most: with one key, dq is 0) it
 // is known before ds is needed and taken off for dq as well.
 //
+// A key dropped by a score of -inf has an infinite element, and 0 times that is NaN in
+// the product that forms dq; so is, in dk's, the query of a row whose scores are all
+// -inf.  Looking for them in every tile would cost several per cent of both kernels, so
+// the results are looked at instead: a column that has NaN in it is formed once more by
+// its wave, pair by pair from memory (RowAgain), leaving out what an infinite element
+// would add, and rows without a finite score.  That hides no NaN there should be: an
+// infinite element makes its score infinite or NaN, so its score gradient 0 or NaN, and
+// where one is NaN (or overflows fp16) the column is left as it is.
+//
 // As in the forward pass, a wave owns NC column blocks of 16 and a block takes
 // a.heads key-value heads one after the other; delta enters as the accumulator
 // that dp starts from.
@@ -68,6 +77,150 @@ __device__ __forceinline__ float exp_base(const AttnArgs& a, float lse) {
   return lse == -INFINITY ? -INFINITY : fmaf(-lse, kLog2e, CAP ? a.c2 + 2.f : 0.f);
 }
 
+// The arguments of this kernel (its only parameter), read from where the launch put them:
+// kept from the start of the kernel for RowAgain they would displace others.
+__device__ __forceinline__ AttnArgs read_args() {
+  typedef const __attribute__((address_space(4))) uint64_t* Words;
+  uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  const Words p = (Words)at;
+  struct {
+    uint64_t w[sizeof(AttnArgs) / 8];
+  } copy;
+  static_assert(sizeof(copy) == sizeof(AttnArgs), "whole words");
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(AttnArgs) / 8; ++i) copy.w[i] = p[i];
+  return __builtin_bit_cast(AttnArgs, copy);
+}
+
+// One query row or key formed again by a wave, 64 rows of the other side at a time:
+// first a lane per row for the score gradients, then a lane per channel for the sums.
+// Slow (2 x 8192 rows, 8 / 4 heads of 64, biased: 1.9 ms for the pass, 60 where a set of
+// them has an infinite key), but it takes next to no registers of the walk's.
+template <typename T, int DP, bool CAP, bool BIAS>
+struct RowAgain {
+  static constexpr int W = DP > 64 ? 2 : 1;  // channels of a lane: lane + 64 w
+  const AttnArgs a = read_args();
+  const int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  bool lost = false;  // a score gradient that no 16-bit number holds
+
+  static __device__ __forceinline__ float dot8(const T* x, const T* y, float sum) {
+    typedef T t8 __attribute__((ext_vector_type(8)));
+    const t8 u = *reinterpret_cast<const t8*>(x), v = *reinterpret_cast<const t8*>(y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(static_cast<float>(u[e]), static_cast<float>(v[e]), sum);
+    return sum;
+  }
+  __device__ __forceinline__ const T* row(const void* m, int64_t r, int64_t stride, int head) const {
+    return static_cast<const T*>(m) + r * stride + static_cast<int64_t>(head) * a.d;
+  }
+  // the score gradient of a query row and a key; p as grad_score gives it
+  __device__ __forceinline__ float pair(int64_t query, int head, int64_t key, int h, float lse, float delta, float* p) {
+    const T *q = row(a.q, query, a.q_stride, head), *k = row(a.k, key, a.k_stride, h);
+    const T *g = row(a.dout, query, a.o_stride, head), *v = row(a.v, key, a.v_stride, h);
+    float s = 0.f, dp = -delta, dist = 0.f, slope = 0.f, w;
+#pragma unroll 1
+    for (int c = 0; c < a.d; c += 8) {
+      s = dot8(q + c, k + c, s);
+      dp = dot8(g + c, v + c, dp);
+    }
+    if constexpr (BIAS) {
+      const f32x4 x = relative(load_place(a.qc, query, a.ndim), load_place(a.kc, key, a.ndim), a.ndim);
+      dist = __builtin_amdgcn_sqrtf(x[3]);
+      slope = a.slopes[head] * kLog2e;
+    }
+    grad_score<CAP, BIAS>(a, a.negate ? -s : s, exp_base<CAP>(a, lse), slope, dist, p, &w);
+    const float ds = w * dp;
+    lost |= !(fabsf(static_cast<float>(static_cast<T>(ds))) < INFINITY);
+    return ds;
+  }
+  // sum += f times this lane's channels of a row; any: infinities and NaN too
+  __device__ __forceinline__ void add(const T* x, float f, float (&sum)[W], bool any) const {
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      if (lane + 64 * w < a.d) {
+        const float v = static_cast<float>(x[lane + 64 * w]);
+        sum[w] = fmaf(f, any || fabsf(v) < INFINITY ? v : 0.f, sum[w]);
+      }
+  }
+  // f times the sums to a row of results, or to a split's part
+  __device__ __forceinline__ void put(const float (&sum)[W], float f, T* out, float* part) const {
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      if (lane + 64 * w < a.d) {
+        if (a.splits > 1)
+          part[lane + 64 * w] = sum[w] * f;
+        else
+          out[lane + 64 * w] = static_cast<T>(sum[w] * f);
+      }
+  }
+  static __device__ __forceinline__ float of_lane(float x, int i) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), i));
+  }
+  // dq of packed row r of the set whose queries begin at q0 over n keys from `first`
+  __device__ __forceinline__ void query(int64_t q0, uint32_t r, int h, int64_t first, int n, int split) {
+    const int64_t q = q0 + r / static_cast<uint32_t>(a.grp);
+    const int head = h * a.grp + static_cast<int>(r % static_cast<uint32_t>(a.grp));
+    const float lse = a.lse[q * a.hq + head];
+    const T *g = row(a.dout, q, a.o_stride, head), *o = row(a.o, q, a.o_stride, head);
+    float delta = 0.f, sum[W] = {};
+    if (a.splits == 1)
+      delta = a.delta[q * a.hq + head];  // this wave's, corrected
+    else
+#pragma unroll 1
+      for (int c = 0; c < a.d; c += 8) delta = dot8(g + c, o + c, delta);
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += 64) {
+      float p, ds = 0.f;
+      if (k0 + lane < n) ds = pair(q, head, first + k0 + lane, h, lse, delta, &p);
+      if (__any(lost)) return;
+      const T* k = row(a.k, first + k0, a.k_stride, h);
+      const int rows = n - k0 < 64 ? n - k0 : 64;
+#pragma unroll 1
+      for (int i = 0; i < rows; i += 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // (past the last row ds is 0)
+          add(k + (i + e < rows ? i + e : rows - 1) * a.k_stride, of_lane(ds, i + e), sum, false);
+    }
+    put(sum, a.scale, const_cast<T*>(row(a.dq, q, a.q_stride, head)),
+        a.part + ((static_cast<int64_t>(split) * a.nq + q) * a.hq + head) * DP);
+  }
+  // dk and dv of a key over n packed rows from `beg` of the set whose queries begin at q0
+  __device__ __forceinline__ void key(int64_t k, int h, int64_t q0, uint32_t beg, int n, int split) {
+    const uint32_t grp = a.grp;
+    float dk[W] = {}, dv[W] = {};
+#pragma unroll 1
+    for (int r0 = 0; r0 < n; r0 += 64) {
+      const uint32_t r = beg + r0 + lane;
+      const int64_t q = q0 + r / grp;
+      const int head = h * a.grp + static_cast<int>(r % grp);
+      const float lse = r0 + lane < n ? a.lse[q * a.hq + head] : -INFINITY;
+      float p = 0.f, ds = 0.f;
+      if (lse != -INFINITY) ds = pair(q, head, k, h, lse, a.delta[q * a.hq + head], &p);
+      if (__any(lost)) return;
+#pragma unroll 1
+      for (uint64_t seen = __ballot(lse != -INFINITY); seen != 0; seen &= seen - 1) {
+        const int i = __ffsll(static_cast<unsigned long long>(seen)) - 1;
+        const uint32_t ri = beg + r0 + i, qi = ri / grp;
+        const int hi = h * a.grp + static_cast<int>(ri - qi * grp);
+        add(row(a.q, q0 + qi, a.q_stride, hi), of_lane(ds, i), dk, false);
+        add(row(a.dout, q0 + qi, a.o_stride, hi), of_lane(p, i), dv, true);
+      }
+    }
+    const int64_t rows = a.nk * a.hk;
+    float* part = a.part + (static_cast<int64_t>(split) * rows + k * a.hk + h) * DP;
+    put(dk, a.scale, const_cast<T*>(row(a.dk, k, a.k_stride, h)), part);
+    put(dv, CAP ? 0.25f : 1.f, const_cast<T*>(row(a.dv, k, a.v_stride, h)), part + a.splits * rows * DP);
+  }
+};
+
+// The columns (of the 16 lanes share) in which some lane has a value that is not a number.
+__device__ __forceinline__ uint64_t nan_columns(float sum, bool live) {
+  uint64_t m = __ballot(live && sum != sum);
+  m |= m >> 32;
+  return (m | m >> 16) & 0xffffu;
+}
+
 template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS>
 __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_attn_dq(const AttnArgs a) {
   typedef typename AMfma<T>::frag Frag;
@@ -96,8 +249,10 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   // NC 2: not held as uniform, or both forms of a step are scheduled as one and their
   // registers do not fit (2 x 8192 rows, dk and dv: 1225 against 1020 us, dq 1010 / 945)
   const int n_keys = static_cast<int>(NC == 2 ? late(kend - kbeg) : kend - kbeg);
-  int h = blockIdx.y * a.heads;
+  const int h0 = blockIdx.y * a.heads;
+  int h = h0;
   const int h_end = !MULTI ? h + 1 : h + a.heads < a.hk ? h + a.heads : a.hk;
+  uint64_t again = 0;  // columns to form again: 16 bits for each head (at most 4) or column block
 
   const QueryCols<NC, KS> col(a, st, BM);
   uint32_t qoff[NC], ooff[NC];
@@ -259,9 +414,20 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
     }
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < DI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += dq[j][i][e];
+      again |= nan_columns(sum, col.live[j] && base[j] != -INFINITY) << (16 * (MULTI ? h - h0 : j));
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
       if (!col.live[j]) continue;
       const int64_t query = col.query0 + late(col.dq[j]);
       const int head = h * a.grp + static_cast<int>(late(col.place[j]));
+      const bool none = base[j] == -INFINITY;  // no finite score
+      if (none) rho[j] = delta[j] = 0.f;  // (its dout may be anything)
       if (g == 0) {
         // rho: what delta was short of
         if (split == 0) a.delta[query * a.hq + head] = a.splits == 1 ? delta[j] + rho[j] : delta[j];
@@ -273,7 +439,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
       for (int i = 0; i < DI; ++i) {
         f32x4 y = dq[j][i];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] *= a.scale;
+        for (int e = 0; e < 4; ++e) y[e] = none ? 0.f : y[e] * a.scale;
         if (a.splits > 1)
           *reinterpret_cast<f32x4*>(part + i * 16 + g * 4) = y;
         else
@@ -320,6 +486,13 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
     if (MULTI && wrap) begin();
     keys.put(tk[b ^ 1], tv[b ^ 1], true, tc[b ^ 1], far_rows[b ^ 1], org, a.ndim);
   }
+  if (again == 0) return;
+  __threadfence();  // the columns as first written
+  for (; again != 0; again &= again - 1) {
+    const int bit = __ffsll(static_cast<unsigned long long>(again)) - 1, c = bit & 15, u = bit >> 4;
+    const uint32_t r = static_cast<uint32_t>(st.row0) + (KS ? 0 : (MULTI ? 0 : u * 4) + wave) * 16 + c;
+    RowAgain<T, DP, CAP, BIAS>().query(st.own0, r, MULTI ? h0 + u : h0, keys.first, n_keys, split);
+  }
 }
 
 template <typename T, int DP, int NC, bool CAP, bool BIAS>
@@ -345,8 +518,10 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4;
   const int n_rows = static_cast<int>(NC == 2 ? late(rend - rbeg) : rend - rbeg);  // see k_attn_dq
-  int h = blockIdx.y * a.heads;
+  const int h0 = blockIdx.y * a.heads;
+  int h = h0;
   const int h_end = !MULTI ? h + 1 : h + a.heads < a.hk ? h + a.heads : a.hk;
+  uint64_t again = 0;  // see k_attn_dq
   const int width = a.grp * a.d;
 
   // columns: keys
@@ -537,6 +712,15 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
   auto finish = [&]() {
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < DI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += dk[j][i][e] + dv[j][i][e];
+      again |= nan_columns(sum, live[j]) << (16 * (MULTI ? h - h0 : j));
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
       if (!live[j]) continue;
       const int64_t key = key0 + late(ck[j]), rows = a.nk * a.hk;
       T* kd = static_cast<T*>(a.dk) + key * a.k_stride + static_cast<int64_t>(h) * a.d;
@@ -595,6 +779,13 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
     r0 = rn;
     if (MULTI && wrap) begin();
     put(b ^ 1);
+  }
+  if (again == 0) return;
+  __threadfence();
+  for (; again != 0; again &= again - 1) {
+    const int bit = __ffsll(static_cast<unsigned long long>(again)) - 1, c = bit & 15, u = bit >> 4;
+    RowAgain<T, DP, CAP, BIAS>().key(key0 + ((MULTI ? 0 : u * 4) + wave) * 16 + c, MULTI ? h0 + u : h0, st.st0,
+                                     static_cast<uint32_t>(rbeg), n_rows, split);
   }
 }
 

@@ -547,7 +547,10 @@ ts_status ts_conv_bwd_dgrad_noalloc(const ts_kmap* map, const void* dy, int cout
  * are exact up to 2^24, and have to lie below 2^31.  slopes are constants of the call (no gradient);
  * cap and slopes are optional.  A query row without keys, or whose scores are
  * all -inf, and a query row that no set owns, get zeros, lse = -inf and zero
- * gradients; so do keys that no query of theirs sees.
+ * gradients, and add nothing to others, whatever their dout holds; so do keys that
+ * no query of theirs sees.  An infinite element of q or k makes its score infinite
+ * and adds nothing to the gradients where that drops the key (z = -inf) or
+ * saturates the cap; other infinities and NaN carry on as in the formulas.
  *
  * Starts that decrease or leave [0, nq] / [0, nk] raise TS_FLAG_RANGE in
  * err_flags (may be NULL): no access leaves the buffers, the results are

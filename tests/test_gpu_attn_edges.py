@@ -142,3 +142,75 @@ def test_value_gradients_over_many_keys_in_fp16(ts, cap):
     out, lse = ts.attn_fwd(q, k[:1], v[:1], qs, starts([1]), cap=cap)
     _, _, dv = ts.attn_bwd(dout, q, k[:1], v[:1], out, lse, qs, starts([1]), cap=cap)
     assert (dv == 20000.0).all()
+
+
+# query rows, keys, hq, hk, d: the waves share the keys; one column block a wave; two
+FORMS = [(3, 40, 1, 1, 16), (3, 2000, 4, 2, 40), (70, 90, 4, 2, 32), (130, 200, 2, 1, 128), (1100, 700, 64, 64, 16)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("nq,nk,hq,hk,d", FORMS, ids=str)
+def test_gradients_with_infinite_keys_and_queries(ts, nq, nk, hq, hk, d, dtype):
+    """Keys dropped by scores of -inf leave the gradients of the rest as if they were not there, and a row whose scores are
+    all -inf has none, whatever its q and dout hold."""
+    scale = d ** -0.5
+    q, dout = half(nq, hq, d, seed=1, dtype=dtype), half(nq, hq, d, seed=2, dtype=dtype)
+    k, v = half(nk, hk, d, seed=3, dtype=dtype), half(nk, hk, d, seed=4, dtype=dtype)
+    q[:, :, 0] = q[:, :, 0].abs() + 0.1
+    kept = torch.arange(nk) % 3 != 1
+    kept[nk // 2:] &= torch.arange(nk // 2, nk) % 7 != 0
+    k[~kept.cuda(), :, 0] = -math.inf
+    qs, ks = starts([nq]), starts([nk])
+    out, lse = ts.attn_fwd(q, k, v, qs, ks)
+    dq, dk, dv = ts.attn_bwd(dout, q, k, v, out, lse, qs, ks)
+    kn, vn = k[kept.cuda()].contiguous(), v[kept.cuda()].contiguous()
+    ref, tol = reference(q, kn, vn, [0, nq], [0, int(kept.sum())], scale, dout=dout, dtype=dtype)
+    got = {"out": out, "lse": lse, "dq": dq, "dk": dk[kept.cuda()], "dv": dv[kept.cuda()]}
+    check(got, ref, tol, "dropped keys")
+    assert (dk[~kept.cuda()] == 0).all() and (dv[~kept.cuda()] == 0).all()
+    # rows that see nothing
+    k, lost = kn, torch.arange(nq) % 2 == 0
+    k[:, :, 0] = k[:, :, 0].abs() + 0.1
+    q[lost.cuda(), :, 0] = -math.inf
+    q[lost.cuda(), :, 1] = 0.0
+    k[:, :, 2:] = 0.0
+    q[lost.cuda(), :, 2:] = 0.0
+    dout[lost.cuda()] = math.nan
+    n2 = k.shape[0]
+    ks = starts([n2])
+    out, lse = ts.attn_fwd(q, k, vn, qs, ks)
+    dq, dk, dv = ts.attn_bwd(dout, q, k, vn, out, lse, qs, ks)
+    assert (out[lost.cuda()] == 0).all() and (lse[lost.cuda()] == -math.inf).all() and (dq[lost.cuda()] == 0).all()
+    seen = ~lost.cuda()
+    ref, tol = reference(q[seen], k, vn, [0, int(seen.sum())], [0, n2], scale, dout=dout[seen], dtype=dtype)
+    got = {"out": out[seen], "lse": lse[seen], "dq": dq[seen], "dk": dk, "dv": dv}
+    check(got, ref, tol, "rows without scores")
+
+
+def test_infinite_keys_between_sets_and_heads(ts):
+    """Head after head in one block, sets with and without dropped keys: as each set by itself."""
+    n, h, d, m = 1100, 4, 32, 40
+    q, k, v, dout = (half(n * m, h, d, seed=s) for s in range(4))
+    q[:, :, 0] = q[:, :, 0].abs() + 0.1
+    k[7 * m + 3, 1, 0] = -math.inf   # set 7, the second head
+    k[9 * m + 30, :, 0] = -math.inf  # set 9, every head
+    qs = starts([m] * n)
+    out, lse = ts.attn_fwd(q, k, v, qs)
+    whole = (out, lse, *ts.attn_bwd(dout, q, k, v, out, lse, qs))
+    assert all(torch.isfinite(t).all() for t in whole)
+    clean = k.clone()
+    clean[clean.isinf()] = 0.0
+    out, lse = ts.attn_fwd(q, clean, v, qs)
+    plain = (out, lse, *ts.attn_bwd(dout, q, clean, v, out, lse, qs))
+    rest = [i for i in range(n * m) if i // m not in (7, 9)]
+    for a, b in zip(whole, plain):
+        assert torch.equal(a[rest], b[rest])
+        assert torch.equal(a[7 * m:8 * m, [0, 2, 3]], b[7 * m:8 * m, [0, 2, 3]])
+    for s, drop in ((7, 3), (9, 30)):
+        rows = slice(s * m, s * m + m)
+        keep = [i for i in range(m) if i != drop]
+        ref, tol = reference(q[rows], k[rows][keep], v[rows][keep], [0, m], [0, m - 1], d ** -0.5, dout=dout[rows])
+        heads = [1] if s == 7 else [0, 1, 2, 3]
+        got = dict(zip(("out", "lse", "dq", "dk", "dv"), (t[rows][keep] if i > 2 else t[rows] for i, t in enumerate(whole))))
+        for name in got:
+            check({name: got[name][:, heads]}, {name: ref[name][:, heads]}, {name: tol[name][:, heads]}, f"set {s}")
