@@ -3,7 +3,9 @@
 // 6, 1), kept as the byte e; a value is the integer clamp(rint(x / quantum),
 // -127, 127), half to even.  A power-of-two quantum makes both directions
 // exact but for that one rounding: x / quantum is a change of exponent, and
-// an integer of 7 bits times the quantum is a value of every feature type.
+// an integer of 7 bits times the quantum is an fp32 and a bf16 number, and an fp16
+// number too where x was one.  (Of other values fp16's range may lack some: above
+// 65504 they are read as infinity, and bits below 2^-24 are rounded off.)
 // A block that holds an infinity or a NaN keeps byte 255 and stands for NaN.
 //
 // Threads work on 8 consecutive channels; the 4 threads of a block are 4

@@ -18,8 +18,8 @@
 // step.
 //
 // x may also come in 8 bits (act8.h): the staging threads of x then read 8 codes
-// and their block's byte per row and turn them into 16-bit values, exactly, on
-// the way to LDS; nothing else differs.  That form takes channel counts in
+// and their block's byte per row and turn them into 16-bit values (act8.h) on the way to
+// LDS; nothing else differs.  That form takes channel counts in
 // multiples of 8 and halves the bytes gathered from x.
 #include "act8.h"
 #include "common.h"
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(256, 2) void k_wgrad_mfma(const int32_t* __restrict
         act8_decode(ux2{in[r][0], in[r][1]}, act8_quantum(in[r][2]), f);
         Frag t;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = static_cast<T>(f[e]);  // exact
+        for (int e = 0; e < 8; ++e) t[e] = static_cast<T>(f[e]);
         in[r] = __builtin_bit_cast(u32x4, t);
       }
     }
@@ -337,8 +337,9 @@ __global__ __launch_bounds__(256) void k_wgrad_fma(const int32_t* __restrict__ c
     const int64_t i = dbg_req(pair_in[p], n_x, TS_DEBUG_SRC_ROW);
     float xv;
     if constexpr (ACT8)
-      xv = static_cast<float>(x8.codes[i * cin + ci]) *
-           act8_quantum(x8.scales[i * ceil_div(cin, kActBlock) + ci / kActBlock]);
+      // as a T: what the other forms multiply, and what unpacking gives
+      xv = static_cast<float>(static_cast<T>(static_cast<float>(x8.codes[i * cin + ci]) *
+                                             act8_quantum(x8.scales[i * ceil_div(cin, kActBlock) + ci / kActBlock])));
     else
       xv = static_cast<float>(x[i * cin + ci]);
     acc = fmaf(xv,

@@ -867,7 +867,8 @@ def act_pack(x: torch.Tensor, stream=None) -> Act8:
 
 
 def act_unpack(a: Act8, dtype: torch.dtype, stream=None) -> torch.Tensor:
-    """The values `a` stands for; exact in every feature type."""
+    """The values `a` stands for, in `dtype`: exact in fp32, bf16 and the type they
+    were packed from; in fp16 from another one rounded where its range ends."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return act_unpack(a, dtype)

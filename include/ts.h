@@ -608,8 +608,10 @@ ts_status ts_attn_bwd(const ts_attn* at, const void* q, const void* k, const voi
  * kept as the byte e; a value is held as clamp(rint(x / quantum), -127, 127)
  * (half to even), so it is off by at most quantum (max|x| / 64; half of it below
  * 127 quanta).  A power of two costs up to one bit against max|x| / 127, and
- * makes the held value exactly representable in every feature type: reading a
- * checkpoint back never rounds.  A block that holds an infinity or a NaN gets
+ * makes the held value exactly representable in fp32, in bf16 and in the type x
+ * was packed from: reading it back there never rounds.  Read in fp16 from another
+ * type, or from ts_norm_fwd's y8, a value is rounded like any float: to infinity
+ * above 65504, to a multiple of 2^-24 below 2^-14.  A block that holds an infinity or a NaN gets
  * byte 255 and reads back as NaN, so an overflow is not hidden. */
 #define TS_ACT8_BLOCK 32
 typedef struct ts_act8 {
@@ -625,7 +627,7 @@ ts_status ts_act_unpack(const ts_act8* a, int64_t n, int c, void* x, ts_dtype dt
 
 /* ts_conv_bwd_wgrad with x read from a checkpoint (n_in rows of cin channels):
  * dy in dtype (fp16 or bf16; TS_F32 is TS_ERR_UNSUPPORTED), dw fp32, the same
- * sums as over the unpacked x.  ws holds ts_conv_wgrad_act8_workspace_bytes. */
+ * sums as over x unpacked in dtype.  ws holds ts_conv_wgrad_act8_workspace_bytes. */
 size_t ts_conv_wgrad_act8_workspace_bytes(const ts_kmap* map, int cin, int cout);
 ts_status ts_conv_bwd_wgrad_act8(const ts_kmap* map, const ts_act8* x, int cin, const void* dy, int cout,
                                  ts_dtype dtype, float* dw, void* ws, size_t ws_bytes, hipStream_t stream);
