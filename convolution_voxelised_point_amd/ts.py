@@ -788,15 +788,44 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch.
     return out, lse
 
 
+def _laid_out_like(*tensors: torch.Tensor) -> list:
+    """New tensors [n][heads][d] with the rows of the given ones; columns of one
+    matrix where those are."""
+    new, groups = [None] * len(tensors), {}
+    for i, t in enumerate(tensors):
+        n, h, d = t.shape
+        if n < 2 or t.stride(0) == h * d:
+            new[i] = torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
+        else:
+            groups.setdefault((n, t.stride(0), t.untyped_storage().data_ptr()), []).append((t.storage_offset(), i))
+    for (n, stride, _), columns in groups.items():
+        columns.sort()
+        while columns:
+            # as many as follow each other within a row
+            first, _ = columns[0]
+            end, taken = first, 0
+            for at, i in columns:
+                width = tensors[i].shape[1] * tensors[i].shape[2]
+                if at < end or at + width > first + stride:
+                    break
+                end, taken = at + width, taken + 1
+            t = tensors[columns[0][1]]
+            whole = torch.empty((n - 1) * stride + end - first, dtype=t.dtype, device=t.device)
+            for at, i in columns[:taken]:
+                new[i] = whole.as_strided(tensors[i].shape, tensors[i].stride(), at - first)
+            columns = columns[taken:]
+    return new
+
+
 def attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
              lse: torch.Tensor, q_starts: torch.Tensor, k_starts: Optional[torch.Tensor] = None,
              scale: Optional[float] = None, cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
              q_coords: Optional[torch.Tensor] = None, k_coords: Optional[torch.Tensor] = None,
              err_flags: Optional[torch.Tensor] = None, stream=None,
              into: Optional[Sequence[torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    """(dq, dk, dv) of attn_fwd with the same arguments, laid out like q, k, v.
-    They are written to the three tensors of `into`, say the columns of one
-    matrix, or to new ones."""
+    """(dq, dk, dv) of attn_fwd with the same arguments, laid out like q, k, v:
+    where those are columns of one matrix, so are the gradients.  They are
+    written to the three tensors of `into`, or to new ones."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return attn_bwd(dout, q, k, v, out, lse, q_starts, k_starts, scale, cap, slopes, q_coords, k_coords, err_flags,
@@ -818,8 +847,7 @@ def attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
         for g, t in zip(into, like))), "attention: dq, dk, dv are laid out like q, k, v")
     # their own buffers where q, k or v was copied or the library could not write there
     direct = into is not None and all(_aligned(g) is g and t is l for g, t, l in zip(into, (q, k, v), like))
-    dq, dk, dv = into if direct else [torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
-                                      for t in (q, k, v)]
+    dq, dk, dv = into if direct else _laid_out_like(q, k, v)
     n = _lib_attn_workspace_bytes(ref, 1)
     ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
     _check(_lib_attn_bwd(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),

@@ -214,3 +214,27 @@ def test_infinite_keys_between_sets_and_heads(ts):
         got = dict(zip(("out", "lse", "dq", "dk", "dv"), (t[rows][keep] if i > 2 else t[rows] for i, t in enumerate(whole))))
         for name in got:
             check({name: got[name][:, heads]}, {name: ref[name][:, heads]}, {name: tol[name][:, heads]}, f"set {s}")
+
+
+def test_gradients_of_columns_take_one_matrix(ts):
+    """Operands that are columns of one matrix get gradients that are columns of one, no larger than it."""
+    n, hq, hk, d = 200, 4, 2, 32
+    qs = starts([120, 80])
+    dout = half(n, hq, d, seed=1)
+    heads = lambda t, *w: t.view(n, -1, d).split(w, dim=1)  # noqa: E731
+    m = half(n, (hq + 2 * hk) * d, seed=2)
+    q, k, v = heads(m, hq, hk, hk)
+    out, lse = ts.attn_fwd(q, k, v, qs)
+    want = ts.attn_bwd(dout, q.contiguous(), k.contiguous(), v.contiguous(), out, lse, qs)
+    for tensors, bytes_ in (((q, k, v), m.nbytes),
+                            ((q.contiguous(), k, v), q.nbytes + m.nbytes),
+                            ((q.contiguous(), k.contiguous(), v.contiguous()), q.nbytes + 2 * k.nbytes)):
+        got = ts.attn_bwd(dout, *tensors, out, lse, qs)
+        assert all(torch.equal(a, b) and a.stride() == t.stride() for a, b, t in zip(got, want, tensors))
+        held = {t.untyped_storage().data_ptr(): t.untyped_storage().nbytes() for t in got}
+        assert sum(held.values()) <= bytes_
+    # the same keys as values, and columns that overlap: apart
+    out, lse = ts.attn_fwd(q, k, k, qs)
+    _, dk, dv = ts.attn_bwd(dout, q, k, k, out, lse, qs)
+    _, dk2, dv2 = ts.attn_bwd(dout, q, k, k.clone(), out, lse, qs)
+    assert torch.equal(dk, dk2) and torch.equal(dv, dv2) and not torch.equal(dk, dv)
