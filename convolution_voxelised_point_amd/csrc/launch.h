@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "attn_plan.h"
 #include "ts.h"
 
 namespace ts {
@@ -125,7 +126,6 @@ hipError_t launch_wgrad(const ts_kmap* map, const void* x, int cin, const void* 
 
 // attn_fwd.hip, attn_bwd.hip
 struct AttnArgs;
-constexpr int kAttnMaxSplits = 512;
 // Up to this many splits are joined by a thread per 4 elements instead of a block per
 // row: 131k rows of 4 splits 14 us instead of 134, 2.6k rows of 3 splits 4.1 instead of 5.3.
 constexpr int kAttnFewSplits = 8;
@@ -140,13 +140,6 @@ constexpr int attn_waves_dq(int dp, int nc, bool cap, bool bias, bool share_keys
 constexpr int attn_waves_dkv(int dp, int nc, bool bias) {
   return dp == 128 ? 1 : dp == 32 && nc == 1 ? 3 : 2;
 }
-// How a walk is cut up: columns per block, column blocks per wave, key-value heads
-// per block, parts of the other side, and whether the waves of a block share one
-// column block.
-struct AttnPlan {
-  int bm, nc, heads, splits;
-  bool share_keys;
-};
 // Rows of 16-bit heads copied to another stride and head width (zeros beyond the source's).
 hipError_t launch_attn_repack(const void* src, int64_t src_stride, int src_d, void* dst, int64_t dst_stride, int dst_d,
                               int64_t n, int heads, hipStream_t s);
