@@ -49,6 +49,7 @@ ts_status check_attn(const ts_attn* at) {
 }
 
 AttnPlan plan_fwd(const ts_attn* at) { return ts::plan_fwd(at->nq, at->nk, at->n_sets, at->hq, at->hk, at->d); }
+AttnPlan plan_dq(const ts_attn* at) { return ts::plan_dq(at->nq, at->nk, at->n_sets, at->hq, at->hk, at->d); }
 AttnPlan plan_dkv(const ts_attn* at) { return ts::plan_dkv(at->nq, at->nk, at->n_sets, at->hq, at->hk, at->d); }
 
 size_t part_floats(const ts_attn* at, const AttnPlan& p, int64_t rows, int extra) {
@@ -78,7 +79,7 @@ size_t fwd_bytes(const ts_attn* at) {
 // q, out, dout, dq; k, v, dk, dv
 size_t delta_bytes(const ts_attn* at) { return align_up(static_cast<size_t>(at->nq) * at->hq * 4, 256); }
 size_t bwd_bytes(const ts_attn* at) {
-  const size_t q = part_floats(at, plan_fwd(at), at->nq * at->hq, 1);
+  const size_t q = part_floats(at, plan_dq(at), at->nq * at->hq, 1);
   const size_t k = 2 * part_floats(at, plan_dkv(at), at->nk * at->hk, 0);
   return (repacks(at) ? 4 * q_copy_bytes(at) + 4 * k_copy_bytes(at) : 0) + delta_bytes(at) + (q > k ? q : k) * 4;
 }
@@ -206,7 +207,7 @@ ts_status ts_attn_bwd(const ts_attn* at, const void* q, const void* k, const voi
     return TS_ERR_INVALID_ARG;
   const size_t need = bwd_bytes(at);
   if (need > 0 && (!ws || ws_bytes < need || !at16(ws))) return TS_ERR_INVALID_ARG;
-  const AttnPlan pq = plan_fwd(at), pk = plan_dkv(at);
+  const AttnPlan pq = plan_dq(at), pk = plan_dkv(at);
   if (!grid_ok(at, pq, at->nq, at->hq / at->hk) || !grid_ok(at, pk, at->nk, 1)) return TS_ERR_UNSUPPORTED;
   AttnArgs a = attn_args(at, q, k, v, err_flags);
   a.o = out;

@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   constexpr int BN = KS ? 128 : 64, NT = KS ? 2 : 4, BM = KS ? 16 : 64 * NC;
   constexpr int TB = BN * DP * 2;
   constexpr bool MULTI = NC == 1 && !KS && DP <= 64;
-  static_assert(!KS || NC == 1, "one column block when the waves share the keys");
+  static_assert(!KS || (NC == 1 && DP <= 64), "one column block of at most 64 channels when the waves share the keys");
   __shared__ __attribute__((aligned(16))) char tk[2][TB], tv[2][TB];
   __shared__ f32x4 tc[2][BIAS ? BN : 1];
   __shared__ uint32_t far_rows[2][2];
@@ -836,8 +836,8 @@ void run_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t s)
     a.tiles = attn_tiles(a.nq, a.grp, pq.bm, a.n_sets);
     a.splits = pq.splits;
     a.heads = pq.heads;
-    if (pq.share_keys)
-      run_dq<T, DP, 1, CAP, BIAS, true>(a, s);
+    if (DP <= 64 && pq.share_keys)
+      run_dq<T, DP, 1, CAP, BIAS, DP <= 64>(a, s);
     else if (DP <= 64 && pq.nc == 2)
       run_dq<T, DP, DP <= 64 ? 2 : 1, CAP, BIAS, false>(a, s);
     else

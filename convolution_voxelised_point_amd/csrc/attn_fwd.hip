@@ -63,7 +63,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_
   constexpr int BM = KS ? 16 : 64 * NC;
   constexpr int TB = BN * DP * 2;
   constexpr bool MULTI = NC == 1 && !KS && DP <= 64;  // a.heads may be more than 1
-  static_assert(!KS || NC == 1, "one column block when the waves share the keys");
+  static_assert(!KS || (NC == 1 && DP <= 64), "one column block of at most 64 channels when the waves share the keys");
   __shared__ __attribute__((aligned(16))) char tk[2][TB], tv[2][TB];
   constexpr int TCS = MULTI ? kCoordTiles : 2;
   __shared__ f32x4 tc[TCS][BIAS ? BN : 1];
@@ -506,8 +506,8 @@ void run_fwd(AttnArgs& a, const AttnPlan& p, bool cap, hipStream_t s) {
   a.tiles = attn_tiles(a.nq, a.grp, p.bm, a.n_sets);
   a.splits = p.splits;
   a.heads = p.heads;
-  if (p.share_keys)
-    run_fwd<T, DP, 1, true>(a, cap, s);
+  if (DP <= 64 && p.share_keys)
+    run_fwd<T, DP, 1, DP <= 64>(a, cap, s);
   else if (DP <= 64 && p.nc == 2)
     run_fwd<T, DP, DP <= 64 ? 2 : 1, false>(a, cap, s);
   else

@@ -19,21 +19,32 @@ inline int64_t parts(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
 inline int padded_width(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
 
+enum class Walk { kForward, kDq, kDkv };
+
 // How the walk over `other` rows for `own` rows (both counted over all sets,
 // the heads that share a key head included) is cut up:
-//   - up to 16 rows a set: the waves of a block share the keys (attn_fwd.hip);
+//   - up to 16 rows a set, of at most 64 channels: the waves of a block may share the keys
+//     (attn_fwd.hip).  Forward where there are so few sets and heads that every block is
+//     waited for: 4 in all, 8 at 32 channels (us, shared / not: one query of 2 key heads
+//     over 10,000 keys of 64 channels 9.1 / 10.9, of 8 over 100,000 of 32 38 / 44, of 64
+//     53 / 47; 16 sets of 20,000 keys of 32 33 / 30; 2000 sets of 12 rows of 64 107 / 32).
+//     dq from 128 keys a set on (500 sets of 60 keys of 64 channels 31 / 25, of 150 38 / 40,
+//     of 500 57 / 81; of 32 channels 19 / 15, 23 / 22, 42 / 44).  At 128 channels it lost
+//     everywhere (one query over 100,000 keys 29 / 21 forward, 30 / 26 dq) and is not built;
 //   - long sets, with enough blocks for every CU: two column blocks a wave (2 x 8192
-//     rows, dk and dv: 1030 us, with one 1325);
+//     rows of 64 channels, dk and dv: 1030 us, with one 1325; of 32 850 / 916, dq 877 / 950,
+//     forward 559 / 638);
 //   - short walks: a block takes several heads one after the other (2400 windows: forward
 //     161 us, with one head a block 191; dq 226 / 252; dk and dv 266 / 304).
-inline AttnPlan plan_walk(int64_t own, int64_t other, int64_t n_sets, int hk, int dp, bool may_share, int max_nc) {
+inline AttnPlan plan_walk(int64_t own, int64_t other, int64_t n_sets, int hk, int dp, Walk walk) {
   AttnPlan p{64, 1, 1, 1, false};
   const int64_t sets = n_sets > 0 ? n_sets : 1;
   const int64_t own_per = parts(own, sets), other_per = other / sets;
-  if (may_share && own_per <= 16) {
+  const bool few = walk == Walk::kForward ? n_sets * hk <= (dp == 32 ? 8 : 4) : walk == Walk::kDq && other_per >= 128;
+  if (own_per <= 16 && few && dp <= 64) {
     p.share_keys = true;
     p.bm = 16;
-  } else if (max_nc >= 2 && own_per >= 512 && parts(own, 128) * hk >= 256) {
+  } else if (dp <= 64 && own_per >= 512 && parts(own, 128) * hk >= 256) {
     p.nc = 2;
     p.bm = 128;
   } else if (dp <= 64 && other_per <= 512) {
@@ -61,12 +72,13 @@ inline AttnPlan plan_walk(int64_t own, int64_t other, int64_t n_sets, int hk, in
 
 // Query rows walk over keys (forward, dq); keys walk over query rows (dk and dv).
 inline AttnPlan plan_fwd(int64_t nq, int64_t nk, int64_t n_sets, int hq, int hk, int d) {
-  const int dp = padded_width(d);
-  return plan_walk(nq * (hq / hk), nk, n_sets, hk, dp, true, dp <= 64 ? 2 : 1);
+  return plan_walk(nq * (hq / hk), nk, n_sets, hk, padded_width(d), Walk::kForward);
+}
+inline AttnPlan plan_dq(int64_t nq, int64_t nk, int64_t n_sets, int hq, int hk, int d) {
+  return plan_walk(nq * (hq / hk), nk, n_sets, hk, padded_width(d), Walk::kDq);
 }
 inline AttnPlan plan_dkv(int64_t nq, int64_t nk, int64_t n_sets, int hq, int hk, int d) {
-  const int dp = padded_width(d);
-  return plan_walk(nk, nq * (hq / hk), n_sets, hk, dp, false, dp <= 64 ? 2 : 1);
+  return plan_walk(nk, nq * (hq / hk), n_sets, hk, padded_width(d), Walk::kDkv);
 }
 
 }  // namespace ts

@@ -132,10 +132,10 @@ constexpr int kAttnFewSplits = 8;
 // Waves per SIMD that the registers of a kernel of this shape allow without spilling
 // (windows of 32 channels: forward 5 against 4 waves 164 / 174 us, dq 4 against 3 230 / 252).
 constexpr int attn_waves_fwd(int dp, int nc, bool cap, bool bias, bool share_keys) {
-  return share_keys ? (dp == 128 ? 1 : 2) : nc == 2 || dp == 128 ? 2 : dp == 64 ? (bias ? 2 : 3) : cap && bias ? 4 : 5;
+  return share_keys || nc == 2 || dp == 128 ? 2 : dp == 64 ? (bias ? 2 : 3) : cap && bias ? 4 : 5;
 }
 constexpr int attn_waves_dq(int dp, int nc, bool cap, bool bias, bool share_keys) {
-  return share_keys ? (dp == 128 ? 1 : 2) : nc == 2 || dp >= 64 || (cap && bias) ? 2 : 4;
+  return share_keys || nc == 2 || dp >= 64 || (cap && bias) ? 2 : 4;
 }
 constexpr int attn_waves_dkv(int dp, int nc, bool bias) {
   return dp == 128 ? 1 : dp == 32 && nc == 1 ? 3 : 2;

@@ -1,7 +1,7 @@
 """Attention calls for each way the library cuts up its work: the call, and the
 plan it is there for, (column blocks per wave, key-value heads per block,
-splits, waves share the keys), of the walk over keys (forward, dq) and of the
-walk over query rows (dk, dv)."""
+splits, waves share the keys), of the walks over keys (forward and dq, one plan
+where they have the same) and of the walk over query rows (dk, dv)."""
 
 def ragged(sets, low, high, long=0, length=0):
     """Lengths that step through [low, high], every 9th set empty, `long` sets of `length` among them."""
@@ -11,7 +11,7 @@ def ragged(sets, low, high, long=0, length=0):
     return n
 
 
-# name, dtype, query lengths, key lengths (None: the same rows), hq, hk, d, cap, bias, plan over keys, plan over rows
+# name, dtype, query lengths, key lengths (None: the same rows), hq, hk, d, cap, bias, plan over keys (or those of forward and dq), plan over rows
 FORMS = [
     # one head after the other in a block: the last group whole and not, sets of one tile, of several whose coordinates
     # stay in LDS and of more than four that are read again, shared heads
@@ -27,5 +27,8 @@ FORMS = [
     # one column block and split walks, either way; waves that share the keys, split
     ("one_split", "f16", [40], [2100], 4, 2, 128, 0.0, True, (1, 1, 8, False), (1, 1, 1, False)),
     ("rows_split", "bf16", [2000], [40], 4, 2, 32, 3.0, True, (1, 1, 1, False), (1, 1, 15, False)),
+    ("share_forward", "f16", [2, 1, 0, 3], [90, 17, 30, 60], 4, 2, 24, 0.0, True, ((1, 1, 1, True), (1, 1, 1, False)), (1, 1, 1, False)),
+    ("share_dq", "bf16", ragged(40, 1, 9), ragged(40, 100, 300), 6, 3, 64, 5.0, True, ((1, 1, 1, False), (1, 1, 1, True)), (1, 1, 1, False)),
+    ("short_sets", "f16", ragged(700, 1, 14), None, 4, 4, 64, 0.0, True, (1, 2, 1, False), (1, 2, 1, False)),
     ("share_split", "bf16", [3, 2], [2600, 700], 4, 2, 64, 0.0, True, (1, 1, 6, True), (1, 1, 1, False)),
 ]
