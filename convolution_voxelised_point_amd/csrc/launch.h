@@ -129,13 +129,24 @@ struct AttnArgs;
 // Up to this many splits are joined by a thread per 4 elements instead of a block per
 // row: 131k rows of 4 splits 14 us instead of 134, 2.6k rows of 3 splits 4.1 instead of 5.3.
 constexpr int kAttnFewSplits = 8;
-// Waves per SIMD that the registers of a kernel of this shape allow without spilling
-// (windows of 32 channels: forward 5 against 4 waves 164 / 174 us, dq 4 against 3 230 / 252).
+// Waves per SIMD that the registers of each kernel are held to.  Measured with one more
+// and one fewer (us: as chosen / more / fewer; * spills to scratch memory):
+//   forward, 32 channels: 2400 windows, cap and bias 187 / 190 / 194, bias 164 / * / 174;
+//     64: 1200 windows, bias 117 / 124 / 126; 2 x 8192 rows (two column blocks) with cap and
+//     bias 700 / 732* / 737, without 326 / 324 / 368; at 32 560 / 560 / 637;
+//     128: 1200 windows, bias 236 / 252 / 249
+//   dq, 32: windows, cap and bias 291 / 300 / 371, bias 230 / 252* / 252, none 170 / 188* / 170;
+//     64: windows, bias 206 / 220* / 200, cap 156 / - / 184; 2 x 8192 rows 1041 / 2074* / 1140;
+//     at 32 877 / 841* / 955; 128: windows 338 / 600 / 597
+//   dk and dv, 32: windows, bias 270 / 298* / -, cap and bias 297 / 287* / 292; 2 x 8192 rows 849 /
+//     887* / 938; 64: windows 216 / 259* / 220, 2 x 8192 rows 1058 / 2600* / 1585; 128: windows
+//     673 / 1167* (one is the least).
+// Sharing the keys, a kernel's LDS holds it to two.
 constexpr int attn_waves_fwd(int dp, int nc, bool cap, bool bias, bool share_keys) {
   return share_keys || nc == 2 || dp == 128 ? 2 : dp == 64 ? (bias ? 2 : 3) : cap && bias ? 4 : 5;
 }
 constexpr int attn_waves_dq(int dp, int nc, bool cap, bool bias, bool share_keys) {
-  return share_keys || nc == 2 || dp >= 64 || (cap && bias) ? 2 : 4;
+  return share_keys || nc == 2 || dp == 128 || (cap && bias) ? 2 : dp == 64 ? (bias ? 2 : 3) : 4;
 }
 constexpr int attn_waves_dkv(int dp, int nc, bool bias) {
   return dp == 128 ? 1 : dp == 32 && nc == 1 ? 3 : 2;
