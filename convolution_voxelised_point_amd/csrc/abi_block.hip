@@ -76,10 +76,13 @@ size_t fwd_bytes(const ts_attn* at) {
          part_floats(at, plan_fwd(at), at->nq * at->hq, 2) * 4;
 }
 
+// floats beside a row's part of dq where it is mended
+int mend_width(const ts_attn* at) { return mends_dq(at->d, at->nq * at->hq) ? padded_width(at->d) : 0; }
+
 // q, out, dout, dq; k, v, dk, dv
 size_t delta_bytes(const ts_attn* at) { return align_up(static_cast<size_t>(at->nq) * at->hq * 4, 256); }
 size_t bwd_bytes(const ts_attn* at) {
-  const size_t q = part_floats(at, plan_dq(at), at->nq * at->hq, 1);
+  const size_t q = part_floats(at, plan_dq(at), at->nq * at->hq, 1 + mend_width(at));
   const size_t k = 2 * part_floats(at, plan_dkv(at), at->nk * at->hk, 0);
   return (repacks(at) ? 4 * q_copy_bytes(at) + 4 * k_copy_bytes(at) : 0) + delta_bytes(at) + (q > k ? q : k) * 4;
 }
@@ -138,6 +141,8 @@ AttnArgs attn_args(const ts_attn* at, const void* q, const void* k, const void* 
   a.ndim = at->ndim;
   a.scale = at->scale;
   a.negate = at->scale < 0.f;
+  a.two = few_rows(at->nq * at->hq);
+  a.mend = mends_dq(at->d, at->nq * at->hq);
   if (at->cap > 0.f) {
     a.c1 = cap_factor(at);
     a.c2 = at->cap * kLog2e;
@@ -232,7 +237,7 @@ ts_status ts_attn_bwd(const ts_attn* at, const void* q, const void* k, const voi
   }
   a.delta = static_cast<float*>(c.take(delta_bytes(at)));
   a.part = static_cast<float*>(c.take(0));
-  a.part_ml = a.part + static_cast<size_t>(pq.splits) * at->nq * at->hq * padded_width(at->d);
+  a.part_ml = a.part + static_cast<size_t>(pq.splits) * at->nq * at->hq * (padded_width(at->d) + mend_width(at));
   TS_TRY(launch_attn_bwd(a, pq, pk, at->dtype, at->cap > 0.f, stream));
   if (repacks(at)) {
     TS_TRY(copy_out(at, a.dq, at->hq, at->nq, dq, at->q_stride, stream));

@@ -154,6 +154,8 @@ struct AttnArgs {
   // and negate says that q enters with its sign turned
   float c1, c2, scale;
   bool negate;
+  bool two;    // 16-bit operands made of probabilities and score gradients go in as two parts
+  bool mend;   // dq: what delta was short of is taken off at the end (attn_bwd.hip)
 };
 
 // Rows of set i, counted with an empty-keyed set before the first and after

@@ -11,14 +11,20 @@
 // 1 - tanh^2 = 4 r (1 - r) with r = 1 / (exp(2x) + 1); the 4 is taken into the
 // exponent of p (so dv is scaled back by 1/4 when it is written; in fp16, see kValueScale).
 //
-// Roundings to 16 bits: p for dv and ds for dk once per term.  For dq, ds goes in as
-// two parts, ds and what its rounding left, because delta is formed from an out that
-// is rounded already: that error and one rounding of ds together made dq 1.6 to 1.8
-// times as far from the exact one as its own last rounding does (now 1.2 to 1.45; the
-// second product costs 12 % of this kernel).  The sum of p (dp - delta) over a row is
-// 0 in exact arithmetic: what it comes to is added to the delta that dk uses, and
-// where a row has at most 32 keys (there it matters most: with one key, dq is 0) it
-// is known before ds is needed and taken off for dq as well.
+// Roundings to 16 bits.  p for dv and ds for dk once per term: both are 1.4 times as far
+// from 64 bits as their last rounding alone.  dq would be 1.2 to 1.7 times as far off with
+// ds in two parts (ds, and what its rounding left) and up to 5 times where few keys
+// matter, because delta is formed from an out that is rounded already.  The sum of
+// p (dp - delta) over a row is 0 in exact arithmetic: what it comes to, rho, is what delta
+// was short of.  dk uses delta + rho.  For dq the sum of w k (ds = w (dp - delta)) is
+// formed beside that of ds k, and rho times it taken off at the end (MEND; by k_attn_sum
+// where the walk is split); where a row has at most 32 keys rho is known before ds is
+// needed and taken off there.  Two parts and MEND: 1.0 (2400 windows of 32 channels,
+// biased, 280 us, without MEND 237; of 16 channels 235 / 194; 1200 of 64 202 / 207).
+//   - Two column blocks of 64 channels have registers for one part and MEND only: 1.45
+//     (2 x 8192 rows 920 us, two parts without MEND 1016).
+//   - Heads wider than 64 have them for two parts only: 1.05 to 1.35.
+//   - Calls of few rows (attn_plan.h) have all of it, dk and dv of two parts too: 1.0.
 //
 // A key dropped by a score of -inf has an infinite element, and 0 times that is NaN in
 // the product that forms dq; so is, in dk's, the query of a row whose scores are all
@@ -34,9 +40,11 @@
 // that dp starts from.
 //
 // Bound by vector instructions, as the forward pass, and with two to four waves per
-// SIMD by the latency of LDS reads and matrix results.  Measured: 2 x 8192 rows, 8
-// query and 4 key heads of 64, cap and bias: dq 1013 us, dk and dv 1030 (NC 1: 1274 and
-// 1325); 2400 windows of about 127 rows, 4 heads of 32, biased: dq 230, dk and dv 270.
+// SIMD by the latency of LDS reads and matrix results.  Measured (by the profiler, as
+// every time beside a kernel here: twelve calls after a pause; long runs are 10 to 15 %
+// faster): 2 x 8192 rows, 8 query and 4 key heads of 64, cap and bias: dq 930 us, dk and
+// dv 1020 (NC 1: 1274 and 1325); 2400 windows of about 127 rows, 4 heads of 32, biased:
+// dq 280, dk and dv 270.
 #include "attn.h"
 
 namespace ts {
@@ -182,8 +190,12 @@ struct RowAgain {
         for (int e = 0; e < 4; ++e)  // (past the last row ds is 0)
           add(k + (i + e < rows ? i + e : rows - 1) * a.k_stride, of_lane(ds, i + e), sum, false);
     }
-    put(sum, a.scale, const_cast<T*>(row(a.dq, q, a.q_stride, head)),
-        a.part + ((static_cast<int64_t>(split) * a.nq + q) * a.hq + head) * DP);
+    float* part = a.part + ((static_cast<int64_t>(split) * a.nq + q) * a.hq + head) * DP;
+    put(sum, a.scale, const_cast<T*>(row(a.dq, q, a.q_stride, head)), part);
+    if (a.mend && a.splits > 1)  // nothing to take off
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (lane + 64 * w < a.d) part[a.splits * a.nq * a.hq * DP + lane + 64 * w] = 0.f;
   }
   // dk and dv of a key over n packed rows from `beg` of the set whose queries begin at q0
   __device__ __forceinline__ void key(int64_t k, int h, int64_t q0, uint32_t beg, int n, int split) {
@@ -221,13 +233,14 @@ __device__ __forceinline__ uint64_t nan_columns(float sum, bool live) {
   return (m | m >> 16) & 0xffffu;
 }
 
-template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS>
-__global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_attn_dq(const AttnArgs a) {
+template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS, bool MEND>
+__global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS, MEND)) void k_attn_dq(const AttnArgs a) {
   typedef typename AMfma<T>::frag Frag;
   constexpr int KB = DP / 32, DI = DP / 16;
   constexpr int BN = KS ? 128 : 64, NT = KS ? 2 : 4, BM = KS ? 16 : 64 * NC;
   constexpr int TB = BN * DP * 2;
   constexpr bool MULTI = NC == 1 && !KS && DP <= 64;
+  constexpr bool REST = !(NC == 2 && DP == 64);  // ds in two parts
   static_assert(!KS || (NC == 1 && DP <= 64), "one column block of at most 64 channels when the waves share the keys");
   __shared__ __attribute__((aligned(16))) char tk[2][TB], tv[2][TB];
   __shared__ f32x4 tc[2][BIAS ? BN : 1];
@@ -247,7 +260,8 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
   const int kt0 = KS ? wave * 32 : 0;
   // NC 2: not held as uniform, or both forms of a step are scheduled as one and their
-  // registers do not fit (2 x 8192 rows, dk and dv: 1225 against 1020 us, dq 1010 / 945)
+  // registers do not fit (2 x 8192 rows, dk and dv: 1225 against 1020 us; dq, where the gain
+  // was first seen, 1010 / 945 before it had MEND)
   const int n_keys = static_cast<int>(NC == 2 ? late(kend - kbeg) : kend - kbeg);
   const int h0 = blockIdx.y * a.heads;
   int h = h0;
@@ -303,7 +317,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
 
   const f32x4 zero{0.f, 0.f, 0.f, 0.f};
   Frag qf[NC][KB], gf[NC][KB];
-  f32x4 dq[NC][DI];
+  f32x4 dq[NC][DI], pk[NC][MEND ? DI : 1];  // pk: sum of w k, ds = w dp
   float base[NC], delta[NC], rho[NC];
   const float rho_scale = CAP ? 0.25f : 1.f;
   const bool whole = a.splits == 1 && kend - kbeg <= 32;  // one step sees the whole row
@@ -324,7 +338,10 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
       if constexpr (BIAS) slope[j] = next_slope[j] * kLog2e;
       rho[j] = 0.f;
 #pragma unroll
-      for (int i = 0; i < DI; ++i) dq[j][i] = zero;
+      for (int i = 0; i < DI; ++i) {
+        dq[j][i] = zero;
+        if constexpr (MEND) pk[j][i] = zero;
+      }
     }
   };
 
@@ -344,10 +361,10 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
           dp[j][n] = AMfma<T>::run(fv, gf[j][kb], kb == 0 ? f32x4{-delta[j], -delta[j], -delta[j], -delta[j]} : dp[j][n]);
         }
       }
-    Frag df[NC], dr[NC];
+    Frag df[NC], dr[REST ? NC : 1], wf[MEND ? NC : 1];
     auto split = [&](int j, int e, float ds) {
       df[j][e] = static_cast<T>(ds);
-      dr[j][e] = static_cast<T>(ds - static_cast<float>(df[j][e]));
+      if constexpr (REST) dr[j][e] = static_cast<T>(ds - static_cast<float>(df[j][e]));
     };
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -364,6 +381,7 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
           if constexpr (PART)
             if (u * 32 + n * 16 + 4 * g + e >= left) p = w = 0.f;
           rho[j] = fmaf(p, dp[j][n][e], rho[j]);
+          if constexpr (MEND) wf[j][n * 4 + e] = static_cast<T>(w);
           if constexpr (PART)
             s[j][n][e] = w;
           else
@@ -384,22 +402,64 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
     for (int i = 0; i < DI; ++i) {
       const Frag f = tile_frag_t<T, DP>(tk[b], kt0 + u * 32, i, lane);
 #pragma unroll
-      for (int j = 0; j < NC; ++j) dq[j][i] = AMfma<T>::run(f, dr[j], AMfma<T>::run(f, df[j], dq[j][i]));
+      for (int j = 0; j < NC; ++j) {
+        dq[j][i] = AMfma<T>::run(f, df[j], dq[j][i]);
+        if constexpr (REST) dq[j][i] = AMfma<T>::run(f, dr[j], dq[j][i]);
+        if constexpr (MEND) pk[j][i] = AMfma<T>::run(f, wf[j], pk[j][i]);
+      }
     }
+  };
+
+  // dq with what delta was short of taken off: known here if the walk is not split
+  auto mend = [&](int j, float short_of) {
+    if constexpr (MEND)
+      if (a.splits == 1 && !whole)
+#pragma unroll
+        for (int i = 0; i < DI; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dq[j][i][e] = fmaf(-short_of, pk[j][i][e], dq[j][i][e]);
   };
 
   auto finish = [&]() {
 #pragma unroll
-    for (int j = 0; j < NC; ++j) rho[j] = col_sum(rho[j]) * rho_scale;
+    for (int j = 0; j < NC; ++j) {
+      rho[j] = col_sum(rho[j]) * rho_scale;
+      if constexpr (!KS) mend(j, rho[j]);
+    }
     if constexpr (KS) {
       float* jo = reinterpret_cast<float*>(tv);  // [4][16][DP]
       float* jr = reinterpret_cast<float*>(tk);  // [4][16]
       __syncthreads();
       if (g == 0) jr[wave * 16 + lane] = rho[0];
+      if constexpr (MEND) {
+        __syncthreads();
+        float all = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) all += jr[x * 16 + (lane & 15)];
+        mend(0, all);
+      }
 #pragma unroll
       for (int i = 0; i < DI; ++i)
         *reinterpret_cast<f32x4*>(jo + (wave * 16 + (lane & 15)) * DP + i * 16 + g * 4) = dq[0][i];
       __syncthreads();
+      if constexpr (MEND)
+        if (a.splits > 1) {  // the same of pk, and so to both parts
+          float* jp = reinterpret_cast<float*>(tk) + 64;
+#pragma unroll
+          for (int i = 0; i < DI; ++i)
+            *reinterpret_cast<f32x4*>(jp + (wave * 16 + (lane & 15)) * DP + i * 16 + g * 4) = pk[0][i];
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < DI; ++i) {
+            pk[0][i] = zero;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const f32x4 y = *reinterpret_cast<const f32x4*>(jp + (x * 16 + (lane & 15)) * DP + i * 16 + g * 4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) pk[0][i][e] += y[e];
+            }
+          }
+        }
       if (wave != 0) return;
 #pragma unroll
       for (int x = 1; x < 4; ++x) rho[0] += jr[x * 16 + (lane & 15)];
@@ -418,7 +478,10 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
 #pragma unroll
       for (int i = 0; i < DI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum += dq[j][i][e];
+        for (int e = 0; e < 4; ++e) {
+          sum += dq[j][i][e];
+          if constexpr (MEND) sum += pk[j][i][e];
+        }
       again |= nan_columns(sum, col.live[j] && base[j] != -INFINITY) << (16 * (MULTI ? h - h0 : j));
     }
 #pragma unroll
@@ -440,6 +503,13 @@ __global__ __launch_bounds__(256, attn_waves_dq(DP, NC, CAP, BIAS, KS)) void k_a
         f32x4 y = dq[j][i];
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = none ? 0.f : y[e] * a.scale;
+        if constexpr (MEND)
+          if (a.splits > 1) {
+            f32x4 x = pk[j][i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = none ? 0.f : x[e] * a.scale;
+            *reinterpret_cast<f32x4*>(part + a.splits * a.nq * a.hq * DP + i * 16 + g * 4) = x;
+          }
         if (a.splits > 1)
           *reinterpret_cast<f32x4*>(part + i * 16 + g * 4) = y;
         else
@@ -673,6 +743,18 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
     }
     constexpr float PS = kValueScale<T> == 1.f ? 1.f : kValueScale<T> * (CAP ? 0.25f : 1.f);
     Frag pf[NC], df[NC];
+    auto gather = [&]() {
+#pragma unroll
+      for (int i = 0; i < DI; ++i) {
+        const Frag fg = tile_frag_t<T, DP>(tg[b], u * 32, i, lane);
+        const Frag fq = tile_frag_t<T, DP>(tq[b], u * 32, i, lane);
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          dv[j][i] = AMfma<T>::run(fg, pf[j], dv[j][i]);
+          dk[j][i] = AMfma<T>::run(fq, df[j], dk[j][i]);
+        }
+      }
+    };
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int r = u * 32 + n * 16 + 4 * g;
@@ -691,21 +773,28 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
           float ds = w * dp[j][n][e];
           if constexpr (PART)
             if (r + e >= left) p = ds = 0.f;  // a zero row times an infinite key is NaN
-          pf[j][n * 4 + e] = static_cast<T>(PS == 1.f ? p : p * PS);
+          if constexpr (PS != 1.f) p *= PS;
+          pf[j][n * 4 + e] = static_cast<T>(p);
           df[j][n * 4 + e] = static_cast<T>(ds);
+          if constexpr (PART && NC == 1) {
+            s[j][n][e] = p;
+            dp[j][n][e] = ds;
+          }
         }
       }
     }
+    gather();
+    if constexpr (PART && NC == 1)
+      if (a.two) {  // and what the roundings left
 #pragma unroll
-    for (int i = 0; i < DI; ++i) {
-      const Frag fg = tile_frag_t<T, DP>(tg[b], u * 32, i, lane);
-      const Frag fq = tile_frag_t<T, DP>(tq[b], u * 32, i, lane);
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        dv[j][i] = AMfma<T>::run(fg, pf[j], dv[j][i]);
-        dk[j][i] = AMfma<T>::run(fq, df[j], dk[j][i]);
+          for (int e = 0; e < 4; ++e) {
+            pf[0][n * 4 + e] = static_cast<T>(s[0][n][e] - static_cast<float>(pf[0][n * 4 + e]));
+            df[0][n * 4 + e] = static_cast<T>(dp[0][n][e] - static_cast<float>(df[0][n * 4 + e]));
+          }
+        gather();
       }
-    }
   };
 
   const float vs = kValueScale<T> == 1.f ? (CAP ? 0.25f : 1.f) : 1.f / kValueScale<T>;
@@ -767,7 +856,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
 #pragma unroll
       for (int u = 0; u < BN / 32; ++u) {
         if (u * 32 >= left) continue;
-        if (u * 32 + 32 <= left && !far)
+        if (u * 32 + 32 <= left && !far && !(NC == 1 && a.two))
           step(Flag<false>{}, b, u, left, false);
         else
           step(Flag<true>{}, b, u, left, far);
@@ -794,7 +883,7 @@ __global__ __launch_bounds__(256, attn_waves_dkv(DP, NC, BIAS)) void k_attn_dkv(
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void k_attn_sum(const float* __restrict__ part, int64_t rows, int splits, int heads,
                                                   int d, T* out, int64_t stride, const float* __restrict__ short_of,
-                                                  float* delta) {
+                                                  float* delta, const float* __restrict__ pk) {
   constexpr int Q = DP / 4;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = i / Q;
   const int d0 = static_cast<int>(i % Q) * 4;
@@ -805,6 +894,18 @@ __global__ __launch_bounds__(256) void k_attn_sum(const float* __restrict__ part
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] += v[e];
   }
+  if (pk) {  // dq: delta was short of this sum
+    f32x4 x{0.f, 0.f, 0.f, 0.f};
+    float rho = 0.f;
+    for (int s = 0; s < splits; ++s) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(pk + (s * rows + row) * DP + d0);
+      rho += short_of[s * rows + row];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] += v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = fmaf(-rho, x[e], y[e]);
+  }
   const int64_t n = row / heads;
   store4(out + n * stride + (row - n * heads) * d, d0, d, y);
   if (delta && d0 == 0) {
@@ -814,16 +915,62 @@ __global__ __launch_bounds__(256) void k_attn_sum(const float* __restrict__ part
   }
 }
 
+// The same for many splits, a block per row: the splits in shares, joined in order.
 template <typename T, int DP>
-void run_sum(const float* part, int64_t rows, int splits, int heads, const AttnArgs& a, void* out, int64_t stride,
-             float* delta, hipStream_t s) {
-  k_attn_sum<T, DP><<<static_cast<unsigned>(ceil_div<int64_t>(rows * (DP / 4), 256)), 256, 0, s>>>(
-      part, rows, splits, heads, a.d, static_cast<T*>(out), stride, a.part_ml, delta);
+__global__ __launch_bounds__(256) void k_attn_sum_many(const float* __restrict__ part, int64_t rows, int splits,
+                                                       int heads, int d, T* out, int64_t stride,
+                                                       const float* __restrict__ short_of, float* delta,
+                                                       const float* __restrict__ pk) {
+  constexpr int Q = DP / 4, SH = 256 / Q;
+  __shared__ f32x4 acc[2][SH][Q];
+  __shared__ float red[4];
+  const int64_t row = blockIdx.x;
+  const int d4 = threadIdx.x % Q, sh = threadIdx.x / Q;
+  f32x4 y{0.f, 0.f, 0.f, 0.f}, x = y;
+  float rho = 0.f;
+#pragma unroll 4
+  for (int s = sh; s < splits; s += SH) {
+    const int64_t at = (s * rows + row) * DP + d4 * 4;
+    y += *reinterpret_cast<const f32x4*>(part + at);
+    if (pk) x += *reinterpret_cast<const f32x4*>(pk + at);
+  }
+  if (delta)
+    for (int s = threadIdx.x; s < splits; s += 256) rho += short_of[s * rows + row];
+#pragma unroll
+  for (int i = 32; i > 0; i >>= 1) rho += __shfl_xor(rho, i);
+  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = rho;
+  acc[0][sh][d4] = y;
+  acc[1][sh][d4] = x;
+  __syncthreads();
+  if (sh != 0) return;
+  rho = (red[0] + red[1]) + (red[2] + red[3]);
+#pragma unroll
+  for (int i = 1; i < SH; ++i) {
+    y += acc[0][i][d4];
+    x += acc[1][i][d4];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = fmaf(-rho, x[e], y[e]);
+  const int64_t n = row / heads;
+  store4(out + n * stride + (row - n * heads) * d, d4 * 4, d, y);
+  if (delta && d4 == 0) delta[row] += rho;
 }
 
-template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS>
+template <typename T, int DP>
+void run_sum(const float* part, int64_t rows, int splits, int heads, const AttnArgs& a, void* out, int64_t stride,
+             float* delta, const float* pk, hipStream_t s) {
+  if (splits > kAttnFewSplits)  // (few rows then)
+    k_attn_sum_many<T, DP><<<static_cast<unsigned>(rows), 256, 0, s>>>(part, rows, splits, heads, a.d, static_cast<T*>(out),
+                                                                       stride, a.part_ml, delta, pk);
+  else
+    k_attn_sum<T, DP><<<static_cast<unsigned>(ceil_div<int64_t>(rows * (DP / 4), 256)), 256, 0, s>>>(
+      part, rows, splits, heads, a.d, static_cast<T*>(out), stride, a.part_ml, delta, pk);
+}
+
+template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS, bool MEND>
 void run_dq(const AttnArgs& a, hipStream_t s) {
-  k_attn_dq<T, DP, NC, CAP, BIAS, KS><<<dim3(attn_grid_x(a.tiles), ceil_div(a.hk, a.heads), a.splits), 256, 0, s>>>(a);
+  k_attn_dq<T, DP, NC, CAP, BIAS, KS, MEND>
+      <<<dim3(attn_grid_x(a.tiles), ceil_div(a.hk, a.heads), a.splits), 256, 0, s>>>(a);
 }
 template <typename T, int DP, int NC, bool CAP, bool BIAS>
 void run_dkv(const AttnArgs& a, hipStream_t s) {
@@ -836,13 +983,21 @@ void run_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t s)
     a.tiles = attn_tiles(a.nq, a.grp, pq.bm, a.n_sets);
     a.splits = pq.splits;
     a.heads = pq.heads;
-    if (DP <= 64 && pq.share_keys)
-      run_dq<T, DP, 1, CAP, BIAS, DP <= 64>(a, s);
-    else if (DP <= 64 && pq.nc == 2)
-      run_dq<T, DP, DP <= 64 ? 2 : 1, CAP, BIAS, false>(a, s);
-    else
-      run_dq<T, DP, 1, CAP, BIAS, false>(a, s);
-    if (a.splits > 1) run_sum<T, DP>(a.part, a.nq * a.hq, a.splits, a.hq, a, a.dq, a.q_stride, a.delta, s);
+    if constexpr (DP == 128) {
+      if (a.mend)
+        run_dq<T, DP, 1, CAP, BIAS, false, true>(a, s);
+      else
+        run_dq<T, DP, 1, CAP, BIAS, false, false>(a, s);
+    } else if (pq.share_keys) {
+      run_dq<T, DP, 1, CAP, BIAS, true, true>(a, s);
+    } else if (pq.nc == 2) {
+      run_dq<T, DP, 2, CAP, BIAS, false, true>(a, s);
+    } else {
+      run_dq<T, DP, 1, CAP, BIAS, false, true>(a, s);
+    }
+    if (a.splits > 1)
+      run_sum<T, DP>(a.part, a.nq * a.hq, a.splits, a.hq, a, a.dq, a.q_stride, a.delta,
+                     a.mend ? a.part + a.splits * a.nq * a.hq * DP : nullptr, s);
   }
   if (a.nk == 0) return;
   a.tiles = attn_tiles(a.nk, 1, pk.bm, a.n_sets);
@@ -854,8 +1009,8 @@ void run_bwd(AttnArgs& a, const AttnPlan& pq, const AttnPlan& pk, hipStream_t s)
     run_dkv<T, DP, 1, CAP, BIAS>(a, s);
   if (a.splits > 1) {
     const int64_t rows = a.nk * a.hk;
-    run_sum<T, DP>(a.part, rows, a.splits, a.hk, a, a.dk, a.k_stride, nullptr, s);
-    run_sum<T, DP>(a.part + a.splits * rows * DP, rows, a.splits, a.hk, a, a.dv, a.v_stride, nullptr, s);
+    run_sum<T, DP>(a.part, rows, a.splits, a.hk, a, a.dk, a.k_stride, nullptr, nullptr, s);
+    run_sum<T, DP>(a.part + a.splits * rows * DP, rows, a.splits, a.hk, a, a.dv, a.v_stride, nullptr, nullptr, s);
   }
 }
 

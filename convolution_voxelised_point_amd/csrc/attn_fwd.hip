@@ -16,6 +16,10 @@
 // accurate form where z and m are large: folding -m in rounds to m's precision.)  With
 // the slow form alone 4 x 4096 capped rows take 354 us instead of 282, 2 x 8192 capped
 // and biased ones 785 instead of 662.
+// Probabilities are rounded to 16 bits for their product with the values (out is 1.05 to
+// 1.41 times as far from 64 bits as its last rounding alone); calls of few rows (TWO,
+// attn_plan.h) take what the rounding left as a second operand (1.0; one query over
+// 102,835 keys 18.1 -> 18.7 us).
 // Rows without a finite score give zeros and lse = -inf.
 //
 // Measured (fp16 or bf16, whole calls): 4 sets of 4096, 8 heads of 64, capped 239 us
@@ -54,8 +58,8 @@ constexpr float kFold = 256.f;
 // over (head, tile): for short sets, finding the set and the first reads would
 // cost more than a head's work, and the next head's rows are read while this one's
 // last tile is computed.
-template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS>
-__global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_attn_fwd(const AttnArgs a) {
+template <typename T, int DP, int NC, bool CAP, bool BIAS, bool KS, bool TWO>
+__global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, TWO)) void k_attn_fwd(const AttnArgs a) {
   typedef typename AMfma<T>::frag Frag;
   constexpr int KB = DP / 32, DI = DP / 16;
   constexpr int BN = KS ? 128 : 64;  // keys per tile
@@ -63,7 +67,7 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_
   constexpr int BM = KS ? 16 : 64 * NC;
   constexpr int TB = BN * DP * 2;
   constexpr bool MULTI = NC == 1 && !KS && DP <= 64;  // a.heads may be more than 1
-  static_assert(!KS || (NC == 1 && DP <= 64), "one column block of at most 64 channels when the waves share the keys");
+  static_assert(!KS || (NC == 1 && DP <= 64 && TWO), "one column block of at most 64 channels, few rows when the waves share the keys");
   __shared__ __attribute__((aligned(16))) char tk[2][TB], tv[2][TB];
   constexpr int TCS = MULTI ? kCoordTiles : 2;
   __shared__ f32x4 tc[TCS][BIAS ? BN : 1];
@@ -178,6 +182,16 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_
     }
   };
 
+  // the same of what rounding the probabilities s to p left
+  auto gather_rest = [&](int b, int u, const f32x4(&s)[NC][NT], Frag(&p)[NC]) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        p[j][e] = static_cast<T>(s[j][2 * u + (e >> 2)][e & 3] - static_cast<float>(p[j][e]));
+    gather(b, u, p);
+  };
+
   // A whole tile against references that hold; false (and nothing changed) if one does not.
   auto fast = [&](int b) {
     f32x4 s[NC][NT];
@@ -216,8 +230,10 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_
           const float x = __builtin_amdgcn_exp2f(s[j][2 * u + (e >> 2)][e & 3]);
           l[j] += x;  // unrounded: the backward pass needs lse to fp32
           p[j][e] = static_cast<T>(x);
+          if constexpr (TWO) s[j][2 * u + (e >> 2)][e & 3] = x;
         }
       gather(b, u, p);
+      if constexpr (TWO) gather_rest(b, u, s, p);
     }
     return true;
   };
@@ -286,9 +302,11 @@ __global__ __launch_bounds__(256, attn_waves_fwd(DP, NC, CAP, BIAS, KS)) void k_
           const float x = __builtin_amdgcn_exp2f(s[j][2 * u + (e >> 2)][e & 3] - ms);
           l[j] += x;
           p[j][e] = static_cast<T>(x);
+          if constexpr (TWO) s[j][2 * u + (e >> 2)][e & 3] = x;
         }
       }
       gather(b, u, p);
+      if constexpr (TWO) gather_rest(b, u, s, p);
     }
   };
 
@@ -487,18 +505,18 @@ __global__ __launch_bounds__(256) void k_attn_join_few(const AttnArgs a) {
   if (d0 == 0) a.lse[row] = lt == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(lt)) * kLn2;
 }
 
-template <typename T, int DP, int NC, bool KS>
+template <typename T, int DP, int NC, bool KS, bool TWO>
 void run_fwd(const AttnArgs& a, bool cap, hipStream_t s) {
   const dim3 grid(attn_grid_x(a.tiles), ceil_div(a.hk, a.heads), a.splits);
   const bool bias = a.slopes != nullptr;
   if (cap && bias)
-    k_attn_fwd<T, DP, NC, true, true, KS><<<grid, 256, 0, s>>>(a);
+    k_attn_fwd<T, DP, NC, true, true, KS, TWO><<<grid, 256, 0, s>>>(a);
   else if (cap)
-    k_attn_fwd<T, DP, NC, true, false, KS><<<grid, 256, 0, s>>>(a);
+    k_attn_fwd<T, DP, NC, true, false, KS, TWO><<<grid, 256, 0, s>>>(a);
   else if (bias)
-    k_attn_fwd<T, DP, NC, false, true, KS><<<grid, 256, 0, s>>>(a);
+    k_attn_fwd<T, DP, NC, false, true, KS, TWO><<<grid, 256, 0, s>>>(a);
   else
-    k_attn_fwd<T, DP, NC, false, false, KS><<<grid, 256, 0, s>>>(a);
+    k_attn_fwd<T, DP, NC, false, false, KS, TWO><<<grid, 256, 0, s>>>(a);
 }
 
 template <typename T, int DP>
@@ -507,11 +525,13 @@ void run_fwd(AttnArgs& a, const AttnPlan& p, bool cap, hipStream_t s) {
   a.splits = p.splits;
   a.heads = p.heads;
   if (DP <= 64 && p.share_keys)
-    run_fwd<T, DP, 1, DP <= 64>(a, cap, s);
+    run_fwd<T, DP, 1, DP <= 64, true>(a, cap, s);  // (few rows always)
   else if (DP <= 64 && p.nc == 2)
-    run_fwd<T, DP, DP <= 64 ? 2 : 1, false>(a, cap, s);
+    run_fwd<T, DP, DP <= 64 ? 2 : 1, false, false>(a, cap, s);
+  else if (a.two)
+    run_fwd<T, DP, 1, false, true>(a, cap, s);
   else
-    run_fwd<T, DP, 1, false>(a, cap, s);
+    run_fwd<T, DP, 1, false, false>(a, cap, s);
   const int64_t rows = a.nq * a.hq;
   if (a.splits > kAttnFewSplits)
     k_attn_join<T, DP><<<static_cast<unsigned>(rows), 256, 0, s>>>(a);

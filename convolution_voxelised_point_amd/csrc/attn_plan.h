@@ -19,6 +19,17 @@ inline int64_t parts(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
 inline int padded_width(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
 
+// So few query rows (times heads) that a result's error is that of a few roundings:
+// probabilities and score gradients then go into their products as two 16-bit parts.
+// (With one part, errors are 1.4 times the last rounding's when many roundings average,
+// but of 185 calls of at most 64 rows every seventh had a result with more than 1.5
+// times, up to 4.9.)  Such calls are bound by latency: 13 x 12 queries over 1000 keys, 6 / 3 heads of 40, forward and
+// backward 53 -> 57 us.
+inline bool few_rows(int64_t rows) { return rows <= 2048; }
+
+// dq: whether what delta was short of is taken off at the end (attn_bwd.hip).
+inline bool mends_dq(int d, int64_t rows) { return d <= 64 || few_rows(rows); }
+
 enum class Walk { kForward, kDq, kDkv };
 
 // How the walk over `other` rows for `own` rows (both counted over all sets,
@@ -44,7 +55,7 @@ inline AttnPlan plan_walk(int64_t own, int64_t other, int64_t n_sets, int hk, in
   if (own_per <= 16 && few && dp <= 64) {
     p.share_keys = true;
     p.bm = 16;
-  } else if (dp <= 64 && own_per >= 512 && parts(own, 128) * hk >= 256) {
+  } else if (dp <= 64 && !(walk == Walk::kDkv && few_rows(other * hk)) && own_per >= 512 && parts(own, 128) * hk >= 256) {
     p.nc = 2;
     p.bm = 128;
   } else if (dp <= 64 && other_per <= 512) {

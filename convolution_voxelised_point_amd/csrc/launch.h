@@ -135,18 +135,17 @@ constexpr int kAttnFewSplits = 8;
 //     64: 1200 windows, bias 117 / 124 / 126; 2 x 8192 rows (two column blocks) with cap and
 //     bias 700 / 732* / 737, without 326 / 324 / 368; at 32 560 / 560 / 637;
 //     128: 1200 windows, bias 236 / 252 / 249
-//   dq, 32: windows, cap and bias 291 / 300 / 371, bias 230 / 252* / 252, none 170 / 188* / 170;
-//     64: windows, bias 206 / 220* / 200, cap 156 / - / 184; 2 x 8192 rows 1041 / 2074* / 1140;
-//     at 32 877 / 841* / 955; 128: windows 338 / 600 / 597
+//   dq, 32: windows, bias 280 / * / 278; 64: 1200 windows, bias 202 / * / -, cap 188 / * / -; 2 x
+//     8192 rows 930 / * / 1470; 128: windows 338 / 600 / 597, few rows (mend) one
 //   dk and dv, 32: windows, bias 270 / 298* / -, cap and bias 297 / 287* / 292; 2 x 8192 rows 849 /
 //     887* / 938; 64: windows 216 / 259* / 220, 2 x 8192 rows 1058 / 2600* / 1585; 128: windows
 //     673 / 1167* (one is the least).
-// Sharing the keys, a kernel's LDS holds it to two.
-constexpr int attn_waves_fwd(int dp, int nc, bool cap, bool bias, bool share_keys) {
-  return share_keys || nc == 2 || dp == 128 ? 2 : dp == 64 ? (bias ? 2 : 3) : cap && bias ? 4 : 5;
+// Sharing the keys, a kernel's LDS holds it to two; calls of few rows (two) have no more.
+constexpr int attn_waves_fwd(int dp, int nc, bool cap, bool bias, bool two) {
+  return two || nc == 2 || dp == 128 ? 2 : dp == 64 ? (bias ? 2 : 3) : cap && bias ? 4 : 5;
 }
-constexpr int attn_waves_dq(int dp, int nc, bool cap, bool bias, bool share_keys) {
-  return share_keys || nc == 2 || dp == 128 || (cap && bias) ? 2 : dp == 64 ? (bias ? 2 : 3) : 4;
+constexpr int attn_waves_dq(int dp, int nc, bool cap, bool bias, bool share_keys, bool mend) {
+  return mend && dp == 128 ? 1 : share_keys || nc == 2 || dp >= 64 || (cap && bias) ? 2 : 3;
 }
 constexpr int attn_waves_dkv(int dp, int nc, bool bias) {
   return dp == 128 ? 1 : dp == 32 && nc == 1 ? 3 : 2;

@@ -544,11 +544,11 @@ ts_status ts_conv_bwd_dgrad_noalloc(const ts_kmap* map, const void* dy, int cout
  *   out_i = sum_j softmax(z)_j v_j,    lse[i][h] = log sum_j exp(z_j)
  * |c_i - c_j| is the Euclidean distance of the voxel coordinates (batch column
  * left out), formed in float32 from their differences to one row of the set: those
- * are exact up to 2^24, and have to lie below 2^31.  slopes are constants of the call (no gradient);
- * cap and slopes are optional.  A query row without keys, or whose scores are
- * all -inf, and a query row that no set owns, get zeros, lse = -inf and zero
- * gradients, and add nothing to others, whatever their dout holds; so do keys that
- * no query of theirs sees.  An infinite element of q or k makes its score infinite
+ * are exact up to 2^24, and have to lie below 2^31.  slopes are constants of the
+ * call (no gradient); cap and slopes are optional.  A query row without keys, or
+ * whose scores are all -inf, and a query row that no set owns, get zeros, lse =
+ * -inf and zero gradients, and add nothing to others, whatever their dout holds;
+ * so do keys that no query of theirs sees.  An infinite element of q or k makes its score infinite
  * and adds nothing to the gradients where that drops the key (z = -inf) or
  * saturates the cap; other infinities and NaN carry on as in the formulas.
  *
@@ -564,8 +564,12 @@ ts_status ts_conv_bwd_dgrad_noalloc(const ts_kmap* map, const void* dy, int cout
  * in the workspace first.  fp16 or bf16 (TS_F32 is TS_ERR_UNSUPPORTED), 1 <= d <=
  * 128, hk divides hq; products are accumulated in fp32, softmax statistics are
  * fp32, probabilities and score gradients are rounded to the feature type for
- * their products (score gradients as two parts for dq).  With fp16, score gradients below 2^-24 vanish and above
- * 65504 overflow, as in any fp16 backward pass: scale the loss.
+ * their products (as two such parts in calls of at most 2048 query rows times
+ * heads, and mostly for dq), which leaves results at most about 1.5 times as far
+ * from the exact ones as their last rounding.  Probabilities are scaled to fp16's
+ * range.  Score gradients are not: with fp16 those below 2^-24
+ * vanish and those above 65504 overflow, as in any fp16 backward pass: scale the
+ * loss.
  * ---------------------------------------------------------------------- */
 typedef struct ts_attn {
   ts_dtype dtype;          /* of q, k, v, out and the gradients                   */
@@ -588,8 +592,9 @@ size_t ts_attn_workspace_bytes(const ts_attn* at, int backward);
 /* out [nq][hq][d] (o_stride) and lse (device float [nq][hq]); every row is
  * written once.  Errors: TS_ERR_INVALID_ARG (null pointers, sizes, strides,
  * a short workspace, scale, cap or scale / cap not finite, cap < 0),
- * TS_ERR_UNSUPPORTED (fp32, d > 128, cap > 1024, more than 2^31 - 1 rows times heads, more than 2^24 tiles of
- * 64 rows, sets counted as at least one, strides above 2^23), TS_ERR_HIP. */
+ * TS_ERR_UNSUPPORTED (fp32, d > 128, cap > 1024, more than 2^31 - 1 rows times
+ * heads, about 2^24 tiles of 16 to 128 rows or more, a set counted as at least
+ * one, strides above 2^23), TS_ERR_HIP. */
 ts_status ts_attn_fwd(const ts_attn* at, const void* q, const void* k, const void* v, void* out, float* lse, void* ws,
                       size_t ws_bytes, uint32_t* err_flags, hipStream_t stream);
 
