@@ -1,9 +1,11 @@
 // Attention within packed sets, forward: one walk over the keys with a running
 // maximum and sum (see attn.h for the operand layout).
 //
-// Vector instructions bound it (4 cycles each, 8 for exp2, rcp and sqrt, against
-// 6 cycles of matrix work per score at 64 channels), so each score gets as few
-// as possible:
+// Vector instructions bound it: 64 scores of 64 channels take 16 cycles of a SIMD in
+// matrix instructions and, with a cap, 36 in vector ones (4 each, 8 for exp2, rcp and
+// sqrt), one after the other; together they fill 80 % of the kernel at 4 x 4096 capped
+// rows, 71 % at 2 x 8192 biased ones and 63 to 68 % in windows of 32 channels, where
+// waves wait for LDS and memory in between.  So each score gets as few as possible:
 //   - scores are kept in units of log 2 and relative to the column's reference
 //     m, which is folded into the multiply-add that scales them;
 //   - m follows the maximum only when a score passes it by more than a slack:
@@ -22,9 +24,13 @@
 // 102,835 keys 18.1 -> 18.7 us).
 // Rows without a finite score give zeros and lse = -inf.
 //
-// Measured (fp16 or bf16, whole calls): 4 sets of 4096, 8 heads of 64, capped 239 us
-// (575 TFLOP/s); 1024 windows of about 100, 4 heads of 32, biased 54 us (1.8 TB/s);
-// one query over 102,835 keys 22 us (2.4 TB/s).
+// Measured, whole calls in long runs: 4 sets of 4096, 8 heads of 64, capped, fp16 235 us
+// (585 TFLOP/s); 1024 windows of about 100, 4 heads of 32, biased, bf16 55 us (1.8 TB/s);
+// one query over 102,835 keys 22.7 us (2.4 TB/s); 1200 windows of about 127, 4 heads of
+// 128, biased, bf16 235 us (2.4 TB/s); 2 sets of 4096, 8 heads of 128, capped 255 us (472
+// TFLOP/s).  Times of one form against another, here and beside the rules, are kernel
+// times by the profiler, twelve calls after a pause, which are up to 15 % longer (the
+// first of these 286).
 #include "attn.h"
 
 namespace ts {
@@ -52,7 +58,7 @@ constexpr float kFold = 256.f;
 // from LDS feeds both (2 x 8192 rows: 662 us, with NC 1 785).  KS (few query rows): all
 // four waves own the same 16 columns and share out the keys of each tile, 32 each;
 // their results are joined in LDS (one query over 102,835 keys: 18.0 us against 19.9 with
-// one wave at work).
+// one wave at work; attn_plan.h says where).
 //
 // A block takes a.heads key-value heads of its rows one after the other, as one walk
 // over (head, tile): for short sets, finding the set and the first reads would

@@ -43,8 +43,8 @@ enum class Walk { kForward, kDq, kDkv };
 //     of 500 57 / 81; of 32 channels 19 / 15, 23 / 22, 42 / 44).  At 128 channels it lost
 //     everywhere (one query over 100,000 keys 29 / 21 forward, 30 / 26 dq) and is not built;
 //   - long sets, with enough blocks for every CU: two column blocks a wave (2 x 8192
-//     rows of 64 channels, dk and dv: 1030 us, with one 1325; of 32 850 / 916, dq 877 / 950,
-//     forward 559 / 638);
+//     rows of 64 channels, dk and dv: 1030 us, with one 1325; of 32 850 / 916, forward 559 /
+//     638);
 //   - short walks: a block takes several heads one after the other (2400 windows: forward
 //     161 us, with one head a block 191; dq 226 / 252; dk and dv 266 / 304).
 inline AttnPlan plan_walk(int64_t own, int64_t other, int64_t n_sets, int hk, int dp, Walk walk) {
