@@ -170,4 +170,11 @@ hipError_t launch_norm_bwd(const void* dy, const void* h, const Act8& h8, const 
                            const void* dh, int64_t n, int c, ts_dtype dt, void* dx, float* dw, void* ws,
                            hipStream_t s);
 
+// combine.hip
+hipError_t launch_combine_fwd(const void* y, int64_t n_rows, const int32_t* place, const float* gates, int64_t n, int top,
+                              int c, ts_dtype dt, void* out, uint32_t* flags, hipStream_t s);
+hipError_t launch_combine_bwd(const void* dout, const void* y, int64_t n_rows, const int32_t* place, const float* gates,
+                              int64_t n, int top, int c, ts_dtype dt, void* dy, float* dgates, uint32_t* flags,
+                              hipStream_t s);
+
 }  // namespace ts

@@ -1,0 +1,44 @@
+// Arguments of the router's kernels (route.hip).
+#pragma once
+
+#include <stdint.h>
+
+#include "launch.h"
+
+namespace ts {
+
+constexpr int kRouteMaxTop = 16, kRouteMaxExperts = 512;
+constexpr int kRouteSmall = 2048;  // pairs that one block takes on alone
+
+struct RouteK {
+  const void* logits;
+  int64_t n;
+  int e, top;
+  bool over_all;
+  int32_t* experts;
+  float* gates;
+  int64_t* starts;
+  int32_t *rows, *place;
+  int32_t* counts;  // [e + 1][blocks]
+  const float* dgates;
+  void* dlogits;
+  // filled in by the launcher
+  int log_lanes, bits, blocks;
+  bool vec;
+};
+
+inline bool route_small(int64_t n, int top) { return n * top <= kRouteSmall; }
+
+// Blocks of 1024 threads: about one pass over a block's rows at most twice per compute
+// unit, and at most 64 counts for each of the scan's threads.
+inline int route_blocks(int64_t n, int e) {
+  int lanes = 1;
+  while (8 * lanes < e) lanes *= 2;
+  const int64_t rows = 1024 / lanes, b = (n + rows - 1) / rows, most = 65536 / (e + 1);
+  const int64_t cap = most < 512 ? most : 512;
+  return static_cast<int>(b < cap ? b : cap);
+}
+
+hipError_t launch_route(RouteK& k, ts_dtype dt, bool back, hipStream_t s);
+
+}  // namespace ts

@@ -1,0 +1,369 @@
+// Router of rows to experts (ts_route_fwd) and its backward pass.
+//
+// A row's `top` largest logits are picked one after the other: the threads of a row hold
+// 8 experts each, order them by (value, lowest expert first) and agree on the largest
+// with shuffles.  Values are compared as integers that order like the floats (-0 made
+// 0, NaN above infinity).  Gates are a softmax in fp32.
+//
+// The chosen pairs (row, j) are then put in order of their expert, by a counting sort
+// without atomics on memory: blocks own runs of rows and count their pairs per expert,
+// one block turns the counts into first places, and every block gives its pairs their
+// places, wave after wave, by counting the lanes before that chose the same expert.
+// Pairs without an expert form one more bucket behind the last.  Small calls do all of it
+// in one block (39 rows: one launch instead of three).
+#include "act8.h"
+#include "launch.h"
+#include "route.h"
+
+namespace ts {
+namespace {
+
+constexpr int kRouteThreads = 1024;
+constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kLow = 0x007fffff;  // of -infinity; what orders at or below it is never picked
+
+__device__ __forceinline__ uint32_t order_of(float z) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, z + 0.f);
+  if (z != z) return ~0u;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __builtin_bit_cast(float, o == ~0u ? 0x7fc00000u : o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+
+// Experts and gates of rows [r0, r1): G threads a row (8 experts each).  on_pick(row, j,
+// expert) is called once per pair, by one thread.  Every thread of the block calls this;
+// zs and es hold a pass's picks, `top` for each of its rows.
+template <typename T, typename F>
+__device__ __forceinline__ void pick(const RouteK& k, int64_t r0, int64_t r1, float* zs, int16_t* es, F&& on_pick) {
+  const int g = 1 << k.log_lanes, lane = threadIdx.x & (g - 1), slot = threadIdx.x >> k.log_lanes;
+  const int per = kRouteThreads >> k.log_lanes;
+  for (int64_t base = r0; base < r1; base += per) {
+    const int64_t row = base + slot;
+    const bool on = row < r1;
+    float z[8];
+    uint32_t key[8];
+    if (on && lane * 8 < k.e) load_unit(static_cast<const T*>(k.logits) + row * k.e, lane * 8, k.e, k.vec, z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) key[i] = on && lane * 8 + i < k.e ? order_of(z[i]) : 0u;
+    float best = 0.f, sum = 0.f;
+    for (int j = 0; j < k.top; ++j) {
+      uint32_t o = 0;
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (key[i] > o) o = key[i], at = i;
+      at += lane * 8;
+      for (int m = 1; m < g; m <<= 1) {
+        const uint32_t oo = __shfl_xor(o, m);
+        const int oa = __shfl_xor(at, m);
+        if (oo > o || (oo == o && oa < at)) o = oo, at = oa;
+      }
+      const bool some = o > static_cast<uint32_t>(kLow);
+      const float v = value_of(o);
+      if (j == 0) best = v;
+      if (some) {
+        if (!k.over_all) sum += expf(v - best);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at == lane * 8 + i) key[i] = 0;
+      }
+      if (on && lane == 0) {
+        zs[slot * k.top + j] = v;
+        es[slot * k.top + j] = static_cast<int16_t>(some ? at : -1);
+      }
+    }
+    if (k.over_all) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += on && lane * 8 + i < k.e ? expf(z[i] - best) : 0.f;
+      for (int m = 1; m < g; m <<= 1) sum += __shfl_xor(sum, m);
+    }
+    // a row's threads lie in one wave: what its first one wrote is there
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (on)
+      for (int j = lane; j < k.top; j += g) {
+        const int e = es[slot * k.top + j];
+        k.experts[row * k.top + j] = e;
+        k.gates[row * k.top + j] = e < 0 ? 0.f : expf(zs[slot * k.top + j] - best) / sum;
+        on_pick(row, j, e);
+      }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Lanes of the wave that hold the same bucket, out of `live` ones.
+__device__ __forceinline__ uint64_t same_bucket(int bucket, int bits, uint64_t live) {
+  uint64_t m = live;
+  for (int b = 0; b < bits; ++b) {
+    const bool set = (bucket >> b) & 1;
+    const uint64_t v = __ballot(set);
+    m &= set ? v : ~v;
+  }
+  return m;
+}
+__device__ __forceinline__ int lanes_before(uint64_t m) {
+  return static_cast<int>(__builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(m), 0u)));
+}
+
+// Places of the pairs [p0, p1) of this wave, in order; next[bucket] is where the bucket's
+// next pair goes (LDS, this wave's own).
+template <typename E>
+__device__ __forceinline__ void give_places(const RouteK& k, int64_t p0, int64_t p1, const E& expert_of, int32_t* next) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t b = p0; b < p1; b += 64) {
+    const int64_t p = b + lane;
+    const bool on = p < p1;
+    const int e = on ? expert_of(p) : 0;
+    const int bucket = e < 0 ? k.e : e;
+    const uint64_t m = same_bucket(bucket, k.bits, __ballot(on));
+    const int before = lanes_before(m);
+    if (on) {
+      const int64_t at = next[bucket] + before;
+      k.rows[at] = e < 0 ? -1 : static_cast<int32_t>(p / k.top);
+      k.place[p] = e < 0 ? -1 : static_cast<int32_t>(at);
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (on && before == 0) next[bucket] += __popcll(m);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+struct Span {
+  int64_t a, b;
+};
+// Run `i` of `n` things in `parts` parts of equal size (the last ones may be empty).
+__device__ __forceinline__ Span span_of(int64_t n, int parts, int i) {
+  const int64_t per = (n + parts - 1) / parts;
+  const int64_t a = per * i < n ? per * i : n, b = a + per < n ? a + per : n;
+  return {a, b};
+}
+
+// One block's rows; counts[bucket][block].
+template <typename T>
+__global__ __launch_bounds__(kRouteThreads) void k_route(const RouteK k) {
+  extern __shared__ float zs[];  // [rows of a pass][top], then the experts
+  int16_t* es = reinterpret_cast<int16_t*>(zs + (kRouteThreads >> k.log_lanes) * k.top);
+  __shared__ int32_t count[kRouteMaxExperts + 1];
+  for (int i = threadIdx.x; i <= k.e; i += kRouteThreads) count[i] = 0;
+  __syncthreads();
+  const Span r = span_of(k.n, k.blocks, blockIdx.x);
+  pick<T>(k, r.a, r.b, zs, es, [&](int64_t, int, int e) { atomicAdd(&count[e < 0 ? k.e : e], 1); });
+  __syncthreads();
+  for (int i = threadIdx.x; i <= k.e; i += kRouteThreads) k.counts[static_cast<int64_t>(i) * k.blocks + blockIdx.x] = count[i];
+}
+
+__device__ __forceinline__ int32_t scan_inclusive(int32_t x) {
+  const int lane = threadIdx.x & 63;
+  for (int m = 1; m < 64; m <<= 1) {
+    const int32_t y = __shfl_up(x, m);
+    if (lane >= m) x += y;
+  }
+  return x;
+}
+
+// counts[bucket][block] -> the first place of each; starts of the experts.  One block, four
+// counts a thread and pass (64 experts x 512 blocks: 8 passes).
+__global__ __launch_bounds__(kRouteThreads) void k_route_scan(const RouteK k) {
+  __shared__ int32_t wave_sum[2][kRouteWaves];
+  const int total = (k.e + 1) * k.blocks;
+  const int wave = threadIdx.x >> 6;
+  int32_t carry = 0, c[4], ahead[4];
+  auto fetch = [&](int at, int32_t (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = at + i < total ? k.counts[at + i] : 0;
+  };
+  fetch(threadIdx.x * 4, ahead);
+  for (int base = 0, pass = 0; base < total; base += 4 * kRouteThreads, pass ^= 1) {
+    const int at = base + static_cast<int>(threadIdx.x) * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = ahead[i];
+    fetch(at + 4 * kRouteThreads, ahead);
+    const int32_t mine = c[0] + c[1] + c[2] + c[3];
+    const int32_t inc = scan_inclusive(mine);
+    if ((threadIdx.x & 63) == 63) wave_sum[pass][wave] = inc;
+    __syncthreads();  // (the other half of wave_sum may still be read)
+    int32_t sum = carry + inc - mine;
+#pragma unroll
+    for (int w = 0; w < kRouteWaves; ++w) {
+      const int32_t v = wave_sum[pass][w];
+      sum += w < wave ? v : 0;
+      carry += v;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (at + i < total) {
+        k.counts[at + i] = sum;
+        if ((at + i) % k.blocks == 0) k.starts[(at + i) / k.blocks] = sum;
+      }
+      sum += c[i];
+    }
+  }
+}
+
+// Places of one block's pairs.
+__global__ __launch_bounds__(kRouteThreads) void k_route_place(const RouteK k) {
+  extern __shared__ int32_t next[];  // [waves][e + 1]
+  const int wave = threadIdx.x >> 6, buckets = k.e + 1;
+  const Span r = span_of(k.n, k.blocks, blockIdx.x);
+  const Span mine = span_of((r.b - r.a) * k.top, kRouteWaves, wave);
+  const int64_t p0 = r.a * k.top + mine.a, p1 = r.a * k.top + mine.b;
+  for (int i = threadIdx.x; i < kRouteWaves * buckets; i += kRouteThreads) next[i] = 0;
+  __syncthreads();
+  for (int64_t p = p0 + (threadIdx.x & 63); p < p1; p += 64) {
+    const int e = k.experts[p];
+    atomicAdd(&next[wave * buckets + (e < 0 ? k.e : e)], 1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < buckets; i += kRouteThreads) {
+    int32_t at = k.counts[static_cast<int64_t>(i) * k.blocks + blockIdx.x];
+    for (int w = 0; w < kRouteWaves; ++w) {
+      const int32_t c = next[w * buckets + i];
+      next[w * buckets + i] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  give_places(k, p0, p1, [&](int64_t p) { return k.experts[p]; }, next + wave * buckets);
+}
+
+// All of it in one block, for calls of at most kRouteSmall pairs.
+template <typename T>
+__global__ __launch_bounds__(kRouteThreads) void k_route_small(const RouteK k) {
+  __shared__ float zs[kRouteSmall];
+  __shared__ int16_t es[kRouteSmall];
+  __shared__ int16_t expert[kRouteSmall];
+  __shared__ int32_t base[kRouteMaxExperts + 2];
+  extern __shared__ int32_t next[];  // [waves][e + 1]
+  const int wave = threadIdx.x >> 6, buckets = k.e + 1;
+  for (int i = threadIdx.x; i < kRouteWaves * buckets; i += kRouteThreads) next[i] = 0;
+  __syncthreads();
+  const int pairs = static_cast<int>(k.n) * k.top;
+  const int per = ceil_div(pairs, kRouteWaves);
+  pick<T>(k, 0, k.n, zs, es, [&](int64_t row, int j, int e) {
+    const int p = static_cast<int>(row) * k.top + j;
+    expert[p] = static_cast<int16_t>(e);
+    atomicAdd(&next[p / per * buckets + (e < 0 ? k.e : e)], 1);
+  });
+  __syncthreads();
+  if (wave == 0) {  // first places of the buckets
+    int32_t carry = 0;
+    for (int b0 = 0; b0 < buckets; b0 += 64) {
+      const int b = b0 + static_cast<int>(threadIdx.x);
+      int32_t c = 0;
+      if (b < buckets)
+        for (int w = 0; w < kRouteWaves; ++w) c += next[w * buckets + b];
+      const int32_t inc = scan_inclusive(c);
+      if (b < buckets) {
+        base[b] = carry + inc - c;
+        k.starts[b] = carry + inc - c;
+      }
+      carry += __shfl(inc, 63);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < buckets; i += kRouteThreads) {
+    int32_t at = base[i];
+    for (int w = 0; w < kRouteWaves; ++w) {
+      const int32_t c = next[w * buckets + i];
+      next[w * buckets + i] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  const Span mine = span_of(pairs, kRouteWaves, wave);
+  give_places(k, mine.a, mine.b, [&](int64_t p) { return static_cast<int>(expert[p]); }, next + wave * buckets);
+}
+
+// dlogits: with normalised gates g_j (dg_j - sum g dg) at the chosen experts, else
+// [chosen] g_j dg_j - p sum g dg at all of them, p = softmax(logits).
+template <typename T>
+__global__ __launch_bounds__(256) void k_route_bwd(const RouteK k) {
+  const int g = 1 << k.log_lanes, lane = threadIdx.x & (g - 1);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (256 >> k.log_lanes);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (256 >> k.log_lanes) + (threadIdx.x >> k.log_lanes); row < k.n; row += step) {
+    float z[8], d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = 0.f;
+    if (k.over_all && lane * 8 < k.e) load_unit(static_cast<const T*>(k.logits) + row * k.e, lane * 8, k.e, k.vec, z);
+    float inner = 0.f;
+    bool some = false;
+    for (int j = 0; j < k.top; ++j) {
+      const int64_t p = row * k.top + j;
+      if (k.experts[p] < 0) continue;
+      some = true;
+      inner = fmaf(k.gates[p], k.dgates[p], inner);
+    }
+    if (some) {  // the same in all of the row's threads
+      for (int j = 0; j < k.top; ++j) {
+        const int64_t p = row * k.top + j;
+        const int e = k.experts[p];
+        const float x = k.gates[p] * (k.over_all ? k.dgates[p] : k.dgates[p] - inner);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e == lane * 8 + i) d[i] += x;
+      }
+      if (k.over_all) {
+        float best = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (lane * 8 + i < k.e) best = z[i] > best || z[i] != z[i] ? z[i] : best;  // NaN stays
+        for (int m = 1; m < g; m <<= 1) {
+          const float o = __shfl_xor(best, m);
+          best = o > best || o != o ? o : best;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          z[i] = lane * 8 + i < k.e ? expf(z[i] - best) : 0.f;
+          sum += z[i];
+        }
+        for (int m = 1; m < g; m <<= 1) sum += __shfl_xor(sum, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = fmaf(-z[i] / sum, inner, d[i]);
+      }
+    }
+    if (lane * 8 < k.e) store_unit(static_cast<T*>(k.dlogits) + row * k.e, lane * 8, k.e, k.vec, d);
+  }
+}
+
+template <typename T>
+void run(const RouteK& k, bool back, hipStream_t s) {
+  if (back) {
+    const int64_t b = ceil_div<int64_t>(k.n, 256 >> k.log_lanes), most = int64_t{1} << 23;
+    k_route_bwd<T><<<static_cast<unsigned>(b < most ? b : most), 256, 0, s>>>(k);
+    return;
+  }
+  const size_t lds = static_cast<size_t>(kRouteWaves) * (k.e + 1) * sizeof(int32_t);
+  if (route_small(k.n, k.top)) {
+    k_route_small<T><<<1, kRouteThreads, lds, s>>>(k);
+    return;
+  }
+  const size_t picks = static_cast<size_t>(kRouteThreads >> k.log_lanes) * k.top * 6;  // at most 48 KB
+  k_route<T><<<k.blocks, kRouteThreads, picks, s>>>(k);
+  k_route_scan<<<1, kRouteThreads, 0, s>>>(k);
+  k_route_place<<<k.blocks, kRouteThreads, lds, s>>>(k);
+}
+
+}  // namespace
+
+hipError_t launch_route(RouteK& k, ts_dtype dt, bool back, hipStream_t s) {
+  if (k.n == 0) return back ? hipSuccess : fill_i64(k.starts, k.e + 1, 0, s);
+  k.log_lanes = 0;
+  while ((8 << k.log_lanes) < k.e) ++k.log_lanes;
+  k.bits = 1;
+  while ((1 << k.bits) < k.e + 1) ++k.bits;
+  k.vec = k.e % 8 == 0 && ((reinterpret_cast<uintptr_t>(k.logits) | reinterpret_cast<uintptr_t>(k.dlogits)) & 15) == 0;
+  k.blocks = route_blocks(k.n, k.e);
+  switch (dt) {
+    case TS_F32: run<float>(k, back, s); break;
+    case TS_F16: run<_Float16>(k, back, s); break;
+    default: run<__bf16>(k, back, s); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace ts

@@ -72,6 +72,16 @@ class TsAct8(ctypes.Structure):
     _fields_ = [("codes", _vp), ("scales", _vp)]
 
 
+class TsRope(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("d", ctypes.c_int32), ("ndim", ctypes.c_int32), ("pairs", ctypes.c_int32 * 3),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float), ("n", _i64), ("coords", _vp), ("freqs", _vp)]
+
+
+class TsRopeHeads(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("x_stride", _i64), ("y_stride", _i64), ("dy_stride", _i64), ("dx_stride", _i64),
+                ("x", _vp), ("w", _vp), ("y", _vp), ("dy", _vp), ("dx", _vp), ("dw", _vp)]
+
+
 def _sig(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -130,6 +140,15 @@ _lib_conv_bwd_wgrad_act8 = _sig("ts_conv_bwd_wgrad_act8", _i32, [_P, _C, _i32, _
 _lib_norm_fwd = _sig("ts_norm_fwd", _i32, [_vp, _vp, _vp, _i64, _i32, ctypes.c_float, _i32, _vp, _vp, _vp, _C, _C, _vp])
 _lib_norm_workspace_bytes = _sig("ts_norm_workspace_bytes", _sz, [_i64, _i32])
 _lib_norm_bwd = _sig("ts_norm_bwd", _i32, [_vp, _vp, _C, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _sz, _vp])
+_R, _H = ctypes.POINTER(TsRope), ctypes.POINTER(TsRopeHeads)
+_lib_rope_workspace_bytes = _sig("ts_rope_workspace_bytes", _sz, [_R, _i32, _i32])
+_lib_rope_fwd = _sig("ts_rope_fwd", _i32, [_R, _H, _H, _vp])
+_lib_rope_bwd = _sig("ts_rope_bwd", _i32, [_R, _H, _H, _vp, _sz, _vp])
+_lib_route_workspace_bytes = _sig("ts_route_workspace_bytes", _sz, [_i64, _i32, _i32])
+_lib_route_fwd = _sig("ts_route_fwd", _i32, [_vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+_lib_route_bwd = _sig("ts_route_bwd", _i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp])
+_lib_combine_fwd = _sig("ts_combine_fwd", _i32, [_vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp])
+_lib_combine_bwd = _sig("ts_combine_bwd", _i32, [_vp, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp])
 _lib_debug_violations = _sig("ts_debug_violations", _i32, [ctypes.POINTER(_u32)])
 
 EXPORTED = ["ts_status_string", "ts_version", "ts_hash_capacity", "ts_hash_table_bytes", "ts_hash_build",
@@ -140,7 +159,9 @@ EXPORTED = ["ts_status_string", "ts_version", "ts_hash_capacity", "ts_hash_table
             "ts_conv_fwd_generative", "ts_conv_transpose_fwd", "ts_pool_fwd", "ts_graph_conv_fwd", "ts_conv_bwd_dgrad",
             "ts_conv_bwd_wgrad", "ts_conv_bwd_dgrad_noalloc", "ts_attn_workspace_bytes", "ts_attn_fwd", "ts_attn_bwd",
             "ts_act_pack", "ts_act_unpack", "ts_conv_wgrad_act8_workspace_bytes", "ts_conv_bwd_wgrad_act8", "ts_norm_fwd",
-            "ts_norm_workspace_bytes", "ts_norm_bwd", "ts_debug_violations"]
+            "ts_norm_workspace_bytes", "ts_norm_bwd", "ts_rope_workspace_bytes", "ts_rope_fwd", "ts_rope_bwd",
+            "ts_route_workspace_bytes", "ts_route_fwd", "ts_route_bwd", "ts_combine_fwd", "ts_combine_bwd",
+            "ts_debug_violations"]
 
 
 class TsError(RuntimeError):
@@ -983,3 +1004,204 @@ def norm_bwd(dy: torch.Tensor, h: Union[torch.Tensor, Act8], w: torch.Tensor, rs
                          rstd.data_ptr(), _ptr(dh), n, c, _DT[dy.dtype], dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), size,
                          _raw_stream(dy)), "ts_norm_bwd")
     return dx, dw
+
+
+# ---------------------------------------------------------------- the rest of a voxel-transformer layer
+def rope_freqs(pairs: Sequence[int], base: float = 100.0, device="cuda") -> torch.Tensor:
+    """Frequencies for `pairs` channel pairs of each axis: base^(-i / m) radians a
+    voxel for pair i of an axis with m."""
+    return torch.cat([base ** (-torch.arange(m, dtype=torch.float64) / max(m, 1)) for m in pairs]).float().to(device)
+
+
+def _rope_args(like: torch.Tensor, coords: Optional[torch.Tensor], freqs: Optional[torch.Tensor], pairs: Sequence[int],
+               eps: float, interleaved: bool) -> TsRope:
+    n, _, d = like.shape
+    pairs = list(pairs)
+    _need(len(pairs) in (2, 3) and min(pairs) >= 0, "rope: pairs are the channel pairs of 2 or 3 axes")
+    if sum(pairs) > 0:
+        _need(coords is not None and coords.is_cuda and coords.dtype is torch.int32 and coords.is_contiguous()
+              and coords.shape == (n, len(pairs) + 1), "rope: coordinates are int32 [n][ndim + 1]")
+        _need(freqs is not None and freqs.is_cuda and freqs.dtype is torch.float32 and freqs.is_contiguous()
+              and freqs.numel() == sum(pairs), "rope: freqs are float32, one for each pair")
+    else:
+        coords = freqs = None
+    _need(like.dtype in _DT, "rope: a feature type")
+    return TsRope(_DT[like.dtype], d, len(pairs), (ctypes.c_int32 * 3)(*(pairs + [0])[:3]), int(interleaved), eps, n, _ptr(coords),
+                  _ptr(freqs))
+
+
+def _rope_rows(t: torch.Tensor, like: torch.Tensor, heads: int, what: str) -> int:
+    st = _row_stride(t)
+    _need(st is not None and t.is_cuda and t.dtype is like.dtype and t.shape == (like.shape[0], heads, like.shape[2]), what)
+    return st
+
+
+def _rope_weight(w: Optional[torch.Tensor], d: int) -> None:
+    _need(w is None or (w.is_cuda and w.dtype is torch.float32 and w.is_contiguous() and w.numel() == d),
+          "rope: the norm's weights are float32 [d]")
+
+
+def rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], coords: Optional[torch.Tensor], freqs: Optional[torch.Tensor],
+             pairs: Sequence[int], wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             interleaved: bool = False, into: Optional[Sequence[Optional[torch.Tensor]]] = None,
+             stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Queries [n][hq][d] and keys [n][hk][d] (or None) of the same voxels, normalised
+    where a weight is given and turned by their positions (see ts_rope in ts.h).  Written
+    to the two tensors of `into`, which may be q and k themselves, or to new ones."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rope_fwd(q, k, coords, freqs, pairs, wq, wk, eps, interleaved, into)
+    _need(q.dim() == 3, "rope: q is [n][heads][d]")
+    args = _rope_args(q, coords, freqs, pairs, eps, interleaved)
+    _need(into is None or len(into) == 2, "rope: results for q and k")
+    sides, out = [], []
+    for i, (x, w) in enumerate(((q, wq), (k, wk))):
+        if x is None:
+            _need(into is None or into[i] is None, "rope: a result without its input")
+            sides.append(None)
+            out.append(None)
+            continue
+        _need(x.dim() == 3, "rope: k is [n][heads][d]")
+        st = _rope_rows(x, q, x.shape[1], "rope: q and k are device tensors [n][heads][d] of one type, with adjacent heads")
+        _rope_weight(w, q.shape[2])
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if into is None else into[i]
+        _need(y is not None, "rope: results for q and k")
+        yst = _rope_rows(y, q, x.shape[1], "rope: results are like q and k")
+        sides.append(TsRopeHeads(x.shape[1], st, yst, 0, 0, x.data_ptr(), _ptr(w), y.data_ptr(), None, None, None))
+        out.append(y)
+    _check(_lib_rope_fwd(ctypes.byref(args), *(None if s is None else ctypes.byref(s) for s in sides), _raw_stream(q)), "ts_rope_fwd")
+    return out[0], out[1]
+
+
+class RopeGrads(NamedTuple):
+    """Gradients of rope_fwd's q, k, wq and wk (None where there is none)."""
+    dq: torch.Tensor
+    dk: Optional[torch.Tensor]
+    dwq: Optional[torch.Tensor]
+    dwk: Optional[torch.Tensor]
+
+
+def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor],
+             coords: Optional[torch.Tensor], freqs: Optional[torch.Tensor], pairs: Sequence[int],
+             wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+             into: Optional[Sequence[Optional[torch.Tensor]]] = None, stream=None) -> RopeGrads:
+    """Gradients from those of rope_fwd's results and its inputs.  Written to the two
+    tensors of `into`, which may be dq and dk themselves, or to new ones."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rope_bwd(dq, dk, q, k, coords, freqs, pairs, wq, wk, eps, interleaved, into)
+    _need(q.dim() == 3 and (dk is None) == (k is None), "rope: q is [n][heads][d], dk comes with k")
+    args = _rope_args(q, coords, freqs, pairs, eps, interleaved)
+    _need(into is None or len(into) == 2, "rope: results for q and k")
+    sides, out, grads = [], [], []
+    for i, (g, x, w) in enumerate(((dq, q, wq), (dk, k, wk))):
+        if x is None:
+            _need(into is None or into[i] is None, "rope: a result without its input")
+            sides.append(None)
+            out.append(None)
+            grads.append(None)
+            continue
+        what = "rope: q, k and their gradients are device tensors [n][heads][d] of one type, with adjacent heads"
+        _need(x.dim() == 3, what)
+        h, d = x.shape[1], q.shape[2]
+        st, gst = _rope_rows(x, q, h, what), _rope_rows(g, q, h, what)
+        _rope_weight(w, d)
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if into is None else into[i]
+        _need(y is not None, "rope: results for q and k")
+        yst = _rope_rows(y, q, h, "rope: results are like q and k")
+        dw = None if w is None else torch.empty(d, dtype=torch.float32, device=x.device)
+        sides.append(TsRopeHeads(h, st, 0, gst, yst, x.data_ptr(), _ptr(w), None, g.data_ptr(), y.data_ptr(), _ptr(dw)))
+        out.append(y)
+        grads.append(dw)
+    ref = ctypes.byref(args)
+    n = _lib_rope_workspace_bytes(ref, q.shape[1], 0 if k is None else k.shape[1])
+    ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    _check(_lib_rope_bwd(ref, *(None if s is None else ctypes.byref(s) for s in sides), _ptr(ws), n, _raw_stream(q)), "ts_rope_bwd")
+    return RopeGrads(out[0], out[1], grads[0], grads[1])
+
+
+class Route(NamedTuple):
+    """What route_fwd returns: experts int32 and gates float32 [n][top]; the grouped rows'
+    starts int64 [n_experts + 1] and rows int32 [n * top], and place int32 [n][top]."""
+    experts: torch.Tensor
+    gates: torch.Tensor
+    starts: torch.Tensor
+    rows: torch.Tensor
+    place: torch.Tensor
+
+
+def route_fwd(logits: torch.Tensor, top: int, over_all: bool = False, stream=None) -> Route:
+    """Each row's `top` experts, their gates, and the pairs grouped by expert (see
+    ts_route_fwd in ts.h)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return route_fwd(logits, top, over_all)
+    _matrix(logits, "route_fwd: logits are a dense device matrix [n][experts]")
+    n, e = logits.shape
+    _need(1 <= top <= e, "route_fwd: 1 <= top <= experts")
+    dev = logits.device
+    experts, rows, place = (torch.empty(s, dtype=torch.int32, device=dev) for s in ((n, top), (n * top,), (n, top)))
+    gates = torch.empty((n, top), dtype=torch.float32, device=dev)
+    starts = torch.empty(e + 1, dtype=torch.int64, device=dev)
+    size = _lib_route_workspace_bytes(n, e, top)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    _check(_lib_route_fwd(logits.data_ptr(), n, e, _DT[logits.dtype], top, int(over_all), experts.data_ptr(), gates.data_ptr(),
+                          starts.data_ptr(), rows.data_ptr(), place.data_ptr(), _ptr(ws), size, _raw_stream(logits)), "ts_route_fwd")
+    return Route(experts, gates, starts, rows, place)
+
+
+def route_bwd(dgates: torch.Tensor, logits: torch.Tensor, route: Route, over_all: bool = False, stream=None) -> torch.Tensor:
+    """Gradient of the logits from that of the gates."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return route_bwd(dgates, logits, route, over_all)
+    _matrix(logits, "route_bwd: logits are a dense device matrix [n][experts]")
+    n, e = logits.shape
+    top = route.experts.shape[1]
+    for t, dt in ((dgates, torch.float32), (route.gates, torch.float32), (route.experts, torch.int32)):
+        _need(t.is_cuda and t.dtype is dt and t.is_contiguous() and t.shape == (n, top), "route_bwd: gates, gradients, experts [n][top]")
+    d = torch.empty_like(logits)
+    _check(_lib_route_bwd(dgates.data_ptr(), logits.data_ptr(), route.experts.data_ptr(), route.gates.data_ptr(), n, e,
+                          _DT[logits.dtype], top, int(over_all), d.data_ptr(), _raw_stream(logits)), "ts_route_bwd")
+    return d
+
+
+def _place(place: torch.Tensor, gates: Optional[torch.Tensor]) -> None:
+    _need(place.is_cuda and place.dtype is torch.int32 and place.dim() == 2 and place.is_contiguous(), "combine: place is int32 [n][top]")
+    _need(gates is None or (gates.is_cuda and gates.dtype is torch.float32 and gates.is_contiguous() and gates.shape == place.shape),
+          "combine: gates are float32 [n][top]")
+
+
+def combine_fwd(y: torch.Tensor, place: torch.Tensor, gates: Optional[torch.Tensor] = None,
+                err_flags: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[t] = sum over j of gates[t][j] y[place[t][j]] (see ts_combine_fwd in ts.h)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return combine_fwd(y, place, gates, err_flags)
+    _matrix(y, "combine: y is a dense device matrix of grouped rows")
+    _place(place, gates)
+    (p, c), (n, top) = y.shape, place.shape
+    out = torch.empty((n, c), dtype=y.dtype, device=y.device)
+    _check(_lib_combine_fwd(y.data_ptr(), p, place.data_ptr(), _ptr(gates), n, top, c, _DT[y.dtype], out.data_ptr(),
+                            _flag_ptr(err_flags), _raw_stream(y)), "ts_combine_fwd")
+    return out
+
+
+def combine_bwd(dout: torch.Tensor, y: torch.Tensor, place: torch.Tensor, gates: torch.Tensor,
+                err_flags: Optional[torch.Tensor] = None, into: Optional[torch.Tensor] = None,
+                stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dy, dgates) of combine_fwd; dy is written to `into` (which may be y) or to a new
+    matrix, whose rows that no place names are not written."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return combine_bwd(dout, y, place, gates, err_flags, into)
+    _matrix(y, "combine: y is a dense device matrix of grouped rows")
+    _place(place, gates)
+    (p, c), (n, top) = y.shape, place.shape
+    _matrix(dout, "combine: dout is like the result", (n, c), y.dtype)
+    dy = torch.empty_like(y) if into is None else into
+    _matrix(dy, "combine: dy is like y", y.shape, y.dtype)
+    dgates = torch.empty((n, top), dtype=torch.float32, device=y.device)
+    _check(_lib_combine_bwd(dout.data_ptr(), y.data_ptr(), p, place.data_ptr(), gates.data_ptr(), n, top, c, _DT[y.dtype],
+                            dy.data_ptr(), dgates.data_ptr(), _flag_ptr(err_flags), _raw_stream(y)), "ts_combine_bwd")
+    return dy, dgates

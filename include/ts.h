@@ -662,6 +662,106 @@ ts_status ts_norm_bwd(const void* dy, const void* h, const ts_act8* h8, const fl
                       size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The rest of a voxel-transformer layer: positions and norms of the queries and
+ * keys that attention reads, and a feed-forward part whose weights are split over
+ * experts.
+ *
+ * Rotation.  A head's vector is normalised and its channel pairs are turned by the
+ * voxel's position, each pair with one axis:
+ *   u = x / sqrt(mean(x^2) + eps) * w      (w given: one weight a channel, shared by the heads)
+ *   (y_a, y_b) = (u_a cos t - u_b sin t, u_a sin t + u_b cos t),  t = coords[axis] * freqs[i]
+ * Pairs 0 .. pairs[0]-1 turn with the first spatial axis, the next pairs[1] with the
+ * second, and so on; with P pairs in all, pair i is channels (i, i + P), or
+ * (2i, 2i + 1) where interleaved.  Channels from 2 P on are not turned.  P may be 0
+ * (coords and freqs are not read then).  The score of a query and a key thus depends
+ * on where they lie to each other only.  Coordinates may be any int32; the angle is
+ * formed and reduced in 64 bits (off by less than 2^-50 of itself) and the rest is fp32.
+ * fp32, fp16 or bf16, 1 <= d <= 128.
+ *
+ * Rows of heads as for attention: the heads of a row adjacent, rows `*_stride`
+ * elements apart, at any alignment, so they may be columns of one projected matrix.
+ * y may be x, and dx may be dy or x, where their strides are equal.
+ * ---------------------------------------------------------------------- */
+typedef struct ts_rope {
+  ts_dtype dtype;
+  int32_t d, ndim;       /* head width; 2 or 3 spatial axes                      */
+  int32_t pairs[3];      /* channel pairs of each axis, 2 * their sum <= d       */
+  int32_t interleaved;   /* 0: pair i is (i, i + P), otherwise (2i, 2i + 1)      */
+  float eps;
+  int64_t n;             /* rows                                                 */
+  const int32_t* coords; /* device [n][ndim + 1], the batch column left out      */
+  const float* freqs;    /* device [P], radians per voxel                        */
+} ts_rope;
+
+/* Queries or keys of a call.  Forward: x, w, y.  Backward: dy, dx, and with w also
+ * x and dw. */
+typedef struct ts_rope_heads {
+  int32_t heads;
+  int64_t x_stride, y_stride, dy_stride, dx_stride; /* elements between rows     */
+  const void* x;  /* device [n][heads][d]                                        */
+  const float* w; /* device [d], or NULL: not normalised                         */
+  void* y;
+  const void* dy; /* gradient of y                                               */
+  void* dx;       /* gradient of x                                               */
+  float* dw;      /* device [d]: gradient of w, overwritten                      */
+} ts_rope_heads;
+
+/* y of the queries and of the keys (either may be NULL, or have 0 heads).  Errors:
+ * TS_ERR_INVALID_ARG (null pointers, sizes, strides, more channels in pairs than d, eps
+ * negative or not finite), TS_ERR_UNSUPPORTED (d > 128, more than 65,535 heads or 2^31 - 1
+ * rows times heads), TS_ERR_HIP. */
+ts_status ts_rope_fwd(const ts_rope* r, const ts_rope_heads* q, const ts_rope_heads* k, hipStream_t stream);
+
+/* Its backward pass.  dw is summed in a fixed order, without atomics; ws holds
+ * ts_rope_workspace_bytes(r, heads of q, heads of k).  Errors as ts_rope_fwd. */
+size_t ts_rope_workspace_bytes(const ts_rope* r, int hq, int hk);
+ts_status ts_rope_bwd(const ts_rope* r, const ts_rope_heads* q, const ts_rope_heads* k, void* ws, size_t ws_bytes,
+                      hipStream_t stream);
+
+/* Routing.  Each row of logits[n][n_experts] (fp32, fp16 or bf16) picks its `top`
+ * largest, the lowest expert first among equals (NaN counts as the largest):
+ *   experts[t][j]  the j-th largest's expert, gates[t][j] its softmax over the picked
+ *                  logits, or (over_all) over all of the row
+ * An expert whose logit is -inf is never picked; a row with fewer than `top` others has
+ * experts -1 and gates 0 at its end.  NaN or +inf in a row makes its gates NaN.
+ * The picked pairs, expert by expert and in order of the rows within one, are the
+ * grouped rows p:
+ *   starts[e]      the first grouped row of expert e, starts[n_experts] their number
+ *   rows[p]        the row p stands for; -1 from starts[n_experts] on
+ *   place[t][j]    the grouped row of pair (t, j), or -1
+ * experts, rows, place: device int32 [n * top]; gates: device float; starts: device
+ * int64 [n_experts + 1].  1 <= top <= n_experts.  No atomics on memory: the same order on
+ * every run.  Errors: TS_ERR_INVALID_ARG, TS_ERR_UNSUPPORTED (more than 512 experts, top >
+ * 16, more than 2^31 - 1 pairs), TS_ERR_HIP.  ws holds ts_route_workspace_bytes. */
+size_t ts_route_workspace_bytes(int64_t n, int n_experts, int top);
+ts_status ts_route_fwd(const void* logits, int64_t n, int n_experts, ts_dtype dtype, int top, int over_all,
+                       int32_t* experts, float* gates, int64_t* starts, int32_t* rows, int32_t* place, void* ws,
+                       size_t ws_bytes, hipStream_t stream);
+
+/* dlogits [n][n_experts] in dtype from dgates [n][top], with what ts_route_fwd returned
+ * (logits are read with over_all only):
+ *   [e = expert j] g_j (dgates_j - sum g dgates), or over_all: [e = expert j] g_j dgates_j - softmax_e sum g dgates
+ * A row without experts gets zeros.  dlogits may be logits. */
+ts_status ts_route_bwd(const float* dgates, const void* logits, const int32_t* experts, const float* gates, int64_t n,
+                       int n_experts, ts_dtype dtype, int top, int over_all, void* dlogits, hipStream_t stream);
+
+/* Sum of what a row's experts returned, from the grouped rows y[n_rows][c]:
+ *   out[t] = sum over j of gates[t][j] y[place[t][j]]     (gates NULL: 1)
+ * place: device int32 [n][top], -1: nothing; any other entry outside [0, n_rows) raises
+ * TS_FLAG_RANGE in err_flags (may be NULL) and counts as -1.  Without gates it is the
+ * gradient of reading rows by ts_route_fwd's `rows`.
+ * Backward: dy[place[t][j]] = gates[t][j] dout[t], dgates[t][j] = <dout[t], y[place[t][j]]> (0
+ * where place is -1).  Rows of dy that no place names are left as they were; a grouped row
+ * that several name gets one of their values.  fp32, fp16 or bf16; sums in fp32.  dy may be
+ * y.  Errors: TS_ERR_INVALID_ARG (null pointers, n or n_rows negative or above 2^31 - 1, top < 1,
+ * c outside [1, 65536]), TS_ERR_HIP. */
+ts_status ts_combine_fwd(const void* y, int64_t n_rows, const int32_t* place, const float* gates, int64_t n, int top, int c,
+                         ts_dtype dtype, void* out, uint32_t* err_flags, hipStream_t stream);
+ts_status ts_combine_bwd(const void* dout, const void* y, int64_t n_rows, const int32_t* place, const float* gates,
+                         int64_t n, int top, int c, ts_dtype dtype, void* dy, float* dgates, uint32_t* err_flags,
+                         hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Bounds-check build.  The library also builds as libts_debug.so, compiled
  * with TS_DEBUG_CHECKS: there the contraction, pooling and weight-gradient
  * kernels check every row index they read from a map (neighbour entries,
