@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "common.h"
+#include "group.h"
 #include "rope.h"
 #include "route.h"
 
@@ -102,6 +103,47 @@ ts_status check_combine(int64_t n, int64_t n_rows, int top, int c, ts_dtype dt) 
   return TS_OK;
 }
 
+// ---------------------------------------------------------------- products grouped by expert
+constexpr int kMaxGroups = 4096;
+
+ts_status check_groups(const ts_groups* g, int cin, int cout, ts_dtype dt) {
+  if (!g || g->n_groups < 1 || g->n_rows < 0 || g->n_rows > kMaxRows || !g->starts || !dtype_ok(dt)) return TS_ERR_INVALID_ARG;
+  if (cin < 1 || cout < 1 || cin > kMaxChannels || cout > kMaxChannels) return TS_ERR_INVALID_ARG;
+  if (g->rows && (g->n_src < 0 || g->n_src > kMaxRows)) return TS_ERR_INVALID_ARG;
+  if (dt == TS_F32 || g->n_groups > kMaxGroups) return TS_ERR_UNSUPPORTED;
+  return TS_OK;
+}
+
+// Blocks are fewer than 2^22: a launch may have 2^32 threads.
+bool grid_ok(const ts_groups* g, GroupOp op, int cin, int columns) {
+  int64_t blocks;
+  if (op == kGroupWgrad) {
+    const int64_t tiles = static_cast<int64_t>(ceil_div(cin, 128)) * ceil_div(columns, 128);
+    blocks = group_grid(group_chunks(g->n_rows, g->n_groups, group_chunk(g->n_rows, cin, columns)), 1) * tiles;
+  } else {
+    const int64_t runs = group_runs(g->n_rows, g->n_groups, group_few(op, g->n_rows, g->n_groups) ? 16 : 128);
+    blocks = group_grid(runs, static_cast<unsigned>(ceil_div(columns, 128)));
+  }
+  return blocks < (int64_t{1} << 22);
+}
+
+GroupK group_args(const ts_groups* g, int cin, int cout, uint32_t* flags) {
+  GroupK k{};
+  k.starts = g->starts;
+  k.rows = g->rows;
+  k.flags = flags;
+  k.n_rows = g->n_rows;
+  k.n_src = g->rows ? g->n_src : g->n_rows;
+  k.e = g->n_groups;
+  k.cin = cin;
+  k.cout = k.ldw = cout;
+  return k;
+}
+
+size_t wgrad_bytes(const ts_groups* g, int cin, int cout) {
+  return static_cast<size_t>(group_chunks(g->n_rows, g->n_groups, group_chunk(g->n_rows, cin, cout))) * cin * cout * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -198,6 +240,59 @@ ts_status ts_combine_bwd(const void* dout, const void* y, int64_t n_rows, const 
   if (st != TS_OK) return st;
   if (n > 0 && (!place || !dout || !gates || !dgates || (n_rows > 0 && (!y || !dy)))) return TS_ERR_INVALID_ARG;
   return status(launch_combine_bwd(dout, y, n_rows, place, gates, n, top, c, dtype, dy, dgates, err_flags, stream));
+}
+
+ts_status ts_group_fwd(const ts_groups* g, const void* x, int cin, const void* w, int cout, ts_dtype dtype, int glu, void* y,
+                       void* h, uint32_t* err_flags, hipStream_t stream) {
+  const ts_status st = check_groups(g, cin, cout, dtype);
+  if (st != TS_OK) return st;
+  if (!w || (h && !glu) || (g->n_rows > 0 && (!y || (!x && (!g->rows || g->n_src > 0))))) return TS_ERR_INVALID_ARG;
+  if (!grid_ok(g, kGroupFwd, cin, glu ? 2 * cout : cout)) return TS_ERR_UNSUPPORTED;
+  if (g->n_rows == 0) return TS_OK;
+  GroupK k = group_args(g, cin, cout, err_flags);
+  k.x = x;
+  k.w = w;
+  k.y = y;
+  k.h_out = h;
+  if (glu) k.ldw = 2 * cout;
+  return status(group_few(kGroupFwd, k.n_rows, k.e) ? launch_group_few(k, kGroupFwd, dtype, glu != 0, stream)
+                                                    : launch_group(k, kGroupFwd, dtype, glu != 0, stream));
+}
+
+ts_status ts_group_bwd_dgrad(const ts_groups* g, const void* dy, int cout, const void* w, int cin, ts_dtype dtype,
+                             const void* h, void* dx, uint32_t* err_flags, hipStream_t stream) {
+  const ts_status st = check_groups(g, cin, cout, dtype);
+  if (st != TS_OK) return st;
+  if (!w || (g->n_rows > 0 && (!dy || !dx))) return TS_ERR_INVALID_ARG;
+  if (!grid_ok(g, kGroupDgrad, cin, cin)) return TS_ERR_UNSUPPORTED;
+  if (g->n_rows == 0) return TS_OK;
+  GroupK k = group_args(g, cin, cout, err_flags);
+  k.dy = dy;
+  k.w = w;
+  k.h = h;
+  k.y = dx;
+  return status(group_few(kGroupDgrad, k.n_rows, k.e) ? launch_group_few(k, kGroupDgrad, dtype, h != nullptr, stream)
+                                                      : launch_group(k, kGroupDgrad, dtype, h != nullptr, stream));
+}
+
+size_t ts_group_wgrad_workspace_bytes(const ts_groups* g, int cin, int cout) {
+  return check_groups(g, cin, cout, TS_F16) == TS_OK ? wgrad_bytes(g, cin, cout) : 0;
+}
+
+ts_status ts_group_bwd_wgrad(const ts_groups* g, const void* x, int cin, const void* dy, int cout, ts_dtype dtype, float* dw,
+                             void* ws, size_t ws_bytes, uint32_t* err_flags, hipStream_t stream) {
+  const ts_status st = check_groups(g, cin, cout, dtype);
+  if (st != TS_OK) return st;
+  if (!dw || (g->n_rows > 0 && (!dy || (!x && (!g->rows || g->n_src > 0))))) return TS_ERR_INVALID_ARG;
+  if (!grid_ok(g, kGroupWgrad, cin, cout)) return TS_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < wgrad_bytes(g, cin, cout)) return TS_ERR_INVALID_ARG;
+  GroupK k = group_args(g, cin, cout, err_flags);
+  k.x = x;
+  k.dy = dy;
+  k.dw = dw;
+  k.part = static_cast<float*>(ws);
+  k.chunk = group_chunk(g->n_rows, cin, cout);
+  return status(launch_group(k, kGroupWgrad, dtype, false, stream));
 }
 
 }  // extern "C"

@@ -82,6 +82,10 @@ class TsRopeHeads(ctypes.Structure):
                 ("x", _vp), ("w", _vp), ("y", _vp), ("dy", _vp), ("dx", _vp), ("dw", _vp)]
 
 
+class TsGroups(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int32), ("n_rows", _i64), ("starts", _vp), ("rows", _vp), ("n_src", _i64)]
+
+
 def _sig(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -149,6 +153,11 @@ _lib_route_fwd = _sig("ts_route_fwd", _i32, [_vp, _i64, _i32, _i32, _i32, _i32, 
 _lib_route_bwd = _sig("ts_route_bwd", _i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp])
 _lib_combine_fwd = _sig("ts_combine_fwd", _i32, [_vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp])
 _lib_combine_bwd = _sig("ts_combine_bwd", _i32, [_vp, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp])
+_G = ctypes.POINTER(TsGroups)
+_lib_group_fwd = _sig("ts_group_fwd", _i32, [_G, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp])
+_lib_group_bwd_dgrad = _sig("ts_group_bwd_dgrad", _i32, [_G, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp])
+_lib_group_wgrad_workspace_bytes = _sig("ts_group_wgrad_workspace_bytes", _sz, [_G, _i32, _i32])
+_lib_group_bwd_wgrad = _sig("ts_group_bwd_wgrad", _i32, [_G, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _sz, _vp, _vp])
 _lib_debug_violations = _sig("ts_debug_violations", _i32, [ctypes.POINTER(_u32)])
 
 EXPORTED = ["ts_status_string", "ts_version", "ts_hash_capacity", "ts_hash_table_bytes", "ts_hash_build",
@@ -160,8 +169,8 @@ EXPORTED = ["ts_status_string", "ts_version", "ts_hash_capacity", "ts_hash_table
             "ts_conv_bwd_wgrad", "ts_conv_bwd_dgrad_noalloc", "ts_attn_workspace_bytes", "ts_attn_fwd", "ts_attn_bwd",
             "ts_act_pack", "ts_act_unpack", "ts_conv_wgrad_act8_workspace_bytes", "ts_conv_bwd_wgrad_act8", "ts_norm_fwd",
             "ts_norm_workspace_bytes", "ts_norm_bwd", "ts_rope_workspace_bytes", "ts_rope_fwd", "ts_rope_bwd",
-            "ts_route_workspace_bytes", "ts_route_fwd", "ts_route_bwd", "ts_combine_fwd", "ts_combine_bwd",
-            "ts_debug_violations"]
+            "ts_route_workspace_bytes", "ts_route_fwd", "ts_route_bwd", "ts_combine_fwd", "ts_combine_bwd", "ts_group_fwd",
+            "ts_group_bwd_dgrad", "ts_group_wgrad_workspace_bytes", "ts_group_bwd_wgrad", "ts_debug_violations"]
 
 
 class TsError(RuntimeError):
@@ -1164,6 +1173,119 @@ def route_bwd(dgates: torch.Tensor, logits: torch.Tensor, route: Route, over_all
     _check(_lib_route_bwd(dgates.data_ptr(), logits.data_ptr(), route.experts.data_ptr(), route.gates.data_ptr(), n, e,
                           _DT[logits.dtype], top, int(over_all), d.data_ptr(), _raw_stream(logits)), "ts_route_bwd")
     return d
+
+
+class Groups(NamedTuple):
+    """Grouped rows (see ts_groups in ts.h): starts int64 [groups + 1], and int32 rows of x they
+    read (None: grouped row p is row p)."""
+    starts: torch.Tensor
+    rows: Optional[torch.Tensor] = None
+
+
+def _groups(g: Groups, x: Optional[torch.Tensor], n_rows: int) -> TsGroups:
+    """Of n_rows grouped rows that read x (None: they read nothing by `rows`)."""
+    starts, rows = g.starts, g.rows
+    _need(starts.is_cuda and starts.dtype is torch.int64 and starts.is_contiguous() and starts.dim() == 1 and starts.numel() >= 2,
+          "groups: starts are int64 [groups + 1]")
+    _need(rows is None or (rows.is_cuda and rows.dtype is torch.int32 and rows.is_contiguous() and rows.shape == (n_rows,)),
+          "groups: rows are int32, one for each grouped row")
+    _need(x is None or rows is not None or x.shape[0] == n_rows, "groups: x has the grouped rows")
+    return TsGroups(starts.numel() - 1, n_rows, starts.data_ptr(), _ptr(rows), 0 if x is None else x.shape[0])
+
+
+def _experts(w: torch.Tensor, groups: TsGroups, cin: int, cout: Optional[int], like: torch.Tensor) -> None:
+    _need(w.is_cuda and w.dim() == 3 and w.is_contiguous() and w.dtype is like.dtype and w.shape[:2] == (groups.n_groups, cin)
+          and cout in (None, w.shape[2]), "groups: weights are a dense device tensor [groups][cin][cout]")
+
+
+def _group_fwd(x, w, groups, glu, want_h, err_flags):
+    _matrix(x, "group_fwd: x is a dense device matrix [n][cin]")
+    p, (n, cin), dev = x.shape[0] if groups.rows is None else groups.rows.numel(), x.shape, x.device
+    g = _groups(groups, x, p)
+    _experts(w, g, cin, None, x)
+    wide = w.shape[2]
+    _need(not glu or wide % 2 == 0, "group_glu_fwd: weights have two columns for each result")
+    cout = wide // 2 if glu else wide
+    y = torch.empty((p, cout), dtype=x.dtype, device=dev)
+    h = torch.empty((p, wide), dtype=x.dtype, device=dev) if want_h else None
+    _check(_lib_group_fwd(ctypes.byref(g), x.data_ptr(), cin, w.data_ptr(), cout, _DT[x.dtype], int(glu), y.data_ptr(), _ptr(h),
+                          _flag_ptr(err_flags), _raw_stream(x)), "ts_group_fwd")
+    return y, h
+
+
+def group_fwd(x: torch.Tensor, w: torch.Tensor, groups: Groups, err_flags: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """y[p] = x[rows[p]] w[e] for the grouped rows p of each group e (see ts_groups in ts.h)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return group_fwd(x, w, groups, err_flags)
+    return _group_fwd(x, w, groups, False, False, err_flags)[0]
+
+
+def group_glu_fwd(x: torch.Tensor, w: torch.Tensor, groups: Groups, want_h: bool = False,
+                  err_flags: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(silu(a) b, h): a and b are the first and the last half of the columns of group_fwd, and h is
+    both, for the backward pass (None unless want_h)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return group_glu_fwd(x, w, groups, want_h, err_flags)
+    return _group_fwd(x, w, groups, True, want_h, err_flags)
+
+
+def _group_dgrad(dy, w, h, groups, err_flags, into=None):
+    _matrix(dy, "group_dgrad: dy is a dense device matrix [grouped rows][cout]")
+    p, cout = dy.shape
+    g = _groups(Groups(groups.starts), None, p)
+    _need(w.dim() == 3, "groups: weights are a dense device tensor [groups][cin][cout]")
+    cin = w.shape[1]
+    _experts(w, g, cin, cout, dy)
+    if h is not None:
+        _matrix(h, "group_glu_dgrad: h is what group_glu_fwd returned", (p, 2 * cin), dy.dtype)
+    dx = torch.empty((p, cin if h is None else 2 * cin), dtype=dy.dtype, device=dy.device) if into is None else into
+    if into is not None:
+        _matrix(into, "group_glu_dgrad: the result is like h", (p, 2 * cin), dy.dtype)
+    _check(_lib_group_bwd_dgrad(ctypes.byref(g), dy.data_ptr(), cout, w.data_ptr(), cin, _DT[dy.dtype], _ptr(h), dx.data_ptr(),
+                                _flag_ptr(err_flags), _raw_stream(dy)), "ts_group_bwd_dgrad")
+    return dx
+
+
+def group_dgrad(dy: torch.Tensor, w: torch.Tensor, groups: Groups, err_flags: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """Gradient of what each grouped row read; where rows of x are read by several, combine_fwd
+    without gates adds them up."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return group_dgrad(dy, w, groups, err_flags)
+    return _group_dgrad(dy, w, None, groups, err_flags)
+
+
+def group_glu_dgrad(dy: torch.Tensor, w: torch.Tensor, h: torch.Tensor, groups: Groups, err_flags: Optional[torch.Tensor] = None,
+                    into: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of h = (a, b), from that of the product with w that silu(a) b went into; written
+    to `into` (which may be h) or to a new matrix."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return group_glu_dgrad(dy, w, h, groups, err_flags, into)
+    return _group_dgrad(dy, w, h, groups, err_flags, into)
+
+
+def group_wgrad(x: torch.Tensor, dy: torch.Tensor, groups: Groups, err_flags: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """float32 gradient of the weights [groups][cin][cout] from x and the gradient of group_fwd's result."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return group_wgrad(x, dy, groups, err_flags)
+    _matrix(x, "group_wgrad: x is a dense device matrix [n][cin]")
+    _matrix(dy, "group_wgrad: dy is a dense device matrix [grouped rows][cout]", dtype=x.dtype)
+    p, cout = dy.shape
+    g, cin = _groups(groups, x, p), x.shape[1]
+    ref = ctypes.byref(g)
+    dw = torch.empty((g.n_groups, cin, cout), dtype=torch.float32, device=x.device)
+    size = _lib_group_wgrad_workspace_bytes(ref, cin, cout)
+    ws = torch.empty(max(size, 1), dtype=torch.uint8, device=x.device)
+    _check(_lib_group_bwd_wgrad(ref, x.data_ptr(), cin, dy.data_ptr(), cout, _DT[x.dtype], dw.data_ptr(), ws.data_ptr(), size,
+                                _flag_ptr(err_flags), _raw_stream(x)), "ts_group_bwd_wgrad")
+    return dw
 
 
 def _place(place: torch.Tensor, gates: Optional[torch.Tensor]) -> None:

@@ -745,6 +745,50 @@ ts_status ts_route_fwd(const void* logits, int64_t n, int n_experts, ts_dtype dt
 ts_status ts_route_bwd(const float* dgates, const void* logits, const int32_t* experts, const float* gates, int64_t n,
                        int n_experts, ts_dtype dtype, int top, int over_all, void* dlogits, hipStream_t stream);
 
+/* Products grouped by expert.  Group e owns the grouped rows [starts[e], starts[e+1]); with
+ * `rows` grouped row p reads row rows[p] of x, without it row p itself.
+ *   forward        y[p] = x[rows[p]] W[e]; with glu W[e] is [cin][2 cout] and
+ *                  y[p] = silu(a) b of a = the first cout columns of x W, b = the others
+ *   dgrad          dx[p] = dy[p] W[e]^T, one row for each grouped row (their sum over `rows` is
+ *                  ts_combine_fwd without gates); with h = (a, b) of the layer before
+ *                  dx[p] = dy[p] W[e]^T times the derivatives of silu(a) b: [n_rows][2 cin]
+ *   wgrad          dW[e] = sum over its grouped rows of x[rows[p]]^T dy[p], in fp32
+ * Lengths may be of any mix, zero among them.  Grouped rows that no group owns get zeros in
+ * y, h and dx, and do not enter dW; a group without rows has dW = 0.  Starts that
+ * decrease or leave [0, n_rows], and rows[p] outside [0, n_src) (read as zeros), raise
+ * TS_FLAG_RANGE in err_flags (may be NULL): no access leaves the buffers; after bad starts
+ * the results are undefined.
+ * fp16 or bf16 (TS_F32 is TS_ERR_UNSUPPORTED); sums are fp32 and rounded once, at the
+ * end.  Any channel counts; multiples of 8 with 16-byte aligned matrices are the fast ones.  No
+ * atomics: the same bits on every run. */
+typedef struct ts_groups {
+  int32_t n_groups;
+  int64_t n_rows;        /* grouped rows                                         */
+  const int64_t* starts; /* device [n_groups + 1]                                */
+  const int32_t* rows;   /* device [n_rows], or NULL                             */
+  int64_t n_src;         /* rows of x; read with `rows` only                     */
+} ts_groups;
+
+/* x: device [n_src or n_rows][cin], w: device [n_groups][cin][cout or 2 cout], y: device
+ * [n_rows][cout]; h (glu only, may be NULL): device [n_rows][2 cout], (a, b) for the backward
+ * pass.  Errors: TS_ERR_INVALID_ARG (null pointers, sizes, channels outside [1, 65536], h
+ * without glu), TS_ERR_UNSUPPORTED (fp32, more than 4096 groups, about 2^22 tiles of 128 x 128
+ * results or more), TS_ERR_HIP. */
+ts_status ts_group_fwd(const ts_groups* g, const void* x, int cin, const void* w, int cout, ts_dtype dtype, int glu, void* y,
+                       void* h, uint32_t* err_flags, hipStream_t stream);
+
+/* dy: device [n_rows][cout], w: device [n_groups][cin][cout], dx: device [n_rows][cin]; with
+ * h (device [n_rows][2 cin]) dx is [n_rows][2 cin] and may be h.  `rows` is not read.  Errors
+ * as ts_group_fwd. */
+ts_status ts_group_bwd_dgrad(const ts_groups* g, const void* dy, int cout, const void* w, int cin, ts_dtype dtype,
+                             const void* h, void* dx, uint32_t* err_flags, hipStream_t stream);
+
+/* dw: device float [n_groups][cin][cout], overwritten.  The rows of a group are summed in
+ * runs, and those in a fixed order; ws (device) holds ts_group_wgrad_workspace_bytes. */
+size_t ts_group_wgrad_workspace_bytes(const ts_groups* g, int cin, int cout);
+ts_status ts_group_bwd_wgrad(const ts_groups* g, const void* x, int cin, const void* dy, int cout, ts_dtype dtype, float* dw,
+                             void* ws, size_t ws_bytes, uint32_t* err_flags, hipStream_t stream);
+
 /* Sum of what a row's experts returned, from the grouped rows y[n_rows][c]:
  *   out[t] = sum over j of gates[t][j] y[place[t][j]]     (gates NULL: 1)
  * place: device int32 [n][top], -1: nothing; any other entry outside [0, n_rows) raises
