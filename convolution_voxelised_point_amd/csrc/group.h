@@ -78,12 +78,6 @@ struct GroupTile {
   int count;          // and how many it has
 };
 
-__device__ __forceinline__ int64_t lane_i64(int64_t x, int lane) {
-  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(x), lane);
-  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(static_cast<uint64_t>(x) >> 32), lane);
-  return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
-}
-
 // Grouped rows [*a, *b) of expert e (empty for e >= k.e); starts that decrease or leave [0,
 // n_rows] are clamped, so no row outside is touched, and raise the flag.
 __device__ __forceinline__ void expert_rows(const GroupK& k, int e, int64_t* a, int64_t* b) {
@@ -95,70 +89,104 @@ __device__ __forceinline__ void expert_rows(const GroupK& k, int e, int64_t* a, 
   if ((s != *a || t != *b) && k.flags) atomicOr(k.flags, TS_FLAG_RANGE);
 }
 
-__device__ __forceinline__ int runs_of(int64_t a, int64_t b, int len) { return static_cast<int>((b - a + len - 1) / len); }
-
-// Runs of all experts.  This and find_tile are called by whole waves; their results are the
-// same in every lane.  (64-bit: starts that make the experts overlap may add up to many.)
-__device__ __forceinline__ int64_t total_runs(const GroupK& k, int len) {
-  const int lane = threadIdx.x & 63;
-  int64_t n = 0;
-  for (int e0 = 0; e0 < k.e; e0 += 64) {
-    int64_t a, b;
-    expert_rows(k, e0 + lane, &a, &b);
-    n += runs_of(a, b, len);
-  }
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) n += __shfl_xor(n, m);
-  return lane_i64(n, 0);
+// (At most 2^24, more than 2^31 rows make in runs of 128; only starts that make the experts
+// overlap could add up to more than 2^31 of them otherwise.)
+__device__ __forceinline__ int runs_of(int64_t a, int64_t b, int len) {
+  const int64_t n = (b - a + len - 1) / len;
+  return n < (1 << 24) ? static_cast<int>(n) : 1 << 24;
 }
 
-__device__ __forceinline__ GroupTile find_tile(const GroupK& k, int64_t index, int len) {
-  const int lane = threadIdx.x & 63;
-  GroupTile t{};
-  t.e = -1;
-  int64_t before = 0;
-  for (int e0 = 0; e0 < k.e; e0 += 64) {
-    int64_t a, b;
-    expert_rows(k, e0 + lane, &a, &b);
-    const int n = runs_of(a, b, len);
-    int64_t inc = n;
+// Finds runs.  Used by all waves of a block, with the same result in every lane; of up to 64
+// experts each one's rows are kept in LDS.
+struct GroupLane {
+  int a, b, n, inc;  // an expert's rows, its runs, and runs up to and with it
+};
+struct GroupFinder {
+  GroupLane* kept;
+  int len;
+  int64_t total;  // all runs
+
+  __device__ __forceinline__ GroupLane batch(const GroupK& k, int e0) const {
+    const int lane = threadIdx.x & 63;
+    int64_t r0, r1;
+    expert_rows(k, e0 + lane, &r0, &r1);
+    GroupLane l;
+    l.a = static_cast<int>(r0);
+    l.b = static_cast<int>(r1);
+    l.n = runs_of(r0, r1, len);
+    l.inc = l.n;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
-      const int64_t up = __shfl_up(inc, m);
-      if (lane >= m) inc += up;
+      const int up = __shfl_up(l.inc, m);
+      if (lane >= m) l.inc += up;
     }
-    const uint64_t hit = __ballot(index < before + inc);
-    if (hit) {
-      const int l = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-      t.e = e0 + l;
-      t.count = __builtin_amdgcn_readlane(n, l);
-      t.first = before + lane_i64(inc, l) - t.count;
-      const int64_t r0 = lane_i64(a, l), r1 = lane_i64(b, l);
-      t.row0 = r0 + (index - t.first) * len;
-      t.rows = r1 - t.row0 < len ? static_cast<int>(r1 - t.row0) : len;
-      return t;
-    }
-    before += lane_i64(inc, 63);
+    return l;
   }
-  return t;
-}
+  // lds: 64 entries.
+  __device__ __forceinline__ GroupFinder(const GroupK& k, int run_rows, GroupLane* lds) : kept(lds), len(run_rows), total(0) {
+    for (int e0 = 0; e0 < k.e; e0 += 64) {
+      const GroupLane l = batch(k, e0);
+      total += __builtin_amdgcn_readlane(l.inc, 63);
+      if (k.e <= 64) kept[threadIdx.x & 63] = l;  // (every wave writes the same, and reads what it wrote itself)
+    }
+  }
+  __device__ __forceinline__ GroupTile find(const GroupK& k, int64_t index) const {
+    GroupTile t{};
+    t.e = -1;
+    int64_t before = 0;
+    for (int e0 = 0; e0 < k.e; e0 += 64) {
+      const GroupLane own = k.e > 64 ? batch(k, e0) : kept[threadIdx.x & 63];
+      const uint64_t hit = __ballot(index - before < own.inc);
+      if (hit) {
+        const int l = __ffsll(static_cast<unsigned long long>(hit)) - 1;
+        t.e = e0 + l;
+        t.count = __builtin_amdgcn_readlane(own.n, l);
+        t.first = before + __builtin_amdgcn_readlane(own.inc, l) - t.count;
+        const int64_t r0 = __builtin_amdgcn_readlane(own.a, l), r1 = __builtin_amdgcn_readlane(own.b, l);
+        t.row0 = r0 + (index - t.first) * len;
+        t.rows = r1 - t.row0 < len ? static_cast<int>(r1 - t.row0) : len;
+        return t;
+      }
+      before += __builtin_amdgcn_readlane(own.inc, 63);
+    }
+    return t;
+  }
+};
 
-// Grouped rows that no expert owns get zeros: run `index` of `len` of them, `cols` wide from
-// column c0, in a matrix of `width` columns.
+// Grouped rows that no expert owns.
+struct GroupRest {
+  int64_t before, last, n;  // rows before the first expert's; the first behind the last one's; all of them
+};
+__device__ __forceinline__ GroupRest rows_unowned(const GroupK& k) {
+  GroupRest r;
+  int64_t none;
+  expert_rows(k, 0, &r.before, &none);
+  expert_rows(k, k.e - 1, &none, &r.last);
+  r.n = r.before + k.n_rows - r.last;
+  return r;
+}
+// They get zeros: those from r0 on, `len` at most, `cols` columns from c0 on in a matrix of
+// `width` columns.
 template <typename T>
-__device__ __forceinline__ void zero_unowned(const GroupK& k, int64_t index, int len, T* y, int width, int c0, int cols) {
-  int64_t a, b, last, none;
-  expert_rows(k, 0, &a, &none);
-  expert_rows(k, k.e - 1, &none, &last);
-  b = k.n_rows - last;
-  const int64_t r0 = index * len;
-  if (r0 >= a + b) return;
-  const int n = static_cast<int>(a + b - r0 < len ? a + b - r0 : len);
+__device__ __forceinline__ void zero_unowned(const GroupRest& rest, int64_t r0, int len, T* y, int width, int c0, int cols) {
+  const int n = static_cast<int>(rest.n - r0 < len ? rest.n - r0 : len);
   const int w = width - c0 < cols ? width - c0 : cols;
   for (int i = threadIdx.x; i < n * w; i += blockDim.x) {
     const int r = i / w;
-    const int64_t at = r0 + r < a ? r0 + r : last + (r0 + r - a);
+    const int64_t at = r0 + r < rest.before ? r0 + r : rest.last + (r0 + r - rest.before);
     y[at * width + c0 + (i - r * w)] = static_cast<T>(0.f);
+  }
+}
+// Of the results of op: columns n0.. (`cols` of them) of y, and of what goes with it.
+template <typename T, GroupOp OP, bool GLU>
+__device__ __forceinline__ void zero_results(const GroupK& k, const GroupRest& rest, int64_t r0, int len, int N, int n0, int cols) {
+  T* y = static_cast<T*>(k.y);
+  if (N - n0 < cols) cols = N - n0;
+  zero_unowned(rest, r0, len, y, OP == kGroupDgrad && GLU ? 2 * N : N, n0, cols);
+  if (GLU) {
+    T* h = OP == kGroupDgrad ? y : static_cast<T*>(k.h_out);
+    if (h && OP == kGroupFwd) zero_unowned(rest, r0, len, h, 2 * N, n0, cols);
+    if (h) zero_unowned(rest, r0, len, h, 2 * N, N + n0, cols);
   }
 }
 

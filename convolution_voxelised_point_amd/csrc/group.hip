@@ -5,15 +5,19 @@
 //   input gradient   dx[p] = dy[p] W[e]^T           reduced over cout
 //   weight gradient  dW[e] = sum over its p of x[rows[p]]^T dy[p]
 //
-// One kernel for the three: a tile of BM x BN results is reduced over steps of 32.  Both
-// operands' steps are copied straight into LDS (16 bytes a lane, no registers), four
-// steps in a ring, three of them in flight while one is multiplied, so a step takes one
-// barrier.  An operand whose rows run along the reduction (x and dy of the first two, W of
-// the second) is read from LDS as it lies; one whose rows run across it is read with the
-// transposing LDS reads.  Chunks of 16 bytes are stored xor-ed with their row so that
-// neither read meets a bank twice.  Gathered rows cost nothing: every lane names its
-// own source anyway.  Sources past the matrix (the last step's, rows that are not there)
-// are 16 bytes of zeros.
+// One kernel for the three: a tile of BM x BN results is reduced over steps of 64.  Both
+// operands' steps are copied straight into LDS (16 bytes a lane, no registers; 128 bytes of a
+// row at once, whole lines), into two places in turn.  A step is done in parts, 32 of a wave's
+// rows over 32 of the reduction each: while one is multiplied the fragments of the next are
+// read, the first ones of the next step among them, so matrix instructions wait neither for
+// LDS nor behind the step's one barrier.  Behind it the step's place is free and the copies of
+// the step after the next start.  Blocks stay for several tiles, and the next one's first copies
+// are under way while a tile's results are written.  An operand whose rows run along the
+// reduction (x and dy of the first two, W of the second) is read from LDS as it lies; one whose
+// rows run across it is read with the transposing LDS reads.  Chunks of 16 bytes are stored
+// xor-ed with their row so that neither read meets a bank twice.  Gathered rows cost nothing:
+// every lane names its own source anyway.  Sources past the matrix (the last step's, rows that
+// are not there) lie behind their buffer's end and read as zeros.
 //
 // Tiles are found from the starts on the device, expert by expert, so lengths of any mix
 // share one launch and nothing is read back.  Blocks of one XCD take neighbouring tiles, in
@@ -27,17 +31,31 @@
 namespace ts {
 namespace {
 
-constexpr int kStep = 32, kRing = 4;
+constexpr int kStep = 64;
+constexpr int kRowHalf = 1024;  // row numbers of the weight gradient in half of their place in LDS
 
-__device__ const gu32x4 kZeros = {0u, 0u, 0u, 0u};
-
-// 16 bytes per lane from memory into LDS: lane l writes dst + 16 l (dst is the same in the wave).
-// Not a template: clang emits no host launch stub for a kernel template whose body names
-// this builtin directly (nor for the transposing reads).
+// 16 bytes per lane from a buffer into LDS: lane l writes dst + 16 l (dst is the same in the
+// wave), zeros where its offset lies behind the buffer's end.  Not a template: clang emits no host
+// launch stub for a kernel template whose body names this builtin directly (nor for the
+// transposing reads).  (Buffer instructions: after the global ones every wait for LDS reads
+// is one for all of them.)
+constexpr uint32_t kNowhere = ~0u;
 typedef __attribute__((address_space(3))) gu32x4 lds_gu32x4;
-__device__ __forceinline__ void to_lds(const void* src, char* dst) {
-  __builtin_amdgcn_global_load_lds(static_cast<const gu32x4*>(src), (lds_gu32x4*)dst, 16, 0, 0);
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, int64_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v)), hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0,
+                                           __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00020000);
 }
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t buf, uint32_t off, char* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_gu32x4*)dst, 16, static_cast<int>(off), 0, 0, 0);
+}
+// 4 bytes per lane: lane l writes dst[l].
+__device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t buf, uint32_t off, int32_t* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_u32*)dst, 4, static_cast<int>(off), 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t further(uint32_t off, uint32_t by) { return __builtin_elementwise_add_sat(off, by); }  // nowhere stays nowhere
 // In each 16-lane group lane q + 4m names 4 consecutive values and lane 4q + r receives value r
 // of the runs named by lanes q, q+4, q+8, q+12.
 typedef __attribute__((__vector_size__(4 * sizeof(__fp16)))) __fp16 gh4;
@@ -56,6 +74,7 @@ __device__ __forceinline__ void wait_copies() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | ((N >> 4) << 14));
 }
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -63,12 +82,26 @@ __device__ __forceinline__ void barrier() {
 }
 
 // Where chunk ch (8 values) of row r lies within its row.
-// Rows along the reduction: 4 chunks, 16 rows a read: rows 2i and 2i + 1 fill 128 bytes.
-__device__ __forceinline__ int along_at(int r, int ch) { return ch ^ ((r >> 1) & 3); }
+// Rows along the reduction: 8 chunks, one of each of 16 rows a read.
+__device__ __forceinline__ int along_at(int r, int ch) { return ch ^ (r & 7); }
 // Rows across it: a read takes 32 bytes of rows 8g + m and 8g + 4 + m.
 __device__ __forceinline__ int across_at(int r, int ch) { return ch ^ (((r & 3) << 1) | (((r >> 3) & 1) << 3)); }
 
-// (only starts that make the experts overlap have more runs than there are partial sums)
+// The value as if it were new: what is computed from it is not kept in registers over the steps.
+template <typename V>
+__device__ __forceinline__ V fresh(V v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+// Lane group g of 4 holds elements 4g..4g+3 of two blocks of 16 columns, p and q: afterwards
+// it holds 8 consecutive ones, group 0 and 1 of p's, 2 and 3 of q's.
+__device__ __forceinline__ void join8(unsigned& p, unsigned& q) {
+  const auto a = __builtin_amdgcn_permlane32_swap(p, q, false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[1], false, false);
+  p = b[0];
+  q = b[1];
+}
+// Partial sums of the weight gradient that there is room for.
 __device__ __forceinline__ int64_t group_chunks_on_device(const GroupK& k) { return k.n_rows / k.chunk + k.e; }
 
 // A loose 16 bytes: columns c0.. of a row of `width` values, zeros past it.
@@ -89,155 +122,196 @@ template <typename T, int R, int NT, int ACROSS>
 struct Operand {
   static constexpr int kChunks = R * kStep / 8;
   static constexpr int kCopies = kChunks / NT;
-  static constexpr int kPerRow = ACROSS ? R / 8 : 4;
+  static constexpr int kPerRow = ACROSS ? R / 8 : kStep / 8;
   static constexpr int kBytes = R * kStep * 2;
   static_assert(kChunks % NT == 0, "whole copies");
 };
 
-// BM x BN results a block, WM x WN waves.  VEC: rows in whole, aligned 16-byte chunks;
+// A tile and where this lane's copies of its first step come from.
+template <int CA, int CB>
+struct TileSource {
+  GroupTile t;
+  int m0, n0, steps, K, run;
+  // VEC: offsets within the buffers.  Otherwise: rows of x or dy (-1: none); columns of W or dy
+  uint32_t va[CA], vb[CB];
+};
+
+// BM x BN results a tile, WM x WN waves.  VEC: rows in whole, aligned 16-byte chunks;
 // otherwise chunks go through registers.
 template <typename T, GroupOp OP, bool GLU, int BM, int BN, int WM, int WN, bool VEC>
-__global__ __launch_bounds__(WM* WN * 64) void k_group(const GroupK k) {
+__global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) void k_group(const GroupK k) {
   constexpr int NT = WM * WN * 64;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   constexpr bool A_ACROSS = OP == kGroupWgrad, B_ACROSS = OP != kGroupDgrad;
   typedef Operand<T, BM, NT, A_ACROSS> OA;
   typedef Operand<T, BN, NT, B_ACROSS> OB;
   constexpr int CA = OA::kCopies, CB = OB::kCopies;
-  __shared__ __attribute__((aligned(16))) char lds_a[kRing * OA::kBytes];
-  __shared__ __attribute__((aligned(16))) char lds_b[kRing * OB::kBytes];
+  constexpr int kCols = GLU && OP == kGroupFwd ? BN / 2 : BN;
+  __shared__ __attribute__((aligned(16))) char lds_a[2 * OA::kBytes];
+  __shared__ __attribute__((aligned(16))) char lds_b[2 * OB::kBytes];
+  __shared__ int32_t lds_rows[A_ACROSS ? 2 * kRowHalf : 1];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int len = OP == kGroupWgrad ? k.chunk : BM;
   const int along = OP == kGroupWgrad ? ceil_div(k.cin, BM) : 1;  // weight gradient: tiles along cin of each run
-  const int64_t runs = total_runs(k, len);
-  const GroupBlock block = group_block(runs, k.n_tiles * along);
-  const int N = OP == kGroupDgrad ? k.cin : k.cout;  // columns of the result
-  constexpr int kCols = GLU && OP == kGroupFwd ? BN / 2 : BN;
-  if (block.at < 0) {
-    if (OP == kGroupWgrad || block.spare < 0) return;
-    const int64_t run = block.spare / k.n_tiles;
-    const int n0 = static_cast<int>(block.spare - run * k.n_tiles) * kCols, cols = N - n0 < kCols ? N - n0 : kCols;
-    T* y = static_cast<T*>(k.y);
-    zero_unowned(k, run, BM, y, OP == kGroupDgrad && GLU ? 2 * N : N, n0, cols);
-    if (GLU) {
-      T* h = OP == kGroupDgrad ? y : static_cast<T*>(k.h_out);
-      if (h && OP == kGroupFwd) zero_unowned(k, run, BM, h, 2 * N, n0, cols);
-      if (h) zero_unowned(k, run, BM, h, 2 * N, N + n0, cols);
-    }
-    return;
-  }
-  // row tiles in fours (weight gradient: a run's tiles one after the other)
-  constexpr int64_t kHigh = OP == kGroupWgrad ? 1 : 4;
-  const int64_t band = block.at / (kHigh * k.n_tiles), in = block.at - band * kHigh * k.n_tiles;
-  const int64_t rows = runs * along - band * kHigh, high = rows < kHigh ? rows : kHigh;
-  const int nt = static_cast<int>(in / high), n0 = nt * kCols;
-  const int64_t mt = band * kHigh + (in - nt * high), run = mt / along;
-  const int m0 = static_cast<int>(mt - run * along) * BM;
-  const GroupTile t = find_tile(k, run, len);
-  if (t.e < 0 || (OP == kGroupWgrad && run >= group_chunks_on_device(k))) return;
-  const int K = OP == kGroupFwd ? k.cin : OP == kGroupDgrad ? k.cout : t.rows;
-  const int steps = ceil_div(K, kStep);
-  const T* zeros = reinterpret_cast<const T*>(&kZeros);
-  const T* wt = static_cast<const T*>(k.w) + static_cast<int64_t>(t.e) * k.cin * k.ldw;
-
-  // Source of this lane's copies: of the first step, and how far the next one's lies.  at: what
-  // is compared with K (a row, or a first column).
-  const T* pa[CA];
-  const T* pb[CB];
-  int at_a[CA], at_b[CB], col_a[CA], col_b[CB];
-#pragma unroll
-  for (int i = 0; i < CA; ++i) {
-    const int id = i * NT + tid, r = id / OA::kPerRow, pos = id % OA::kPerRow;
-    if (A_ACROSS) {
-      const int c = m0 + across_at(r, pos) * 8;
-      at_a[i] = r;
-      col_a[i] = c < k.cin ? c : -1;
-      pa[i] = nullptr;  // found row by row
-    } else {
-      const int ch = along_at(r, pos);
-      const int64_t row = t.row0 + (r < t.rows ? r : 0);  // rows past the tile: any, their results go nowhere
-      int64_t src = row;
-      if (OP == kGroupFwd && k.rows) {
-        src = k.rows[row];
-        if (src < 0 || src >= k.n_src) {
-          if (k.flags) atomicOr(k.flags, TS_FLAG_RANGE);
-          src = -1;
-        }
-      }
-      at_a[i] = ch * 8;
-      col_a[i] = src < 0 ? -1 : 0;
-      pa[i] = static_cast<const T*>(OP == kGroupFwd ? k.x : k.dy) + (src < 0 ? 0 : src) * K + ch * 8;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < CB; ++i) {
-    const int id = i * NT + tid, r = id / OB::kPerRow, pos = id % OB::kPerRow;
-    if (B_ACROSS) {
-      const int ch = across_at(r, pos);
-      int c, width;
-      if (GLU) {  // 16 columns of a, 16 of b
-        c = n0 + (ch >> 2) * 16 + (ch & 1) * 8;
-        width = k.cout;
-        col_b[i] = c < width ? c + ((ch >> 1) & 1) * k.cout : -1;
-      } else {
-        c = n0 + ch * 8;
-        col_b[i] = c < k.cout ? c : -1;
-      }
-      at_b[i] = r;
-      pb[i] = OP == kGroupWgrad ? static_cast<const T*>(k.dy) + (t.row0 + r) * k.cout : wt + static_cast<int64_t>(r) * k.ldw;
-    } else {
-      const int ch = along_at(r, pos), n = n0 + r;
-      at_b[i] = ch * 8;
-      col_b[i] = n < N ? 0 : -1;
-      pb[i] = wt + static_cast<int64_t>(n < N ? n : 0) * k.ldw + ch * 8;
-    }
-  }
-
-  // one lane's 16 bytes of step s: their address, or the zeros'
-  auto src_a = [&](int i, int s) -> const T* {
-    const int at = at_a[i] + s * kStep;
-    if (A_ACROSS) {
-      if (at >= K || col_a[i] < 0) return zeros;
-      const int64_t p = t.row0 + at;
-      int64_t row = p;
-      if (k.rows) {
-        row = k.rows[p];
-        if (row < 0 || row >= k.n_src) {
-          if (k.flags) atomicOr(k.flags, TS_FLAG_RANGE);
-          return zeros;
-        }
-      }
-      return static_cast<const T*>(k.x) + row * k.cin + col_a[i];
-    }
-    return at < K && col_a[i] >= 0 ? pa[i] + s * kStep : zeros;
+  const int N = OP == kGroupDgrad ? k.cin : k.cout;               // columns of the result
+  __shared__ GroupLane lds_lanes[64];
+  GroupFinder finder(k, OP == kGroupWgrad ? k.chunk : BM, lds_lanes);
+  // (only starts that make the experts overlap have more runs than were planned for; 32 bits hold
+  // all the tiles there are)
+  const int64_t planned = OP == kGroupWgrad ? group_chunks_on_device(k) : k.n_rows / BM + k.e;
+  const int runs = static_cast<int>(finder.total < planned ? finder.total : planned);
+  // tiles of this block: those of one XCD are neighbours (blocks go to the 8 XCDs in turn)
+  const int n_tiles = k.n_tiles, total = runs * along * n_tiles, per_xcd = (total + 7) / 8;
+  const int xcd_end = ((blockIdx.x & 7) + 1) * per_xcd, end = xcd_end < total ? xcd_end : total;
+  // This lane's copies: the row of the operand's tile, and the chunk of it.  Of the next copy the
+  // row is NT / kPerRow further; the chunk is the same for rows 16 apart, and two take turns
+  // for rows 8 apart.
+  constexpr int NEXT_A = NT / OA::kPerRow, NEXT_B = NT / OB::kPerRow;
+  static_assert(NEXT_A % 8 == 0 && NEXT_B % 8 == 0, "rows 8 apart have the same places, or two in turn");
+  constexpr int TURN_A = A_ACROSS && NEXT_A % 16 ? 2 : 1, TURN_B = B_ACROSS && NEXT_B % 16 ? 2 : 1;
+  typedef TileSource<A_ACROSS ? 1 : CA, OP == kGroupDgrad ? 1 : TURN_B> Source;
+  // (computed where they are used: the accumulators leave few registers to keep them in)
+  auto row_a = [&]() { return fresh(tid) / OA::kPerRow; };
+  auto row_b = [&]() { return fresh(tid) / OB::kPerRow; };
+  auto chunk_a = [&](int i) {
+    const int t = fresh(tid), r = t / OA::kPerRow;
+    return A_ACROSS ? across_at(r + i % TURN_A * NEXT_A, t % OA::kPerRow) : along_at(r, t % 8);
   };
-  auto src_b = [&](int i, int s) -> const T* {
-    const int at = at_b[i] + s * kStep;
-    if (at >= K || col_b[i] < 0) return zeros;
-    return B_ACROSS ? pb[i] + static_cast<int64_t>(s) * kStep * (OP == kGroupWgrad ? k.cout : k.ldw) + col_b[i] : pb[i] + s * kStep;
+  auto chunk_b = [&](int i) {
+    const int t = fresh(tid), r = t / OB::kPerRow;
+    return B_ACROSS ? across_at(r + i % TURN_B * NEXT_B, t % OB::kPerRow) : along_at(r, t % 8);
   };
+  // its first column in the tile; with glu 16 columns of a, then 16 of b
+  auto col_b = [&](int i) {
+    const int ch = chunk_b(i);
+    return GLU && B_ACROSS ? (ch >> 2) * 16 + (ch & 1) * 8 : ch * 8;
+  };
+
+  auto set_up = [&](Source& x, int tile) {
+    // row tiles in fours (weight gradient: a run's tiles one after the other)
+    constexpr int kHigh = OP == kGroupWgrad ? 1 : 4;
+    const int band = tile / (kHigh * n_tiles), in = tile - band * kHigh * n_tiles;
+    const int rows = runs * along - band * kHigh, high = rows < kHigh ? rows : kHigh;
+    const int nt = in / high, mt = band * kHigh + (in - nt * high);
+    x.n0 = nt * kCols;
+    x.run = mt / along;
+    x.m0 = (mt - x.run * along) * BM;
+    x.t = finder.find(k, x.run);
+    x.K = OP == kGroupFwd ? k.cin : OP == kGroupDgrad ? k.cout : x.t.rows;
+    x.steps = ceil_div(x.K, kStep);
+    if constexpr (!A_ACROSS) {
+#pragma unroll
+      for (int i = 0; i < CA; ++i) {
+        const int r = row_a() + i * NEXT_A;
+        int32_t src = r < x.t.rows ? r : -1;  // from the tile's first row on
+        if (OP == kGroupFwd && k.rows) {
+          if (r < x.t.rows) {
+            src = k.rows[x.t.row0 + r];
+            if (src < 0 || src >= k.n_src) {
+              if (k.flags) atomicOr(k.flags, TS_FLAG_RANGE);
+              src = -1;
+            }
+          }
+        }
+        x.va[i] = !VEC || src < 0 ? static_cast<uint32_t>(src)
+                                  : static_cast<uint32_t>(src) * static_cast<uint32_t>(x.K * 2) + static_cast<uint32_t>(chunk_a(0) * 16);
+      }
+    }
+    if constexpr (OP == kGroupDgrad) {
+      x.vb[0] = static_cast<uint32_t>(row_b() * k.ldw * 2 + chunk_b(0) * 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < TURN_B; ++i) {
+        const int c = x.n0 + col_b(i), at = c + (GLU ? ((chunk_b(i) >> 1) & 1) * k.cout : 0);
+        x.vb[i] = c >= k.cout ? kNowhere : static_cast<uint32_t>(VEC ? (row_b() * k.ldw + at) * 2 : at);
+      }
+    }
+  };
+
+  // Weight gradient: which rows of x are read.  Their numbers go through LDS, kRowHalf of them at
+  // once; a lane reads those of its next copies with the fragments.
+  int32_t row_ids[A_ACROSS ? CA : 1];
+  auto fetch_rows = [&](const Source& x, int s) {
+    if constexpr (A_ACROSS) {
+      if (!k.rows) return;
+#pragma unroll
+      for (int i = 0; i < CA; ++i) row_ids[i] = lds_rows[(row_a() + i * NEXT_A + s * kStep) & (2 * kRowHalf - 1)];
+    }
+  };
+  // those from `from` on (a multiple of kRowHalf) on their way into LDS
+  auto copy_rows = [&](const Source& x, int from) {
+    if constexpr (A_ACROSS) {
+      if (!k.rows) return;
+#pragma unroll
+      for (int i = 0; i < kRowHalf / NT; ++i) {
+        const int at = from + i * NT + wave * 64;
+        if (at < x.K) to_lds4(buffer_of(k.rows + x.t.row0, static_cast<int64_t>(x.K) * 4), (at + lane) * 4, &lds_rows[at & (2 * kRowHalf - 1)]);
+      }
+    }
+  };
+  // Copies of step s.  `in` is the same for all of a lane's copies where rows run along.
   gu32x4 ra[VEC ? 1 : CA], rb[VEC ? 1 : CB];
-  auto copy = [&](int s, int slot) {
+  auto copy_a = [&](const Source& x, int s, int slot) {
+    const int from = s * kStep, left = x.K - from;
+    const T* base = static_cast<const T*>(OP == kGroupDgrad ? k.dy : k.x);
+    if constexpr (A_ACROSS) {
+      const int64_t first = k.rows ? 0 : x.t.row0 + from;
+      const __amdgpu_buffer_rsrc_t buf =
+          buffer_of(base + first * k.cin, (k.rows ? k.n_src : static_cast<int64_t>(left < kStep ? left : kStep)) * k.cin * 2);
 #pragma unroll
-    for (int i = 0; i < CA; ++i) {
-      const T* p = src_a(i, s);
-      if constexpr (VEC) {
-        to_lds(p, lds_a + slot * OA::kBytes + (i * NT + wave * 64) * 16);
-      } else {
-        const int left = p == zeros ? 8 : A_ACROSS ? k.cin - col_a[i] : K - at_a[i] - s * kStep;
-        ra[i] = load_loose(p, 0, left);
+      for (int i = 0; i < CA; ++i) {
+        const int r = row_a() + i * NEXT_A, c = x.m0 + chunk_a(i) * 8;
+        const int32_t row = k.rows ? row_ids[i] : r;
+        bool in = r < left && c < k.cin;
+        if (in && k.rows && (row < 0 || row >= k.n_src)) {
+          if (k.flags) atomicOr(k.flags, TS_FLAG_RANGE);
+          in = false;
+        }
+        if constexpr (VEC)
+          to_lds(buf, in ? (static_cast<uint32_t>(row) * static_cast<uint32_t>(k.cin) + c) * 2 : kNowhere,
+                 lds_a + slot * OA::kBytes + (i * NT + wave * 64) * 16);
+        else
+          ra[i] = in ? load_loose(base + (first + row) * k.cin, c, k.cin) : gu32x4{0u, 0u, 0u, 0u};
+      }
+    } else {
+      const bool gather = OP == kGroupFwd && k.rows;
+      const int64_t first = gather ? 0 : x.t.row0;
+      const __amdgpu_buffer_rsrc_t buf = buffer_of(base + first * x.K, (gather ? k.n_src : static_cast<int64_t>(x.t.rows)) * x.K * 2);
+      const int c = chunk_a(0) * 8;
+#pragma unroll
+      for (int i = 0; i < CA; ++i) {
+        if constexpr (VEC) {
+          to_lds(buf, c < left ? further(x.va[i], from * 2) : kNowhere, lds_a + slot * OA::kBytes + (i * NT + wave * 64) * 16);
+        } else {
+          const int32_t row = static_cast<int32_t>(x.va[i]);
+          ra[i] = c < left && row >= 0 ? load_loose(base + (first + row) * x.K, from + c, x.K) : gu32x4{0u, 0u, 0u, 0u};
+        }
       }
     }
+  };
+  auto copy_b = [&](const Source& x, int s, int slot) {
+    const int from = s * kStep, left = x.K - from;
+    const T* base = OP == kGroupWgrad ? static_cast<const T*>(k.dy) : static_cast<const T*>(k.w) + static_cast<int64_t>(x.t.e) * k.cin * k.ldw;
+    const int64_t first = OP == kGroupDgrad ? x.n0 : OP == kGroupWgrad ? x.t.row0 + from : from;  // row of the buffer's start
+    const int rows = OP == kGroupDgrad ? (N - x.n0 < BN ? N - x.n0 : BN) : left < kStep ? left : kStep;
+    const __amdgpu_buffer_rsrc_t buf = buffer_of(base + first * k.ldw, static_cast<int64_t>(rows) * k.ldw * 2);
 #pragma unroll
     for (int i = 0; i < CB; ++i) {
-      const T* p = src_b(i, s);
-      if constexpr (VEC) {
-        to_lds(p, lds_b + slot * OB::kBytes + (i * NT + wave * 64) * 16);
+      char* dst = lds_b + slot * OB::kBytes + (i * NT + wave * 64) * 16;
+      const int r = row_b() + i * NEXT_B;
+      if constexpr (OP == kGroupDgrad) {
+        const int c = chunk_b(0) * 8;
+        if constexpr (VEC)
+          to_lds(buf, c < left ? x.vb[0] + static_cast<uint32_t>(i * NEXT_B * k.ldw + from) * 2 : kNowhere, dst);
+        else
+          rb[i] = c < left && r < rows ? load_loose(base + (first + r) * k.ldw, from + c, x.K) : gu32x4{0u, 0u, 0u, 0u};
       } else {
-        const int c = GLU && col_b[i] >= k.cout ? col_b[i] - k.cout : col_b[i];
-        const int left = p == zeros ? 8 : B_ACROSS ? k.cout - c : K - at_b[i] - s * kStep;
-        rb[i] = load_loose(p, 0, left);
+        const uint32_t v = x.vb[i % TURN_B];
+        if constexpr (VEC)
+          to_lds(buf, further(v, static_cast<uint32_t>(i * NEXT_B * k.ldw * 2)), dst);
+        else
+          rb[i] = r < rows && v != kNowhere ? load_loose(base + (first + r) * k.ldw, static_cast<int>(v), GLU && v < static_cast<uint32_t>(k.cout) ? k.cout : k.ldw)
+                                            : gu32x4{0u, 0u, 0u, 0u};
       }
     }
   };
@@ -249,10 +323,39 @@ __global__ __launch_bounds__(WM* WN * 64) void k_group(const GroupK k) {
       for (int i = 0; i < CB; ++i) *reinterpret_cast<gu32x4*>(lds_b + slot * OB::kBytes + (i * NT + tid) * 16) = rb[i];
     }
   };
+  // The first steps of a tile; nobody reads the ring any more.
+  auto start = [&](const Source& x) {
+    if constexpr (A_ACROSS) {
+      if (k.rows) {
+        copy_rows(x, 0);
+        if (x.K > kRowHalf) copy_rows(x, kRowHalf);
+        wait_copies<0>();
+        barrier();
+      }
+      fetch_rows(x, 0);
+    }
+    copy_a(x, 0, 0);
+    copy_b(x, 0, 0);
+    fetch_rows(x, 1);
+    if (VEC && x.steps > 1) {
+      copy_a(x, 1, 1);
+      copy_b(x, 1, 1);
+      fetch_rows(x, 2);
+    }
+  };
+  // Rows from half of lds_rows further on: that half is free.
+  auto more_rows = [&](const Source& x, int s) {
+    if constexpr (A_ACROSS) {
+      const int from = s * kStep + kRowHalf;
+      if (s > 0 && (s * kStep) % kRowHalf == 0 && from < x.K) copy_rows(x, from);
+    }
+  };
 
   const int wm = wave / WN, wn = wave % WN;
   const int g = lane >> 4, c16 = lane & 15;
-  // LDS addresses of this lane's fragments, without the ring's offset
+  // LDS address of this lane's first fragment, without its place's offset.  Fragment i is 16 rows
+  // or columns further, and half kk of a step 32 along the reduction: one of the two changes
+  // only bits of the chunk's number.
   auto frag_at = [&](bool across, int r0, int width) {
     if (across) {
       const int q = lane & 3, m = (lane >> 2) & 3, row = 8 * g + m;
@@ -260,151 +363,249 @@ __global__ __launch_bounds__(WM* WN * 64) void k_group(const GroupK k) {
     }
     return (r0 + c16) * kStep * 2 + along_at(c16, g) * 16;
   };
-  int fa[MI], fb[NI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i) fa[i] = frag_at(A_ACROSS, wm * MI * 16 + i * 16, BM);
-#pragma unroll
-  for (int i = 0; i < NI; ++i) fb[i] = frag_at(B_ACROSS, wn * NI * 16 + i * 16, BN);
-  auto read_a = [&](int i, int slot) {
-    const char* p = lds_a + slot * OA::kBytes + fa[i];
-    if constexpr (A_ACROSS) return read_tr(p, p + 4 * BM * 2);
-    else return *reinterpret_cast<const gu32x4*>(p);
+  const int fa = frag_at(A_ACROSS, wm * MI * 16, BM), fb = frag_at(B_ACROSS, wn * NI * 16, BN);
+  auto read_a = [&](int i, int kk, int slot) {
+    const char* p = lds_a + slot * OA::kBytes;
+    if constexpr (A_ACROSS) {
+      p += (i ? fresh(fa) ^ (i * 32) : fa) + kk * 64 * BM;
+      return read_tr(p, p + 4 * BM * 2);
+    } else return *reinterpret_cast<const gu32x4*>(p + (fa ^ (kk * 64)) + i * 16 * kStep * 2);
   };
-  auto read_b = [&](int i, int slot) {
-    const char* p = lds_b + slot * OB::kBytes + fb[i];
-    if constexpr (B_ACROSS) return read_tr(p, p + 4 * BN * 2);
-    else return *reinterpret_cast<const gu32x4*>(p);
-  };
-
-  gf32x4 acc[MI][NI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NI; ++j) acc[i][j] = gf32x4{0.f, 0.f, 0.f, 0.f};
-
-  auto multiply = [&](int slot) {
-    gu32x4 b[NI];
-#pragma unroll
-    for (int j = 0; j < NI; ++j) b[j] = read_b(j, slot);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const gu32x4 a = read_a(i, slot);
-#pragma unroll
-      for (int j = 0; j < NI; ++j) acc[i][j] = GMfma<T>::run(b[j], a, acc[i][j]);
-    }
+  auto read_b = [&](int i, int kk, int slot) {
+    const char* p = lds_b + slot * OB::kBytes;
+    if constexpr (B_ACROSS) {
+      p += (i ? fresh(fb) ^ (i * 32) : fb) + kk * 64 * BN;
+      return read_tr(p, p + 4 * BN * 2);
+    } else return *reinterpret_cast<const gu32x4*>(p + (fb ^ (kk * 64)) + i * 16 * kStep * 2);
   };
 
-  if constexpr (VEC) {
-#pragma unroll
-    for (int s = 0; s < kRing - 1; ++s)
-      if (s < steps) copy(s, s);
-    for (int s0 = 0; s0 < steps; s0 += kRing) {
-#pragma unroll
-      for (int slot = 0; slot < kRing; ++slot) {
-        const int s = s0 + slot;
-        if (s >= steps) break;
-        // step s has landed: of the copies after it those of the next two may be out
-        if (s + 2 < steps) wait_copies<2 * (CA + CB)>();
-        else if (s + 1 < steps) wait_copies<CA + CB>();
-        else wait_copies<0>();
-        barrier();  // and everyone is done with the step before, whose place is free
-        if (s + kRing - 1 < steps) copy(s + kRing - 1, (slot + kRing - 1) % kRing);
-        multiply(slot);
-      }
-    }
-  } else {
-    copy(0, 0);
-    for (int s = 0; s < steps; ++s) {
-      const int slot = s & (kRing - 1);
-      put(slot);  // its last readers were done before the barrier three steps ago
-      if (s + 1 < steps) copy(s + 1, 0);
-      __syncthreads();
-      multiply(slot);
-    }
+  int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  Source x;
+  if (tile < end) {
+    set_up(x, tile);
+    start(x);
   }
-
-  // Lane (g, c16) holds columns 4g..4g+3 of row c16 of each 16 x 16 tile.
-  if constexpr (OP == kGroupWgrad) {
-    float* out = t.count == 1 ? k.dw + static_cast<int64_t>(t.e) * k.cin * k.cout : k.part + static_cast<int64_t>(run) * k.cin * k.cout;
+  while (tile < end) {
+    gf32x4 acc[MI][NI];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int m = m0 + wm * MI * 16 + i * 16 + c16;
-      if (m >= k.cin) continue;
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        const int n = n0 + wn * NI * 16 + j * 16 + 4 * g;
-        float* p = out + static_cast<int64_t>(m) * k.cout + n;
-        if (VEC) {
-          if (n < k.cout) *reinterpret_cast<gf32x4*>(p) = acc[i][j];
-        } else {
+      for (int j = 0; j < NI; ++j) acc[i][j] = gf32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (VEC) {
+      constexpr int PI = 2, ROWS = MI / PI, PARTS = 2 * ROWS;  // blocks of rows in a part; parts over 32, and of a step
+      gu32x4 a[2][PI], b[2][NI];
+      // the first step has landed (the second one may be out, or stores of the tile before instead)
+      if (x.steps > 1) wait_copies<CA + CB>();
+      else wait_copies<0>();
+      barrier();
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < k.cout) p[r] = acc[i][j][r];
-        }
-      }
-    }
-    return;
-  } else {
-    typedef T t4 __attribute__((ext_vector_type(4)));
-    auto store = [&](T* row, int n, int width, gf32x4 v) {
-      if (VEC) {
-        if (n < width) *reinterpret_cast<t4*>(row + n) = __builtin_convertvector(v, t4);
-      } else {
+      for (int j = 0; j < NI; ++j) b[0][j] = read_b(j, 0, 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (n + r < width) row[n + r] = static_cast<T>(v[r]);
-      }
-    };
-    T* y = static_cast<T*>(k.y);
+      for (int i = 0; i < PI; ++i) a[0][i] = read_a(i, 0, 0);
+      for (int s0 = 0; s0 < x.steps; s0 += 2) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int r = wm * MI * 16 + i * 16 + c16;
-      if (r >= t.rows) continue;
-      const int64_t row = t.row0 + r;
-      if constexpr (GLU && OP == kGroupFwd) {
+        for (int slot = 0; slot < 2; ++slot) {
+          const int s = s0 + slot;
+          if (s >= x.steps) break;
 #pragma unroll
-        for (int j = 0; j < NI; j += 2) {
-          const int n = n0 + wn * NI * 8 + j * 8 + 4 * g;
-          const gf32x4 a = acc[i][j], b = acc[i][j + 1];
-          gf32x4 v;
+          for (int part = 0; part < PARTS; ++part) {
+            if (part + 1 < PARTS) {
+              const int kk = (part + 1) / ROWS, row = (part + 1) % ROWS * PI;
+              wait_lds();  // this part's fragments, before the next one's are asked for
+              if (row == 0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = a[e] * sigmoid(a[e]) * b[e];
-          store(y + row * N, n, N, v);
-          if (k.h_out) {
-            T* h = static_cast<T*>(k.h_out) + row * 2 * N;
-            store(h, n, N, a);
-            store(h + N, n, N, b);
+                for (int j = 0; j < NI; ++j) b[kk][j] = read_b(j, kk, slot);
+              }
+#pragma unroll
+              for (int i = 0; i < PI; ++i) a[(part + 1) & 1][i] = read_a(row + i, kk, slot);
+            } else {
+              wait_copies<0>();  // step s is in registers, and this wave's copies of step s + 1 have landed
+              barrier();
+              if (s + 1 < x.steps) {
+#pragma unroll
+                for (int j = 0; j < NI; ++j) b[0][j] = read_b(j, 0, slot ^ 1);
+#pragma unroll
+                for (int i = 0; i < PI; ++i) a[0][i] = read_a(i, 0, slot ^ 1);
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // the copies of the next step but one begin where everyone has read this one
+            if (part == PARTS - 1 && s + 2 < x.steps) {
+              more_rows(x, s);
+              copy_a(x, s + 2, slot);
+            }
+            if (part == 0 && s > 0 && s + 1 < x.steps) copy_b(x, s + 1, slot ^ 1);
+            if (part == 1) fetch_rows(x, s + 2);
+#pragma unroll
+            for (int i = 0; i < PI; ++i)
+#pragma unroll
+              for (int j = 0; j < NI; ++j) {
+                gf32x4& c = acc[part % ROWS * PI + i][j];
+                c = GMfma<T>::run(b[part / ROWS][j], a[part & 1][i], c);
+              }
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
-      } else if constexpr (GLU) {
+      }
+    } else {
+      for (int s = 0; s < x.steps; ++s) {
+        const int slot = s & 1;
+        put(slot);  // its last readers were done before the last barrier
+        more_rows(x, s);
+        if (s + 1 < x.steps) {
+          copy_a(x, s + 1, 0);
+          copy_b(x, s + 1, 0);
+        }
+        wait_copies<0>();
+        barrier();
+        fetch_rows(x, s + 2);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          gu32x4 b[NI];
+#pragma unroll
+          for (int j = 0; j < NI; ++j) b[j] = read_b(j, kk, slot);
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            const gu32x4 a = read_a(i, kk, slot);
+#pragma unroll
+            for (int j = 0; j < NI; ++j) acc[i][j] = GMfma<T>::run(b[j], a, acc[i][j]);
+          }
+        }
+      }
+      wait_copies<0>();
+      barrier();
+    }
+
+    // Lane (g, c16) holds columns 4g..4g+3 of row c16 of each 16 x 16 block.
+    const int g = fresh(tid) >> 4 & 3, c16 = fresh(tid) & 15;
+    const GroupTile t = x.t;
+    const int m0 = x.m0, n0 = x.n0;
+    const int run = x.run;
+    tile += gridDim.x >> 3;
+    if (tile < end) set_up(x, tile);
+    if (tile < end) start(x);
+
+    if constexpr (OP == kGroupWgrad) {
+      float* out = t.count == 1 ? k.dw + static_cast<int64_t>(t.e) * k.cin * k.cout : k.part + static_cast<int64_t>(run) * k.cin * k.cout;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int m = m0 + wm * MI * 16 + i * 16 + c16;
+        if (m >= k.cin) continue;
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
           const int n = n0 + wn * NI * 16 + j * 16 + 4 * g;
-          if (n >= N) continue;
-          const T* h = static_cast<const T*>(k.h) + row * 2 * N + n;
-          gf32x4 a{}, b{}, da, db;
+          float* p = out + static_cast<int64_t>(m) * k.cout + n;
           if (VEC) {
-            a = __builtin_convertvector(*reinterpret_cast<const t4*>(h), gf32x4);
-            b = __builtin_convertvector(*reinterpret_cast<const t4*>(h + N), gf32x4);
+            if (n < k.cout) *reinterpret_cast<gf32x4*>(p) = acc[i][j];
           } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (n + e < N) a[e] = static_cast<float>(h[e]), b[e] = static_cast<float>(h[N + e]);
+            for (int r = 0; r < 4; ++r)
+              if (n + r < k.cout) p[r] = acc[i][j][r];
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float s = sigmoid(a[e]), d = acc[i][j][e];
-            da[e] = d * b[e] * s * fmaf(a[e], 1.f - s, 1.f);
-            db[e] = d * a[e] * s;
-          }
-          T* out = y + row * 2 * N;
-          store(out, n, N, da);
-          store(out + N, n, N, db);
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < NI; ++j) store(y + row * N, n0 + wn * NI * 16 + j * 16 + 4 * g, N, acc[i][j]);
       }
+    } else {
+      typedef T t4 __attribute__((ext_vector_type(4)));
+      typedef T t8 __attribute__((ext_vector_type(8)));
+      typedef unsigned u2 __attribute__((ext_vector_type(2)));
+      T* y = static_cast<T*>(k.y);
+      // Blocks j0 and j1 of a row, whose first columns are c and c + 16: 64 bytes of 4 lanes at
+      // once (a lane's own 8 bytes would make twice the requests).
+      auto store = [&](T* row, int c, gf32x4 p, gf32x4 q) {
+        if (VEC) {
+          u2 a = __builtin_bit_cast(u2, __builtin_convertvector(p, t4)), b = __builtin_bit_cast(u2, __builtin_convertvector(q, t4));
+          unsigned a0 = a[0], a1 = a[1], b0 = b[0], b1 = b[1];
+          join8(a0, b0);
+          join8(a1, b1);
+          if (row && c + 8 * g < N) *reinterpret_cast<gu32x4*>(row + c + 8 * g) = gu32x4{a0, a1, b0, b1};
+        } else if (row) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (c + 4 * g + r < N) row[c + 4 * g + r] = static_cast<T>(p[r]);
+            if (c + 16 + 4 * g + r < N) row[c + 16 + 4 * g + r] = static_cast<T>(q[r]);
+          }
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int r = wm * MI * 16 + i * 16 + c16;
+        const bool in = r < t.rows;  // (all lanes take part in the exchange)
+        const int64_t row = t.row0 + r;
+        if constexpr (GLU && OP == kGroupFwd) {
+          T* yr = in ? y + row * N : nullptr;
+          T* h = in && k.h_out ? static_cast<T*>(k.h_out) + row * 2 * N : nullptr;
+          gf32x4 v[NI / 2];
+#pragma unroll
+          for (int j = 0; j < NI / 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[j][e] = acc[i][2 * j][e] * sigmoid(acc[i][2 * j][e]) * acc[i][2 * j + 1][e];
+#pragma unroll
+          for (int j = 0; j < NI / 2; j += 2) {
+            const int c = n0 + wn * NI * 8 + j * 16;
+            store(yr, c, v[j], v[j + 1]);
+            if (k.h_out) {
+              store(h, c, acc[i][2 * j], acc[i][2 * j + 2]);
+              store(h ? h + N : h, c, acc[i][2 * j + 1], acc[i][2 * j + 3]);
+            }
+          }
+        } else if constexpr (GLU) {
+          const T* h = in ? static_cast<const T*>(k.h) + row * 2 * N : nullptr;
+          T* out = in ? y + row * 2 * N : nullptr;
+#pragma unroll
+          for (int j = 0; j < NI; j += 2) {
+            const int c = n0 + wn * NI * 16 + j * 16;
+            if constexpr (VEC) {
+              const int n = c + 8 * g;
+              t8 a{}, b{};
+              if (in && n < N) {
+                a = *reinterpret_cast<const t8*>(h + n);
+                b = *reinterpret_cast<const t8*>(h + N + n);
+              }
+              float d[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                unsigned p = __builtin_bit_cast(unsigned, static_cast<float>(acc[i][j][e])), q = __builtin_bit_cast(unsigned, static_cast<float>(acc[i][j + 1][e]));
+                join8(p, q);
+                d[e] = __builtin_bit_cast(float, p);
+                d[4 + e] = __builtin_bit_cast(float, q);
+              }
+              t8 da, db;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float av = static_cast<float>(a[e]), bv = static_cast<float>(b[e]), s = sigmoid(av);
+                da[e] = static_cast<T>(d[e] * bv * s * fmaf(av, 1.f - s, 1.f));
+                db[e] = static_cast<T>(d[e] * av * s);
+              }
+              if (in && n < N) {
+                *reinterpret_cast<t8*>(out + n) = da;
+                *reinterpret_cast<t8*>(out + N + n) = db;
+              }
+            } else if (in) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int n = c + (e >> 2) * 16 + 4 * g + (e & 3);
+                if (n >= N) continue;
+                const float av = static_cast<float>(h[n]), bv = static_cast<float>(h[N + n]), s = sigmoid(av), d = acc[i][j + (e >> 2)][e & 3];
+                out[n] = static_cast<T>(d * bv * s * fmaf(av, 1.f - s, 1.f));
+                out[N + n] = static_cast<T>(d * av * s);
+              }
+            }
+          }
+        } else {
+          T* yr = in ? y + row * N : nullptr;
+#pragma unroll
+          for (int j = 0; j < NI; j += 2) store(yr, n0 + wn * NI * 16 + j * 16, acc[i][j], acc[i][j + 1]);
+        }
+      }
+    }
+  }
+
+  if constexpr (OP != kGroupWgrad) {
+    const GroupRest rest = rows_unowned(k);
+    for (int64_t i = blockIdx.x;; i += gridDim.x) {
+      const int64_t r = i / k.n_tiles;
+      if (r * BM >= rest.n) break;
+      zero_results<T, OP, GLU>(k, rest, r * BM, BM, N, static_cast<int>(i - r * k.n_tiles) * kCols, kCols);
     }
   }
 }
@@ -455,15 +656,17 @@ template <typename T, GroupOp OP, bool GLU, int BM, int BN, int WM, int WN, bool
 void run(GroupK& k, hipStream_t s) {
   const int N = OP == kGroupDgrad ? k.cin : k.cout;
   k.n_tiles = ceil_div(N, GLU && OP == kGroupFwd ? BN / 2 : BN);
-  const int64_t grid = OP == kGroupWgrad ? group_grid(group_chunks(k.n_rows, k.e, k.chunk), k.n_tiles * ceil_div(k.cin, BM))
-                                         : group_grid(group_runs(k.n_rows, k.e, BM), k.n_tiles);
-  k_group<T, OP, GLU, BM, BN, WM, WN, VEC><<<static_cast<unsigned>(grid), WM * WN * 64, 0, s>>>(k);
+  // as many blocks as are resident: one of 128 KB, or two of 64 KB, of LDS on each of 256 CUs
+  const int64_t runs = OP == kGroupWgrad ? group_chunks(k.n_rows, k.e, k.chunk) * ceil_div(k.cin, BM) : group_runs(k.n_rows, k.e, BM);
+  const int64_t tiles = (runs * k.n_tiles + 7) / 8 * 8, most = BM == 256 ? 256 : 512;
+  k_group<T, OP, GLU, BM, BN, WM, WN, VEC><<<static_cast<unsigned>(tiles < most ? tiles : most), WM * WN * 64, 0, s>>>(k);
 }
 
 template <typename T, GroupOp OP, bool GLU>
 void run(GroupK& k, hipStream_t s) {
   const bool vec = k.cin % 8 == 0 && k.cout % 8 == 0 && aligned16(k.x) && aligned16(k.dy) && aligned16(k.w) && aligned16(k.h) &&
-                   aligned16(k.y) && aligned16(k.h_out) && aligned16(k.dw) && aligned16(k.part);
+                   aligned16(k.y) && aligned16(k.h_out) && aligned16(k.dw) && aligned16(k.part) &&
+                   (!k.rows || k.n_src * k.cin < (int64_t{1} << 31) - 8);  // rows looked up have 32-bit offsets
   if (!vec) return run<T, OP, GLU, 128, 128, 2, 2, false>(k, s);
   const int N = OP == kGroupDgrad ? k.cin : k.ldw;
   const bool large = N >= 256 && (OP == kGroupWgrad ? k.cin >= 256 : k.n_rows / k.e >= 512);

@@ -41,26 +41,22 @@ __global__ __launch_bounds__(kWaves * 64) void k_group_few(const GroupK k) {
   constexpr bool PAIR = GLU && OP == kGroupFwd;  // 64 columns of a, 64 of b
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, c16 = lane & 15;
-  const int64_t runs = total_runs(k, BM);
-  const GroupBlock block = group_block(runs, k.n_tiles);
+  __shared__ GroupLane lanes[64];
+  GroupFinder finder(k, BM, lanes);
+  const GroupBlock block = group_block(finder.total, k.n_tiles);
   const int N = OP == kGroupDgrad ? k.cin : k.cout, K = OP == kGroupDgrad ? k.cout : k.cin;
   constexpr int kOut = PAIR ? kCols / 2 : kCols;
   T* y = static_cast<T*>(k.y);
   if (block.at < 0) {
     if (block.spare < 0) return;
     const int64_t run = block.spare / k.n_tiles;
-    const int n0 = static_cast<int>(block.spare - run * k.n_tiles) * kOut, cols = N - n0 < kOut ? N - n0 : kOut;
-    zero_unowned(k, run, BM, y, OP == kGroupDgrad && GLU ? 2 * N : N, n0, cols);
-    if (GLU) {
-      T* h = OP == kGroupDgrad ? y : static_cast<T*>(k.h_out);
-      if (h && OP == kGroupFwd) zero_unowned(k, run, BM, h, 2 * N, n0, cols);
-      if (h) zero_unowned(k, run, BM, h, 2 * N, N + n0, cols);
-    }
+    const GroupRest rest = rows_unowned(k);
+    if (run * BM < rest.n) zero_results<T, OP, GLU>(k, rest, run * BM, BM, N, static_cast<int>(block.spare - run * k.n_tiles) * kOut, kOut);
     return;
   }
   const int64_t run = block.at / k.n_tiles;
   const int n0 = static_cast<int>(block.at - run * k.n_tiles) * kOut;
-  const GroupTile t = find_tile(k, run, BM);
+  const GroupTile t = finder.find(k, run);
   if (t.e < 0) return;
   const T* wt = static_cast<const T*>(k.w) + static_cast<int64_t>(t.e) * k.cin * k.ldw;
 
