@@ -119,7 +119,7 @@ bool grid_ok(const ts_groups* g, GroupOp op, int cin, int columns) {
   int64_t blocks;
   if (op == kGroupWgrad) {
     const int64_t tiles = static_cast<int64_t>(ceil_div(cin, 128)) * ceil_div(columns, 128);
-    blocks = group_grid(group_chunks(g->n_rows, g->n_groups, group_chunk(g->n_rows, cin, columns)), 1) * tiles;
+    blocks = group_grid(group_chunks(g->n_rows, g->n_groups, group_chunk(g->n_rows, g->n_groups, cin, columns)), 1) * tiles;
   } else {
     const int64_t runs = group_runs(g->n_rows, g->n_groups, group_few(op, g->n_rows, g->n_groups) ? 16 : 128);
     blocks = group_grid(runs, static_cast<unsigned>(ceil_div(columns, 128)));
@@ -141,7 +141,7 @@ GroupK group_args(const ts_groups* g, int cin, int cout, uint32_t* flags) {
 }
 
 size_t wgrad_bytes(const ts_groups* g, int cin, int cout) {
-  return static_cast<size_t>(group_chunks(g->n_rows, g->n_groups, group_chunk(g->n_rows, cin, cout))) * cin * cout * sizeof(float);
+  return static_cast<size_t>(group_chunks(g->n_rows, g->n_groups, group_chunk(g->n_rows, g->n_groups, cin, cout))) * cin * cout * sizeof(float);
 }
 
 }  // namespace
@@ -291,7 +291,7 @@ ts_status ts_group_bwd_wgrad(const ts_groups* g, const void* x, int cin, const v
   k.dy = dy;
   k.dw = dw;
   k.part = static_cast<float*>(ws);
-  k.chunk = group_chunk(g->n_rows, cin, cout);
+  k.chunk = group_chunk(g->n_rows, g->n_groups, cin, cout);
   return status(launch_group(k, kGroupWgrad, dtype, false, stream));
 }
 

@@ -74,8 +74,8 @@ struct GroupTile {
   int e;              // -1: past the last run
   int64_t row0;       // first grouped row
   int rows;           // of this run
-  int64_t first;      // the expert's first run
-  int count;          // and how many it has
+  int64_t run;        // its number, expert by expert
+  int count;          // runs of the expert
 };
 
 // Grouped rows [*a, *b) of expert e (empty for e >= k.e); starts that decrease or leave [0,
@@ -97,37 +97,58 @@ __device__ __forceinline__ int runs_of(int64_t a, int64_t b, int len) {
 }
 
 // Finds runs.  Used by all waves of a block, with the same result in every lane; of up to 64
-// experts each one's rows are kept in LDS.
+// experts each one's rows are kept in LDS.  SORTED: these in the order of their lengths, the longest
+// first, so that what is taken last is short (a run's number `first` stays that of the experts' own
+// order).
 struct GroupLane {
   int a, b, n, inc;  // an expert's rows, its runs, and runs up to and with it
+  int e, first;      // SORTED: which expert, and its first run
 };
+template <bool SORTED>
 struct GroupFinder {
   GroupLane* kept;
   int len;
   int64_t total;  // all runs
 
+  static __device__ __forceinline__ int scan(int x) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const int up = __shfl_up(x, m);
+      if (static_cast<int>(threadIdx.x & 63) >= m) x += up;
+    }
+    return x;
+  }
   __device__ __forceinline__ GroupLane batch(const GroupK& k, int e0) const {
-    const int lane = threadIdx.x & 63;
     int64_t r0, r1;
-    expert_rows(k, e0 + lane, &r0, &r1);
+    expert_rows(k, e0 + (threadIdx.x & 63), &r0, &r1);
     GroupLane l;
     l.a = static_cast<int>(r0);
     l.b = static_cast<int>(r1);
     l.n = runs_of(r0, r1, len);
-    l.inc = l.n;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int up = __shfl_up(l.inc, m);
-      if (lane >= m) l.inc += up;
-    }
+    l.inc = scan(l.n);
+    l.e = e0 + (threadIdx.x & 63);
+    l.first = l.inc - l.n;
     return l;
   }
   // lds: 64 entries.
   __device__ __forceinline__ GroupFinder(const GroupK& k, int run_rows, GroupLane* lds) : kept(lds), len(run_rows), total(0) {
+    const int lane = threadIdx.x & 63;
     for (int e0 = 0; e0 < k.e; e0 += 64) {
-      const GroupLane l = batch(k, e0);
+      GroupLane l = batch(k, e0);
       total += __builtin_amdgcn_readlane(l.inc, 63);
-      if (k.e <= 64) kept[threadIdx.x & 63] = l;  // (every wave writes the same, and reads what it wrote itself)
+      if (k.e > 64) continue;
+      int at = lane;
+      if (SORTED) {
+        at = 0;
+        l.inc = l.n;
+        for (int o = 0; o < 64; ++o) {
+          const int rows = __builtin_amdgcn_readlane(l.b - l.a, o), n = __builtin_amdgcn_readlane(l.n, o);
+          const bool ahead = rows > l.b - l.a || (rows == l.b - l.a && o < lane);
+          at += ahead;
+          l.inc += ahead ? n : 0;
+        }
+      }
+      kept[at] = l;  // (every wave writes the same, once, and reads what it wrote itself)
     }
   }
   __device__ __forceinline__ GroupTile find(const GroupK& k, int64_t index) const {
@@ -139,11 +160,12 @@ struct GroupFinder {
       const uint64_t hit = __ballot(index - before < own.inc);
       if (hit) {
         const int l = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-        t.e = e0 + l;
+        t.e = __builtin_amdgcn_readlane(own.e, l);
         t.count = __builtin_amdgcn_readlane(own.n, l);
-        t.first = before + __builtin_amdgcn_readlane(own.inc, l) - t.count;
+        const int64_t nth = index - (before + __builtin_amdgcn_readlane(own.inc, l) - t.count);
+        t.run = (SORTED && k.e <= 64 ? __builtin_amdgcn_readlane(own.first, l) : index - nth) + nth;
         const int64_t r0 = __builtin_amdgcn_readlane(own.a, l), r1 = __builtin_amdgcn_readlane(own.b, l);
-        t.row0 = r0 + (index - t.first) * len;
+        t.row0 = r0 + nth * len;
         t.rows = r1 - t.row0 < len ? static_cast<int>(r1 - t.row0) : len;
         return t;
       }
@@ -190,14 +212,22 @@ __device__ __forceinline__ void zero_results(const GroupK& k, const GroupRest& r
   }
 }
 
-// silu(a) b and its derivatives
-__device__ __forceinline__ float sigmoid(float a) { return 1.f / (1.f + expf(-a)); }
+// 1 / (1 + exp(-a)), off by about 4 * 2^-24 of itself: the exponential through exp2 of the product
+// with log2(e) in two parts (one part alone is off by |a| 2^-24; the instruction itself by one
+// unit), at a third of the instructions of expf and a division.  (Beyond 10^4 either way the
+// result is 0 or 1; infinities stay out of the second part.)
+__device__ __forceinline__ float sigmoid(float a) {
+  const float q = __builtin_amdgcn_fmed3f(-a, -1e4f, 1e4f);
+  const float hi = q * 1.44269504f, lo = fmaf(q, 1.92596299e-8f, fmaf(q, 1.44269504f, -hi));
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return __builtin_amdgcn_rcpf(fmaf(e, fmaf(lo, 0.693147181f, 1.f), 1.f));
+}
 
 // group.hip, group_few.hip
 bool group_few(GroupOp op, int64_t n_rows, int e);
 hipError_t launch_group(GroupK& k, GroupOp op, ts_dtype dt, bool glu, hipStream_t s);
 hipError_t launch_group_few(GroupK& k, GroupOp op, ts_dtype dt, bool glu, hipStream_t s);
-int group_chunk(int64_t n_rows, int cin, int cout);
+int group_chunk(int64_t n_rows, int e, int cin, int cout);
 // Partial sums of the weight gradient at most: every expert may end in a short one.
 inline int64_t group_chunks(int64_t n_rows, int e, int chunk) { return n_rows / chunk + e; }
 

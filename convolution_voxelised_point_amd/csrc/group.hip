@@ -109,13 +109,35 @@ template <typename T>
 struct __attribute__((packed, aligned(2))) Loose8 {
   T e[8];
 };
+// (Of a row's last, partial chunk the row's last 8 values are read instead and moved down.)
 template <typename T>
 __device__ __forceinline__ gu32x4 load_loose(const T* row, int c0, int width) {
-  if (c0 + 8 <= width) return __builtin_bit_cast(gu32x4, *reinterpret_cast<const Loose8<T>*>(row + c0));
-  T v[8];
+  if (width < 8) {
+    T v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = c0 + i < width ? row[c0 + i] : static_cast<T>(0.f);
-  return __builtin_bit_cast(gu32x4, v);
+    for (int i = 0; i < 8; ++i) v[i] = c0 + i < width ? row[c0 + i] : static_cast<T>(0.f);
+    return __builtin_bit_cast(gu32x4, v);
+  }
+  const int by = c0 + 8 <= width ? 0 : c0 + 8 - width;
+  gu32x4 v = __builtin_bit_cast(gu32x4, *reinterpret_cast<const Loose8<T>*>(row + (c0 - by)));
+  if (by & 4) v = gu32x4{v[2], v[3], 0u, 0u};
+  if (by & 2) v = gu32x4{v[1], v[2], v[3], 0u};
+  if (by & 1) v = gu32x4{(v[0] >> 16) | (v[1] << 16), (v[1] >> 16) | (v[2] << 16), (v[2] >> 16) | (v[3] << 16), v[3] >> 16};
+  return v;
+}
+struct __attribute__((packed, aligned(4))) Loose4 {
+  float e[4];
+};
+template <typename T>
+__device__ __forceinline__ void store_loose(T* row, int c0, int width, gu32x4 v) {
+  if (c0 + 8 <= width) {
+    *reinterpret_cast<Loose8<T>*>(row + c0) = __builtin_bit_cast(Loose8<T>, v);
+  } else {
+    const Loose8<T> w = __builtin_bit_cast(Loose8<T>, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i < width) row[c0 + i] = w.e[i];
+  }
 }
 
 template <typename T, int R, int NT, int ACROSS>
@@ -131,7 +153,7 @@ struct Operand {
 template <int CA, int CB>
 struct TileSource {
   GroupTile t;
-  int m0, n0, steps, K, run;
+  int m0, n0, steps, K;
   // VEC: offsets within the buffers.  Otherwise: rows of x or dy (-1: none); columns of W or dy
   uint32_t va[CA], vb[CB];
 };
@@ -155,14 +177,24 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   const int along = OP == kGroupWgrad ? ceil_div(k.cin, BM) : 1;  // weight gradient: tiles along cin of each run
   const int N = OP == kGroupDgrad ? k.cin : k.cout;               // columns of the result
   __shared__ GroupLane lds_lanes[64];
-  GroupFinder finder(k, OP == kGroupWgrad ? k.chunk : BM, lds_lanes);
+  const GroupFinder<OP == kGroupWgrad> finder(k, OP == kGroupWgrad ? k.chunk : BM, lds_lanes);
   // (only starts that make the experts overlap have more runs than were planned for; 32 bits hold
   // all the tiles there are)
   const int64_t planned = OP == kGroupWgrad ? group_chunks_on_device(k) : k.n_rows / BM + k.e;
   const int runs = static_cast<int>(finder.total < planned ? finder.total : planned);
-  // tiles of this block: those of one XCD are neighbours (blocks go to the 8 XCDs in turn)
+  // The i-th tile of this block.  Blocks go to the 8 XCDs in turn: those of one XCD take neighbouring
+  // tiles.  Weight gradient: the runs have lengths of their own, the longest ones first, so blocks
+  // take them to and fro; of a run each XCD gets some columns.
   const int n_tiles = k.n_tiles, total = runs * along * n_tiles, per_xcd = (total + 7) / 8;
-  const int xcd_end = ((blockIdx.x & 7) + 1) * per_xcd, end = xcd_end < total ? xcd_end : total;
+  auto tile_of = [&](int i) {
+    const int grid = gridDim.x, block = blockIdx.x;
+    if (OP == kGroupWgrad) {
+      const int tile = i * grid + (i & 1 ? grid - 1 - block : block);
+      return tile < total ? tile : -1;
+    }
+    const int in = (block >> 3) + i * (grid >> 3), tile = (block & 7) * per_xcd + in;
+    return in < per_xcd && tile < total ? tile : -1;
+  };
   // This lane's copies: the row of the operand's tile, and the chunk of it.  Of the next copy the
   // row is NT / kPerRow further; the chunk is the same for rows 16 apart, and two take turns
   // for rows 8 apart.
@@ -194,9 +226,9 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     const int rows = runs * along - band * kHigh, high = rows < kHigh ? rows : kHigh;
     const int nt = in / high, mt = band * kHigh + (in - nt * high);
     x.n0 = nt * kCols;
-    x.run = mt / along;
-    x.m0 = (mt - x.run * along) * BM;
-    x.t = finder.find(k, x.run);
+    const int run = mt / along;
+    x.m0 = (mt - run * along) * BM;
+    x.t = finder.find(k, run);
     x.K = OP == kGroupFwd ? k.cin : OP == kGroupDgrad ? k.cout : x.t.rows;
     x.steps = ceil_div(x.K, kStep);
     if constexpr (!A_ACROSS) {
@@ -379,13 +411,13 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     } else return *reinterpret_cast<const gu32x4*>(p + (fb ^ (kk * 64)) + i * 16 * kStep * 2);
   };
 
-  int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  int tile = tile_of(0), done = 0;
   Source x;
-  if (tile < end) {
+  if (tile >= 0) {
     set_up(x, tile);
     start(x);
   }
-  while (tile < end) {
+  while (tile >= 0) {
     gf32x4 acc[MI][NI];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -480,13 +512,14 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     const int g = fresh(tid) >> 4 & 3, c16 = fresh(tid) & 15;
     const GroupTile t = x.t;
     const int m0 = x.m0, n0 = x.n0;
-    const int run = x.run;
-    tile += gridDim.x >> 3;
-    if (tile < end) set_up(x, tile);
-    if (tile < end) start(x);
+    tile = tile_of(++done);
+    if (tile >= 0) {
+      set_up(x, tile);
+      start(x);
+    }
 
     if constexpr (OP == kGroupWgrad) {
-      float* out = t.count == 1 ? k.dw + static_cast<int64_t>(t.e) * k.cin * k.cout : k.part + static_cast<int64_t>(run) * k.cin * k.cout;
+      float* out = t.count == 1 ? k.dw + static_cast<int64_t>(t.e) * k.cin * k.cout : k.part + t.run * k.cin * k.cout;
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const int m = m0 + wm * MI * 16 + i * 16 + c16;
@@ -497,6 +530,8 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
           float* p = out + static_cast<int64_t>(m) * k.cout + n;
           if (VEC) {
             if (n < k.cout) *reinterpret_cast<gf32x4*>(p) = acc[i][j];
+          } else if (n + 4 <= k.cout) {
+            *reinterpret_cast<Loose4*>(p) = __builtin_bit_cast(Loose4, acc[i][j]);
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -512,19 +547,15 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       // Blocks j0 and j1 of a row, whose first columns are c and c + 16: 64 bytes of 4 lanes at
       // once (a lane's own 8 bytes would make twice the requests).
       auto store = [&](T* row, int c, gf32x4 p, gf32x4 q) {
-        if (VEC) {
-          u2 a = __builtin_bit_cast(u2, __builtin_convertvector(p, t4)), b = __builtin_bit_cast(u2, __builtin_convertvector(q, t4));
-          unsigned a0 = a[0], a1 = a[1], b0 = b[0], b1 = b[1];
-          join8(a0, b0);
-          join8(a1, b1);
-          if (row && c + 8 * g < N) *reinterpret_cast<gu32x4*>(row + c + 8 * g) = gu32x4{a0, a1, b0, b1};
-        } else if (row) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if (c + 4 * g + r < N) row[c + 4 * g + r] = static_cast<T>(p[r]);
-            if (c + 16 + 4 * g + r < N) row[c + 16 + 4 * g + r] = static_cast<T>(q[r]);
-          }
-        }
+        const u2 a = __builtin_bit_cast(u2, __builtin_convertvector(p, t4)), b = __builtin_bit_cast(u2, __builtin_convertvector(q, t4));
+        unsigned a0 = a[0], a1 = a[1], b0 = b[0], b1 = b[1];
+        join8(a0, b0);
+        join8(a1, b1);
+        const gu32x4 v{a0, a1, b0, b1};
+        const int n = c + 8 * g;
+        if (!row || n >= N) return;
+        if (VEC) *reinterpret_cast<gu32x4*>(row + n) = v;
+        else store_loose(row, n, N, v);
       };
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
@@ -554,40 +585,39 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
 #pragma unroll
           for (int j = 0; j < NI; j += 2) {
             const int c = n0 + wn * NI * 16 + j * 16;
-            if constexpr (VEC) {
-              const int n = c + 8 * g;
-              t8 a{}, b{};
-              if (in && n < N) {
+            const int n = c + 8 * g;
+            t8 a{}, b{};
+            if (in && n < N) {
+              if constexpr (VEC) {
                 a = *reinterpret_cast<const t8*>(h + n);
                 b = *reinterpret_cast<const t8*>(h + N + n);
+              } else {
+                a = __builtin_bit_cast(t8, load_loose(h, n, N));
+                b = __builtin_bit_cast(t8, load_loose(h + N, n, N));
               }
-              float d[8];
+            }
+            float d[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                unsigned p = __builtin_bit_cast(unsigned, static_cast<float>(acc[i][j][e])), q = __builtin_bit_cast(unsigned, static_cast<float>(acc[i][j + 1][e]));
-                join8(p, q);
-                d[e] = __builtin_bit_cast(float, p);
-                d[4 + e] = __builtin_bit_cast(float, q);
-              }
-              t8 da, db;
+            for (int e = 0; e < 4; ++e) {
+              unsigned p = __builtin_bit_cast(unsigned, static_cast<float>(acc[i][j][e])), q = __builtin_bit_cast(unsigned, static_cast<float>(acc[i][j + 1][e]));
+              join8(p, q);
+              d[e] = __builtin_bit_cast(float, p);
+              d[4 + e] = __builtin_bit_cast(float, q);
+            }
+            t8 da, db;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float av = static_cast<float>(a[e]), bv = static_cast<float>(b[e]), s = sigmoid(av);
-                da[e] = static_cast<T>(d[e] * bv * s * fmaf(av, 1.f - s, 1.f));
-                db[e] = static_cast<T>(d[e] * av * s);
-              }
-              if (in && n < N) {
+            for (int e = 0; e < 8; ++e) {
+              const float av = static_cast<float>(a[e]), bv = static_cast<float>(b[e]), s = sigmoid(av);
+              da[e] = static_cast<T>(d[e] * bv * s * fmaf(av, 1.f - s, 1.f));
+              db[e] = static_cast<T>(d[e] * av * s);
+            }
+            if (in && n < N) {
+              if constexpr (VEC) {
                 *reinterpret_cast<t8*>(out + n) = da;
                 *reinterpret_cast<t8*>(out + N + n) = db;
-              }
-            } else if (in) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int n = c + (e >> 2) * 16 + 4 * g + (e & 3);
-                if (n >= N) continue;
-                const float av = static_cast<float>(h[n]), bv = static_cast<float>(h[N + n]), s = sigmoid(av), d = acc[i][j + (e >> 2)][e & 3];
-                out[n] = static_cast<T>(d * bv * s * fmaf(av, 1.f - s, 1.f));
-                out[N + n] = static_cast<T>(d * av * s);
+              } else {
+                store_loose(out, n, N, __builtin_bit_cast(gu32x4, da));
+                store_loose(out + N, n, N, __builtin_bit_cast(gu32x4, db));
               }
             }
           }
@@ -650,6 +680,8 @@ __global__ __launch_bounds__(256) void k_group_sum(const GroupK k) {
   }
 }
 
+bool large_wgrad(int cin, int cout) { return cin >= 256 && cout >= 256; }
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <typename T, GroupOp OP, bool GLU, int BM, int BN, int WM, int WN, bool VEC>
@@ -658,7 +690,7 @@ void run(GroupK& k, hipStream_t s) {
   k.n_tiles = ceil_div(N, GLU && OP == kGroupFwd ? BN / 2 : BN);
   // as many blocks as are resident: one of 128 KB, or two of 64 KB, of LDS on each of 256 CUs
   const int64_t runs = OP == kGroupWgrad ? group_chunks(k.n_rows, k.e, k.chunk) * ceil_div(k.cin, BM) : group_runs(k.n_rows, k.e, BM);
-  const int64_t tiles = (runs * k.n_tiles + 7) / 8 * 8, most = BM == 256 ? 256 : 512;
+  const int64_t tiles = (runs * k.n_tiles + 7) / 8 * 8, most = BM == 128 ? 512 : 256;
   k_group<T, OP, GLU, BM, BN, WM, WN, VEC><<<static_cast<unsigned>(tiles < most ? tiles : most), WM * WN * 64, 0, s>>>(k);
 }
 
@@ -669,8 +701,15 @@ void run(GroupK& k, hipStream_t s) {
                    (!k.rows || k.n_src * k.cin < (int64_t{1} << 31) - 8);  // rows looked up have 32-bit offsets
   if (!vec) return run<T, OP, GLU, 128, 128, 2, 2, false>(k, s);
   const int N = OP == kGroupDgrad ? k.cin : k.ldw;
-  const bool large = N >= 256 && (OP == kGroupWgrad ? k.cin >= 256 : k.n_rows / k.e >= 512);
-  if (large) return run<T, OP, GLU, 256, 256, 2, 4, true>(k, s);
+  const bool large = OP == kGroupWgrad ? large_wgrad(k.cin, k.cout) : N >= 256 && k.n_rows / k.e >= 512;
+  if (large) {
+    if constexpr (OP != kGroupWgrad) {
+      // 192 rows a tile where that fills the rounds of the 256 CUs better (half a tile an expert is lost)
+      auto cost = [&](int bm) { return ceil_div<int64_t>((k.n_rows / bm + k.e / 2) * ceil_div(N, 256), 256) * bm; };
+      if (cost(192) < cost(256)) return run<T, OP, GLU, 192, 256, 2, 4, true>(k, s);
+    }
+    return run<T, OP, GLU, 256, 256, 2, 4, true>(k, s);
+  }
   run<T, OP, GLU, 128, 128, 2, 2, true>(k, s);
 }
 
@@ -680,18 +719,22 @@ void run(GroupK& k, GroupOp op, bool glu, hipStream_t s) {
   if (op == kGroupDgrad) return glu ? run<T, kGroupDgrad, true>(k, s) : run<T, kGroupDgrad, false>(k, s);
   run<T, kGroupWgrad, false>(k, s);
   const int64_t size = static_cast<int64_t>(k.cin) * k.cout;
-  const int64_t blocks = ceil_div<int64_t>(size, 1024);
-  k_group_sum<<<dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), k.e), 256, 0, s>>>(k);
+  // (most experts have nothing to add up: a few thousand blocks in all)
+  const int64_t blocks = ceil_div<int64_t>(size, 1024), most = k.e < 2048 ? 4096 / k.e : 2;
+  k_group_sum<<<dim3(static_cast<unsigned>(blocks < most ? blocks : most), k.e), 256, 0, s>>>(k);
 }
 
 }  // namespace
 
-// Rows of a partial sum: about 512 blocks of 128 x 128 in all, 256 to 4096 rows each.
-int group_chunk(int64_t n_rows, int cin, int cout) {
-  const int64_t tiles = static_cast<int64_t>(ceil_div(cin, 128)) * ceil_div(cout, 128);
-  const int64_t want = ceil_div<int64_t>(512, tiles), rows = ceil_div<int64_t>(n_rows, want);
-  const int64_t c = rows < 256 ? 256 : rows > 4096 ? 4096 : rows;
-  return static_cast<int>((c + kStep - 1) / kStep * kStep);
+// Rows of a run of the weight gradient.  Where every expert's rows can be one run without leaving
+// blocks idle, a run is what one block has to do on average; otherwise as many runs as there are
+// blocks (an expert may end in a short one).
+int group_chunk(int64_t n_rows, int e, int cin, int cout) {
+  const bool large = large_wgrad(cin, cout);
+  const int edge = large ? 256 : 128, slots = large ? 256 : 512;
+  const int64_t tiles = static_cast<int64_t>(ceil_div(cin, edge)) * ceil_div(cout, edge), whole = e * tiles;
+  const int64_t c = ceil_div<int64_t>(n_rows * tiles, whole < slots / 2 ? slots - whole : slots);
+  return static_cast<int>((c < 256 ? 256 : c) + kStep - 1) / kStep * kStep;
 }
 
 hipError_t launch_group(GroupK& k, GroupOp op, ts_dtype dt, bool glu, hipStream_t s) {

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_group_few(const GroupK k) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, c16 = lane & 15;
   __shared__ GroupLane lanes[64];
-  GroupFinder finder(k, BM, lanes);
+  const GroupFinder<false> finder(k, BM, lanes);
   const GroupBlock block = group_block(finder.total, k.n_tiles);
   const int N = OP == kGroupDgrad ? k.cin : k.cout, K = OP == kGroupDgrad ? k.cout : k.cin;
   constexpr int kOut = PAIR ? kCols / 2 : kCols;
