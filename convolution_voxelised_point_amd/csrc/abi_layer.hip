@@ -87,7 +87,7 @@ RopeK rope_args(const ts_rope* r, const ts_rope_heads* q, const ts_rope_heads* k
 }
 
 size_t rope_bytes(const ts_rope* r, int hq, int hk) {
-  return (static_cast<size_t>(rope_blocks(r->n, hq)) + rope_blocks(r->n, hk)) * r->d * sizeof(float);
+  return 2 * static_cast<size_t>(rope_blocks(r->n, hq + hk)) * r->d * sizeof(float);
 }
 
 // ---------------------------------------------------------------- routing
@@ -174,14 +174,13 @@ ts_status ts_rope_bwd(const ts_rope* r, const ts_rope_heads* q, const ts_rope_he
   if (hq + hk == 0) return TS_OK;
   RopeK a = rope_args(r, q, k);
   a.part = static_cast<float*>(ws);
-  a.blocks_q = rope_blocks(r->n, hq);
-  a.blocks_k = rope_blocks(r->n, hk);
+  a.blocks = rope_blocks(r->n, hq + hk);
   return status(launch_rope_bwd(a, r->dtype, r->interleaved != 0, stream));
 }
 
 size_t ts_route_workspace_bytes(int64_t n, int n_experts, int top) {
   if (check_route(n, n_experts, TS_F32, top) != TS_OK || n == 0 || route_small(n, top)) return 0;
-  return static_cast<size_t>(n_experts + 1) * route_blocks(n, n_experts) * sizeof(int32_t);
+  return static_cast<size_t>(n_experts + 1) * (route_blocks(n, n_experts) + 1) * sizeof(int32_t);
 }
 
 ts_status ts_route_fwd(const void* logits, int64_t n, int n_experts, ts_dtype dtype, int top, int over_all,

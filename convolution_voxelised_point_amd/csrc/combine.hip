@@ -25,8 +25,6 @@ struct CombineK {
   bool vec, vec_d;  // 16-byte accesses allowed: y, out and dy; dout
 };
 
-constexpr int kAhead = 4;  // grouped rows of a row read at once
-
 // Grouped row of (t, j), -1 where there is none.
 __device__ __forceinline__ int64_t row_at(const CombineK& k, int64_t t, int j) {
   const int32_t p = k.place[t * k.top + j];
@@ -37,26 +35,27 @@ __device__ __forceinline__ int64_t row_at(const CombineK& k, int64_t t, int j) {
   return p;
 }
 
-template <typename T>
+// AHEAD grouped rows of a row are read at once.
+template <typename T, int AHEAD>
 __global__ __launch_bounds__(256) void k_combine_fwd(const CombineK k) {
   const int64_t items = k.n * k.units;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < items; i += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t t = items <= UINT32_MAX ? static_cast<uint32_t>(i) / static_cast<uint32_t>(k.units) : i / k.units;
     const int c0 = static_cast<int>(i - t * k.units) * 8;
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < k.top; j0 += kAhead) {
-      float f[kAhead][8], g[kAhead];
-      int64_t p[kAhead];
+    for (int j0 = 0; j0 < k.top; j0 += AHEAD) {
+      float f[AHEAD][8], g[AHEAD];
+      int64_t p[AHEAD];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
+      for (int j = 0; j < AHEAD; ++j) {
         p[j] = j0 + j < k.top ? row_at(k, t, j0 + j) : -1;
         g[j] = p[j] < 0 ? 0.f : k.gates ? k.gates[t * k.top + j0 + j] : 1.f;
       }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j)
+      for (int j = 0; j < AHEAD; ++j)
         if (p[j] >= 0) load_unit(static_cast<const T*>(k.y) + p[j] * k.c, c0, k.c, k.vec, f[j]);
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j)
+      for (int j = 0; j < AHEAD; ++j)
         if (p[j] >= 0) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) sum[e] = fmaf(g[j], f[j][e], sum[e]);
@@ -121,7 +120,11 @@ void run_bwd(const CombineK& k, hipStream_t s) {
 template <typename T>
 void run(const CombineK& k, bool back, hipStream_t s) {
   if (!back) {
-    k_combine_fwd<T><<<blocks_for(ceil_div<int64_t>(k.n * k.units, 256)), 256, 0, s>>>(k);
+    const unsigned grid = blocks_for(ceil_div<int64_t>(k.n * k.units, 256));
+    if (k.top <= 2)
+      k_combine_fwd<T, 2><<<grid, 256, 0, s>>>(k);
+    else
+      k_combine_fwd<T, 4><<<grid, 256, 0, s>>>(k);
     return;
   }
   if (k.units <= 1) return run_bwd<T, 1>(k, s);

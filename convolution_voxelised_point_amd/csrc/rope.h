@@ -12,7 +12,8 @@ constexpr int kRopeMaxWidth = 128;
 // Queries or keys; heads 0: absent.
 struct RopeSide {
   int heads;
-  int64_t x_stride, y_stride, dy_stride, dx_stride, tiles;
+  unsigned by_heads;  // filled in by the launcher: 2^32 / heads, rounded up
+  int64_t x_stride, y_stride, dy_stride, dx_stride;
   const void* x;
   const float* w;  // null: no norm
   void* y;
@@ -25,20 +26,21 @@ struct RopeK {
   RopeSide side[2];
   const int32_t* coords;
   const float* freqs;
-  float* part;  // dw shares [blocks_q + blocks_k][d]
+  float* part;  // dw shares [2][blocks][d]
   int64_t n;
   float eps, inv_d;
   int d, ndim, pairs, upto[2];  // pairs of all axes; of the first and of the first two
   int rest;                     // pairs of channels that are not turned; odd: and one channel more
   bool odd;
-  int blocks_q, blocks_k;
+  int blocks;                   // of the backward pass
   // filled in by the launcher
-  int slots, turned_slots, log_lanes, table_pairs;
+  int slots, turned_slots, log_lanes, table_pairs, rows;
+  unsigned by_pairs;
+  int64_t tiles;
 };
 
-// Blocks of the backward pass for a side: each leaves one share of dw.
+// Blocks of the backward pass at most: each leaves one share of dw.
 inline int rope_blocks(int64_t n, int heads) {
-  if (heads == 0) return 0;
   const int64_t b = (n * heads + 63) / 64;
   return static_cast<int>(b < 1024 ? b : 1024);
 }

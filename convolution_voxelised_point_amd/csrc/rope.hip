@@ -9,13 +9,14 @@
 // head (two accesses of V elements), the next power of two of a head's threads lie side
 // by side in a wave and sum with shuffles.  Where V does not divide a head's pairs the
 // last thread starts earlier and shares some with the one before: both write the same
-// values, and its sums leave them out.  The rows' sines and cosines are computed once per
-// block into LDS and serve all heads of the row.
+// values, and its sums leave them out.  A block takes some rows: it computes their sines and
+// cosines once, into LDS, for all query and key heads.
 //
 // Angles.  The product of coordinate and frequency is formed and reduced to an eighth of a
 // turn either way in fp64 (a position of 32,768 times 1 rad needs 15 bits more than fp32
 // has), sine and cosine there are Taylor polynomials in fp32, off by about 2^-24.
 #include "common.h"
+#include "lanes.h"
 #include "launch.h"
 #include "rope.h"
 
@@ -31,9 +32,9 @@ struct __attribute__((packed, aligned(sizeof(T)))) Vals {
 
 // cos and sin of c * f
 __device__ __forceinline__ float2 turn_of(int32_t c, float f) {
-  const double q = static_cast<double>(c) * static_cast<double>(f) * 0.63661977236758134308;  // in quarter turns
-  const double n = rint(q);
-  const float x = static_cast<float>((q - n) * 1.57079632679489661923);
+  const double turns = static_cast<double>(c) * static_cast<double>(f) * 0.15915494309189533577;
+  const double part = __builtin_amdgcn_fract(turns), n = rint(4.0 * part);  // which quarter, 0 to 4
+  const float x = static_cast<float>(fma(4.0, part, -n)) * 1.57079632679f;
   const float z = x * x;
   float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
   s = fmaf(z, s, 8.3333333e-3f);
@@ -44,10 +45,9 @@ __device__ __forceinline__ float2 turn_of(int32_t c, float f) {
   k = fmaf(z, k, 4.1666667e-2f);
   k = fmaf(z, k, -0.5f);
   k = fmaf(z, k, 1.f);
-  // which quarter: n mod 4, also where n passes 32 bits
-  const int m = static_cast<int>(n - 4.0 * floor(n * 0.25));
-  const float cs = (m & 1) ? s : k, sn = (m & 1) ? k : s;
-  return float2{m == 1 || m == 2 ? -cs : cs, m >= 2 ? -sn : sn};
+  const unsigned m = static_cast<unsigned>(static_cast<int>(n));
+  const unsigned cs = __builtin_bit_cast(unsigned, (m & 1) ? s : k), sn = __builtin_bit_cast(unsigned, (m & 1) ? k : s);
+  return float2{__builtin_bit_cast(float, cs ^ ((m + 1) << 30 & 0x80000000u)), __builtin_bit_cast(float, sn ^ (m << 30 & 0x80000000u))};
 }
 
 // What a thread works on within a head.
@@ -129,84 +129,56 @@ __device__ __forceinline__ void load_w(const float* w, const Slot& s, float (&wa
   to_pairs<float, V, IL>(t, wa, wb);
 }
 
-__device__ __forceinline__ float sum_lanes(float x, int lanes) {
-  for (int m = 1; m < lanes; m <<= 1) x += __shfl_xor(x, m);
-  return x;
-}
-
-// Rows of a tile of `per` heads that starts at head number h0 (over all rows).
-struct Rows {
-  int64_t first;
-  int at;  // heads of the first row that lie before the tile
-  int n;
-};
-__device__ __forceinline__ Rows rows_of(int64_t h0, int per, int heads) {
-  Rows r;
-  r.first = h0 / heads;
-  r.at = static_cast<int>(h0 - r.first * heads);
-  r.n = (r.at + per - 1) / heads + 1;
-  return r;
-}
-
-// The block's table of angles: [row][table_pairs] (cos, sin).
-__device__ __forceinline__ void fill_angles(const RopeK& k, const Rows& r, float2* tab) {
-  const int total = r.n * k.table_pairs;
-  for (int i = threadIdx.x; i < total; i += kRopeThreads) {
-    const int row = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(k.table_pairs));
-    const int p = i - row * k.table_pairs;
+// The table of angles of rows row0.. (`rows` of them): [row][table_pairs] (cos, sin).
+__device__ __forceinline__ void fill_angles(const RopeK& k, int64_t row0, int rows, float2* tab) {
+  for (int i = threadIdx.x; i < rows * k.table_pairs; i += kRopeThreads) {
+    const int row = static_cast<int>(__umulhi(i, k.by_pairs)), p = i - row * k.table_pairs;
     float2 t{1.f, 0.f};
-    if (r.first + row < k.n && p < k.pairs) {
+    if (p < k.pairs) {
       const int axis = p < k.upto[0] ? 0 : p < k.upto[1] ? 1 : 2;
-      t = turn_of(k.coords[(r.first + row) * (k.ndim + 1) + 1 + axis], k.freqs[p]);
+      t = turn_of(k.coords[(row0 + row) * (k.ndim + 1) + 1 + axis], k.freqs[p]);
     }
     tab[i] = t;
   }
 }
 
-template <typename T, int V, bool IL, int U>
-__global__ __launch_bounds__(kRopeThreads) void k_rope_fwd(const RopeK k) {
-  extern __shared__ float2 smem[];
-  const bool is_k = blockIdx.x >= static_cast<unsigned>(k.blocks_q);
-  const RopeSide side = is_k ? k.side[1] : k.side[0];
-  const int block = is_k ? blockIdx.x - k.blocks_q : blockIdx.x, blocks = is_k ? k.blocks_k : k.blocks_q;
-  const int tid = threadIdx.x, per = kRopeThreads * U >> k.log_lanes;
-  const int lanes = 1 << k.log_lanes;
-  const Slot s = slot_of<V, IL>(k, tid & (lanes - 1));
-  const bool first = (tid & (lanes - 1)) == 0;
-  float2* tab = smem;
-  const T* x = static_cast<const T*>(side.x);
-  T* y = static_cast<T*>(side.y);
-  float wa[V], wb[V], w_odd = 1.f;
+// This thread's items of a block's rows: a slot of a head each.
+struct Item {
+  int row, head;
+  bool on;
+};
+__device__ __forceinline__ Item item_of(const RopeK& k, const RopeSide& side, int i, int rows) {
+  const int rh = i >> k.log_lanes;
+  Item it;
+  it.row = side.heads == 1 ? rh : static_cast<int>(__umulhi(rh, side.by_heads));
+  it.head = rh - it.row * side.heads;
+  it.on = it.row < rows;
+  return it;
+}
 
-  // one tile a block, but for the largest calls
-  for (int64_t tile = block; tile < side.tiles; tile += blocks) {
-    const Rows rows = rows_of(tile * per, per, side.heads);
-    // reads in flight while the angles are computed
+template <typename T, int V, bool IL, int U>
+__device__ __forceinline__ void rope_fwd_side(const RopeK& k, const RopeSide& side, const Slot& s, int64_t row0, int rows,
+                                              const float2* tab) {
+  const int lanes = 1 << k.log_lanes, count = (rows * side.heads) << k.log_lanes;
+  const bool first = (threadIdx.x & (lanes - 1)) == 0;
+  const T* x = static_cast<const T*>(side.x) + row0 * side.x_stride;
+  T* y = static_cast<T*>(side.y) + row0 * side.y_stride;
+  float wa[V], wb[V], w_odd = 1.f;
+  if (side.w) {
+    load_w<V, IL>(side.w, s, wa, wb);
+    if (k.odd) w_odd = side.w[k.d - 1];
+  }
+  for (int i0 = threadIdx.x; i0 < count; i0 += U * kRopeThreads) {
     T v[U][2 * V];
     T odd[U];
-    int64_t at[U];
-    int lrow[U];
-    bool on[U];
+    Item it[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = rows.at + ((u * kRopeThreads + tid) >> k.log_lanes);
-      lrow[u] = static_cast<int>(static_cast<unsigned>(h) / static_cast<unsigned>(side.heads));
-      const int head = h - lrow[u] * side.heads;
-      const int64_t row = rows.first + lrow[u];
-      on[u] = s.live && row < k.n;
-      const int64_t from = on[u] ? row * side.x_stride + head * k.d : 0;
-      at[u] = row * side.y_stride + head * k.d;
-      load2<T, V>(x + from, s, v[u]);
-      odd[u] = k.odd ? x[from + k.d - 1] : static_cast<T>(0.f);
-    }
-    if (tile == block && side.w) {
-      load_w<V, IL>(side.w, s, wa, wb);
-      if (k.odd) w_odd = side.w[k.d - 1];
-    }
-    if (k.table_pairs) {
-      if (tile != block) __syncthreads();  // the table of the tile before has been read
-      fill_angles(k, rows, tab);
-      __syncthreads();
+      it[u] = item_of(k, side, i0 + u * kRopeThreads, rows);
+      it[u].on = it[u].on && s.live;
+      const T* p = x + (it[u].on ? it[u].row * side.x_stride + it[u].head * k.d : 0);
+      load2<T, V>(p, s, v[u]);
+      odd[u] = k.odd ? p[k.d - 1] : static_cast<T>(0.f);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -223,7 +195,7 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope_fwd(const RopeK k) {
         last *= rstd * w_odd;
       }
       if (s.pair >= 0 && k.table_pairs) {
-        const float2* t = tab + lrow[u] * k.table_pairs + s.pair;
+        const float2* t = tab + (it[u].on ? it[u].row * k.table_pairs : 0) + s.pair;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float2 cs = t[e];
@@ -232,74 +204,71 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope_fwd(const RopeK k) {
           b[e] = fmaf(p, cs.y, q * cs.x);
         }
       }
-      if (on[u]) {
-        store2<T, V, IL>(y + at[u], s, a, b);
-        if (k.odd && first) y[at[u] + k.d - 1] = static_cast<T>(last);
+      if (it[u].on) {
+        T* p = y + (it[u].row * side.y_stride + it[u].head * k.d);
+        store2<T, V, IL>(p, s, a, b);
+        if (k.odd && first) p[k.d - 1] = static_cast<T>(last);
       }
     }
   }
 }
 
-// Each block walks over tiles and adds up its share of dw; dw is summed from those
-// shares in a fixed order afterwards.
 template <typename T, int V, bool IL, int U>
-__global__ __launch_bounds__(kRopeThreads) void k_rope_bwd(const RopeK k) {
-  extern __shared__ float2 smem[];
-  __shared__ float red[kRopeThreads / 64][kRopeMaxWidth + 1];
-  const bool is_k = blockIdx.x >= static_cast<unsigned>(k.blocks_q);
-  const RopeSide side = is_k ? k.side[1] : k.side[0];
-  const int block = is_k ? blockIdx.x - k.blocks_q : blockIdx.x, blocks = is_k ? k.blocks_k : k.blocks_q;
-  const int tid = threadIdx.x, per = kRopeThreads * U >> k.log_lanes;
-  const int lanes = 1 << k.log_lanes;
-  const Slot s = slot_of<V, IL>(k, tid & (lanes - 1));
-  const bool first = (tid & (lanes - 1)) == 0;
-  float2* tab = smem;
-  const T* x = static_cast<const T*>(side.x);
-  const T* dy = static_cast<const T*>(side.dy);
-  T* dx = static_cast<T*>(side.dx);
+__global__ __launch_bounds__(kRopeThreads) void k_rope_fwd(const RopeK k) {
+  extern __shared__ float2 tab[];
+  const Slot s = slot_of<V, IL>(k, threadIdx.x & ((1 << k.log_lanes) - 1));
+  for (int64_t tile = blockIdx.x; tile < k.tiles; tile += gridDim.x) {
+    const int64_t row0 = tile * k.rows;
+    const int rows = static_cast<int>(k.n - row0 < k.rows ? k.n - row0 : k.rows);
+    if (k.table_pairs) {
+      if (tile != blockIdx.x) __syncthreads();  // the table of the tile before has been read
+      fill_angles(k, row0, rows, tab);
+      __syncthreads();
+    }
+    rope_fwd_side<T, V, IL, U>(k, k.side[0], s, row0, rows, tab);
+    rope_fwd_side<T, V, IL, U>(k, k.side[1], s, row0, rows, tab);
+  }
+}
+
+// Gradients of a block's rows, and what they add to dw.
+template <typename T, int V, bool IL, int U>
+__device__ __forceinline__ void rope_bwd_side(const RopeK& k, const RopeSide& side, const Slot& s, int64_t row0, int rows,
+                                              const float2* tab, float (&da)[V], float (&db)[V], float& d_odd) {
+  const int lanes = 1 << k.log_lanes, count = (rows * side.heads) << k.log_lanes;
+  const bool first = (threadIdx.x & (lanes - 1)) == 0;
+  const T* x = static_cast<const T*>(side.x) + row0 * side.x_stride;
+  const T* dy = static_cast<const T*>(side.dy) + row0 * side.dy_stride;
+  T* dx = static_cast<T*>(side.dx) + row0 * side.dx_stride;
   float wa[V], wb[V], w_odd = 1.f;
   if (side.w) {
     load_w<V, IL>(side.w, s, wa, wb);
     if (k.odd) w_odd = side.w[k.d - 1];
   }
-  float da[V], db[V], d_odd = 0.f;
-#pragma unroll
-  for (int e = 0; e < V; ++e) da[e] = db[e] = 0.f;
-
-  for (int64_t tile = block; tile < side.tiles; tile += blocks) {
-    const Rows rows = rows_of(tile * per, per, side.heads);
+  for (int i0 = threadIdx.x; i0 < count; i0 += U * kRopeThreads) {
     T v[U][2 * V], gv[U][2 * V];
     T odd[U], godd[U];
-    int64_t at[U];
-    int lrow[U];
-    bool on[U];
+    Item it[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = rows.at + ((u * kRopeThreads + tid) >> k.log_lanes);
-      lrow[u] = static_cast<int>(static_cast<unsigned>(h) / static_cast<unsigned>(side.heads));
-      const int head = h - lrow[u] * side.heads;
-      const int64_t row = rows.first + lrow[u];
-      on[u] = s.live && row < k.n;
-      const int64_t from = on[u] ? row * side.x_stride + head * k.d : 0;
-      const int64_t gfrom = on[u] ? row * side.dy_stride + head * k.d : 0;
-      at[u] = row * side.dx_stride + head * k.d;
+      it[u] = item_of(k, side, i0 + u * kRopeThreads, rows);
+      it[u].on = it[u].on && s.live;
+      const int col = it[u].head * k.d;
+      const T* p = dy + (it[u].on ? it[u].row * side.dy_stride + col : 0);
+      load2<T, V>(p, s, gv[u]);
+      godd[u] = k.odd ? p[k.d - 1] : static_cast<T>(0.f);
       if (side.w) {
-        load2<T, V>(x + from, s, v[u]);
-        odd[u] = k.odd ? x[from + k.d - 1] : static_cast<T>(0.f);
+        p = x + (it[u].on ? it[u].row * side.x_stride + col : 0);
+        load2<T, V>(p, s, v[u]);
+        odd[u] = k.odd ? p[k.d - 1] : static_cast<T>(0.f);
       }
-      load2<T, V>(dy + gfrom, s, gv[u]);
-      godd[u] = k.odd ? dy[gfrom + k.d - 1] : static_cast<T>(0.f);
     }
-    __syncthreads();  // the table of the tile before has been read
-    if (k.table_pairs) fill_angles(k, rows, tab);
-    __syncthreads();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float a[V], b[V];
       to_pairs<T, V, IL>(gv[u], a, b);
       float last = static_cast<float>(godd[u]);
       if (s.pair >= 0 && k.table_pairs) {
-        const float2* t = tab + lrow[u] * k.table_pairs + s.pair;
+        const float2* t = tab + (it[u].on ? it[u].row * k.table_pairs : 0) + s.pair;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float2 cs = t[e];
@@ -325,7 +294,7 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope_bwd(const RopeK k) {
         const float c = dot * rstd * k.inv_d;  // mean(g w xn)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const bool mine = on[u] && e >= s.skip;
+          const bool mine = it[u].on && e >= s.skip;
           const float na = xa[e] * rstd, nb = xb[e] * rstd;
           da[e] = mine ? fmaf(a[e], na, da[e]) : da[e];
           db[e] = mine ? fmaf(b[e], nb, db[e]) : db[e];
@@ -334,43 +303,79 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope_bwd(const RopeK k) {
         }
         if (k.odd) {
           const float no = xo * rstd;
-          d_odd = on[u] && first ? fmaf(last, no, d_odd) : d_odd;
+          d_odd = it[u].on && first ? fmaf(last, no, d_odd) : d_odd;
           last = fmaf(-no, c, last * w_odd) * rstd;
         }
       }
-      if (on[u]) {
-        store2<T, V, IL>(dx + at[u], s, a, b);
-        if (k.odd && first) dx[at[u] + k.d - 1] = static_cast<T>(last);
+      if (it[u].on) {
+        T* p = dx + (it[u].row * side.dx_stride + it[u].head * k.d);
+        store2<T, V, IL>(p, s, a, b);
+        if (k.odd && first) p[k.d - 1] = static_cast<T>(last);
       }
     }
   }
-  if (!side.w) return;
+}
 
-  // the threads of one slot, within the wave, then over the waves
-  for (int m = lanes; m < 64; m <<= 1) {
+// Each block walks over tiles and adds up its share of dw; dw is summed from those
+// shares in a fixed order afterwards.
+// (304,878 x 8 heads of 32, bf16, a pass forward and back: three waves per SIMD with two items a
+// thread 177 us, with one 178, four waves 186 with spills; fp32, 102,835 x 9 of 40: four waves 186,
+// three 197.)
+constexpr int rope_bwd_waves(int v) { return v == 8 ? 3 : 4; }
+template <typename T, int V, bool IL, int U>
+__global__ __launch_bounds__(kRopeThreads, rope_bwd_waves(V)) void k_rope_bwd(const RopeK k) {
+  extern __shared__ float2 tab[];
+  __shared__ float red[kRopeThreads / 64][kRopeMaxWidth + 1];
+  const int tid = threadIdx.x, lanes = 1 << k.log_lanes;
+  const Slot s = slot_of<V, IL>(k, tid & (lanes - 1));
+  float da[2][V], db[2][V], d_odd[2] = {0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      da[e] += __shfl_xor(da[e], m);
-      db[e] += __shfl_xor(db[e], m);
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < V; ++e) da[h][e] = db[h][e] = 0.f;
+
+  for (int64_t tile = blockIdx.x; tile < k.tiles; tile += gridDim.x) {
+    const int64_t row0 = tile * k.rows;
+    const int rows = static_cast<int>(k.n - row0 < k.rows ? k.n - row0 : k.rows);
+    if (k.table_pairs) {
+      if (tile != blockIdx.x) __syncthreads();  // the table of the tile before has been read
+      fill_angles(k, row0, rows, tab);
+      __syncthreads();
     }
-    d_odd += __shfl_xor(d_odd, m);
-  }
-  if ((tid & 63) < lanes && s.live) {
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e >= s.skip) {
-        red[tid >> 6][IL ? s.a + 2 * e : s.a + e] = da[e];
-        red[tid >> 6][IL ? s.a + 2 * e + 1 : s.b + e] = db[e];
+    for (int h = 0; h < 2; ++h) rope_bwd_side<T, V, IL, U>(k, k.side[h], s, row0, rows, tab, da[h], db[h], d_odd[h]);
+  }
+
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (!k.side[h].dw) continue;
+    // the threads of one slot, within the wave, then over the waves
+    for (int m = lanes; m < 64; m <<= 1) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        da[h][e] += __shfl_xor(da[h][e], m);
+        db[h][e] += __shfl_xor(db[h][e], m);
       }
-    if (k.odd && first) red[tid >> 6][k.d - 1] = d_odd;
-  }
-  __syncthreads();
-  float* part = k.part + (static_cast<int64_t>(is_k ? k.blocks_q : 0) + block) * k.d;
-  for (int i = tid; i < k.d; i += kRopeThreads) {
-    float sum = 0.f;
+      d_odd[h] += __shfl_xor(d_odd[h], m);
+    }
+    __syncthreads();
+    if ((tid & 63) < lanes && s.live) {
 #pragma unroll
-    for (int wv = 0; wv < kRopeThreads / 64; ++wv) sum += red[wv][i];
-    part[i] = sum;
+      for (int e = 0; e < V; ++e)
+        if (e >= s.skip) {
+          red[tid >> 6][IL ? s.a + 2 * e : s.a + e] = da[h][e];
+          red[tid >> 6][IL ? s.a + 2 * e + 1 : s.b + e] = db[h][e];
+        }
+      if (k.odd && (tid & (lanes - 1)) == 0) red[tid >> 6][k.d - 1] = d_odd[h];
+    }
+    __syncthreads();
+    float* part = k.part + (static_cast<int64_t>(h) * k.blocks + blockIdx.x) * k.d;
+    for (int i = tid; i < k.d; i += kRopeThreads) {
+      float sum = 0.f;
+#pragma unroll
+      for (int wv = 0; wv < kRopeThreads / 64; ++wv) sum += red[wv][i];
+      part[i] = sum;
+    }
   }
 }
 
@@ -379,8 +384,8 @@ __global__ __launch_bounds__(1024) void k_rope_dw(const RopeK k) {
   __shared__ float red[64][17];
   const RopeSide side = k.side[blockIdx.y];
   if (!side.dw) return;
-  const int rows = blockIdx.y ? k.blocks_k : k.blocks_q;
-  const float* part = k.part + (blockIdx.y ? static_cast<int64_t>(k.blocks_q) * k.d : 0);
+  const int rows = k.blocks;
+  const float* part = k.part + static_cast<int64_t>(blockIdx.y) * k.blocks * k.d;
   const int x = threadIdx.x & 15, share = threadIdx.x >> 4, ch = blockIdx.x * 16 + x;
   float s = 0.f;
   if (ch < k.d)
@@ -395,11 +400,12 @@ __global__ __launch_bounds__(1024) void k_rope_dw(const RopeK k) {
   side.dw[ch] = s;
 }
 
-// Pairs per thread: as many as both the turned and the remaining part of a head hold.
-// 16-byte accesses for 16-bit types at 8; below, the same sectors in more instructions.
-int pairs_per_thread(const RopeK& k, bool il) {
-  const int turned = il ? k.d / 2 : k.pairs, rest = il ? 0 : k.rest;
-  for (int v = 8; v > 1; v /= 2)
+// Pairs per thread: as many as both the turned and the remaining part of a head hold, up to
+// 16 bytes an access.
+template <typename T, bool IL>
+int pairs_per_thread(const RopeK& k) {
+  const int turned = IL ? k.d / 2 : k.pairs, rest = IL ? 0 : k.rest;
+  for (int v = 16 / sizeof(T); v > 1; v /= 2)
     if ((turned == 0 || turned >= v) && (rest == 0 || rest >= v)) return v;
   return 1;
 }
@@ -412,47 +418,31 @@ void run(RopeK& k, bool back, hipStream_t s) {
   k.log_lanes = 0;
   while ((1 << k.log_lanes) < k.slots) ++k.log_lanes;
   k.table_pairs = k.pairs == 0 ? 0 : IL ? k.d / 2 : k.pairs;
-  // heads of both sides: small calls spread over the card with one item a thread; the table
-  // of a side with few heads has many rows and stays within 32 KB
-  const int64_t items = k.n * (k.side[0].heads + k.side[1].heads) << k.log_lanes;
-  int u = back ? 2 : items <= int64_t{4} * 256 * kRopeThreads ? 1 : 4;
-  size_t lds = 0;
-  for (;; u /= 2) {
-    const int per = kRopeThreads * u >> k.log_lanes;
-    int rows = 0;
-    for (RopeSide& side : k.side) {
-      if (side.heads == 0) continue;
-      const int r = (side.heads - 1 + per - 1) / side.heads + 1;
-      rows = rows > r ? rows : r;
-      side.tiles = ceil_div<int64_t>(k.n * side.heads, per);
-    }
-    lds = static_cast<size_t>(rows) * k.table_pairs * sizeof(float2);
-    if (u == 1 || lds <= 32 * 1024) break;
-  }
-  if (!back) {
-    // at most 2^22 blocks of a side: a launch may have 2^32 threads
-    k.blocks_q = static_cast<int>(k.side[0].tiles < (1 << 22) ? k.side[0].tiles : 1 << 22);
-    k.blocks_k = static_cast<int>(k.side[1].tiles < (1 << 22) ? k.side[1].tiles : 1 << 22);
-  }
-  const unsigned grid = static_cast<unsigned>(k.blocks_q + k.blocks_k);
+  if (k.table_pairs) k.by_pairs = static_cast<unsigned>((uint64_t{1} << 32) / k.table_pairs + 1);
+  for (RopeSide& side : k.side)
+    if (side.heads > 1) side.by_heads = static_cast<unsigned>((uint64_t{1} << 32) / side.heads + 1);
+  // Rows of a tile: 1024 items, in a table of at most 32 KB; fewer where that leaves CUs without a tile.
+  const int heads = k.side[0].heads + k.side[1].heads;
+  int64_t rows = 4 * kRopeThreads / (heads << k.log_lanes);
+  if (k.table_pairs && rows > 4096 / k.table_pairs) rows = 4096 / k.table_pairs;
+  if (rows > k.n / 512) rows = k.n / 512;
+  k.rows = static_cast<int>(rows < 1 ? 1 : rows);
+  k.tiles = ceil_div<int64_t>(k.n, k.rows);
+  const size_t lds = static_cast<size_t>(k.rows) * k.table_pairs * sizeof(float2);
   if (back) {
-    if (u == 1)
-      k_rope_bwd<T, V, IL, 1><<<grid, kRopeThreads, lds, s>>>(k);
-    else
-      k_rope_bwd<T, V, IL, 2><<<grid, kRopeThreads, lds, s>>>(k);
-  } else if (u == 1) {
-    k_rope_fwd<T, V, IL, 1><<<grid, kRopeThreads, lds, s>>>(k);
-  } else if (u == 2) {
-    k_rope_fwd<T, V, IL, 2><<<grid, kRopeThreads, lds, s>>>(k);
-  } else {
-    k_rope_fwd<T, V, IL, 4><<<grid, kRopeThreads, lds, s>>>(k);
-  }
+    const int resident = 256 * rope_bwd_waves(V);
+    k.blocks = k.blocks < resident ? k.blocks : resident;
+    k_rope_bwd<T, V, IL, V == 8 ? 2 : 1><<<k.blocks, kRopeThreads, lds, s>>>(k);
+  } else  // (at most 2^23 blocks: a launch may have 2^32 threads)
+    k_rope_fwd<T, V, IL, 2><<<static_cast<unsigned>(k.tiles < (1 << 23) ? k.tiles : 1 << 23), kRopeThreads, lds, s>>>(k);
 }
 
 template <typename T, bool IL>
 void run(RopeK& k, bool back, hipStream_t s) {
-  switch (pairs_per_thread(k, IL)) {
-    case 8: return run<T, 8, IL>(k, back, s);
+  switch (pairs_per_thread<T, IL>(k)) {
+    case 8:
+      if constexpr (sizeof(T) == 2) return run<T, 8, IL>(k, back, s);
+      break;
     case 4: return run<T, 4, IL>(k, back, s);
     case 2: return run<T, 2, IL>(k, back, s);
     default: return run<T, 1, IL>(k, back, s);
@@ -477,8 +467,6 @@ hipError_t launch_rope_fwd(RopeK& k, ts_dtype dt, bool interleaved, hipStream_t 
 
 hipError_t launch_rope_bwd(RopeK& k, ts_dtype dt, bool interleaved, hipStream_t s) {
   if (k.n > 0) run(k, dt, interleaved, true, s);
-  else
-    k.blocks_q = k.blocks_k = 0;
   if (k.side[0].dw || k.side[1].dw) k_rope_dw<<<dim3(ceil_div(k.d, 16), 2), 1024, 0, s>>>(k);
   return hipGetLastError();
 }

@@ -19,7 +19,7 @@ struct RouteK {
   float* gates;
   int64_t* starts;
   int32_t *rows, *place;
-  int32_t* counts;  // [e + 1][blocks]
+  int32_t* counts;  // [e + 1][blocks], and their sums [e + 1]
   const float* dgates;
   void* dlogits;
   // filled in by the launcher
@@ -29,12 +29,11 @@ struct RouteK {
 
 inline bool route_small(int64_t n, int top) { return n * top <= kRouteSmall; }
 
-// Blocks of 1024 threads: about one pass over a block's rows at most twice per compute
-// unit, and at most 64 counts for each of the scan's threads.
+// Blocks of 1024 threads: two for each CU, and at most 2^18 counts.
 inline int route_blocks(int64_t n, int e) {
   int lanes = 1;
   while (8 * lanes < e) lanes *= 2;
-  const int64_t rows = 1024 / lanes, b = (n + rows - 1) / rows, most = 65536 / (e + 1);
+  const int64_t rows = 1024 / lanes, b = (n + rows - 1) / rows, most = (1 << 18) / (e + 1);
   const int64_t cap = most < 512 ? most : 512;
   return static_cast<int>(b < cap ? b : cap);
 }

@@ -1,17 +1,19 @@
 // Router of rows to experts (ts_route_fwd) and its backward pass.
 //
 // A row's `top` largest logits are picked one after the other: the threads of a row hold
-// 8 experts each, order them by (value, lowest expert first) and agree on the largest
-// with shuffles.  Values are compared as integers that order like the floats (-0 made
-// 0, NaN above infinity).  Gates are a softmax in fp32.
+// 8 experts each and agree on the largest.  Values are compared as integers that order like
+// the floats (-0 made 0, NaN above infinity); 16-bit ones share a word with their expert's number,
+// so that one maximum finds both and the lowest expert wins among equals.  Gates are a softmax
+// in fp32.  (All of this is vector instructions, about as long as reading 64 bf16 logits.)
 //
 // The chosen pairs (row, j) are then put in order of their expert, by a counting sort
-// without atomics on memory: blocks own runs of rows and count their pairs per expert,
-// one block turns the counts into first places, and every block gives its pairs their
-// places, wave after wave, by counting the lanes before that chose the same expert.
-// Pairs without an expert form one more bucket behind the last.  Small calls do all of it
-// in one block (39 rows: one launch instead of three).
+// without atomics on memory: blocks own runs of rows and count their pairs per expert, a
+// block per expert adds up these counts, and every block gives its pairs their places, wave
+// after wave, by counting the lanes before that chose the same expert.  Pairs without an
+// expert form one more bucket behind the last.  Small calls do all of it in one block (39
+// rows: one launch instead of three).
 #include "act8.h"
+#include "lanes.h"
 #include "launch.h"
 #include "route.h"
 
@@ -20,15 +22,79 @@ namespace {
 
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / 64;
-constexpr int kLow = 0x007fffff;  // of -infinity; what orders at or below it is never picked
 
-__device__ __forceinline__ uint32_t order_of(float z) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, z + 0.f);
-  if (z != z) return ~0u;
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+// A logit as an integer that orders like it; what orders at or below that of -infinity is
+// never picked.
+template <typename T>
+struct Order;
+template <>
+struct Order<float> {
+  static constexpr uint32_t kLow = 0x007fffffu;
+  static __device__ __forceinline__ uint32_t of(float z) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, z + 0.f);
+    return z != z ? ~0u : b & 0x80000000u ? ~b : b | 0x80000000u;
+  }
+  static __device__ __forceinline__ float value(uint32_t o) {
+    return __builtin_bit_cast(float, o == ~0u ? 0x7fc00000u : o & 0x80000000u ? o & 0x7fffffffu : ~o);
+  }
+};
+template <typename T, uint32_t LOW, uint32_t INF>
+struct Order16 {
+  static constexpr uint32_t kLow = LOW;
+  static __device__ __forceinline__ uint32_t of(T z) {
+    uint32_t b = __builtin_bit_cast(uint16_t, z);
+    b = b == 0x8000u ? 0u : b;
+    return (b & 0x7fffu) > INF ? 0xffffu : b & 0x8000u ? ~b & 0xffffu : b | 0x8000u;
+  }
+  static __device__ __forceinline__ float value(uint32_t o) {
+    const uint32_t b = o & 0x8000u ? o & 0x7fffu : ~o & 0xffffu;  // (0xffff stays a NaN)
+    return static_cast<float>(__builtin_bit_cast(T, static_cast<uint16_t>(b)));
+  }
+};
+template <>
+struct Order<_Float16> : Order16<_Float16, 0x03ffu, 0x7c00u> {};
+template <>
+struct Order<__bf16> : Order16<__bf16, 0x007fu, 0x7f80u> {};
+
+// Logits c0..c0+7 of a row.
+template <typename T>
+__device__ __forceinline__ void load_logits(const T* row, int c0, int c, bool vec, T (&v)[8]) {
+  if (c0 + 8 <= c) {
+    Unit<T> u;
+    if (vec) u = *reinterpret_cast<const Unit<T>*>(row + c0);
+    else
+      __builtin_memcpy(&u, row + c0, sizeof u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = u.e[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c0 + e < c ? row[c0 + e] : static_cast<T>(0.f);
+  }
 }
-__device__ __forceinline__ float value_of(uint32_t o) {
-  return __builtin_bit_cast(float, o == ~0u ? 0x7fc00000u : o & 0x80000000u ? o & 0x7fffffffu : ~o);
+
+// The largest of the row's keys (0: no expert) and its expert, in all of the row's threads;
+// taken out of the keys.
+template <typename T>
+__device__ __forceinline__ uint32_t take_largest(uint32_t (&key)[8], int first, int lanes, int* expert) {
+  uint32_t o = key[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) o = key[i] > o ? key[i] : o;
+  o = max_lanes(o, lanes);
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) key[i] = key[i] == o ? 0u : key[i];
+    *expert = 0xffff - static_cast<int>(o & 0xffffu);
+    return o >> 16;
+  } else {
+    uint32_t at = ~0u;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) at = key[i] == o ? static_cast<uint32_t>(first + i) : at;
+    at = min_lanes(at, lanes);
+    *expert = static_cast<int>(at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) key[i] = at == static_cast<uint32_t>(first + i) ? 0u : key[i];
+    return o;
+  }
 }
 
 // Experts and gates of rows [r0, r1): G threads a row (8 experts each).  on_pick(row, j,
@@ -41,33 +107,23 @@ __device__ __forceinline__ void pick(const RouteK& k, int64_t r0, int64_t r1, fl
   for (int64_t base = r0; base < r1; base += per) {
     const int64_t row = base + slot;
     const bool on = row < r1;
-    float z[8];
+    T z[8];
     uint32_t key[8];
-    if (on && lane * 8 < k.e) load_unit(static_cast<const T*>(k.logits) + row * k.e, lane * 8, k.e, k.vec, z);
+    if (on && lane * 8 < k.e) load_logits(static_cast<const T*>(k.logits) + row * k.e, lane * 8, k.e, k.vec, z);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) key[i] = on && lane * 8 + i < k.e ? order_of(z[i]) : 0u;
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane * 8 + i;
+      const uint32_t o = Order<T>::of(z[i]);
+      key[i] = !on || e >= k.e ? 0u : sizeof(T) == 2 ? o << 16 | (0xffffu - e) : o;
+    }
     float best = 0.f, sum = 0.f;
     for (int j = 0; j < k.top; ++j) {
-      uint32_t o = 0;
-      int at = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (key[i] > o) o = key[i], at = i;
-      at += lane * 8;
-      for (int m = 1; m < g; m <<= 1) {
-        const uint32_t oo = __shfl_xor(o, m);
-        const int oa = __shfl_xor(at, m);
-        if (oo > o || (oo == o && oa < at)) o = oo, at = oa;
-      }
-      const bool some = o > static_cast<uint32_t>(kLow);
-      const float v = value_of(o);
+      int at;
+      const uint32_t o = take_largest<T>(key, lane * 8, g, &at);
+      const bool some = o > Order<T>::kLow;
+      const float v = Order<T>::value(o);
       if (j == 0) best = v;
-      if (some) {
-        if (!k.over_all) sum += expf(v - best);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (at == lane * 8 + i) key[i] = 0;
-      }
+      if (some && !k.over_all) sum += exp_below(v - best);
       if (on && lane == 0) {
         zs[slot * k.top + j] = v;
         es[slot * k.top + j] = static_cast<int16_t>(some ? at : -1);
@@ -75,8 +131,8 @@ __device__ __forceinline__ void pick(const RouteK& k, int64_t r0, int64_t r1, fl
     }
     if (k.over_all) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += on && lane * 8 + i < k.e ? expf(z[i] - best) : 0.f;
-      for (int m = 1; m < g; m <<= 1) sum += __shfl_xor(sum, m);
+      for (int i = 0; i < 8; ++i) sum += on && lane * 8 + i < k.e ? exp_below(static_cast<float>(z[i]) - best) : 0.f;
+      sum = sum_lanes(sum, g);
     }
     // a row's threads lie in one wave: what its first one wrote is there
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -86,7 +142,7 @@ __device__ __forceinline__ void pick(const RouteK& k, int64_t r0, int64_t r1, fl
       for (int j = lane; j < k.top; j += g) {
         const int e = es[slot * k.top + j];
         k.experts[row * k.top + j] = e;
-        k.gates[row * k.top + j] = e < 0 ? 0.f : expf(zs[slot * k.top + j] - best) / sum;
+        k.gates[row * k.top + j] = e < 0 ? 0.f : exp_below(zs[slot * k.top + j] - best) / sum;
         on_pick(row, j, e);
       }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -166,48 +222,35 @@ __device__ __forceinline__ int32_t scan_inclusive(int32_t x) {
   return x;
 }
 
-// counts[bucket][block] -> the first place of each; starts of the experts.  One block, four
-// counts a thread and pass (64 experts x 512 blocks: 8 passes).
-__global__ __launch_bounds__(kRouteThreads) void k_route_scan(const RouteK k) {
-  __shared__ int32_t wave_sum[2][kRouteWaves];
-  const int total = (k.e + 1) * k.blocks;
+// counts[bucket][block] -> the pairs of the bucket in the blocks before; their number behind them.
+__global__ __launch_bounds__(256) void k_route_scan(const RouteK k) {
+  __shared__ int32_t wave_sum[4];
+  int32_t* row = k.counts + static_cast<int64_t>(blockIdx.x) * k.blocks;
   const int wave = threadIdx.x >> 6;
-  int32_t carry = 0, c[4], ahead[4];
-  auto fetch = [&](int at, int32_t (&v)[4]) {
+  int32_t carry = 0;
+  for (int base = 0; base < k.blocks; base += 512) {  // two counts a thread; once for up to 512 blocks
+    const int at = base + static_cast<int>(threadIdx.x) * 2;
+    const int32_t a = at < k.blocks ? row[at] : 0, b = at + 1 < k.blocks ? row[at + 1] : 0;
+    const int32_t inc = scan_inclusive(a + b);
+    if (base) __syncthreads();
+    if ((threadIdx.x & 63) == 63) wave_sum[wave] = inc;
+    __syncthreads();
+    int32_t sum = carry + inc - a - b;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = at + i < total ? k.counts[at + i] : 0;
-  };
-  fetch(threadIdx.x * 4, ahead);
-  for (int base = 0, pass = 0; base < total; base += 4 * kRouteThreads, pass ^= 1) {
-    const int at = base + static_cast<int>(threadIdx.x) * 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = ahead[i];
-    fetch(at + 4 * kRouteThreads, ahead);
-    const int32_t mine = c[0] + c[1] + c[2] + c[3];
-    const int32_t inc = scan_inclusive(mine);
-    if ((threadIdx.x & 63) == 63) wave_sum[pass][wave] = inc;
-    __syncthreads();  // (the other half of wave_sum may still be read)
-    int32_t sum = carry + inc - mine;
-#pragma unroll
-    for (int w = 0; w < kRouteWaves; ++w) {
-      const int32_t v = wave_sum[pass][w];
-      sum += w < wave ? v : 0;
-      carry += v;
+    for (int w = 0; w < 4; ++w) {
+      sum += w < wave ? wave_sum[w] : 0;
+      carry += wave_sum[w];
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (at + i < total) {
-        k.counts[at + i] = sum;
-        if ((at + i) % k.blocks == 0) k.starts[(at + i) / k.blocks] = sum;
-      }
-      sum += c[i];
-    }
+    if (at < k.blocks) row[at] = sum;
+    if (at + 1 < k.blocks) row[at + 1] = sum + a;
   }
+  if (threadIdx.x == 0) k.counts[static_cast<int64_t>(k.e + 1) * k.blocks + blockIdx.x] = carry;
 }
 
 // Places of one block's pairs.
 __global__ __launch_bounds__(kRouteThreads) void k_route_place(const RouteK k) {
   extern __shared__ int32_t next[];  // [waves][e + 1]
+  __shared__ int32_t base[kRouteMaxExperts + 1];
   const int wave = threadIdx.x >> 6, buckets = k.e + 1;
   const Span r = span_of(k.n, k.blocks, blockIdx.x);
   const Span mine = span_of((r.b - r.a) * k.top, kRouteWaves, wave);
@@ -218,9 +261,22 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(const RouteK k) {
     const int e = k.experts[p];
     atomicAdd(&next[wave * buckets + (e < 0 ? k.e : e)], 1);
   }
+  if (wave == 0) {  // first places of the buckets
+    int32_t carry = 0;
+    for (int b0 = 0; b0 < buckets; b0 += 64) {
+      const int b = b0 + static_cast<int>(threadIdx.x);
+      const int32_t c = b < buckets ? k.counts[static_cast<int64_t>(buckets) * k.blocks + b] : 0;
+      const int32_t inc = scan_inclusive(c);
+      if (b < buckets) {
+        base[b] = carry + inc - c;
+        if (blockIdx.x == 0) k.starts[b] = carry + inc - c;
+      }
+      carry += __shfl(inc, 63);
+    }
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < buckets; i += kRouteThreads) {
-    int32_t at = k.counts[static_cast<int64_t>(i) * k.blocks + blockIdx.x];
+    int32_t at = base[i] + k.counts[static_cast<int64_t>(i) * k.blocks + blockIdx.x];
     for (int w = 0; w < kRouteWaves; ++w) {
       const int32_t c = next[w * buckets + i];
       next[w * buckets + i] = at;
@@ -280,16 +336,18 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_small(const RouteK k) {
 }
 
 // dlogits: with normalised gates g_j (dg_j - sum g dg) at the chosen experts, else
-// [chosen] g_j dg_j - p sum g dg at all of them, p = softmax(logits).
+// [chosen] g_j dg_j - p sum g dg at all of them, p = softmax(logits) = g_0 exp(logits - the largest).
 template <typename T>
 __global__ __launch_bounds__(256) void k_route_bwd(const RouteK k) {
   const int g = 1 << k.log_lanes, lane = threadIdx.x & (g - 1);
   const int64_t step = static_cast<int64_t>(gridDim.x) * (256 >> k.log_lanes);
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * (256 >> k.log_lanes) + (threadIdx.x >> k.log_lanes); row < k.n; row += step) {
-    float z[8], d[8];
+    const T* logits = static_cast<const T*>(k.logits) + row * k.e;
+    T z[8];
+    float d[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) d[i] = 0.f;
-    if (k.over_all && lane * 8 < k.e) load_unit(static_cast<const T*>(k.logits) + row * k.e, lane * 8, k.e, k.vec, z);
+    if (k.over_all && lane * 8 < k.e) load_logits(logits, lane * 8, k.e, k.vec, z);
     float inner = 0.f;
     bool some = false;
     for (int j = 0; j < k.top; ++j) {
@@ -308,22 +366,12 @@ __global__ __launch_bounds__(256) void k_route_bwd(const RouteK k) {
           if (e == lane * 8 + i) d[i] += x;
       }
       if (k.over_all) {
-        float best = -INFINITY, sum = 0.f;
+        // the first expert has the largest logit, and its gate is 1 over the softmax's sum
+        const int64_t p = row * k.top;
+        const int top1 = k.experts[p];
+        const float best = static_cast<float>(logits[top1 < 0 ? 0 : top1 < k.e ? top1 : k.e - 1]), c = inner * k.gates[p];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (lane * 8 + i < k.e) best = z[i] > best || z[i] != z[i] ? z[i] : best;  // NaN stays
-        for (int m = 1; m < g; m <<= 1) {
-          const float o = __shfl_xor(best, m);
-          best = o > best || o != o ? o : best;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          z[i] = lane * 8 + i < k.e ? expf(z[i] - best) : 0.f;
-          sum += z[i];
-        }
-        for (int m = 1; m < g; m <<= 1) sum += __shfl_xor(sum, m);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = fmaf(-z[i] / sum, inner, d[i]);
+        for (int i = 0; i < 8; ++i) d[i] = fmaf(-exp_below(static_cast<float>(z[i]) - best), c, d[i]);
       }
     }
     if (lane * 8 < k.e) store_unit(static_cast<T*>(k.dlogits) + row * k.e, lane * 8, k.e, k.vec, d);
@@ -344,7 +392,7 @@ void run(const RouteK& k, bool back, hipStream_t s) {
   }
   const size_t picks = static_cast<size_t>(kRouteThreads >> k.log_lanes) * k.top * 6;  // at most 48 KB
   k_route<T><<<k.blocks, kRouteThreads, picks, s>>>(k);
-  k_route_scan<<<1, kRouteThreads, 0, s>>>(k);
+  k_route_scan<<<k.e + 1, 256, 0, s>>>(k);
   k_route_place<<<k.blocks, kRouteThreads, lds, s>>>(k);
 }
 
