@@ -24,7 +24,6 @@ struct RouteK {
   void* dlogits;
   // filled in by the launcher
   int log_lanes, bits, blocks;
-  bool vec;
 };
 
 inline bool route_small(int64_t n, int top) { return n * top <= kRouteSmall; }

@@ -56,19 +56,31 @@ struct Order<_Float16> : Order16<_Float16, 0x03ffu, 0x7c00u> {};
 template <>
 struct Order<__bf16> : Order16<__bf16, 0x007fu, 0x7f80u> {};
 
-// Logits c0..c0+7 of a row.
+// Logits c0..c0+7 of a row of c, anything past it.  VEC: whole, aligned units only.  Otherwise the
+// last unit is the row's last 8 logits moved down (a branch of its own would break up the whole
+// ones' accesses as well).
 template <typename T>
-__device__ __forceinline__ void load_logits(const T* row, int c0, int c, bool vec, T (&v)[8]) {
-  if (c0 + 8 <= c) {
-    Unit<T> u;
-    if (vec) u = *reinterpret_cast<const Unit<T>*>(row + c0);
-    else
-      __builtin_memcpy(&u, row + c0, sizeof u);
+struct __attribute__((packed, aligned(sizeof(T)))) LooseLogits {
+  T e[8];
+};
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_logits(const T* row, int c0, int c, T (&v)[8]) {
+  if (VEC) {
+    const Unit<T> u = *reinterpret_cast<const Unit<T>*>(row + c0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = u.e[e];
-  } else {
+  } else if (c < 8) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c0 + e < c ? row[c0 + e] : static_cast<T>(0.f);
+    for (int e = 0; e < 8; ++e) v[e] = e < c ? row[e] : static_cast<T>(0.f);
+  } else {
+    const int by = c0 + 8 <= c ? 0 : c0 + 8 - c;
+    const LooseLogits<T> u = *reinterpret_cast<const LooseLogits<T>*>(row + c0 - by);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = u.e[e];
+#pragma unroll
+    for (int m = 4; m > 0; m >>= 1)
+#pragma unroll
+      for (int e = 0; e + m < 8; ++e) v[e] = by & m ? v[e + m] : v[e];
   }
 }
 
@@ -100,16 +112,22 @@ __device__ __forceinline__ uint32_t take_largest(uint32_t (&key)[8], int first, 
 // Experts and gates of rows [r0, r1): G threads a row (8 experts each).  on_pick(row, j,
 // expert) is called once per pair, by one thread.  Every thread of the block calls this;
 // zs and es hold a pass's picks, `top` for each of its rows.
-template <typename T, typename F>
+template <typename T, bool VEC, typename F>
 __device__ __forceinline__ void pick(const RouteK& k, int64_t r0, int64_t r1, float* zs, int16_t* es, F&& on_pick) {
   const int g = 1 << k.log_lanes, lane = threadIdx.x & (g - 1), slot = threadIdx.x >> k.log_lanes;
   const int per = kRouteThreads >> k.log_lanes;
+  T z[8], ahead[8];  // logits of this pass and of the next
+  auto load = [&](int64_t row, T (&v)[8]) {
+    if (row < r1 && lane * 8 < k.e) load_logits<T, VEC>(static_cast<const T*>(k.logits) + row * k.e, lane * 8, k.e, v);
+  };
+  load(r0 + slot, ahead);
   for (int64_t base = r0; base < r1; base += per) {
     const int64_t row = base + slot;
     const bool on = row < r1;
-    T z[8];
     uint32_t key[8];
-    if (on && lane * 8 < k.e) load_logits(static_cast<const T*>(k.logits) + row * k.e, lane * 8, k.e, k.vec, z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = ahead[i];
+    load(row + per, ahead);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = lane * 8 + i;
@@ -130,8 +148,11 @@ __device__ __forceinline__ void pick(const RouteK& k, int64_t r0, int64_t r1, fl
       }
     }
     if (k.over_all) {
+      // (the exponent in one part: off by |d| 2^-24 at the distance d below the largest, where a term
+      // is worth exp(d) of the sum, which is less than the sum's own rounding)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += on && lane * 8 + i < k.e ? exp_below(static_cast<float>(z[i]) - best) : 0.f;
+      for (int i = 0; i < 8; ++i)
+        sum += on && lane * 8 + i < k.e ? __builtin_amdgcn_exp2f((static_cast<float>(z[i]) - best) * 1.44269504f) : 0.f;
       sum = sum_lanes(sum, g);
     }
     // a row's threads lie in one wave: what its first one wrote is there
@@ -200,7 +221,7 @@ __device__ __forceinline__ Span span_of(int64_t n, int parts, int i) {
 }
 
 // One block's rows; counts[bucket][block].
-template <typename T>
+template <typename T, bool VEC>
 __global__ __launch_bounds__(kRouteThreads) void k_route(const RouteK k) {
   extern __shared__ float zs[];  // [rows of a pass][top], then the experts
   int16_t* es = reinterpret_cast<int16_t*>(zs + (kRouteThreads >> k.log_lanes) * k.top);
@@ -208,7 +229,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(const RouteK k) {
   for (int i = threadIdx.x; i <= k.e; i += kRouteThreads) count[i] = 0;
   __syncthreads();
   const Span r = span_of(k.n, k.blocks, blockIdx.x);
-  pick<T>(k, r.a, r.b, zs, es, [&](int64_t, int, int e) { atomicAdd(&count[e < 0 ? k.e : e], 1); });
+  pick<T, VEC>(k, r.a, r.b, zs, es, [&](int64_t, int, int e) { atomicAdd(&count[e < 0 ? k.e : e], 1); });
   __syncthreads();
   for (int i = threadIdx.x; i <= k.e; i += kRouteThreads) k.counts[static_cast<int64_t>(i) * k.blocks + blockIdx.x] = count[i];
 }
@@ -288,7 +309,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(const RouteK k) {
 }
 
 // All of it in one block, for calls of at most kRouteSmall pairs.
-template <typename T>
+template <typename T, bool VEC>
 __global__ __launch_bounds__(kRouteThreads) void k_route_small(const RouteK k) {
   __shared__ float zs[kRouteSmall];
   __shared__ int16_t es[kRouteSmall];
@@ -300,7 +321,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_small(const RouteK k) {
   __syncthreads();
   const int pairs = static_cast<int>(k.n) * k.top;
   const int per = ceil_div(pairs, kRouteWaves);
-  pick<T>(k, 0, k.n, zs, es, [&](int64_t row, int j, int e) {
+  pick<T, VEC>(k, 0, k.n, zs, es, [&](int64_t row, int j, int e) {
     const int p = static_cast<int>(row) * k.top + j;
     expert[p] = static_cast<int16_t>(e);
     atomicAdd(&next[p / per * buckets + (e < 0 ? k.e : e)], 1);
@@ -337,7 +358,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_small(const RouteK k) {
 
 // dlogits: with normalised gates g_j (dg_j - sum g dg) at the chosen experts, else
 // [chosen] g_j dg_j - p sum g dg at all of them, p = softmax(logits) = g_0 exp(logits - the largest).
-template <typename T>
+template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void k_route_bwd(const RouteK k) {
   const int g = 1 << k.log_lanes, lane = threadIdx.x & (g - 1);
   const int64_t step = static_cast<int64_t>(gridDim.x) * (256 >> k.log_lanes);
@@ -347,7 +368,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(const RouteK k) {
     float d[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) d[i] = 0.f;
-    if (k.over_all && lane * 8 < k.e) load_logits(logits, lane * 8, k.e, k.vec, z);
+    if (k.over_all && lane * 8 < k.e) load_logits<T, VEC>(logits, lane * 8, k.e, z);
     float inner = 0.f;
     bool some = false;
     for (int j = 0; j < k.top; ++j) {
@@ -374,24 +395,24 @@ __global__ __launch_bounds__(256) void k_route_bwd(const RouteK k) {
         for (int i = 0; i < 8; ++i) d[i] = fmaf(-exp_below(static_cast<float>(z[i]) - best), c, d[i]);
       }
     }
-    if (lane * 8 < k.e) store_unit(static_cast<T*>(k.dlogits) + row * k.e, lane * 8, k.e, k.vec, d);
+    if (lane * 8 < k.e) store_unit(static_cast<T*>(k.dlogits) + row * k.e, lane * 8, k.e, VEC, d);
   }
 }
 
-template <typename T>
+template <typename T, bool VEC>
 void run(const RouteK& k, bool back, hipStream_t s) {
   if (back) {
     const int64_t b = ceil_div<int64_t>(k.n, 256 >> k.log_lanes), most = int64_t{1} << 23;
-    k_route_bwd<T><<<static_cast<unsigned>(b < most ? b : most), 256, 0, s>>>(k);
+    k_route_bwd<T, VEC><<<static_cast<unsigned>(b < most ? b : most), 256, 0, s>>>(k);
     return;
   }
   const size_t lds = static_cast<size_t>(kRouteWaves) * (k.e + 1) * sizeof(int32_t);
   if (route_small(k.n, k.top)) {
-    k_route_small<T><<<1, kRouteThreads, lds, s>>>(k);
+    k_route_small<T, VEC><<<1, kRouteThreads, lds, s>>>(k);
     return;
   }
   const size_t picks = static_cast<size_t>(kRouteThreads >> k.log_lanes) * k.top * 6;  // at most 48 KB
-  k_route<T><<<k.blocks, kRouteThreads, picks, s>>>(k);
+  k_route<T, VEC><<<k.blocks, kRouteThreads, picks, s>>>(k);
   k_route_scan<<<k.e + 1, 256, 0, s>>>(k);
   k_route_place<<<k.blocks, kRouteThreads, lds, s>>>(k);
 }
@@ -404,12 +425,12 @@ hipError_t launch_route(RouteK& k, ts_dtype dt, bool back, hipStream_t s) {
   while ((8 << k.log_lanes) < k.e) ++k.log_lanes;
   k.bits = 1;
   while ((1 << k.bits) < k.e + 1) ++k.bits;
-  k.vec = k.e % 8 == 0 && ((reinterpret_cast<uintptr_t>(k.logits) | reinterpret_cast<uintptr_t>(k.dlogits)) & 15) == 0;
+  const bool vec = k.e % 8 == 0 && ((reinterpret_cast<uintptr_t>(k.logits) | reinterpret_cast<uintptr_t>(k.dlogits)) & 15) == 0;
   k.blocks = route_blocks(k.n, k.e);
   switch (dt) {
-    case TS_F32: run<float>(k, back, s); break;
-    case TS_F16: run<_Float16>(k, back, s); break;
-    default: run<__bf16>(k, back, s); break;
+    case TS_F32: vec ? run<float, true>(k, back, s) : run<float, false>(k, back, s); break;
+    case TS_F16: vec ? run<_Float16, true>(k, back, s) : run<_Float16, false>(k, back, s); break;
+    default: vec ? run<__bf16, true>(k, back, s) : run<__bf16, false>(k, back, s); break;
   }
   return hipGetLastError();
 }

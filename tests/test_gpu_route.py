@@ -198,7 +198,8 @@ def test_combine_places_out_of_range(ts):
     assert torch.equal(out, torch.stack([y[0], y[3], torch.zeros(16, device="cuda")]))
     flags.zero_()
     dy, dg = ts.combine_bwd(d, y, place, gates, err_flags=flags, into=torch.zeros_like(y))
-    assert int(flags) == ts.TS_FLAG_RANGE and torch.equal(dy[[0, 3]], d[:2]) and float(dy.abs().sum()) == float(dy[[0, 3]].abs().sum())
+    assert int(flags) == ts.TS_FLAG_RANGE and torch.equal(dy[[0, 3]], d[:2])
+    assert (dy[[1, 2, 4, 5, 6, 7, 8, 9]] == 0).all()
     assert (dg.reshape(-1)[[1, 2, 4, 5]] == 0).all()
     assert torch.equal(ts.combine_fwd(y, place, gates), out)  # without a flag word
 
