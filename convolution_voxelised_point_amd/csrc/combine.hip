@@ -7,6 +7,7 @@
 // of a row, so a row is one or a few wide accesses wherever it lies.  Gathering by
 // `place` keeps the order of the sum fixed, and needs no atomics.  Sums are fp32.
 #include "act8.h"
+#include "lanes.h"
 #include "launch.h"
 
 namespace ts {
@@ -35,6 +36,16 @@ __device__ __forceinline__ int64_t row_at(const CombineK& k, int64_t t, int j) {
   return p;
 }
 
+// 8 channels of a result.
+template <typename T>
+__device__ __forceinline__ void put_unit(T* row, int c0, int c, bool vec, const float (&f)[8]) {
+  if (!vec) return store_unit(row, c0, c, vec, f);
+  Unit<T> v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v.e[e] = static_cast<T>(f[e]);
+  store_once(row + c0, v);
+}
+
 // AHEAD grouped rows of a row are read at once.
 template <typename T, int AHEAD>
 __global__ __launch_bounds__(256) void k_combine_fwd(const CombineK k) {
@@ -61,7 +72,7 @@ __global__ __launch_bounds__(256) void k_combine_fwd(const CombineK k) {
           for (int e = 0; e < 8; ++e) sum[e] = fmaf(g[j], f[j][e], sum[e]);
         }
     }
-    store_unit(static_cast<T*>(k.out) + t * k.c, c0, k.c, k.vec, sum);
+    put_unit(static_cast<T*>(k.out) + t * k.c, c0, k.c, k.vec, sum);
   }
 }
 
@@ -91,12 +102,11 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const CombineK k) {
             dot = fmaf(d[e], f[e], dot);
             r[e] = g * d[e];
           }
-          store_unit(dy, u * 8, k.c, k.vec, r);
+          put_unit(dy, u * 8, k.c, k.vec, r);
           if (ONE) break;
         }
       }
-#pragma unroll
-      for (int m = 1; m < LPR; m <<= 1) dot += __shfl_xor(dot, m);
+      dot = sum_lanes(dot, LPR);
       if (lane == 0) k.dgates[t * k.top + j] = dot;
     }
   }

@@ -169,6 +169,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   typedef Operand<T, BN, NT, B_ACROSS> OB;
   constexpr int CA = OA::kCopies, CB = OB::kCopies;
   constexpr int kCols = GLU && OP == kGroupFwd ? BN / 2 : BN;
+  constexpr bool EARLY = MI < 8;  // whether registers are left to look up the next tile's rows meanwhile
   __shared__ __attribute__((aligned(16))) char lds_a[2 * OA::kBytes];
   __shared__ __attribute__((aligned(16))) char lds_b[2 * OB::kBytes];
   __shared__ int32_t lds_rows[A_ACROSS ? 2 * kRowHalf : 1];
@@ -219,7 +220,8 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     return GLU && B_ACROSS ? (ch >> 2) * 16 + (ch & 1) * 8 : ch * 8;
   };
 
-  auto set_up = [&](Source& x, int tile) {
+  // Where a tile lies; the rows that its copies read are asked for early.
+  auto locate = [&](Source& x, int tile) {
     // row tiles in fours (weight gradient: a run's tiles one after the other)
     constexpr int kHigh = OP == kGroupWgrad ? 1 : 4;
     const int band = tile / (kHigh * n_tiles), in = tile - band * kHigh * n_tiles;
@@ -236,14 +238,19 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       for (int i = 0; i < CA; ++i) {
         const int r = row_a() + i * NEXT_A;
         int32_t src = r < x.t.rows ? r : -1;  // from the tile's first row on
-        if (OP == kGroupFwd && k.rows) {
-          if (r < x.t.rows) {
-            src = k.rows[x.t.row0 + r];
-            if (src < 0 || src >= k.n_src) {
-              if (k.flags) atomicOr(k.flags, TS_FLAG_RANGE);
-              src = -1;
-            }
-          }
+        if (OP == kGroupFwd && k.rows && r < x.t.rows) src = k.rows[x.t.row0 + r];
+        x.va[i] = static_cast<uint32_t>(src);
+      }
+    }
+  };
+  auto set_up = [&](Source& x) {
+    if constexpr (!A_ACROSS) {
+#pragma unroll
+      for (int i = 0; i < CA; ++i) {
+        int32_t src = static_cast<int32_t>(x.va[i]);
+        if (OP == kGroupFwd && k.rows && (src < 0 || src >= k.n_src)) {
+          if (row_a() + i * NEXT_A < x.t.rows && k.flags) atomicOr(k.flags, TS_FLAG_RANGE);
+          src = -1;
         }
         x.va[i] = !VEC || src < 0 ? static_cast<uint32_t>(src)
                                   : static_cast<uint32_t>(src) * static_cast<uint32_t>(x.K * 2) + static_cast<uint32_t>(chunk_a(0) * 16);
@@ -414,10 +421,16 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   int tile = tile_of(0), done = 0;
   Source x;
   if (tile >= 0) {
-    set_up(x, tile);
+    locate(x, tile);
+    set_up(x);
     start(x);
   }
   while (tile >= 0) {
+    Source next;
+    tile = tile_of(++done);
+    if constexpr (EARLY) {
+      if (tile >= 0) locate(next, tile);
+    }
     gf32x4 acc[MI][NI];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -512,9 +525,11 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     const int g = fresh(tid) >> 4 & 3, c16 = fresh(tid) & 15;
     const GroupTile t = x.t;
     const int m0 = x.m0, n0 = x.n0;
-    tile = tile_of(++done);
     if (tile >= 0) {
-      set_up(x, tile);
+      if constexpr (EARLY) x = next;
+      else
+        locate(x, tile);
+      set_up(x);
       start(x);
     }
 
@@ -702,7 +717,9 @@ void run(GroupK& k, hipStream_t s) {
   if (!vec) return run<T, OP, GLU, 128, 128, 2, 2, false>(k, s);
   const int N = OP == kGroupDgrad ? k.cin : k.ldw;
   const bool large = OP == kGroupWgrad ? large_wgrad(k.cin, k.cout) : N >= 256 && k.n_rows / k.e >= 512;
-  if (large) {
+  // (with glu the input gradient's epilogue is most of its work where the reduction is short: two
+  // blocks a CU take turns at it; 609,756 rows 128 -> 2 x 256 333 us instead of 348)
+  if (large && !(OP == kGroupDgrad && GLU && k.cout <= 256)) {
     if constexpr (OP != kGroupWgrad) {
       // 192 rows a tile where that fills the rounds of the 256 CUs better (half a tile an expert is lost)
       auto cost = [&](int bm) { return ceil_div<int64_t>((k.n_rows / bm + k.e / 2) * ceil_div(N, 256), 256) * bm; };

@@ -118,8 +118,8 @@ __device__ __forceinline__ void store2(T* p, const Slot& s, const float (&a)[V],
     v[i / V].e[i % V] = static_cast<T>(a[e]);
     v[j / V].e[j % V] = static_cast<T>(b[e]);
   }
-  *reinterpret_cast<Vals<T, V>*>(p + s.a) = v[0];
-  *reinterpret_cast<Vals<T, V>*>(p + s.b) = v[1];
+  store_once(p + s.a, v[0]);
+  store_once(p + s.b, v[1]);
 }
 
 template <int V, bool IL>
