@@ -750,8 +750,10 @@ int group_chunk(int64_t n_rows, int e, int cin, int cout) {
   const bool large = large_wgrad(cin, cout);
   const int edge = large ? 256 : 128, slots = large ? 256 : 512;
   const int64_t tiles = static_cast<int64_t>(ceil_div(cin, edge)) * ceil_div(cout, edge), whole = e * tiles;
-  const int64_t c = ceil_div<int64_t>(n_rows * tiles, whole < slots / 2 ? slots - whole : slots);
-  return static_cast<int>((c < 256 ? 256 : c) + kStep - 1) / kStep * kStep;
+  const int64_t share = whole < slots / 2 ? slots - whole : slots;
+  const int64_t c = n_rows / share * tiles + ceil_div<int64_t>(n_rows % share * tiles, share);
+  const int64_t most = int64_t{1} << 30;
+  return static_cast<int>(((c < 256 ? 256 : c > most ? most : c) + kStep - 1) / kStep * kStep);
 }
 
 hipError_t launch_group(GroupK& k, GroupOp op, ts_dtype dt, bool glu, hipStream_t s) {

@@ -10,8 +10,17 @@ form: the backward pass keeps only that for the convolution's weight
 gradient, and only the 8-bit form of x for the first norm's.  Dense
 projections are torch matrix products.
 
+With --experts E it is a layer of a mixture of experts:
+
+    x -> norm -> q, k normalised and turned by position -> attention -> + x -> norm -> top 2 of E experts -> + -> out
+
+Positions enter by the rotation of queries and keys instead of a bias, and the
+feed-forward part is split over experts: the router groups the voxels by expert,
+each expert's products run over its own, and every voxel adds up what its experts
+returned.
+
 Usage: python examples/voxel_block.py [--steps K] [--channels C] [--heads H]
-                                      [--kv-heads G] [--window W] [--scale S]
+                                      [--kv-heads G] [--window W] [--scale S] [--experts E]
 Trains one block towards a fixed random map of its input (synthetic ring-scan
 scene, random features) and prints the loss and the time per step.
 """
@@ -113,8 +122,105 @@ class Block:
         return dx, Params(d_norm1, d_w.float(), d_out.float(), d_norm2, d_conv)
 
 
-def typed(p: Params, dtype: torch.dtype) -> Params:
-    return Params(p.norm1, p.qkv.to(dtype), p.out.to(dtype), p.norm2, p.conv.to(dtype))
+class LayerParams(NamedTuple):
+    """Of the layer with experts; also the gradients, in the same order, in float32."""
+    norm1: torch.Tensor   # float32 [c]
+    qkv: torch.Tensor     # [c][(hq + 2 hk) d]
+    norm_q: torch.Tensor  # float32 [d]
+    norm_k: torch.Tensor  # float32 [d]
+    out: torch.Tensor     # [hq d][c]
+    norm2: torch.Tensor   # float32 [c]
+    router: torch.Tensor  # [c][experts]
+    up: torch.Tensor      # [experts][c][2 * hidden]
+    down: torch.Tensor    # [experts][hidden][c]
+
+
+class LayerSaved(NamedTuple):
+    x8: ts.Act8
+    rstd1: torch.Tensor
+    n1: torch.Tensor
+    qkv: torch.Tensor
+    q: torch.Tensor
+    k: torch.Tensor
+    att: torch.Tensor
+    lse: torch.Tensor
+    h: torch.Tensor
+    rstd2: torch.Tensor
+    n2: torch.Tensor
+    logits: torch.Tensor
+    route: ts.Route
+    wide: torch.Tensor    # what the experts' first products returned, and silu(a) b of it
+    hidden: torch.Tensor
+    z: torch.Tensor
+
+
+class Layer:
+    def __init__(self, channels: int, heads: int, kv_heads: int, experts: int, hidden: int, top: int = 2):
+        self.c, self.hq, self.hk, self.d = channels, heads, kv_heads, channels // heads
+        self.experts, self.hidden, self.top = experts, hidden, top
+        # the head's pairs shared out to x, y and z
+        third = self.d // 2 // 3
+        self.pairs = (self.d // 2 - 2 * third, third, third)
+        self.freqs = ts.rope_freqs(self.pairs)
+
+    def init(self, seed: int) -> LayerParams:
+        g = torch.Generator("cuda").manual_seed(seed)
+
+        def normal(*shape, fan):
+            return torch.randn(*shape, generator=g, device="cuda") * fan ** -0.5
+        c, d, e, f = self.c, self.d, self.experts, self.hidden
+        ones = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+        return LayerParams(ones(c), normal(c, (self.hq + 2 * self.hk) * d, fan=c), ones(d), ones(d), normal(self.hq * d, c, fan=c),
+                           ones(c), normal(c, e, fan=c), normal(e, c, 2 * f, fan=c), normal(e, f, c, fan=f))
+
+    _heads = Block._heads
+
+    def _rope(self, s: Scene, p: LayerParams):
+        return (s.coords, self.freqs, self.pairs), dict(wq=p.norm_q, wk=p.norm_k)
+
+    def forward(self, s: Scene, p: LayerParams, x: torch.Tensor):
+        """p's matrices in x's type (see typed)."""
+        a = ts.norm_fwd(x, p.norm1, h8=True)
+        qkv = a.y @ p.qkv
+        q, k, v = self._heads(qkv)
+        at, norms = self._rope(s, p)
+        q, k = ts.rope_fwd(q, k, *at, **norms)
+        att, lse = ts.attn_fwd(q, k, v, s.starts)
+        b = ts.norm_fwd(att.flatten(1) @ p.out, p.norm2, residual=x)
+        logits = b.y @ p.router
+        r = ts.route_fwd(logits, self.top)
+        hidden, wide = ts.group_glu_fwd(b.y, p.up, ts.Groups(r.starts, r.rows), want_h=True)
+        z = ts.group_fwd(hidden, p.down, ts.Groups(r.starts))
+        y = b.h + ts.combine_fwd(z, r.place, r.gates)
+        return y, LayerSaved(a.h8, a.rstd, a.y, qkv, q, k, att, lse, b.h, b.rstd, b.y, logits, r, wide, hidden, z)
+
+    def backward(self, s: Scene, p: LayerParams, k: LayerSaved, dy: torch.Tensor):
+        """(gradient of x, gradients of the parameters); k.wide is overwritten."""
+        r, own = k.route, ts.Groups(k.route.starts)
+        groups = ts.Groups(r.starts, r.rows)
+        dz, d_gates = ts.combine_bwd(dy, k.z, r.place, r.gates)
+        d_down = ts.group_wgrad(k.hidden, dz, own)
+        d_wide = ts.group_glu_dgrad(dz, p.down, k.wide, own, into=k.wide)
+        d_up = ts.group_wgrad(k.n2, d_wide, groups)
+        d_logits = ts.route_bwd(d_gates, k.logits, r)
+        d_n2 = ts.combine_fwd(ts.group_dgrad(d_wide, p.up, groups), r.place) + d_logits @ p.router.t()
+        d_router = torch.mm(k.n2.t(), d_logits)
+        dh, d_norm2 = ts.norm_bwd(d_n2, k.h, p.norm2, k.rstd2, dh=dy)
+        d_out = torch.mm(k.att.flatten(1).t(), dh)
+        d_att = (dh @ p.out.t()).view_as(k.att)
+        d_qkv = torch.empty_like(k.qkv)
+        (q, kk, v), (dq, dk, dv) = self._heads(k.qkv), self._heads(d_qkv)
+        tq, tk, _ = ts.attn_bwd(d_att, k.q, k.k, v, k.att, k.lse, s.starts, into=(torch.empty_like(k.q), torch.empty_like(k.k), dv))
+        at, norms = self._rope(s, p)
+        g = ts.rope_bwd(tq, tk, q, kk, *at, **norms, into=(dq, dk))
+        d_w = torch.mm(k.n1.t(), d_qkv)
+        dx, d_norm1 = ts.norm_bwd(d_qkv @ p.qkv.t(), k.x8, p.norm1, k.rstd1, dh=dh)
+        return dx, LayerParams(d_norm1, d_w.float(), g.dwq, g.dwk, d_out.float(), d_norm2, d_router.float(), d_up, d_down)
+
+
+def typed(p, dtype: torch.dtype):
+    """Matrices in dtype; the norms' weights stay as they are."""
+    return type(p)(*(t if name.startswith("norm") else t.to(dtype) for name, t in zip(p._fields, p)))
 
 
 def main():
@@ -126,10 +232,14 @@ def main():
     ap.add_argument("--window", type=int, default=16)
     ap.add_argument("--scale", type=float, default=0.2, help="part of the 103k-voxel scene")
     ap.add_argument("--lr", type=float, default=0.05)
+    ap.add_argument("--experts", type=int, default=0, help="a layer of that many experts instead of the convolution")
     args = ap.parse_args()
     scene = Scene.of(synth.make("lidar", args.scale).coords, args.window)
     n = scene.coords.shape[0]
-    block = Block(args.channels, args.heads, args.kv_heads)
+    if args.experts:
+        block = Layer(args.channels, args.heads, args.kv_heads, args.experts, 2 * args.channels, min(2, args.experts))
+    else:
+        block = Block(args.channels, args.heads, args.kv_heads)
     g = torch.Generator("cuda").manual_seed(1)
     x = torch.randn(n, args.channels, generator=g, device="cuda", dtype=torch.bfloat16)
     target, _ = block.forward(scene, typed(block.init(2), x.dtype), x)
