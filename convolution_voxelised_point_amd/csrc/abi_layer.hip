@@ -87,7 +87,7 @@ RopeK rope_args(const ts_rope* r, const ts_rope_heads* q, const ts_rope_heads* k
 }
 
 size_t rope_bytes(const ts_rope* r, int hq, int hk) {
-  return 2 * static_cast<size_t>(rope_blocks(r->n, hq + hk)) * r->d * sizeof(float);
+  return 2 * static_cast<size_t>(rope_blocks(r->n, hq + hk, r->d)) * r->d * sizeof(float);
 }
 
 // ---------------------------------------------------------------- routing
@@ -174,7 +174,7 @@ ts_status ts_rope_bwd(const ts_rope* r, const ts_rope_heads* q, const ts_rope_he
   if (hq + hk == 0) return TS_OK;
   RopeK a = rope_args(r, q, k);
   a.part = static_cast<float*>(ws);
-  a.blocks = rope_blocks(r->n, hq + hk);
+  a.blocks = rope_blocks(r->n, hq + hk, r->d);
   return status(launch_rope_bwd(a, r->dtype, r->interleaved != 0, stream));
 }
 

@@ -39,9 +39,9 @@ struct RopeK {
   int64_t tiles;
 };
 
-// Blocks of the backward pass at most: each leaves one share of dw.
-inline int rope_blocks(int64_t n, int heads) {
-  const int64_t b = (n * heads + 63) / 64;
+// Blocks of the backward pass at most, of 2048 channels or more: each leaves one share of dw.
+inline int rope_blocks(int64_t n, int heads, int d) {
+  const int64_t b = ceil_div<int64_t>(n * heads * d, 2048);
   return static_cast<int>(b < 1024 ? b : 1024);
 }
 

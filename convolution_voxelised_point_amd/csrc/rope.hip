@@ -132,7 +132,7 @@ __device__ __forceinline__ void load_w(const float* w, const Slot& s, float (&wa
 // The table of angles of rows row0.. (`rows` of them): [row][table_pairs] (cos, sin).
 __device__ __forceinline__ void fill_angles(const RopeK& k, int64_t row0, int rows, float2* tab) {
   for (int i = threadIdx.x; i < rows * k.table_pairs; i += kRopeThreads) {
-    const int row = static_cast<int>(__umulhi(i, k.by_pairs)), p = i - row * k.table_pairs;
+    const int row = k.table_pairs == 1 ? i : static_cast<int>(__umulhi(i, k.by_pairs)), p = i - row * k.table_pairs;
     float2 t{1.f, 0.f};
     if (p < k.pairs) {
       const int axis = p < k.upto[0] ? 0 : p < k.upto[1] ? 1 : 2;
@@ -418,14 +418,16 @@ void run(RopeK& k, bool back, hipStream_t s) {
   k.log_lanes = 0;
   while ((1 << k.log_lanes) < k.slots) ++k.log_lanes;
   k.table_pairs = k.pairs == 0 ? 0 : IL ? k.d / 2 : k.pairs;
-  if (k.table_pairs) k.by_pairs = static_cast<unsigned>((uint64_t{1} << 32) / k.table_pairs + 1);
+  if (k.table_pairs > 1) k.by_pairs = static_cast<unsigned>((uint64_t{1} << 32) / k.table_pairs + 1);
   for (RopeSide& side : k.side)
     if (side.heads > 1) side.by_heads = static_cast<unsigned>((uint64_t{1} << 32) / side.heads + 1);
-  // Rows of a tile: 1024 items, in a table of at most 32 KB; fewer where that leaves CUs without a tile.
+  // Rows of a tile: 1024 items, in a table of at most 32 KB; fewer where that leaves CUs without a
+  // tile, though on the way back no fewer than give each block one.
   const int heads = k.side[0].heads + k.side[1].heads;
   int64_t rows = 4 * kRopeThreads / (heads << k.log_lanes);
+  const int64_t few = back ? std::max<int64_t>(k.n / 512, ceil_div<int64_t>(k.n, k.blocks)) : k.n / 512;
+  if (rows > few) rows = few;
   if (k.table_pairs && rows > 4096 / k.table_pairs) rows = 4096 / k.table_pairs;
-  if (rows > k.n / 512) rows = k.n / 512;
   k.rows = static_cast<int>(rows < 1 ? 1 : rows);
   k.tiles = ceil_div<int64_t>(k.n, k.rows);
   const size_t lds = static_cast<size_t>(k.rows) * k.table_pairs * sizeof(float2);

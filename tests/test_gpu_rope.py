@@ -103,6 +103,14 @@ def test_rope(ts, shape, il, dt):
         check(ts, dt, q, k, coords, freqs, pairs, wq, wk, il, dq, dk)
 
 
+@pytest.mark.parametrize("n", [2, 1500, 70000])
+@pytest.mark.parametrize("il,d,pairs", [(False, 4, (1, 0)), (False, 5, (0, 0, 1)), (True, 2, (0, 1)), (True, 3, (1, 0))])
+def test_one_pair(ts, n, il, d, pairs):
+    """A head with a single pair of channels to turn, in tiles of one row and of many."""
+    q, k, coords, freqs, pairs, wq, wk, dq, dk = inputs("f32", n, 2, 1, d, pairs)
+    check(ts, "f32", q, k, coords, freqs, pairs, wq, wk, il, dq, dk)
+
+
 @pytest.mark.parametrize("reach", [2 ** 15, 2 ** 31 - 1])
 def test_far_positions(ts, reach):
     """Angles of positions over all of int32: the reference's own product is off by 2^-53 of an angle of up to
