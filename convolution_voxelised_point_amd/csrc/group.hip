@@ -109,21 +109,28 @@ template <typename T>
 struct __attribute__((packed, aligned(2))) Loose8 {
   T e[8];
 };
-// (Of a row's last, partial chunk the row's last 8 values are read instead and moved down.)
+// (Of a row's last, partial chunk the row's last 8 values are read instead and moved down by
+// `over`; where that is done later the load need not have ended before.)
+__device__ __forceinline__ int over(int c0, int width) { return width < 8 || c0 + 8 <= width ? 0 : c0 + 8 - width; }
+__device__ __forceinline__ gu32x4 moved_down(gu32x4 v, int by) {
+  if (by & 4) v = gu32x4{v[2], v[3], 0u, 0u};
+  if (by & 2) v = gu32x4{v[1], v[2], v[3], 0u};
+  if (by & 1) v = gu32x4{(v[0] >> 16) | (v[1] << 16), (v[1] >> 16) | (v[2] << 16), (v[2] >> 16) | (v[3] << 16), v[3] >> 16};
+  return v;
+}
 template <typename T>
-__device__ __forceinline__ gu32x4 load_loose(const T* row, int c0, int width) {
+__device__ __forceinline__ gu32x4 load_unmoved(const T* row, int c0, int width) {
   if (width < 8) {
     T v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = c0 + i < width ? row[c0 + i] : static_cast<T>(0.f);
     return __builtin_bit_cast(gu32x4, v);
   }
-  const int by = c0 + 8 <= width ? 0 : c0 + 8 - width;
-  gu32x4 v = __builtin_bit_cast(gu32x4, *reinterpret_cast<const Loose8<T>*>(row + (c0 - by)));
-  if (by & 4) v = gu32x4{v[2], v[3], 0u, 0u};
-  if (by & 2) v = gu32x4{v[1], v[2], v[3], 0u};
-  if (by & 1) v = gu32x4{(v[0] >> 16) | (v[1] << 16), (v[1] >> 16) | (v[2] << 16), (v[2] >> 16) | (v[3] << 16), v[3] >> 16};
-  return v;
+  return __builtin_bit_cast(gu32x4, *reinterpret_cast<const Loose8<T>*>(row + (c0 - over(c0, width))));
+}
+template <typename T>
+__device__ __forceinline__ gu32x4 load_loose(const T* row, int c0, int width) {
+  return moved_down(load_unmoved(row, c0, width), over(c0, width));
 }
 struct __attribute__((packed, aligned(4))) Loose4 {
   float e[4];
@@ -310,7 +317,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
           to_lds(buf, in ? (static_cast<uint32_t>(row) * static_cast<uint32_t>(k.cin) + c) * 2 : kNowhere,
                  lds_a + slot * OA::kBytes + (i * NT + wave * 64) * 16);
         else
-          ra[i] = in ? load_loose(base + (first + row) * k.cin, c, k.cin) : gu32x4{0u, 0u, 0u, 0u};
+          ra[i] = in ? load_unmoved(base + (first + row) * k.cin, c, k.cin) : gu32x4{0u, 0u, 0u, 0u};
       }
     } else {
       const bool gather = OP == kGroupFwd && k.rows;
@@ -323,11 +330,12 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
           to_lds(buf, c < left ? further(x.va[i], from * 2) : kNowhere, lds_a + slot * OA::kBytes + (i * NT + wave * 64) * 16);
         } else {
           const int32_t row = static_cast<int32_t>(x.va[i]);
-          ra[i] = c < left && row >= 0 ? load_loose(base + (first + row) * x.K, from + c, x.K) : gu32x4{0u, 0u, 0u, 0u};
+          ra[i] = c < left && row >= 0 ? load_unmoved(base + (first + row) * x.K, from + c, x.K) : gu32x4{0u, 0u, 0u, 0u};
         }
       }
     }
   };
+  auto end_b = [&](uint32_t column) { return GLU && column < static_cast<uint32_t>(k.cout) ? k.cout : k.ldw; };
   auto copy_b = [&](const Source& x, int s, int slot) {
     const int from = s * kStep, left = x.K - from;
     const T* base = OP == kGroupWgrad ? static_cast<const T*>(k.dy) : static_cast<const T*>(k.w) + static_cast<int64_t>(x.t.e) * k.cin * k.ldw;
@@ -343,23 +351,34 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
         if constexpr (VEC)
           to_lds(buf, c < left ? x.vb[0] + static_cast<uint32_t>(i * NEXT_B * k.ldw + from) * 2 : kNowhere, dst);
         else
-          rb[i] = c < left && r < rows ? load_loose(base + (first + r) * k.ldw, from + c, x.K) : gu32x4{0u, 0u, 0u, 0u};
+          rb[i] = c < left && r < rows ? load_unmoved(base + (first + r) * k.ldw, from + c, x.K) : gu32x4{0u, 0u, 0u, 0u};
       } else {
         const uint32_t v = x.vb[i % TURN_B];
         if constexpr (VEC)
           to_lds(buf, further(v, static_cast<uint32_t>(i * NEXT_B * k.ldw * 2)), dst);
         else
-          rb[i] = r < rows && v != kNowhere ? load_loose(base + (first + r) * k.ldw, static_cast<int>(v), GLU && v < static_cast<uint32_t>(k.cout) ? k.cout : k.ldw)
-                                            : gu32x4{0u, 0u, 0u, 0u};
+          rb[i] = r < rows && v != kNowhere ? load_unmoved(base + (first + r) * k.ldw, static_cast<int>(v), end_b(v)) : gu32x4{0u, 0u, 0u, 0u};
       }
     }
   };
-  auto put = [&](int slot) {
+  // Step s of chunks in registers into LDS.  Few waves hold a row's last chunk.
+  auto put = [&](const Source& x, int s, int slot) {
     if constexpr (!VEC) {
 #pragma unroll
-      for (int i = 0; i < CA; ++i) *reinterpret_cast<gu32x4*>(lds_a + slot * OA::kBytes + (i * NT + tid) * 16) = ra[i];
+      for (int i = 0; i < CA; ++i) {
+        const int by = A_ACROSS ? over(x.m0 + chunk_a(i) * 8, k.cin) : over(s * kStep + chunk_a(0) * 8, x.K);
+        if (__builtin_amdgcn_ballot_w64(by != 0)) ra[i] = moved_down(ra[i], by);
+        *reinterpret_cast<gu32x4*>(lds_a + slot * OA::kBytes + (i * NT + tid) * 16) = ra[i];
+      }
 #pragma unroll
-      for (int i = 0; i < CB; ++i) *reinterpret_cast<gu32x4*>(lds_b + slot * OB::kBytes + (i * NT + tid) * 16) = rb[i];
+      for (int i = 0; i < CB; ++i) {
+        int by;
+        if constexpr (OP == kGroupDgrad) by = over(s * kStep + chunk_b(0) * 8, x.K);
+        else
+          by = x.vb[i % TURN_B] == kNowhere ? 0 : over(static_cast<int>(x.vb[i % TURN_B]), end_b(x.vb[i % TURN_B]));
+        if (__builtin_amdgcn_ballot_w64(by != 0)) rb[i] = moved_down(rb[i], by);
+        *reinterpret_cast<gu32x4*>(lds_b + slot * OB::kBytes + (i * NT + tid) * 16) = rb[i];
+      }
     }
   };
   // The first steps of a tile; nobody reads the ring any more.
@@ -495,13 +514,13 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     } else {
       for (int s = 0; s < x.steps; ++s) {
         const int slot = s & 1;
-        put(slot);  // its last readers were done before the last barrier
+        put(x, s, slot);  // its last readers were done before the last barrier
         more_rows(x, s);
         if (s + 1 < x.steps) {
           copy_a(x, s + 1, 0);
           copy_b(x, s + 1, 0);
         }
-        wait_copies<0>();
+        wait_lds();  // (the copies stay under way; row numbers come 14 steps before they are read)
         barrier();
         fetch_rows(x, s + 2);
 #pragma unroll
