@@ -697,19 +697,19 @@ __global__ __launch_bounds__(256) void k_group_sum(const GroupK k) {
   float* dw = k.dw + e * size;
   const float* part = k.part + first * size;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
-  if (size % 4 == 0) {
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < size / 4; i += step) {
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < size; i += 4 * step) {
+    if (i + 4 <= size) {
       gf32x4 s{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-      for (int c = 0; c < count; ++c) s += *reinterpret_cast<const gf32x4*>(part + c * size + 4 * i);
-      *reinterpret_cast<gf32x4*>(dw + 4 * i) = s;
-    }
-  } else {
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < size; i += step) {
-      float s = 0.f;
+      for (int c = 0; c < count; ++c) s += __builtin_bit_cast(gf32x4, *reinterpret_cast<const Loose4*>(part + c * size + i));
+      *reinterpret_cast<Loose4*>(dw + i) = __builtin_bit_cast(Loose4, s);
+    } else {
+      for (int64_t j = i; j < size; ++j) {
+        float s = 0.f;
 #pragma unroll 8
-      for (int c = 0; c < count; ++c) s += part[c * size + i];
-      dw[i] = s;
+        for (int c = 0; c < count; ++c) s += part[c * size + j];
+        dw[j] = s;
+      }
     }
   }
 }

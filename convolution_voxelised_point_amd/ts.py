@@ -1022,27 +1022,33 @@ def rope_freqs(pairs: Sequence[int], base: float = 100.0, device="cuda") -> torc
     return torch.cat([base ** (-torch.arange(m, dtype=torch.float64) / max(m, 1)) for m in pairs]).float().to(device)
 
 
+_I3 = ctypes.c_int32 * 3
+
+
 def _rope_args(like: torch.Tensor, coords: Optional[torch.Tensor], freqs: Optional[torch.Tensor], pairs: Sequence[int],
                eps: float, interleaved: bool) -> TsRope:
     n, _, d = like.shape
-    pairs = list(pairs)
+    pairs = tuple(pairs)
     _need(len(pairs) in (2, 3) and min(pairs) >= 0, "rope: pairs are the channel pairs of 2 or 3 axes")
-    if sum(pairs) > 0:
+    turned = sum(pairs)
+    if turned > 0:
         _need(coords is not None and coords.is_cuda and coords.dtype is torch.int32 and coords.is_contiguous()
               and coords.shape == (n, len(pairs) + 1), "rope: coordinates are int32 [n][ndim + 1]")
         _need(freqs is not None and freqs.is_cuda and freqs.dtype is torch.float32 and freqs.is_contiguous()
-              and freqs.numel() == sum(pairs), "rope: freqs are float32, one for each pair")
+              and freqs.numel() == turned, "rope: freqs are float32, one for each pair")
     else:
         coords = freqs = None
     _need(like.dtype in _DT, "rope: a feature type")
-    return TsRope(_DT[like.dtype], d, len(pairs), (ctypes.c_int32 * 3)(*(pairs + [0])[:3]), int(interleaved), eps, n, _ptr(coords),
-                  _ptr(freqs))
+    return TsRope(_DT[like.dtype], d, len(pairs), _I3(*pairs), int(interleaved), eps, n, _ptr(coords), _ptr(freqs))
 
 
-def _rope_rows(t: torch.Tensor, like: torch.Tensor, heads: int, what: str) -> int:
-    st = _row_stride(t)
-    _need(st is not None and t.is_cuda and t.dtype is like.dtype and t.shape == (like.shape[0], heads, like.shape[2]), what)
-    return st
+def _rope_rows(t: torch.Tensor, like: torch.Tensor, shape: Tuple[int, int, int], what: str) -> int:
+    """_row_stride of a tensor of this shape and of like's type."""
+    _need(t.shape == shape and t.dtype is like.dtype and t.is_cuda, what)
+    n, h, d = shape
+    row, head, one = t.stride()
+    _need((one == 1 or d <= 1) and (head == d or h <= 1) and (row >= h * d or n <= 1), what)
+    return row if n > 1 else h * d
 
 
 def _rope_weight(w: Optional[torch.Tensor], d: int) -> None:
@@ -1063,23 +1069,28 @@ def rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], coords: Optional[torch.
     _need(q.dim() == 3, "rope: q is [n][heads][d]")
     args = _rope_args(q, coords, freqs, pairs, eps, interleaved)
     _need(into is None or len(into) == 2, "rope: results for q and k")
-    sides, out = [], []
-    for i, (x, w) in enumerate(((q, wq), (k, wk))):
-        if x is None:
-            _need(into is None or into[i] is None, "rope: a result without its input")
-            sides.append(None)
-            out.append(None)
-            continue
-        _need(x.dim() == 3, "rope: k is [n][heads][d]")
-        st = _rope_rows(x, q, x.shape[1], "rope: q and k are device tensors [n][heads][d] of one type, with adjacent heads")
-        _rope_weight(w, q.shape[2])
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if into is None else into[i]
+    yq, yk = into or (None, None)
+    yq, side_q = _rope_fwd_side(q, q, wq, yq, into is None)
+    yk, side_k = _rope_fwd_side(k, q, wk, yk, into is None)
+    _check(_lib_rope_fwd(ctypes.byref(args), side_q, side_k, _raw_stream(q)), "ts_rope_fwd")
+    return yq, yk
+
+
+def _rope_fwd_side(x, q, w, y, new):
+    if x is None:
+        _need(y is None, "rope: a result without its input")
+        return None, None
+    _need(x.dim() == 3, "rope: k is [n][heads][d]")
+    n, _, d = q.shape
+    h = x.shape[1]
+    st = _rope_rows(x, q, (n, h, d), "rope: q and k are device tensors [n][heads][d] of one type, with adjacent heads")
+    _rope_weight(w, d)
+    if new:
+        y, yst = torch.empty((n, h, d), dtype=q.dtype, device=q.device), h * d
+    else:
         _need(y is not None, "rope: results for q and k")
-        yst = _rope_rows(y, q, x.shape[1], "rope: results are like q and k")
-        sides.append(TsRopeHeads(x.shape[1], st, yst, 0, 0, x.data_ptr(), _ptr(w), y.data_ptr(), None, None, None))
-        out.append(y)
-    _check(_lib_rope_fwd(ctypes.byref(args), *(None if s is None else ctypes.byref(s) for s in sides), _raw_stream(q)), "ts_rope_fwd")
-    return out[0], out[1]
+        yst = _rope_rows(y, q, (n, h, d), "rope: results are like q and k")
+    return y, ctypes.byref(TsRopeHeads(h, st, yst, 0, 0, x.data_ptr(), _ptr(w), y.data_ptr()))
 
 
 class RopeGrads(NamedTuple):
@@ -1100,33 +1111,34 @@ def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, k: O
         with torch.cuda.stream(stream):
             return rope_bwd(dq, dk, q, k, coords, freqs, pairs, wq, wk, eps, interleaved, into)
     _need(q.dim() == 3 and (dk is None) == (k is None), "rope: q is [n][heads][d], dk comes with k")
-    args = _rope_args(q, coords, freqs, pairs, eps, interleaved)
+    args = ctypes.byref(_rope_args(q, coords, freqs, pairs, eps, interleaved))
     _need(into is None or len(into) == 2, "rope: results for q and k")
-    sides, out, grads = [], [], []
-    for i, (g, x, w) in enumerate(((dq, q, wq), (dk, k, wk))):
-        if x is None:
-            _need(into is None or into[i] is None, "rope: a result without its input")
-            sides.append(None)
-            out.append(None)
-            grads.append(None)
-            continue
-        what = "rope: q, k and their gradients are device tensors [n][heads][d] of one type, with adjacent heads"
-        _need(x.dim() == 3, what)
-        h, d = x.shape[1], q.shape[2]
-        st, gst = _rope_rows(x, q, h, what), _rope_rows(g, q, h, what)
-        _rope_weight(w, d)
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if into is None else into[i]
-        _need(y is not None, "rope: results for q and k")
-        yst = _rope_rows(y, q, h, "rope: results are like q and k")
-        dw = None if w is None else torch.empty(d, dtype=torch.float32, device=x.device)
-        sides.append(TsRopeHeads(h, st, 0, gst, yst, x.data_ptr(), _ptr(w), None, g.data_ptr(), y.data_ptr(), _ptr(dw)))
-        out.append(y)
-        grads.append(dw)
-    ref = ctypes.byref(args)
-    n = _lib_rope_workspace_bytes(ref, q.shape[1], 0 if k is None else k.shape[1])
+    yq, yk = into or (None, None)
+    yq, dwq, side_q = _rope_bwd_side(dq, q, q, wq, yq, into is None)
+    yk, dwk, side_k = _rope_bwd_side(dk, k, q, wk, yk, into is None)
+    n = _lib_rope_workspace_bytes(args, q.shape[1], 0 if k is None else k.shape[1])
     ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-    _check(_lib_rope_bwd(ref, *(None if s is None else ctypes.byref(s) for s in sides), _ptr(ws), n, _raw_stream(q)), "ts_rope_bwd")
-    return RopeGrads(out[0], out[1], grads[0], grads[1])
+    _check(_lib_rope_bwd(args, side_q, side_k, _ptr(ws), n, _raw_stream(q)), "ts_rope_bwd")
+    return RopeGrads(yq, yk, dwq, dwk)
+
+
+def _rope_bwd_side(g, x, q, w, y, new):
+    if x is None:
+        _need(y is None, "rope: a result without its input")
+        return None, None, None
+    what = "rope: q, k and their gradients are device tensors [n][heads][d] of one type, with adjacent heads"
+    _need(x.dim() == 3, what)
+    n, _, d = q.shape
+    h = x.shape[1]
+    st, gst = _rope_rows(x, q, (n, h, d), what), _rope_rows(g, q, (n, h, d), what)
+    _rope_weight(w, d)
+    if new:
+        y, yst = torch.empty((n, h, d), dtype=q.dtype, device=q.device), h * d
+    else:
+        _need(y is not None, "rope: results for q and k")
+        yst = _rope_rows(y, q, (n, h, d), "rope: results are like q and k")
+    dw = None if w is None else torch.empty(d, dtype=torch.float32, device=q.device)
+    return y, dw, ctypes.byref(TsRopeHeads(h, st, 0, gst, yst, x.data_ptr(), _ptr(w), None, g.data_ptr(), y.data_ptr(), _ptr(dw)))
 
 
 class Route(NamedTuple):
@@ -1149,7 +1161,8 @@ def route_fwd(logits: torch.Tensor, top: int, over_all: bool = False, stream=Non
     n, e = logits.shape
     _need(1 <= top <= e, "route_fwd: 1 <= top <= experts")
     dev = logits.device
-    experts, rows, place = (torch.empty(s, dtype=torch.int32, device=dev) for s in ((n, top), (n * top,), (n, top)))
+    experts = torch.empty((n, top), dtype=torch.int32, device=dev)
+    rows, place = torch.empty(n * top, dtype=torch.int32, device=dev), torch.empty_like(experts)
     gates = torch.empty((n, top), dtype=torch.float32, device=dev)
     starts = torch.empty(e + 1, dtype=torch.int64, device=dev)
     size = _lib_route_workspace_bytes(n, e, top)
