@@ -553,11 +553,13 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     }
 
     if constexpr (OP == kGroupWgrad) {
+      // (of experts that overlap the longest runs, taken first, may be numbered past the planned ones)
+      const bool room = t.count == 1 || t.run < planned;
       float* out = t.count == 1 ? k.dw + static_cast<int64_t>(t.e) * k.cin * k.cout : k.part + t.run * k.cin * k.cout;
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const int m = m0 + wm * MI * 16 + i * 16 + c16;
-        if (m >= k.cin) continue;
+        if (m >= k.cin || !room) continue;
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
           const int n = n0 + wn * NI * 16 + j * 16 + 4 * g;
@@ -714,7 +716,17 @@ __global__ __launch_bounds__(256) void k_group_sum(const GroupK k) {
   }
 }
 
-bool large_wgrad(int cin, int cout) { return cin >= 256 && cout >= 256; }
+// Whether the weight gradient's tiles are 256 x 256 (a block a CU) rather than 128 x 128 (two).  Large
+// ones read less, but where there is about one for each CU a long expert's keep the others waiting, and a
+// short run is all prologue and epilogue.  (Rows an expert, us large / small: 16 experts of 512 x 512,
+// 256: 37 / 31, 1024: 46 / 50, 8000: 120 / 191; 8 of 1024 x 1024, 512: 66 / 50, 2048: 108 / 103, 8000: 271 / 315;
+// 16 of 1024 x 2048, 512: 95 / 83, 2000: 226 / 242; 64 of 1024 x 1376, 96: 108 / 124, 768: 263 / 335.)
+bool large_wgrad(int64_t n_rows, int e, int cin, int cout) {
+  if (cin < 256 || cout < 256) return false;
+  const int64_t tiles = static_cast<int64_t>(ceil_div(cin, 256)) * ceil_div(cout, 256), whole = e * tiles;
+  const int64_t rows_a_cu = n_rows / 256 * tiles;
+  return whole >= 1024 || rows_a_cu >= (whole < 128 ? 200 : 1536);
+}
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -735,7 +747,7 @@ void run(GroupK& k, hipStream_t s) {
                    (!k.rows || k.n_src * k.cin < (int64_t{1} << 31) - 8);  // rows looked up have 32-bit offsets
   if (!vec) return run<T, OP, GLU, 128, 128, 2, 2, false>(k, s);
   const int N = OP == kGroupDgrad ? k.cin : k.ldw;
-  const bool large = OP == kGroupWgrad ? large_wgrad(k.cin, k.cout) : N >= 256 && k.n_rows / k.e >= 512;
+  const bool large = OP == kGroupWgrad ? large_wgrad(k.n_rows, k.e, k.cin, k.cout) : N >= 256 && k.n_rows / k.e >= 512;
   // (with glu the input gradient's epilogue is most of its work where the reduction is short: two
   // blocks a CU take turns at it; 609,756 rows 128 -> 2 x 256 333 us instead of 348)
   if (large && !(OP == kGroupDgrad && GLU && k.cout <= 256)) {
@@ -766,7 +778,7 @@ void run(GroupK& k, GroupOp op, bool glu, hipStream_t s) {
 // blocks idle, a run is what one block has to do on average; otherwise as many runs as there are
 // blocks (an expert may end in a short one).
 int group_chunk(int64_t n_rows, int e, int cin, int cout) {
-  const bool large = large_wgrad(cin, cout);
+  const bool large = large_wgrad(n_rows, e, cin, cout);
   const int edge = large ? 256 : 128, slots = large ? 256 : 512;
   const int64_t tiles = static_cast<int64_t>(ceil_div(cin, edge)) * ceil_div(cout, edge), whole = e * tiles;
   const int64_t share = whole < slots / 2 ? slots - whole : slots;

@@ -112,6 +112,38 @@ def test_group(ts, case, dt):
     Case(ts, dt, lens, cin, cout, gather=False, before=3, behind=150).check()
 
 
+LONG = [  # long runs of the weight gradient, and many of them; many groups of many rows
+    ([9000, 0, 4100, 300], 264, 520, ("wgrad",)), ([40000, 7, 23000], 256, 256, ("wgrad",)),
+    ([5, 0, 900] * 90, 512, 512, ("wgrad",)), ([700, 0, 1200] * 24, 64, 256, ("fwd", "glu", "wgrad")),
+    ([700, 0, 1200] * 24, 256, 64, ("dgrad", "glu_dgrad")),
+]
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("case", LONG, ids=lambda c: f"{len(c[0])}x{max(c[0])}_{c[1]}_{c[2]}")
+def test_long_groups(ts, case, dt):
+    lens, cin, cout, what = case
+    Case(ts, dt, lens, cin, cout).check(what)
+    Case(ts, dt, lens, cin, cout, gather=False, before=70, behind=300).check(what)
+
+
+def test_long_groups_with_bad_rows_and_starts(ts):
+    c = Case(ts, "bf16", [40000, 0, 23000], 256, 256)
+    c.groups.rows[::1000], c.groups.rows[c.p - 1] = -1, c.x.shape[0]
+    c.xg = c.xg.clone()
+    c.xg[::1000], c.xg[c.p - 1] = 0, 0
+    dw = ts.group_wgrad(c.x, c.dy, c.groups, err_flags=c.flags)
+    assert int(c.flags) == ts.TS_FLAG_RANGE
+    for e in range(c.e):
+        a, b = c.host[e], c.host[e + 1]
+        x, dy = c.xg[a:b].double().t().contiguous(), c.dy[a:b].double()
+        close(dw[e], x @ dy, (b - a + 8) * E * (x.abs() @ dy.abs()) + 1e-37, f"dw[{e}]")
+    for starts in ([0, 50000, 20, 63000], [0, 63000, 0, 63000], [-5, 10 ** 12, 3, 63000]):
+        c.flags.zero_()
+        ts.group_wgrad(c.x, c.dy, ts.Groups(torch.tensor(starts, device="cuda"), c.groups.rows.clamp(0, 10)), err_flags=c.flags)
+        assert int(c.flags) == ts.TS_FLAG_RANGE
+
+
 @pytest.mark.parametrize("n", [0, 5, 70, 1200])
 def test_rows_without_a_group(ts, n):
     """All rows before or behind the groups: zeros, and no gradient."""
