@@ -121,10 +121,13 @@ unsigned blocks_for(int64_t n) {
 template <typename T, int LPR>
 void run_bwd(const CombineK& k, hipStream_t s) {
   const unsigned grid = blocks_for(ceil_div<int64_t>(k.n, 256 / LPR));
-  if (k.units <= LPR)
-    k_combine_bwd<T, LPR, true><<<grid, 256, 0, s>>>(k);
-  else
-    k_combine_bwd<T, LPR, false><<<grid, 256, 0, s>>>(k);
+  if constexpr (LPR == 64) {
+    if (k.units > LPR) {
+      k_combine_bwd<T, LPR, false><<<grid, 256, 0, s>>>(k);
+      return;
+    }
+  }
+  k_combine_bwd<T, LPR, true><<<grid, 256, 0, s>>>(k);
 }
 
 template <typename T>

@@ -783,7 +783,7 @@ int group_chunk(int64_t n_rows, int e, int cin, int cout) {
   const int64_t tiles = static_cast<int64_t>(ceil_div(cin, edge)) * ceil_div(cout, edge), whole = e * tiles;
   const int64_t share = whole < slots / 2 ? slots - whole : slots;
   const int64_t c = n_rows / share * tiles + ceil_div<int64_t>(n_rows % share * tiles, share);
-  const int64_t most = int64_t{1} << 30;
+  const int64_t most = int64_t{1} << 28;  // (row numbers of a run lie within 32 bits)
   return static_cast<int>(((c < 256 ? 256 : c > most ? most : c) + kStep - 1) / kStep * kStep);
 }
 

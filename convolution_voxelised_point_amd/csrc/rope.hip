@@ -401,11 +401,11 @@ __global__ __launch_bounds__(1024) void k_rope_dw(const RopeK k) {
 }
 
 // Pairs per thread: as many as both the turned and the remaining part of a head hold, up to
-// 16 bytes an access.
+// 16 bytes an access (one where a head is a single channel and has no pair).
 template <typename T, bool IL>
 int pairs_per_thread(const RopeK& k) {
   const int turned = IL ? k.d / 2 : k.pairs, rest = IL ? 0 : k.rest;
-  for (int v = 16 / sizeof(T); v > 1; v /= 2)
+  for (int v = 16 / sizeof(T); v > 1 && turned + rest > 0; v /= 2)
     if ((turned == 0 || turned >= v) && (rest == 0 || rest >= v)) return v;
   return 1;
 }

@@ -111,6 +111,22 @@ def test_one_pair(ts, n, il, d, pairs):
     check(ts, "f32", q, k, coords, freqs, pairs, wq, wk, il, dq, dk)
 
 
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("il", [False, True])
+def test_single_channel(ts, dt, il):
+    """Heads of one channel, which have no pair: many rows, and what lies around the results stays."""
+    n = 1500
+    q, k, coords, freqs, pairs, wq, wk, dq, dk = inputs(dt, n, 3, 2, 1, (0, 0))
+    y, r = check(ts, dt, q, k, coords, freqs, pairs, wq, wk, il, dq, dk)
+    for f, want in ((lambda into: ts.rope_fwd(q, k, coords, freqs, pairs, wq=wq, wk=wk, interleaved=il, into=into), y),
+                    (lambda into: ts.rope_bwd(dq, dk, q, k, coords, freqs, pairs, wq=wq, wk=wk, interleaved=il, into=into), (r.dq, r.dk))):
+        band = torch.full((n + 2, 9, 1), 7.0, dtype=DT[dt], device="cuda")
+        f((band[1:-1, 1:4], band[1:-1, 5:7]))
+        assert torch.equal(band[1:-1, 1:4], want[0]) and torch.equal(band[1:-1, 5:7], want[1])
+        band[1:-1, 1:4], band[1:-1, 5:7] = 7.0, 7.0
+        assert (band == 7).all()
+
+
 @pytest.mark.parametrize("reach", [2 ** 15, 2 ** 31 - 1])
 def test_far_positions(ts, reach):
     """Angles of positions over all of int32: the reference's own product is off by 2^-53 of an angle of up to
