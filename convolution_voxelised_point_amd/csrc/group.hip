@@ -752,9 +752,11 @@ void run(GroupK& k, hipStream_t s) {
   // blocks a CU take turns at it; 609,756 rows 128 -> 2 x 256 333 us instead of 348)
   if (large && !(OP == kGroupDgrad && GLU && k.cout <= 256)) {
     if constexpr (OP != kGroupWgrad) {
-      // 192 rows a tile where that fills the rounds of the 256 CUs better (half a tile an expert is lost)
+      // 192 rows a tile where that fills the rounds of the 256 CUs better by a sixteenth or more (half a tile
+      // an expert is lost; the gradient of 32,768 rows 1024 -> 4096: 290 us, 256 rows 312; 24 experts of 600 rows,
+      // 1120 -> 1888: 78 and 95; where both fill them, 609,756 rows 128 -> 2 x 256: 356 and 347)
       auto cost = [&](int bm) { return ceil_div<int64_t>((k.n_rows / bm + k.e / 2) * ceil_div(N, 256), 256) * bm; };
-      if (cost(192) < cost(256)) return run<T, OP, GLU, 192, 256, 2, 4, true>(k, s);
+      if (16 * cost(192) < 15 * cost(256)) return run<T, OP, GLU, 192, 256, 2, 4, true>(k, s);
     }
     return run<T, OP, GLU, 256, 256, 2, 4, true>(k, s);
   }
