@@ -121,7 +121,7 @@ bool grid_ok(const ts_groups* g, GroupOp op, int cin, int columns) {
     const int64_t tiles = static_cast<int64_t>(ceil_div(cin, 128)) * ceil_div(columns, 128);
     blocks = group_grid(group_chunks(g->n_rows, g->n_groups, group_chunk(g->n_rows, g->n_groups, cin, columns)), 1) * tiles;
   } else {
-    const int64_t runs = group_runs(g->n_rows, g->n_groups, group_few(op, g->n_rows, g->n_groups) ? 16 : 128);
+    const int64_t runs = group_runs(g->n_rows, g->n_groups, group_few(op, g->n_rows, g->n_groups, cin, columns) ? 16 : 128);
     blocks = group_grid(runs, static_cast<unsigned>(ceil_div(columns, 128)));
   }
   return blocks < (int64_t{1} << 22);
@@ -179,7 +179,7 @@ ts_status ts_rope_bwd(const ts_rope* r, const ts_rope_heads* q, const ts_rope_he
 }
 
 size_t ts_route_workspace_bytes(int64_t n, int n_experts, int top) {
-  if (check_route(n, n_experts, TS_F32, top) != TS_OK || n == 0 || route_small(n, top)) return 0;
+  if (check_route(n, n_experts, TS_F32, top) != TS_OK || n == 0 || route_small(n, n_experts, top)) return 0;
   return static_cast<size_t>(n_experts + 1) * (route_blocks(n, n_experts) + 1) * sizeof(int32_t);
 }
 
@@ -254,7 +254,7 @@ ts_status ts_group_fwd(const ts_groups* g, const void* x, int cin, const void* w
   k.y = y;
   k.h_out = h;
   if (glu) k.ldw = 2 * cout;
-  return status(group_few(kGroupFwd, k.n_rows, k.e) ? launch_group_few(k, kGroupFwd, dtype, glu != 0, stream)
+  return status(group_few(kGroupFwd, k.n_rows, k.e, cin, k.ldw) ? launch_group_few(k, kGroupFwd, dtype, glu != 0, stream)
                                                     : launch_group(k, kGroupFwd, dtype, glu != 0, stream));
 }
 
@@ -270,7 +270,7 @@ ts_status ts_group_bwd_dgrad(const ts_groups* g, const void* dy, int cout, const
   k.w = w;
   k.h = h;
   k.y = dx;
-  return status(group_few(kGroupDgrad, k.n_rows, k.e) ? launch_group_few(k, kGroupDgrad, dtype, h != nullptr, stream)
+  return status(group_few(kGroupDgrad, k.n_rows, k.e, cin, cin) ? launch_group_few(k, kGroupDgrad, dtype, h != nullptr, stream)
                                                       : launch_group(k, kGroupDgrad, dtype, h != nullptr, stream));
 }
 

@@ -224,7 +224,7 @@ __device__ __forceinline__ float sigmoid(float a) {
 }
 
 // group.hip, group_few.hip
-bool group_few(GroupOp op, int64_t n_rows, int e);
+bool group_few(GroupOp op, int64_t n_rows, int e, int cin, int columns);
 hipError_t launch_group(GroupK& k, GroupOp op, ts_dtype dt, bool glu, hipStream_t s);
 hipError_t launch_group_few(GroupK& k, GroupOp op, ts_dtype dt, bool glu, hipStream_t s);
 int group_chunk(int64_t n_rows, int e, int cin, int cout);

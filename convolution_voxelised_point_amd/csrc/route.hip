@@ -10,8 +10,11 @@
 // without atomics on memory: blocks own runs of rows and count their pairs per expert, a
 // block per expert adds up these counts, and every block gives its pairs their places, wave
 // after wave, by counting the lanes before that chose the same expert.  Pairs without an
-// expert form one more bucket behind the last.  Small calls do all of it in one block (39
-// rows: one launch instead of three).
+// expert form one more bucket behind the last.  Small calls do all of it in one block.
+//
+// 304,878 rows of 64 bf16 logits, top 2: 28 us for the picks (vector instructions, 81% of the issue
+// cycles; the logits alone are 8 us of reading), 4.7 and 8 for the places, 21 for the gradient over all
+// experts (4.2 TB/s).  39 rows of 8: 5 us, a chain of loads and passes.
 #include "act8.h"
 #include "lanes.h"
 #include "launch.h"
@@ -407,7 +410,7 @@ void run(const RouteK& k, bool back, hipStream_t s) {
     return;
   }
   const size_t lds = static_cast<size_t>(kRouteWaves) * (k.e + 1) * sizeof(int32_t);
-  if (route_small(k.n, k.top)) {
+  if (route_small(k.n, k.e, k.top)) {
     k_route_small<T, VEC><<<1, kRouteThreads, lds, s>>>(k);
     return;
   }
@@ -421,8 +424,7 @@ void run(const RouteK& k, bool back, hipStream_t s) {
 
 hipError_t launch_route(RouteK& k, ts_dtype dt, bool back, hipStream_t s) {
   if (k.n == 0) return back ? hipSuccess : fill_i64(k.starts, k.e + 1, 0, s);
-  k.log_lanes = 0;
-  while ((8 << k.log_lanes) < k.e) ++k.log_lanes;
+  k.log_lanes = route_log_lanes(k.e);
   k.bits = 1;
   while ((1 << k.bits) < k.e + 1) ++k.bits;
   const bool vec = k.e % 8 == 0 && ((reinterpret_cast<uintptr_t>(k.logits) | reinterpret_cast<uintptr_t>(k.dlogits)) & 15) == 0;

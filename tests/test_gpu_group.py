@@ -116,6 +116,9 @@ LONG = [  # long runs of the weight gradient, and many of them; many groups of m
     ([9000, 0, 4100, 300], 264, 520, ("wgrad",)), ([40000, 7, 23000], 256, 256, ("wgrad",)),
     ([5, 0, 900] * 90, 512, 512, ("wgrad",)), ([700, 0, 1200] * 24, 64, 256, ("fwd", "glu", "wgrad")),
     ([700, 0, 1200] * 24, 256, 64, ("dgrad", "glu_dgrad")),
+    # many groups of few rows and many columns
+    ([1, 0, 3, 9] * 16, 128, 1024, ("fwd", "glu")), ([20, 0, 3, 9] * 16, 77, 1029, ("fwd", "glu")),
+    ([1, 0, 3, 9] * 16, 1024, 128, ("dgrad", "glu_dgrad")), ([1, 0, 3, 9] * 16, 1029, 77, ("dgrad", "glu_dgrad")),
     ([50000, 0, 30000], 515, 517, ("wgrad",)), ([50000, 30000], 1024, 1024, ("wgrad",)), ([70000, 30000], 128, 1024, ("wgrad",)),
 ]
 
