@@ -5,7 +5,11 @@
 //
 // Memory bound: every grouped row is read (and written) once; a thread owns 8 channels
 // of a row, so a row is one or a few wide accesses wherever it lies.  Gathering by
-// `place` keeps the order of the sum fixed, and needs no atomics.  Sums are fp32.
+// `place` keeps the order of the sum fixed, and needs no atomics.  Sums are fp32.  Results are
+// stored past the L2, which nothing reads them from (both passes 119 -> 109 us).
+//
+// 304,878 rows of 2 experts of 8, 128 channels, bf16: 36 us (239 MB, 6.6 TB/s: part of what the
+// products wrote is still in the last-level cache), backward 57 (400 MB, 7.0 TB/s likewise).
 #include "act8.h"
 #include "lanes.h"
 #include "launch.h"
@@ -46,7 +50,7 @@ __device__ __forceinline__ void put_unit(T* row, int c0, int c, bool vec, const 
   store_once(row + c0, v);
 }
 
-// AHEAD grouped rows of a row are read at once.
+// AHEAD grouped rows of a row are read at once: as many as there mostly are, up to 4.
 template <typename T, int AHEAD>
 __global__ __launch_bounds__(256) void k_combine_fwd(const CombineK k) {
   const int64_t items = k.n * k.units;

@@ -9,6 +9,9 @@
 //     into fragments of 8 rows of one column; column j of every lane's 8 makes matrix
 //     instruction j.
 //   input gradient: rows of W run along the reduction and are fragments as they lie.
+//
+// One row to 2 of 8 experts, 256 -> 2 x 512, fp16: 5 us, the latency of one load and one sum.  8
+// experts of 2048 x 2048, 24 rows each: 22.5 us (67 MB, 3 TB/s).
 #include "group.h"
 
 namespace ts {

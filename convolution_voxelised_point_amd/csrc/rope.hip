@@ -15,6 +15,10 @@
 // Angles.  The product of coordinate and frequency is formed and reduced to an eighth of a
 // turn either way in fp64 (a position of 32,768 times 1 rad needs 15 bits more than fp32
 // has), sine and cosine there are Taylor polynomials in fp32, off by about 2^-24.
+//
+// 304,878 voxels of 4 + 4 heads of 32, bf16: forward 58 us (317 MB, 5.5 TB/s), backward 96 (473 MB,
+// 4.9 TB/s: fewer waves, for the sums of dw) and 5 for dw.  102,835 of 6 + 3 heads of 40, fp32: 54
+// and 93.  Results are stored past the L2, which nothing reads them from (both passes 184 -> 174 us).
 #include "common.h"
 #include "lanes.h"
 #include "launch.h"
