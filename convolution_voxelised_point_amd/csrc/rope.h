@@ -41,6 +41,7 @@ struct RopeK {
 
 // Blocks of the backward pass at most, of 2048 channels or more: each leaves one share of dw.
 inline int rope_blocks(int64_t n, int heads, int d) {
+  if (heads > 0 && n >= 1 << 21) return 1024;  // (the product below stays within 64 bits)
   const int64_t b = ceil_div<int64_t>(n * heads * d, 2048);
   return static_cast<int>(b < 1024 ? b : 1024);
 }

@@ -83,6 +83,15 @@ def test_rope_heads(ts):
     assert 0 < ts._lib_rope_workspace_bytes(ctypes.byref(rope(ts, n=(1 << 31) - 1, d=128, pairs=(20, 20, 20))), 65535, 65535) < 1 << 24
 
 
+@pytest.mark.parametrize("n", [1, 1 << 20, (1 << 21) - 1, 1 << 21, 1 << 40, (1 << 63) - 1])
+def test_rope_workspace_of_any_length(ts, n):
+    """Two sides' shares of dw from at most 1024 blocks, of 2048 channels or more."""
+    for h, d in ((1, 1), (4, 32), (65535, 128)):
+        blocks = min(-(-n * h * d // 2048), 1024)
+        pairs = (0, 0, 0) if d == 1 else (6, 6, 4)
+        assert ts._lib_rope_workspace_bytes(ctypes.byref(rope(ts, n=n, d=d, pairs=pairs)), h, 0) == 2 * blocks * d * 4
+
+
 def test_route_refuses(ts):
     bad, no = ts.TS_ERR_INVALID_ARG, ts.TS_ERR_UNSUPPORTED
     out = [FAKE] * 5
