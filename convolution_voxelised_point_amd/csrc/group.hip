@@ -755,6 +755,8 @@ void run(GroupK& k, hipStream_t s) {
                    (!k.rows || k.n_src * k.cin < (int64_t{1} << 31) - 8);  // rows looked up have 32-bit offsets
   if (!vec) return run<T, OP, GLU, 128, 128, 2, 2, false>(k, s);
   const int N = OP == kGroupDgrad ? k.cin : k.ldw;
+  // (Forward, rows an expert, us large / 128 x 128: 64 experts of 1024 x 1376, 384: 117 / 97, 768: 196 / 192; 16 of 512 x
+  // 512, 256: 16.2 / 11.1, 1024: 19.5 / 21.9; 8 of 1024 x 2048, 256: 25.5 / 22.0, 512: 28.5 / 33.8, 6000: 195 / 223.)
   const bool large = OP == kGroupWgrad ? large_wgrad(k.n_rows, k.e, k.cin, k.cout) : N >= 256 && k.n_rows / k.e >= 512;
   // (with glu the input gradient's epilogue is most of its work where the reduction is short: two
   // blocks a CU take turns at it; 609,756 rows 128 -> 2 x 256 333 us instead of 348)

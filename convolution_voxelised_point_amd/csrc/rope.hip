@@ -426,7 +426,8 @@ void run(RopeK& k, bool back, hipStream_t s) {
   for (RopeSide& side : k.side)
     if (side.heads > 1) side.by_heads = static_cast<unsigned>((uint64_t{1} << 32) / side.heads + 1);
   // Rows of a tile: 1024 items, in a table of at most 32 KB; fewer where that leaves CUs without a
-  // tile, though on the way back no fewer than give each block one.
+  // tile, though on the way back no fewer than give each block one (440 rows of 4 heads of 40, both
+  // ways: 46 us, with tiles of one row 118).
   const int heads = k.side[0].heads + k.side[1].heads;
   int64_t rows = 4 * kRopeThreads / (heads << k.log_lanes);
   const int64_t few = back ? std::max<int64_t>(k.n / 512, ceil_div<int64_t>(k.n, k.blocks)) : k.n / 512;
