@@ -36,6 +36,7 @@ struct RopeK {
   // filled in by the launcher
   int slots, turned_slots, log_lanes, table_pairs, rows;
   unsigned by_pairs;
+  bool mixed;
   int64_t tiles;
 };
 

@@ -81,7 +81,7 @@ __device__ __forceinline__ Slot slot_of(const RopeK& k, int s) {
   if (IL) {
     o.a = 2 * p0;
     o.b = 2 * p0 + V;
-    o.pair = p0;
+    o.pair = p0 < k.pairs ? p0 : -1;
   } else if (rest) {
     o.a = 2 * k.pairs + p0;
     o.b = o.a + k.rest;
@@ -146,6 +146,28 @@ __device__ __forceinline__ void fill_angles(const RopeK& k, int64_t row0, int ro
   }
 }
 
+// The V pairs whose angles are cs, turned by them, or (BACK) the other way; only the first `n`, if SOME: adjacent
+// pairs behind the turned ones may share their access, and stay as they are (products with a cosine of 1 and
+// a sine of 0 do not leave them so beside a neighbour's infinity).
+template <int V, bool BACK, bool SOME>
+__device__ __forceinline__ void turn(const float2* cs, int n, float (&a)[V], float (&b)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float2 t = cs[e];
+    const float p = a[e], q = b[e];
+    const float ta = fmaf(p, t.x, BACK ? q * t.y : -q * t.y), tb = BACK ? fmaf(q, t.x, -p * t.y) : fmaf(p, t.y, q * t.x);
+    a[e] = !SOME || e < n ? ta : p;
+    b[e] = !SOME || e < n ? tb : q;
+  }
+}
+template <int V, bool IL, bool BACK>
+__device__ __forceinline__ void turn(const RopeK& k, const Slot& s, const float2* row, float (&a)[V], float (&b)[V]) {
+  if (s.pair < 0) return;
+  if (IL && k.mixed) turn<V, BACK, true>(row + s.pair, k.pairs - s.pair, a, b);
+  else
+    turn<V, BACK, false>(row + s.pair, V, a, b);
+}
+
 // This thread's items of a block's rows: a slot of a head each.
 struct Item {
   int row, head;
@@ -198,16 +220,7 @@ __device__ __forceinline__ void rope_fwd_side(const RopeK& k, const RopeSide& si
         for (int e = 0; e < V; ++e) a[e] *= rstd * wa[e], b[e] *= rstd * wb[e];
         last *= rstd * w_odd;
       }
-      if (s.pair >= 0 && k.table_pairs) {
-        const float2* t = tab + (it[u].on ? it[u].row * k.table_pairs : 0) + s.pair;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float2 cs = t[e];
-          const float p = a[e], q = b[e];
-          a[e] = fmaf(p, cs.x, -q * cs.y);
-          b[e] = fmaf(p, cs.y, q * cs.x);
-        }
-      }
+      turn<V, IL, false>(k, s, tab + (it[u].on ? it[u].row * k.table_pairs : 0), a, b);
       if (it[u].on) {
         T* p = y + (it[u].row * side.y_stride + it[u].head * k.d);
         store2<T, V, IL>(p, s, a, b);
@@ -271,16 +284,7 @@ __device__ __forceinline__ void rope_bwd_side(const RopeK& k, const RopeSide& si
       float a[V], b[V];
       to_pairs<T, V, IL>(gv[u], a, b);
       float last = static_cast<float>(godd[u]);
-      if (s.pair >= 0 && k.table_pairs) {
-        const float2* t = tab + (it[u].on ? it[u].row * k.table_pairs : 0) + s.pair;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float2 cs = t[e];
-          const float p = a[e], q = b[e];
-          a[e] = fmaf(p, cs.x, q * cs.y);
-          b[e] = fmaf(q, cs.x, -p * cs.y);
-        }
-      }
+      turn<V, IL, true>(k, s, tab + (it[u].on ? it[u].row * k.table_pairs : 0), a, b);
       if (side.w) {
         float xa[V], xb[V];
         to_pairs<T, V, IL>(v[u], xa, xb);
@@ -421,7 +425,9 @@ void run(RopeK& k, bool back, hipStream_t s) {
   if (k.slots < 1) k.slots = 1;
   k.log_lanes = 0;
   while ((1 << k.log_lanes) < k.slots) ++k.log_lanes;
-  k.table_pairs = k.pairs == 0 ? 0 : IL ? k.d / 2 : k.pairs;
+  // (mixed: an access of adjacent pairs holds turned ones and others; it then reads the table past them)
+  k.mixed = IL && k.pairs > 0 && k.pairs < k.d / 2 && (k.pairs % V != 0 || k.pairs > k.d / 2 - V);
+  k.table_pairs = k.mixed ? k.d / 2 : k.pairs;
   if (k.table_pairs > 1) k.by_pairs = static_cast<unsigned>((uint64_t{1} << 32) / k.table_pairs + 1);
   for (RopeSide& side : k.side)
     if (side.heads > 1) side.by_heads = static_cast<unsigned>((uint64_t{1} << 32) / side.heads + 1);

@@ -1,0 +1,51 @@
+"""Rotation of query and key heads where its parts must not touch each other: channels that are
+not turned, beside values that are no numbers."""
+import pytest
+import torch
+
+from test_gpu_rope import DT, inputs
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+PARTLY = [  # d, pairs: channels left over behind whole and cut accesses, an odd one last, one pair turned
+    (40, (6, 6, 4)), (32, (3, 3, 3)), (41, (6, 6, 4)), (77, (5, 0, 6)), (24, (1, 0)), (7, (1, 1)), (128, (20, 20, 20)),
+]
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("il", [False, True], ids=["halves", "interleaved"])
+@pytest.mark.parametrize("shape", PARTLY, ids=str)
+def test_channels_that_are_not_turned(ts, shape, il, dt):
+    """An infinite or NaN value in one of them stays there, in the results and in the gradients."""
+    d, pairs = shape
+    q, k, coords, freqs, pairs, _, _, dq, dk = inputs(dt, 30, 2, 1, d, pairs, norm=False)
+    q, dq, kw = q.clone(), dq.clone(), dict(interleaved=il)
+    want = ts.rope_fwd(q, k, coords, freqs, pairs, **kw)[0]
+    back = ts.rope_bwd(dq, dk, q, k, coords, freqs, pairs, **kw).dq
+    at = [(i, i % 2, 2 * sum(pairs) + i % (d - 2 * sum(pairs)), (INF, -INF, NAN)[i % 3]) for i in range(30)]
+    for r, h, c, v in at:
+        q[r, h, c] = dq[r, h, c] = v
+    y = ts.rope_fwd(q, k, coords, freqs, pairs, **kw)[0]
+    g = ts.rope_bwd(dq, dk, q, k, coords, freqs, pairs, **kw).dq
+    for r, h, c, v in at:
+        for got, ref in ((y, want), (g, back)):
+            assert torch.equal(got[r, h, c].cpu(), torch.tensor(v).to(got.dtype)) or (v != v and bool(got[r, h, c].isnan())), (r, h, c, v)
+            got[r, h, c] = ref[r, h, c]
+    assert torch.equal(y, want) and torch.equal(g, back)
+
+
+@pytest.mark.parametrize("il", [False, True], ids=["halves", "interleaved"])
+@pytest.mark.parametrize("shape", PARTLY, ids=str)
+def test_channels_that_are_not_turned_with_norm(ts, shape, il):
+    """With the norm an infinite one makes the others of its head zeros (x / infinity) and itself NaN, as the formula has
+    it; an infinite gradient there reaches no other channel of dw."""
+    d, pairs = shape
+    q, k, coords, freqs, pairs, wq, wk, dq, dk = inputs("f32", 30, 2, 1, d, pairs)
+    q, dq, kw, c = q.clone(), dq.clone(), dict(wq=wq, wk=wk, interleaved=il), 2 * sum(pairs)
+    dq[3, 1, c] = INF
+    dw = ts.rope_bwd(dq, dk, q, k, coords, freqs, pairs, **kw).dwq
+    assert not dw[c].isfinite() and dw.isfinite().sum() == d - 1
+    q[5, 0, c] = INF
+    y = ts.rope_fwd(q, k, coords, freqs, pairs, **kw)[0]
+    assert y[5, 0, c].isnan() and (y[5, 0] == 0).sum() == d - 1
