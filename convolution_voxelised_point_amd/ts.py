@@ -1137,7 +1137,8 @@ def _rope_bwd_side(g, x, q, w, y, new):
     else:
         _need(y is not None, "rope: results for q and k")
         yst = _rope_rows(y, q, (n, h, d), "rope: results are like q and k")
-    dw = None if w is None else torch.empty(d, dtype=torch.float32, device=q.device)
+    # (a call without any heads launches nothing)
+    dw = None if w is None else (torch.empty if h else torch.zeros)(d, dtype=torch.float32, device=q.device)
     return y, dw, ctypes.byref(TsRopeHeads(h, st, 0, gst, yst, x.data_ptr(), _ptr(w), None, g.data_ptr(), y.data_ptr(), _ptr(dw)))
 
 

@@ -713,7 +713,9 @@ typedef struct ts_rope_heads {
 ts_status ts_rope_fwd(const ts_rope* r, const ts_rope_heads* q, const ts_rope_heads* k, hipStream_t stream);
 
 /* Its backward pass.  dw is summed in a fixed order, without atomics; ws holds
- * ts_rope_workspace_bytes(r, heads of q, heads of k).  Errors as ts_rope_fwd. */
+ * ts_rope_workspace_bytes(r, heads of q, heads of k).  Zeros where n is 0 or only the other
+ * side has heads; a call in which neither has any does nothing, and leaves dw as it was.
+ * Errors as ts_rope_fwd. */
 size_t ts_rope_workspace_bytes(const ts_rope* r, int hq, int hk);
 ts_status ts_rope_bwd(const ts_rope* r, const ts_rope_heads* q, const ts_rope_heads* k, void* ws, size_t ws_bytes,
                       hipStream_t stream);

@@ -49,3 +49,20 @@ def test_channels_that_are_not_turned_with_norm(ts, shape, il):
     q[5, 0, c] = INF
     y = ts.rope_fwd(q, k, coords, freqs, pairs, **kw)[0]
     assert y[5, 0, c].isnan() and (y[5, 0] == 0).sum() == d - 1
+
+
+@pytest.mark.parametrize("n", [0, 30])
+@pytest.mark.parametrize("hq,hk", [(0, None), (0, 0), (2, 0), (0, 1)])
+def test_gradients_of_weights_without_heads(ts, hq, hk, n):
+    """An empty sum is zero, whatever the memory held before."""
+    d, pairs = 32, (8, 8)
+    new = lambda h: None if h is None else torch.randn(n, h, d, device="cuda")  # noqa: E731
+    q, k, dq, dk = new(hq), new(hk), new(hq), new(hk)
+    wq, wk = torch.ones(d, device="cuda"), None if hk is None else torch.ones(d, device="cuda")
+    coords, freqs = torch.ones(n, 3, dtype=torch.int32, device="cuda"), ts.rope_freqs(pairs)
+    junk = [torch.full((d,), NAN, device="cuda") for _ in range(64)]
+    del junk  # what the allocator hands out next
+    r = ts.rope_bwd(dq, dk, q, k, coords, freqs, pairs, wq=wq, wk=wk)
+    for h, dw in ((hq, r.dwq), (hk, r.dwk)):
+        assert (dw is None) == (h is None) and (dw is None or bool(dw.isfinite().all()))
+        assert h is None or n * h > 0 or (dw == 0).all()
