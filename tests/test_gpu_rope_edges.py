@@ -66,3 +66,23 @@ def test_gradients_of_weights_without_heads(ts, hq, hk, n):
     for h, dw in ((hq, r.dwq), (hk, r.dwk)):
         assert (dw is None) == (h is None) and (dw is None or bool(dw.isfinite().all()))
         assert h is None or n * h > 0 or (dw == 0).all()
+
+
+@pytest.mark.parametrize("reach", [30, 1 << 20])
+def test_sine_and_cosine(ts, reach):
+    """Of (1, 0) the rotation returns cosine and sine themselves.  Over an eighth of a turn either way, in units of
+    E = 2^-24: the angle x <= 0.79 is rounded once, by E / 2, which moves the sine by that and the cosine by 0.71 of it; the
+    last addition is off by E / 2 of a result below 1.  Sine: x^3 <= 0.49 by E / 4 and its factor 1/6 by E / 16, 0.1 E in all.
+    Cosine: x^2 <= 0.62 by E / 2, which moves it by 0.46 of that, and the factor of x^2 by E / 4: 0.4 E in all.  Coefficients and
+    the terms left out 0.05 E, the 2^19 turns of the farthest positions 0.01 E.  So sine 1.16 E, cosine 1.32 E."""
+    n, p = 200000, 16
+    g = torch.Generator().manual_seed(reach)
+    q = torch.zeros(n, 1, 2 * p, device="cuda")
+    q[..., :p] = 1.0
+    coords = torch.randint(-reach, reach + 1, (n, 3), generator=g, dtype=torch.int32)
+    freqs = torch.rand(p, generator=g) * 3
+    y = ts.rope_fwd(q, None, coords.cuda(), freqs.cuda(), (p // 2, p // 2))[0][:, 0].cpu().double()
+    at = torch.tensor([1] * (p // 2) + [2] * (p // 2))
+    angle = coords[:, at].double() * freqs.double()  # exact: 21 and 24 bits
+    for got, ref in ((y[:, :p], torch.cos(angle)), (y[:, p:], torch.sin(angle))):
+        assert float((got - ref).abs().max()) <= 1.4 * 2.0 ** -24
