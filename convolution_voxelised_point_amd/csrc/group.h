@@ -2,11 +2,10 @@
 #pragma once
 
 #include "common.h"
+#include "group_plan.h"
 #include "launch.h"
 
 namespace ts {
-
-enum GroupOp { kGroupFwd = 0, kGroupDgrad = 1, kGroupWgrad = 2 };
 
 struct GroupK {
   const void* x;      // fwd, wgrad: [n_src][cin], read by `rows`
@@ -45,8 +44,6 @@ __device__ __forceinline__ GroupBlock group_block(int64_t runs, unsigned n_tiles
 }
 // Blocks to launch for at most `runs` runs (those of rows that no expert owns among them).
 inline int64_t group_grid(int64_t runs, unsigned n_tiles) { return (runs * n_tiles + 7) / 8 * 8 + 8; }
-// Runs at most: every expert may end in a short one, and so do the rows that none owns.
-inline int64_t group_runs(int64_t n_rows, int e, int len) { return n_rows / len + e + 2; }
 
 typedef unsigned gu32x4 __attribute__((ext_vector_type(4)));
 typedef float gf32x4 __attribute__((ext_vector_type(4)));
@@ -223,12 +220,18 @@ __device__ __forceinline__ float sigmoid(float a) {
   return __builtin_amdgcn_rcpf(fmaf(e, fmaf(lo, 0.693147181f, 1.f), 1.f));
 }
 
+// How a call is done.
+inline GroupForm form_of(const GroupK& k, GroupOp op, bool glu) {
+  uintptr_t bits = 0;
+  for (const void* p : {k.x, k.dy, k.w, k.h, static_cast<const void*>(k.y), static_cast<const void*>(k.h_out),
+                        static_cast<const void*>(k.dw), static_cast<const void*>(k.part)})
+    bits |= reinterpret_cast<uintptr_t>(p);
+  return group_form(op, glu, (bits & 15) == 0, k.n_rows, k.e, k.cin, k.cout,
+                    k.rows && op != kGroupDgrad ? k.n_src : 0);
+}
+
 // group.hip, group_few.hip
-bool group_few(GroupOp op, int64_t n_rows, int e, int cin, int columns);
 hipError_t launch_group(GroupK& k, GroupOp op, ts_dtype dt, bool glu, hipStream_t s);
 hipError_t launch_group_few(GroupK& k, GroupOp op, ts_dtype dt, bool glu, hipStream_t s);
-int group_chunk(int64_t n_rows, int e, int cin, int cout);
-// Partial sums of the weight gradient at most: every expert may end in a short one.
-inline int64_t group_chunks(int64_t n_rows, int e, int chunk) { return n_rows / chunk + e; }
 
 }  // namespace ts

@@ -39,7 +39,7 @@
 namespace ts {
 namespace {
 
-constexpr int kStep = 64;
+constexpr int kStep = kGroupStep;
 constexpr int kRowHalf = 1024;  // row numbers of the weight gradient in half of their place in LDS
 
 // 16 bytes per lane from a buffer into LDS: lane l writes dst + 16 l (dst is the same in the
@@ -724,20 +724,6 @@ __global__ __launch_bounds__(256) void k_group_sum(const GroupK k) {
   }
 }
 
-// Whether the weight gradient's tiles are 256 x 256 (a block a CU) rather than 128 x 128 (two).  Large
-// ones read less, but where there is about one for each CU a long expert's keep the others waiting, and a
-// short run is all prologue and epilogue.  (Rows an expert, us large / small: 16 experts of 512 x 512,
-// 256: 37 / 31, 1024: 46 / 50, 8000: 120 / 191; 8 of 1024 x 1024, 512: 66 / 50, 2048: 108 / 103, 8000: 271 / 315;
-// 16 of 1024 x 2048, 512: 95 / 83, 2000: 226 / 242; 64 of 1024 x 1376, 96: 108 / 124, 768: 263 / 335.)
-bool large_wgrad(int64_t n_rows, int e, int cin, int cout) {
-  if (cin < 256 || cout < 256) return false;
-  const int64_t tiles = static_cast<int64_t>(ceil_div(cin, 256)) * ceil_div(cout, 256), whole = e * tiles;
-  const int64_t rows_a_cu = n_rows / 256 * tiles;
-  return whole >= 1024 || rows_a_cu >= (whole < 128 ? 200 : 1536);
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 template <typename T, GroupOp OP, bool GLU, int BM, int BN, int WM, int WN, bool VEC>
 void run(GroupK& k, hipStream_t s) {
   const int N = OP == kGroupDgrad ? k.cin : k.cout;
@@ -750,27 +736,13 @@ void run(GroupK& k, hipStream_t s) {
 
 template <typename T, GroupOp OP, bool GLU>
 void run(GroupK& k, hipStream_t s) {
-  const bool vec = k.cin % 8 == 0 && k.cout % 8 == 0 && aligned16(k.x) && aligned16(k.dy) && aligned16(k.w) && aligned16(k.h) &&
-                   aligned16(k.y) && aligned16(k.h_out) && aligned16(k.dw) && aligned16(k.part) &&
-                   (!k.rows || k.n_src * k.cin < (int64_t{1} << 31) - 8);  // rows looked up have 32-bit offsets
-  if (!vec) return run<T, OP, GLU, 128, 128, 2, 2, false>(k, s);
-  const int N = OP == kGroupDgrad ? k.cin : k.ldw;
-  // (Forward, rows an expert, us large / 128 x 128: 64 experts of 1024 x 1376, 384: 117 / 97, 768: 196 / 192; 16 of 512 x
-  // 512, 256: 16.2 / 11.1, 1024: 19.5 / 21.9; 8 of 1024 x 2048, 256: 25.5 / 22.0, 512: 28.5 / 33.8, 6000: 195 / 223.)
-  const bool large = OP == kGroupWgrad ? large_wgrad(k.n_rows, k.e, k.cin, k.cout) : N >= 256 && k.n_rows / k.e >= 512;
-  // (with glu the input gradient's epilogue is most of its work where the reduction is short: two
-  // blocks a CU take turns at it; 609,756 rows 128 -> 2 x 256 333 us instead of 348)
-  if (large && !(OP == kGroupDgrad && GLU && k.cout <= 256)) {
-    if constexpr (OP != kGroupWgrad) {
-      // 192 rows a tile where that fills the rounds of the 256 CUs better by a sixteenth or more (half a tile
-      // an expert is lost; the gradient of 32,768 rows 1024 -> 4096: 290 us, 256 rows 312; 24 experts of 600 rows,
-      // 1120 -> 1888: 78 and 95; where both fill them, 609,756 rows 128 -> 2 x 256: 356 and 347)
-      auto cost = [&](int bm) { return ceil_div<int64_t>((k.n_rows / bm + k.e / 2) * ceil_div(N, 256), 256) * bm; };
-      if (16 * cost(192) < 15 * cost(256)) return run<T, OP, GLU, 192, 256, 2, 4, true>(k, s);
-    }
-    return run<T, OP, GLU, 256, 256, 2, 4, true>(k, s);
+  const GroupForm f = form_of(k, OP, GLU);
+  if (!f.whole) return run<T, OP, GLU, 128, 128, 2, 2, false>(k, s);
+  if (f.rows == 128) return run<T, OP, GLU, 128, 128, 2, 2, true>(k, s);
+  if constexpr (OP != kGroupWgrad) {
+    if (f.rows == 192) return run<T, OP, GLU, 192, 256, 2, 4, true>(k, s);
   }
-  run<T, OP, GLU, 128, 128, 2, 2, true>(k, s);
+  run<T, OP, GLU, 256, 256, 2, 4, true>(k, s);
 }
 
 template <typename T>
@@ -785,19 +757,6 @@ void run(GroupK& k, GroupOp op, bool glu, hipStream_t s) {
 }
 
 }  // namespace
-
-// Rows of a run of the weight gradient.  Where every expert's rows can be one run without leaving
-// blocks idle, a run is what one block has to do on average; otherwise as many runs as there are
-// blocks (an expert may end in a short one).
-int group_chunk(int64_t n_rows, int e, int cin, int cout) {
-  const bool large = large_wgrad(n_rows, e, cin, cout);
-  const int edge = large ? 256 : 128, slots = large ? 256 : 512;
-  const int64_t tiles = static_cast<int64_t>(ceil_div(cin, edge)) * ceil_div(cout, edge), whole = e * tiles;
-  const int64_t share = whole < slots / 2 ? slots - whole : slots;
-  const int64_t c = n_rows / share * tiles + ceil_div<int64_t>(n_rows % share * tiles, share);
-  const int64_t most = int64_t{1} << 28;  // (row numbers of a run lie within 32 bits)
-  return static_cast<int>(((c < 256 ? 256 : c > most ? most : c) + kStep - 1) / kStep * kStep);
-}
 
 hipError_t launch_group(GroupK& k, GroupOp op, ts_dtype dt, bool glu, hipStream_t s) {
   if (dt == TS_F16) run<_Float16>(k, op, glu, s);

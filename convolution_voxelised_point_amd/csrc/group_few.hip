@@ -1,5 +1,5 @@
 // Products grouped by expert for few rows an expert: serving single tokens and small batches
-// (forward), and the input gradient of the same sizes (group_few below says which).
+// (forward), and the input gradient of the same sizes (group_few says which).
 //
 // The weights are all there is to read, so they go straight from memory to the registers of
 // the matrix instructions, each once per 16 MT rows.  A wave multiplies up to 16 MT rows
@@ -206,28 +206,23 @@ __global__ __launch_bounds__(kWaves * 64) void k_group_few(const GroupK k) {
   }
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 template <typename T, GroupOp OP, bool GLU, int MT>
-void run(GroupK& k, hipStream_t s) {
+void run(GroupK& k, bool whole, hipStream_t s) {
   const int N = OP == kGroupDgrad ? k.cin : k.cout;
   k.n_tiles = ceil_div(N, GLU && OP == kGroupFwd ? kCols / 2 : kCols);
   const unsigned grid = static_cast<unsigned>(group_grid(group_runs(k.n_rows, k.e, 16 * MT), k.n_tiles));
-  const bool vec = k.cin % 8 == 0 && k.cout % 8 == 0 && aligned16(k.x) && aligned16(k.dy) && aligned16(k.w) && aligned16(k.h) &&
-                   aligned16(k.y) && aligned16(k.h_out);
-  if (vec)
+  if (whole)
     k_group_few<T, OP, GLU, MT, true><<<grid, kWaves * 64, 0, s>>>(k);
   else
     k_group_few<T, OP, GLU, MT, false><<<grid, kWaves * 64, 0, s>>>(k);
 }
 
-// Rows of a run: 32 where most experts have more than 16.  (8 experts of 2048 x 2048, us with 16 / 32:
-// 24 rows each 22.5 / 23.1, 48 rows 32.1 / 23.9; the gradient 25.5 / 27.8 and 42.2 / 28.0.)
 template <typename T, GroupOp OP, bool GLU>
 void run(GroupK& k, hipStream_t s) {
-  if (k.n_rows / k.e <= 24) run<T, OP, GLU, 1>(k, s);
+  const GroupForm f = form_of(k, OP, GLU);
+  if (f.rows == 16) run<T, OP, GLU, 1>(k, f.whole, s);
   else
-    run<T, OP, GLU, 2>(k, s);
+    run<T, OP, GLU, 2>(k, f.whole, s);
 }
 
 template <typename T>
@@ -237,17 +232,6 @@ void run(GroupK& k, GroupOp op, bool glu, hipStream_t s) {
 }
 
 }  // namespace
-
-// Whether this kernel does a call.  Its blocks split the reduction, which is what counts where tiles of
-// 128 columns leave CUs idle; where they do not, the other kernel's copies into LDS have more under way.
-// (Rows an expert, us here / there, weights not in the caches: 8 experts of 2048 x 2048, 8: 22 / 37, 48: 24 / 38;
-// 32 of 1024 x 1024, 4: 17 / 23, 24: 22 / 23, 48: 27 / 24; 64 of them, 1: 20 / 24, 4: 30 / 27, 32: 43 / 30; 64 of 1023 x 1025,
-// whose rows go through registers there, 8: 41 / 59, 48: 76 / 69, the gradient 2: 60 / 40.)
-bool group_few(GroupOp op, int64_t n_rows, int e, int cin, int columns) {
-  const int64_t tiles = (n_rows < e ? n_rows : e) * ceil_div(columns, 128);
-  const bool loose = op == kGroupFwd && (cin % 8 != 0 || columns % 8 != 0);
-  return n_rows / e <= (tiles <= 128 ? 48 : tiles < 384 ? 16 : loose ? 8 : 1);
-}
 
 hipError_t launch_group_few(GroupK& k, GroupOp op, ts_dtype dt, bool glu, hipStream_t s) {
   if (dt == TS_F16) run<_Float16>(k, op, glu, s);
