@@ -39,9 +39,10 @@ inline int route_log_lanes(int e) {
 inline bool route_small(int64_t n, int e, int top) { return n * top <= kRouteSmall && n << route_log_lanes(e) <= 2048; }
 
 // Blocks of 1024 threads: two for each CU, and at most 2^18 counts.
+constexpr int kRouteMaxBlocks = 512;
 inline int route_blocks(int64_t n, int e) {
   const int64_t rows = 1024 >> route_log_lanes(e), b = (n + rows - 1) / rows, most = (1 << 18) / (e + 1);
-  const int64_t cap = most < 512 ? most : 512;
+  const int64_t cap = most < kRouteMaxBlocks ? most : kRouteMaxBlocks;
   return static_cast<int>(b < cap ? b : cap);
 }
 

@@ -248,27 +248,23 @@ __device__ __forceinline__ int32_t scan_inclusive(int32_t x) {
 
 // counts[bucket][block] -> the pairs of the bucket in the blocks before; their number behind them.
 __global__ __launch_bounds__(256) void k_route_scan(const RouteK k) {
+  static_assert(kRouteMaxBlocks <= 2 * 256, "two counts a thread");
   __shared__ int32_t wave_sum[4];
   int32_t* row = k.counts + static_cast<int64_t>(blockIdx.x) * k.blocks;
-  const int wave = threadIdx.x >> 6;
-  int32_t carry = 0;
-  for (int base = 0; base < k.blocks; base += 512) {  // two counts a thread; once for up to 512 blocks
-    const int at = base + static_cast<int>(threadIdx.x) * 2;
-    const int32_t a = at < k.blocks ? row[at] : 0, b = at + 1 < k.blocks ? row[at + 1] : 0;
-    const int32_t inc = scan_inclusive(a + b);
-    if (base) __syncthreads();
-    if ((threadIdx.x & 63) == 63) wave_sum[wave] = inc;
-    __syncthreads();
-    int32_t sum = carry + inc - a - b;
+  const int wave = threadIdx.x >> 6, at = static_cast<int>(threadIdx.x) * 2;
+  const int32_t a = at < k.blocks ? row[at] : 0, b = at + 1 < k.blocks ? row[at + 1] : 0;
+  const int32_t inc = scan_inclusive(a + b);
+  if ((threadIdx.x & 63) == 63) wave_sum[wave] = inc;
+  __syncthreads();
+  int32_t sum = inc - a - b, all = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      sum += w < wave ? wave_sum[w] : 0;
-      carry += wave_sum[w];
-    }
-    if (at < k.blocks) row[at] = sum;
-    if (at + 1 < k.blocks) row[at + 1] = sum + a;
+  for (int w = 0; w < 4; ++w) {
+    sum += w < wave ? wave_sum[w] : 0;
+    all += wave_sum[w];
   }
-  if (threadIdx.x == 0) k.counts[static_cast<int64_t>(k.e + 1) * k.blocks + blockIdx.x] = carry;
+  if (at < k.blocks) row[at] = sum;
+  if (at + 1 < k.blocks) row[at + 1] = sum + a;
+  if (threadIdx.x == 0) k.counts[static_cast<int64_t>(k.e + 1) * k.blocks + blockIdx.x] = all;
 }
 
 // Places of one block's pairs.
