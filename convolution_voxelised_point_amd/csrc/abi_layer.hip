@@ -114,7 +114,8 @@ ts_status check_groups(const ts_groups* g, int cin, int cout, ts_dtype dt) {
   return TS_OK;
 }
 
-// Blocks are fewer than 2^22: a launch may have 2^32 threads.
+// Tiles are fewer than 2^22.  The kernel for few rows has a block of 512 threads for each, and a launch may
+// have 2^32 threads; the other one's few blocks number them in 32 bits, in bands of four rows of tiles.
 bool grid_ok(const ts_groups* g, GroupOp op, int cin, int columns) {
   int64_t blocks;
   if (op == kGroupWgrad) {

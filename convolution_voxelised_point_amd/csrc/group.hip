@@ -165,12 +165,12 @@ struct Operand {
 };
 
 // A tile and where this lane's copies of its first step come from.
-template <int CA, int CB>
+template <int CA>
 struct TileSource {
   GroupTile t;
   int m0, n0, steps, K;
   // VEC: offsets within the buffers.  Otherwise: rows of x or dy (-1: none); columns of W or dy
-  uint32_t va[CA], vb[CB];
+  uint32_t va[CA], vb;
 };
 
 // BM x BN results a tile, WM x WN waves.  VEC: rows in whole, aligned 16-byte chunks;
@@ -212,26 +212,24 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     return in < per_xcd && tile < total ? tile : -1;
   };
   // This lane's copies: the row of the operand's tile, and the chunk of it.  Of the next copy the
-  // row is NT / kPerRow further; the chunk is the same for rows 16 apart, and two take turns
-  // for rows 8 apart.
+  // row is NT / kPerRow further, and the chunk the same.
   constexpr int NEXT_A = NT / OA::kPerRow, NEXT_B = NT / OB::kPerRow;
-  static_assert(NEXT_A % 8 == 0 && NEXT_B % 8 == 0, "rows 8 apart have the same places, or two in turn");
-  constexpr int TURN_A = A_ACROSS && NEXT_A % 16 ? 2 : 1, TURN_B = B_ACROSS && NEXT_B % 16 ? 2 : 1;
-  typedef TileSource<A_ACROSS ? 1 : CA, OP == kGroupDgrad ? 1 : TURN_B> Source;
+  static_assert(NEXT_A % (A_ACROSS ? 16 : 8) == 0 && NEXT_B % (B_ACROSS ? 16 : 8) == 0, "such rows store their chunks in the same places");
+  typedef TileSource<A_ACROSS ? 1 : CA> Source;
   // (computed where they are used: the accumulators leave few registers to keep them in)
   auto row_a = [&]() { return fresh(tid) / OA::kPerRow; };
   auto row_b = [&]() { return fresh(tid) / OB::kPerRow; };
-  auto chunk_a = [&](int i) {
+  auto chunk_a = [&]() {
     const int t = fresh(tid), r = t / OA::kPerRow;
-    return A_ACROSS ? across_at(r + i % TURN_A * NEXT_A, t % OA::kPerRow) : along_at(r, t % 8);
+    return A_ACROSS ? across_at(r, t % OA::kPerRow) : along_at(r, t % 8);
   };
-  auto chunk_b = [&](int i) {
+  auto chunk_b = [&]() {
     const int t = fresh(tid), r = t / OB::kPerRow;
-    return B_ACROSS ? across_at(r + i % TURN_B * NEXT_B, t % OB::kPerRow) : along_at(r, t % 8);
+    return B_ACROSS ? across_at(r, t % OB::kPerRow) : along_at(r, t % 8);
   };
   // its first column in the tile; with glu 16 columns of a, then 16 of b
-  auto col_b = [&](int i) {
-    const int ch = chunk_b(i);
+  auto col_b = [&]() {
+    const int ch = chunk_b();
     return GLU && B_ACROSS ? (ch >> 2) * 16 + (ch & 1) * 8 : ch * 8;
   };
 
@@ -268,17 +266,14 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
           src = -1;
         }
         x.va[i] = !VEC || src < 0 ? static_cast<uint32_t>(src)
-                                  : static_cast<uint32_t>(src) * static_cast<uint32_t>(x.K * 2) + static_cast<uint32_t>(chunk_a(0) * 16);
+                                  : static_cast<uint32_t>(src) * static_cast<uint32_t>(x.K * 2) + static_cast<uint32_t>(chunk_a() * 16);
       }
     }
     if constexpr (OP == kGroupDgrad) {
-      x.vb[0] = static_cast<uint32_t>(row_b() * k.ldw * 2 + chunk_b(0) * 16);
+      x.vb = static_cast<uint32_t>(row_b() * k.ldw * 2 + chunk_b() * 16);
     } else {
-#pragma unroll
-      for (int i = 0; i < TURN_B; ++i) {
-        const int c = x.n0 + col_b(i), at = c + (GLU ? ((chunk_b(i) >> 1) & 1) * k.cout : 0);
-        x.vb[i] = c >= k.cout ? kNowhere : static_cast<uint32_t>(VEC ? (row_b() * k.ldw + at) * 2 : at);
-      }
+      const int c = x.n0 + col_b(), at = c + (GLU ? ((chunk_b() >> 1) & 1) * k.cout : 0);
+      x.vb = c >= k.cout ? kNowhere : static_cast<uint32_t>(VEC ? (row_b() * k.ldw + at) * 2 : at);
     }
   };
 
@@ -314,7 +309,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
           buffer_of(base + first * k.cin, (k.rows ? k.n_src : static_cast<int64_t>(left < kStep ? left : kStep)) * k.cin * 2);
 #pragma unroll
       for (int i = 0; i < CA; ++i) {
-        const int r = row_a() + i * NEXT_A, c = x.m0 + chunk_a(i) * 8;
+        const int r = row_a() + i * NEXT_A, c = x.m0 + chunk_a() * 8;
         const int32_t row = k.rows ? row_ids[i] : r;
         bool in = r < left && c < k.cin;
         if (in && k.rows && (row < 0 || row >= k.n_src)) {
@@ -331,7 +326,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       const bool gather = OP == kGroupFwd && k.rows;
       const int64_t first = gather ? 0 : x.t.row0;
       const __amdgpu_buffer_rsrc_t buf = buffer_of(base + first * x.K, (gather ? k.n_src : static_cast<int64_t>(x.t.rows)) * x.K * 2);
-      const int c = chunk_a(0) * 8;
+      const int c = chunk_a() * 8;
 #pragma unroll
       for (int i = 0; i < CA; ++i) {
         if constexpr (VEC) {
@@ -355,13 +350,13 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       char* dst = lds_b + slot * OB::kBytes + (i * NT + wave * 64) * 16;
       const int r = row_b() + i * NEXT_B;
       if constexpr (OP == kGroupDgrad) {
-        const int c = chunk_b(0) * 8;
+        const int c = chunk_b() * 8;
         if constexpr (VEC)
-          to_lds(buf, c < left ? x.vb[0] + static_cast<uint32_t>(i * NEXT_B * k.ldw + from) * 2 : kNowhere, dst);
+          to_lds(buf, c < left ? x.vb + static_cast<uint32_t>(i * NEXT_B * k.ldw + from) * 2 : kNowhere, dst);
         else
           rb[i] = c < left && r < rows ? load_unmoved(base + (first + r) * k.ldw, from + c, x.K) : gu32x4{0u, 0u, 0u, 0u};
       } else {
-        const uint32_t v = x.vb[i % TURN_B];
+        const uint32_t v = x.vb;
         if constexpr (VEC)
           to_lds(buf, further(v, static_cast<uint32_t>(i * NEXT_B * k.ldw * 2)), dst);
         else
@@ -374,16 +369,16 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     if constexpr (!VEC) {
 #pragma unroll
       for (int i = 0; i < CA; ++i) {
-        const int by = A_ACROSS ? over(x.m0 + chunk_a(i) * 8, k.cin) : over(s * kStep + chunk_a(0) * 8, x.K);
+        const int by = A_ACROSS ? over(x.m0 + chunk_a() * 8, k.cin) : over(s * kStep + chunk_a() * 8, x.K);
         if (__builtin_amdgcn_ballot_w64(by != 0)) ra[i] = moved_down(ra[i], by);
         *reinterpret_cast<gu32x4*>(lds_a + slot * OA::kBytes + (i * NT + tid) * 16) = ra[i];
       }
 #pragma unroll
       for (int i = 0; i < CB; ++i) {
         int by;
-        if constexpr (OP == kGroupDgrad) by = over(s * kStep + chunk_b(0) * 8, x.K);
+        if constexpr (OP == kGroupDgrad) by = over(s * kStep + chunk_b() * 8, x.K);
         else
-          by = x.vb[i % TURN_B] == kNowhere ? 0 : over(static_cast<int>(x.vb[i % TURN_B]), end_b(x.vb[i % TURN_B]));
+          by = x.vb == kNowhere ? 0 : over(static_cast<int>(x.vb), end_b(x.vb));
         if (__builtin_amdgcn_ballot_w64(by != 0)) rb[i] = moved_down(rb[i], by);
         *reinterpret_cast<gu32x4*>(lds_b + slot * OB::kBytes + (i * NT + tid) * 16) = rb[i];
       }
