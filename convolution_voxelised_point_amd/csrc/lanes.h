@@ -37,9 +37,9 @@ __device__ __forceinline__ uint32_t min_lanes(uint32_t x, int lanes) {
 }
 
 // exp(d) for d <= 0, off by about 3 * 2^-24 of itself: exp2 of the product with log2(e) in two
-// parts (one alone is off by |d| 2^-24), at half of expf's instructions.  NaN stays.
+// parts (one alone is off by |d| 2^-24), at half of expf's instructions.  NaN stays (in the maximum too).
 __device__ __forceinline__ float exp_below(float d) {
-  d = d < -1e4f ? -1e4f : d;
+  d = __builtin_elementwise_maximum(d, -1e4f);
   const float hi = d * 1.44269504f, lo = fmaf(d, 1.92596299e-8f, fmaf(d, 1.44269504f, -hi));
   const float e = __builtin_amdgcn_exp2f(hi);
   return fmaf(e, lo * 0.693147181f, e);

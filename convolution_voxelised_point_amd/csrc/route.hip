@@ -4,7 +4,7 @@
 // 8 experts each and agree on the largest.  Values are compared as integers that order like
 // the floats (-0 made 0, NaN above infinity); 16-bit ones share a word with their expert's number,
 // so that one maximum finds both and the lowest expert wins among equals.  Gates are a softmax
-// in fp32.  (All of this is vector instructions, about as long as reading 64 bf16 logits.)
+// in fp32.
 //
 // The chosen pairs (row, j) are then put in order of their expert, by a counting sort
 // without atomics on memory: blocks own runs of rows and count their pairs per expert, a
@@ -12,9 +12,10 @@
 // after wave, by counting the lanes before that chose the same expert.  Pairs without an
 // expert form one more bucket behind the last.  Small calls do all of it in one block.
 //
-// 304,878 rows of 64 bf16 logits, top 2: 28 us for the picks (vector instructions, 81% of the issue
-// cycles; the logits alone are 8 us of reading), 4.7 and 8 for the places, 21 for the gradient over all
-// experts (4.2 TB/s).  39 rows of 8: 5 us, a chain of loads and passes.
+// 304,878 rows of 64 bf16 logits, top 2 over all experts: 29 us for the picks, 4.7 and 8 for the places, 21 for the
+// gradient (4.2 TB/s).  Reading the logits is 8 us of the 29; the rest is vector instructions, which take 85% of the
+// issue cycles: about 370 for the 8 logits of a thread, 50 of them for each pick, 75 for the exponentials
+// over all experts, most of the others to make the keys.  39 rows of 8: 5 us, a chain of loads and passes.
 #include "act8.h"
 #include "lanes.h"
 #include "launch.h"
@@ -151,11 +152,12 @@ __device__ __forceinline__ void pick(const RouteK& k, int64_t r0, int64_t r1, fl
       }
     }
     if (k.over_all) {
-      // (the exponent in one part: off by |d| 2^-24 at the distance d below the largest, where a term
-      // is worth exp(d) of the sum, which is less than the sum's own rounding)
+      // (the terms that the backward pass forms again.  With the exponent in one part, off by |d| 1.2 2^-24 at the
+      // distance d, 511 experts at 3 to 7 below the largest left its gate off by 8.0 2^-24 at most, instead of
+      // 5.9; k_route 28 us instead of 29)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        sum += on && lane * 8 + i < k.e ? __builtin_amdgcn_exp2f((static_cast<float>(z[i]) - best) * 1.44269504f) : 0.f;
+        sum += on && lane * 8 + i < k.e ? exp_below(static_cast<float>(z[i]) - best) : 0.f;
       sum = sum_lanes(sum, g);
     }
     // a row's threads lie in one wave: what its first one wrote is there
