@@ -1326,8 +1326,8 @@ def combine_fwd(y: torch.Tensor, place: torch.Tensor, gates: Optional[torch.Tens
 def combine_bwd(dout: torch.Tensor, y: torch.Tensor, place: torch.Tensor, gates: torch.Tensor,
                 err_flags: Optional[torch.Tensor] = None, into: Optional[torch.Tensor] = None,
                 stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
-    """(dy, dgates) of combine_fwd; dy is written to `into` (which may be y) or to a new
-    matrix, whose rows that no place names are not written."""
+    """(dy, dgates) of combine_fwd; dy is written to `into` (which may be y, if no two places
+    name the same row) or to a new matrix, whose rows that no place names are not written."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return combine_bwd(dout, y, place, gates, err_flags, into)
