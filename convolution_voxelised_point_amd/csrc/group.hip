@@ -584,7 +584,10 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       typedef unsigned u2 __attribute__((ext_vector_type(2)));
       T* y = static_cast<T*>(k.y);
       // Blocks j0 and j1 of a row, whose first columns are c and c + 16: 64 bytes of 4 lanes at
-      // once (a lane's own 8 bytes would make twice the requests).
+      // once (a lane's own 8 bytes would make twice the requests).  Results stay in L2.  (Stored past it, us
+      // plain / past, 609,756 rows 128 -> 2 x 256 with h: the same call over and over 363 / 276, but 345 / 392 after any
+      // other one, the product that reads y 128 / 111, the gradient with glu 327 / 353 as part of a step; a layer's
+      // products and sum forward 527 / 553, and back 1223 / 1277.)
       auto store = [&](T* row, int c, gf32x4 p, gf32x4 q) {
         const u2 a = __builtin_bit_cast(u2, __builtin_convertvector(p, t4)), b = __builtin_bit_cast(u2, __builtin_convertvector(q, t4));
         unsigned a0 = a[0], a1 = a[1], b0 = b[0], b1 = b[1];

@@ -74,8 +74,17 @@ inline GroupForm group_form(GroupOp op, bool glu, bool aligned, int64_t n_rows, 
   if (op == kGroupWgrad) return large_wgrad(n_rows, e, cin, cout) ? GroupForm{false, 256, 256, true} : GroupForm{false, 128, 128, true};
   // (Forward, rows an expert, us large / 128 x 128: 64 experts of 1024 x 1376, 384: 117 / 97, 768: 196 / 192; 16 of 512 x
   // 512, 256: 16.2 / 11.1, 1024: 19.5 / 21.9; 8 of 1024 x 2048, 256: 25.5 / 22.0, 512: 28.5 / 33.8, 6000: 195 / 223.)
-  // (with glu the input gradient's epilogue is most of its work where the reduction is short: two
-  // blocks a CU take turns at it; 609,756 rows 128 -> 2 x 256 333 us instead of 348)
+  // With glu the input gradient's epilogue, which reads and writes 2 N columns, is most of its work where the
+  // reduction (cout) is short: two blocks a CU take turns at it.  (bf16, us 128 x 128 / 192 or 256 rows, at a reduction
+  // of 64, 128, 256 | beyond the rule 264, 512, 1024:
+  //   8 experts of 76,000 rows, N 256: 313 / 328, 336 / 349, 378 / 378 | 435 / 428, 464 / 449, 646 / 599
+  //                             N 512: 651 / 614, 675 / 651, 745 / 702 | 876 / 791, 898 / 815
+  //   16 of 2000,               N 256: 28.6 / 26.5, 30.2 / 28.1, 34.0 / 30.2 | 36.6 / 32.6, 46.3 / 42.0, 62.3 / 52.7
+  //                             N 512: 53.6 / 57.3, 54.9 / 60.3, 59.0 / 63.4 | 63.7 / 68.3, 70.4 / 72.8, 94.6 / 90.8
+  //   24 of 600,                N 256: 18.9 / 25.1, 20.0 / 27.0, 23.2 / 28.6 | 24.3 / 30.5, 24.4 / 32.6, 30.2 / 40.7
+  // So it costs up to 8% where large tiles would fill the CUs, and where they do not, beyond it, the small ones were
+  // faster too.  The forward product with glu, whose epilogue only writes, has no such rule: 8 of 76,000, 2 x 256
+  // columns, 64, 128, 256: 295 / 255, 382 / 332, 466 / 376; 16 of 2000: 27.2 / 28.9, 28.6 / 31.8, 33.7 / 35.7.)
   if (N < 256 || n_rows / e < 512 || (op == kGroupDgrad && glu && cout <= 256)) return {false, 128, 128, true};
   // 192 rows a tile where that fills the rounds of the 256 CUs better by a sixteenth or more (half a tile
   // an expert is lost; the gradient of 32,768 rows 1024 -> 4096: 290 us, 256 rows 312; 24 experts of 600 rows,

@@ -788,7 +788,7 @@ ts_status ts_group_bwd_dgrad(const ts_groups* g, const void* dy, int cout, const
 
 /* dw: device float [n_groups][cin][cout], overwritten.  The rows of a group are summed in
  * runs, and those in a fixed order; ws (device) holds ts_group_wgrad_workspace_bytes: a place
- * like dw[e] for every group and one more for each run, so always more than dw itself.  (The
+ * like dw[e] for every group and one more for each run, so never less than dw itself.  (The
  * place of a group whose rows are one run is not touched.) */
 size_t ts_group_wgrad_workspace_bytes(const ts_groups* g, int cin, int cout);
 ts_status ts_group_bwd_wgrad(const ts_groups* g, const void* x, int cin, const void* dy, int cout, ts_dtype dtype, float* dw,
