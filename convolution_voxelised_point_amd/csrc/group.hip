@@ -27,9 +27,9 @@
 // silu(a) b is formed in the lane that holds both.  The input gradient with glu goes on
 // through silu(a) b in its epilogue.
 //
-// 32,768 rows to 16 experts of 1024 x 4096, bf16: forward 290 us (0.95 PFLOP/s), input gradient 295,
-// weight gradient 325 and 9 for its partial sums; matrix instructions keep 38 to 50% of a SIMD's
-// cycles busy, the rest is a tile's prologue and epilogue, LDS latency and experts that end in a
+// 32,768 rows to 16 experts of 1024 x 4096, bf16: forward 292 us (0.94 PFLOP/s), input gradient 298,
+// weight gradient 336 and 9 for its partial sums; the matrix units are busy for 49, 51 and 38% of
+// the cycles, the rest is a tile's prologue and epilogue, LDS latency and experts that end in a
 // part of a tile.  609,756 rows to 8 experts of 128 -> 2 x 256 with silu(a) b and h: 346 us, its
 // gradient 351: two steps a tile, so writing 0.94 GB (0.67 GB, and 0.4 read) is most of the work.
 // 4,999 x 3 rows of 77 -> 133: 11, 11 and 20 us, latency.  256 rows to 64 experts of 1024 x 1024:

@@ -18,7 +18,7 @@
 // most 1.2 and 1.4 times 2^-24.
 //
 // 304,878 voxels of 4 + 4 heads of 32, bf16: forward 58 us (317 MB, 5.5 TB/s), backward 96 (473 MB,
-// 4.9 TB/s: fewer waves, for the sums of dw) and 5 for dw.  102,835 of 6 + 3 heads of 40, fp32: 54
+// 4.9 TB/s: fewer waves, for the sums of dw) and 5 for dw.  102,835 of 6 + 3 heads of 40, fp32: 53
 // and 93.  Results are stored past the L2, which nothing reads them from (both passes 184 -> 174 us).
 #include "common.h"
 #include "lanes.h"
